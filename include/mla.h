@@ -281,6 +281,79 @@ int mla_prefill_paged(const void* q, const void* k_pages, const void* v_pages, c
                       int page_size, int max_pages_per_seq, int64_t num_pages, int max_seqlen_q,
                       int total_q, float scale, void* out, float* lse, void* stream);
 
+/* One pass that prepares a step's queries and latent keys and writes the keys into the paged
+ * latent cache that mla_decode reads: norm, position rotation and (quantised) paged write.
+ * For token n at position x = positions[n] (all arithmetic in fp32, one rounding at the store):
+ *   key  : c = kv_in[n, :512]; c' = c / sqrt(mean(c^2) + eps) * kv_weight (kv_weight NULL: c' = c);
+ *          the latent row [c', rot(kv_in[n, 512:576], x)] goes to pool row slots[n], as bf16, or as
+ *          the codes of the values over kv_scale (nearest, ties to even; saturated to +-448 or
+ *          +-127; a NaN encodes as the e4m3 NaN, as int8 0).
+ *   query: v = q_in[n, h, :q_dim]; v' = v / sqrt(mean(v^2) + eps) * q_weight over the whole width
+ *          (q_weight NULL: v' = v); q_out[n, h] = [v'[:q_dim-64], rot(v'[q_dim-64:], x)].
+ *   rot  : pair i of 32 is columns (2i, 2i+1) (interleaved != 0) or (i, i+32); (a, b) becomes
+ *          (a cos - b sin, b cos + a sin) with cos = cos_sin[x, i], sin = cos_sin[x, 32 + i].
+ *   q_in, q_out : bf16, element [n, h, c] at n * token_stride + h * head_stride + c; strides are
+ *                 in elements, multiples of 8 (q_in's may be 0; q_out's rows may not overlap).
+ *                 q_out may be q_in with the same strides; else the two spans of memory are apart.
+ *                 q_in NULL: keys only (every q argument is ignored).
+ *   q_dim       : 64..576, a multiple of 8: 64 rotates a [.., 64] view alone (for example columns
+ *                 512.. of absorbed queries), 192 is the prefill's width.
+ *   q_weight    : [q_dim] bf16 or NULL.   kv_weight : [512] bf16 or NULL.
+ *   kv_in       : bf16 [num_tokens, 576], rows kv_in_token_stride apart (a multiple of 8).
+ *                 NULL: queries only (slots, kv_pages, num_slots are ignored).
+ *   cos_sin     : [max_positions, 64] fp32, 16-byte aligned.
+ *   positions   : [num_tokens] int32.
+ *   slots       : [num_tokens] int64: page id * page_size + offset of the key's pool row; negative =
+ *                 a padded token whose key is not stored (its queries still are).  Slots that are
+ *                 not negative must differ: a row that two tokens name holds bytes of either.
+ *   kv_pages    : the pool, num_slots = num_pages * page_size rows of 576 elements of kv_dtype.
+ *   kv_scale    : scale of an e4m3 or int8 pool (ignored for bf16).
+ * Pointers are 16-byte aligned (positions 4, slots 8).  Rows that no token names are left as
+ * they were.  num_tokens 0 does nothing.  Launched as a programmatic dependent like mla_decode.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (num_heads > 1024, another q_dim, num_tokens >
+ * 2^20, an MLA_KV_INT8_PAGE pool, whose page scales cannot follow new rows), MLA_ERR_CUDA.
+ * Device-side, recorded as MLA_ERR_DEVICE_ARG: a position outside [0, max_positions) (the token's
+ * rows are left unwritten; a padded token's position counts too unless kv_in alone is given) and a
+ * slot >= num_slots (its key is left unwritten). */
+int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head_stride, void* q_out,
+                  int64_t q_out_token_stride, int64_t q_out_head_stride, int num_heads, int q_dim,
+                  const void* q_weight, const void* kv_in, int64_t kv_in_token_stride, const void* kv_weight,
+                  float eps, const float* cos_sin, int max_positions, const int32_t* positions,
+                  const int64_t* slots, int num_tokens, int interleaved, void* kv_pages, int64_t num_slots,
+                  int kv_dtype, float kv_scale, void* stream);
+
+/* Eviction by accumulated attention weight: choose the keys that each request keeps and copy their
+ * latent rows, in order, into new pages of the same pool.  Request b with L = seq_lens[b] cached
+ * keys keeps K = min(keep_lens[b], L): the first s = min(sink, K), the last r = min(recent, K - s),
+ * and the K - s - r keys between them with the largest mass[b, j] (equal masses: the lower index;
+ * -0 equals 0; NaN is below every number).  With kept = those keys in ascending order:
+ *   row i of the destination pages = row kept[i] of the source pages, i < K
+ *   kept[b, i] = kept[i], mass_out[b, i] = mass[b, kept[i]], new_lens[b] = K
+ * Entries of kept and mass_out from K on, and pool rows that are no destination, are left as they
+ * were.  Rows are copied because a source page may be a prefix that other requests share; the
+ * caller releases the old pages.  Keys keep the rotation of their old positions.
+ *   kv_pages       : [num_pages, page_size, 576] of kv_dtype (bf16, e4m3 or int8).
+ *   page_table     : [batch, max_pages_per_seq] int32 source pages.
+ *   seq_lens, keep_lens : [batch] int32 (device).
+ *   mass           : fp32, row b at mass + b * mass_stride (elements; >= max_seq_len).
+ *   dst_page_table : [batch, max_dst_pages] int32 destination pages, which must be distinct and no
+ *                    source page of any request of the call.
+ *   max_seq_len, max_keep : host bounds on the lengths and on K.
+ *   kept, mass_out : row b at b * kept_stride / b * mass_out_stride (elements; >= max_keep).
+ *                    mass_out may not overlap mass, new_lens neither seq_lens nor keep_lens.
+ * Two kernels on `stream` (selection, copy), programmatic dependents like mla_decode.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (page_size not 8..256, batch > 65535,
+ * max_seq_len > 2^24, an MLA_KV_INT8_PAGE pool, whose codes mean something else under another
+ * page's scale), MLA_ERR_CUDA.  Device-side, recorded as MLA_ERR_DEVICE_ARG: a length below 0,
+ * beyond max_seq_len or beyond its page-table row, keep_lens[b] < 0, K beyond max_keep or the
+ * destination row (the request is skipped, nothing of it written), and a page id outside
+ * [0, num_pages) (its rows are not copied). */
+int mla_kv_evict(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype, const int32_t* page_table,
+                 int max_pages_per_seq, const int32_t* seq_lens, const int32_t* keep_lens, const float* mass,
+                 int64_t mass_stride, const int32_t* dst_page_table, int max_dst_pages, int batch, int sink,
+                 int recent, int max_seq_len, int max_keep, int32_t* kept, int64_t kept_stride,
+                 int32_t* new_lens, float* mass_out, int64_t mass_out_stride, void* stream);
+
 /* Read and clear the current device's status word after synchronising `stream`.
  * Returns MLA_OK, MLA_ERR_TIMEOUT or MLA_ERR_DEVICE_ARG (first recorded), or
  * MLA_ERR_CUDA if the read itself fails.  This call synchronises: keep it off the hot

@@ -26,8 +26,8 @@ namespace mla {
 __device__ unsigned int g_status_word = 0;
 
 namespace {
-
 constexpr int kMaxDevices = 64;
+}  // namespace
 
 unsigned* status_ptr() {
   static std::mutex mu;
@@ -43,6 +43,8 @@ unsigned* status_ptr() {
   return ptrs[dev];
 }
 
+namespace {
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
     void* ptr = nullptr;
@@ -56,11 +58,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Tiled tensor map (128-byte swizzle unless given).  dims/strides innermost first; strides
-// in bytes for dims 1..rank-1.
+}  // namespace
+
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
-              const uint64_t* strides, const uint32_t* box,
-              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+              const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
   cuuint64_t d[5];
@@ -79,9 +80,7 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base
   return r == CUDA_SUCCESS;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool page_size_ok(int P) { return P == 8 || P == 16 || P == 32 || P == 64 || P == 128 || P == 256; }
+namespace {
 
 thread_local cudaEvent_t g_prof_start = nullptr;
 thread_local cudaEvent_t g_prof_stop = nullptr;

@@ -1,0 +1,161 @@
+// mla_cache_api.cu -- host side of the entry points that keep the paged latent cache
+// (include/mla.h): mla_kv_append writes it and mla_kv_evict shrinks it.
+// Argument checks run before anything is enqueued; nothing is allocated and no stream is
+// synchronised.
+#include <cstring>
+
+#include "../../include/mla.h"
+#include "mla_internal.h"
+
+using namespace mla;
+
+namespace {
+
+// Whether heads x tokens rows of `dim` elements at these strides are rows of their own.
+bool rows_apart(int64_t token, int64_t head, int tokens, int heads, int dim) {
+  if (token < 0 || head < 0) return false;
+  if (tokens == 1 && heads == 1) return true;
+  if (tokens == 1) return head >= dim;
+  if (heads == 1) return token >= dim;
+  return (head >= dim && token >= (heads - 1) * head + dim) || (token >= dim && head >= (tokens - 1) * token + dim);
+}
+
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bn && y < x + an;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head_stride, void* q_out,
+                  int64_t q_out_token_stride, int64_t q_out_head_stride, int num_heads, int q_dim,
+                  const void* q_weight, const void* kv_in, int64_t kv_in_token_stride, const void* kv_weight, float eps,
+                  const float* cos_sin, int max_positions, const int32_t* positions, const int64_t* slots,
+                  int num_tokens, int interleaved, void* kv_pages, int64_t num_slots, int kv_dtype, float kv_scale,
+                  void* stream) {
+  const bool has_q = q_in != nullptr, has_kv = kv_in != nullptr;
+  if (num_tokens < 0 || max_positions < 1 || !(eps >= 0.f)) return MLA_ERR_INVALID_ARG;
+  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_E4M3 && kv_dtype != MLA_KV_INT8 && kv_dtype != MLA_KV_INT8_PAGE)
+    return MLA_ERR_INVALID_ARG;
+  if (has_q) {
+    if (num_heads < 1 || q_in_token_stride < 0 || q_in_head_stride < 0) return MLA_ERR_INVALID_ARG;
+    if (num_heads > 1024 || q_dim < 64 || q_dim > 576 || q_dim % 8 != 0) return MLA_ERR_UNSUPPORTED;
+  }
+  if (num_tokens > (1 << 20)) return MLA_ERR_UNSUPPORTED;
+  // the scale of a page that already holds rows cannot follow a new row's range
+  if (has_kv && kv_dtype == MLA_KV_INT8_PAGE) return MLA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return MLA_OK;
+  if (!has_q && !has_kv) return MLA_ERR_INVALID_ARG;
+  if (!cos_sin || !positions || !aligned(cos_sin, 16) || !aligned(positions, 4)) return MLA_ERR_INVALID_ARG;
+  if (has_q) {
+    if (!q_out || !aligned(q_in, 16) || !aligned(q_out, 16) || (q_weight && !aligned(q_weight, 16)))
+      return MLA_ERR_INVALID_ARG;
+    if ((q_in_token_stride | q_in_head_stride | q_out_token_stride | q_out_head_stride) % 8 != 0)
+      return MLA_ERR_INVALID_ARG;
+    if (!rows_apart(q_out_token_stride, q_out_head_stride, num_tokens, num_heads, q_dim)) return MLA_ERR_INVALID_ARG;
+    // in place, or apart: a warp writes its row while others still read theirs
+    const bool in_place = q_in == q_out && (num_tokens == 1 || q_in_token_stride == q_out_token_stride) &&
+                          (num_heads == 1 || q_in_head_stride == q_out_head_stride);
+    const auto span = [&](int64_t token, int64_t head) {
+      return static_cast<size_t>((num_tokens - 1) * token + (num_heads - 1) * head + q_dim) * 2;
+    };
+    if (!in_place && overlap(q_in, span(q_in_token_stride, q_in_head_stride), q_out, span(q_out_token_stride, q_out_head_stride)))
+      return MLA_ERR_INVALID_ARG;
+  }
+  if (has_kv) {
+    if (!kv_pages || !slots || num_slots < 1 || !aligned(kv_in, 16) || !aligned(kv_pages, 16) || !aligned(slots, 8) ||
+        (kv_weight && !aligned(kv_weight, 16)) || kv_in_token_stride < 0 || kv_in_token_stride % 8 != 0)
+      return MLA_ERR_INVALID_ARG;
+    if (kv_dtype != MLA_KV_BF16 && !(kv_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  }
+  AppendParams p;
+  memset(&p, 0, sizeof p);
+  p.status = status_ptr();
+  if (!p.status) return MLA_ERR_CUDA;
+  if (has_q) {
+    p.q_in = static_cast<const __nv_bfloat16*>(q_in);
+    p.q_out = static_cast<__nv_bfloat16*>(q_out);
+    p.q_in_token = q_in_token_stride;
+    p.q_in_head = q_in_head_stride;
+    p.q_out_token = q_out_token_stride;
+    p.q_out_head = q_out_head_stride;
+    p.heads = num_heads;
+    p.q_dim = q_dim;
+    p.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
+  }
+  if (has_kv) {
+    p.kv_in = static_cast<const __nv_bfloat16*>(kv_in);
+    p.kv_in_token = kv_in_token_stride;
+    p.kv_weight = static_cast<const __nv_bfloat16*>(kv_weight);
+    p.slots = slots;
+    p.kv_pages = static_cast<uint8_t*>(kv_pages);
+    p.num_slots = num_slots;
+  }
+  p.eps = eps;
+  p.cos_sin = cos_sin;
+  p.max_positions = max_positions;
+  p.positions = positions;
+  p.tokens = num_tokens;
+  p.interleaved = interleaved;
+  p.kv_dtype = kv_dtype;
+  p.kv_scale = kv_scale;
+  return launch_kv_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_kv_evict(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype, const int32_t* page_table,
+                 int max_pages_per_seq, const int32_t* seq_lens, const int32_t* keep_lens, const float* mass,
+                 int64_t mass_stride, const int32_t* dst_page_table, int max_dst_pages, int batch, int sink, int recent,
+                 int max_seq_len, int max_keep, int32_t* kept, int64_t kept_stride, int32_t* new_lens, float* mass_out,
+                 int64_t mass_out_stride, void* stream) {
+  if (batch < 1 || num_pages < 1 || max_pages_per_seq < 1 || max_dst_pages < 1 || sink < 0 || recent < 0 ||
+      max_seq_len < 0 || max_keep < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_E4M3 && kv_dtype != MLA_KV_INT8 && kv_dtype != MLA_KV_INT8_PAGE)
+    return MLA_ERR_INVALID_ARG;
+  // a row's codes mean something else under another page's scale
+  if (kv_dtype == MLA_KV_INT8_PAGE) return MLA_ERR_UNSUPPORTED;
+  if (!page_size_ok(page_size) || batch > 65535 || max_seq_len > (1 << 24)) return MLA_ERR_UNSUPPORTED;
+  if (!kv_pages || !page_table || !seq_lens || !keep_lens || !mass || !dst_page_table || !kept || !new_lens || !mass_out)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(kv_pages, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(keep_lens, 4) ||
+      !aligned(mass, 4) || !aligned(dst_page_table, 4) || !aligned(kept, 4) || !aligned(new_lens, 4) ||
+      !aligned(mass_out, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (mass_stride < max_seq_len || kept_stride < max_keep || mass_out_stride < max_keep) return MLA_ERR_INVALID_ARG;
+  // the copy reads mass while it writes mass_out, and lengths while it writes new ones
+  const size_t B = static_cast<size_t>(batch);
+  if (overlap(mass, B * mass_stride * 4, mass_out, B * mass_out_stride * 4) || overlap(seq_lens, B * 4, new_lens, B * 4) ||
+      overlap(keep_lens, B * 4, new_lens, B * 4))
+    return MLA_ERR_INVALID_ARG;
+  EvictParams p;
+  memset(&p, 0, sizeof p);
+  p.status = status_ptr();
+  if (!p.status) return MLA_ERR_CUDA;
+  p.kv_pages = static_cast<uint8_t*>(kv_pages);
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.row_bytes = kLatentDim * (kv_dtype == MLA_KV_BF16 ? 2 : 1);
+  p.page_table = page_table;
+  p.max_pages = max_pages_per_seq;
+  p.seq_lens = seq_lens;
+  p.keep_lens = keep_lens;
+  p.mass = mass;
+  p.mass_stride = mass_stride;
+  p.dst_page_table = dst_page_table;
+  p.max_dst_pages = max_dst_pages;
+  p.B = batch;
+  p.sink = sink;
+  p.recent = recent;
+  p.max_seq = max_seq_len;
+  p.max_keep = max_keep;
+  p.kept = kept;
+  p.kept_stride = kept_stride;
+  p.new_lens = new_lens;
+  p.mass_out = mass_out;
+  p.mass_out_stride = mass_out_stride;
+  return launch_kv_evict(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // extern "C"

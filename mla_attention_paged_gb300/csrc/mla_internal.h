@@ -64,6 +64,65 @@ struct PrefillParams {
   int64_t num_pages;
 };
 
+// One pass that norms and rotates queries and latent keys and writes the keys into the pages.
+struct AppendParams {
+  const __nv_bfloat16* q_in;    // null: keys only
+  __nv_bfloat16* q_out;
+  int64_t q_in_token, q_in_head, q_out_token, q_out_head;  // strides in elements
+  int heads, q_dim;
+  const __nv_bfloat16* q_weight;   // [q_dim] or null (no norm)
+  const __nv_bfloat16* kv_in;      // null: queries only
+  int64_t kv_in_token;
+  const __nv_bfloat16* kv_weight;  // [512] or null (no norm)
+  float eps;
+  const float* cos_sin;         // [max_positions][64]: 32 cosines, 32 sines
+  int max_positions;
+  const int32_t* positions;
+  const int64_t* slots;
+  int tokens;
+  int interleaved;
+  uint8_t* kv_pages;
+  int64_t num_slots;
+  int kv_dtype;
+  float kv_scale;
+  unsigned* status;
+};
+
+// Eviction: selection of the kept keys, then the copy of their rows into new pages.
+struct EvictParams {
+  uint8_t* kv_pages;
+  int64_t num_pages;
+  int page_size, row_bytes;
+  const int32_t* page_table;
+  int max_pages;
+  const int32_t* seq_lens;
+  const int32_t* keep_lens;
+  const float* mass;
+  int64_t mass_stride;
+  const int32_t* dst_page_table;
+  int max_dst_pages;
+  int B, sink, recent, max_seq, max_keep;
+  int32_t* kept;
+  int64_t kept_stride;
+  int32_t* new_lens;
+  float* mass_out;
+  int64_t mass_out_stride;
+  unsigned* status;
+};
+
+// Host helpers of mla_api.cu that every entry point uses.
+unsigned* status_ptr();  // device address of the current device's status word
+// Tiled tensor map (128-byte swizzle unless given).  dims/strides innermost first; strides
+// in bytes for dims 1..rank-1.
+bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
+              const uint64_t* strides, const uint32_t* box,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool page_size_ok(int P) { return P == 8 || P == 16 || P == 32 || P == 64 || P == 128 || P == 256; }
+
+cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t stream);
+
 // Decode: split-KV partial kernel (tensor maps over q and the latent pool).
 cudaError_t launch_decode_partial(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv,
                                   int head_groups, cudaStream_t stream);

@@ -30,7 +30,7 @@ MLA_KV_INT8_PAGE = 3
 EXPORTED = ["mla_decode_plan", "mla_decode", "mla_decode_partial", "mla_decode_combine", "mla_decode_noalloc",
             "mla_decode_int8_paged",
             "mla_prefill_varlen", "mla_prefill_paged", "mla_get_status", "mla_status_string", "mla_version", "mla_set_profile_events",
-            "mla_profile_elapsed_ms", "mla_selftest_wait_timeout"]
+            "mla_profile_elapsed_ms", "mla_selftest_wait_timeout", "mla_kv_append", "mla_kv_evict"]
 
 
 class MlaError(RuntimeError):
@@ -73,6 +73,12 @@ def _load() -> ctypes.CDLL:
     lib.mla_prefill_varlen.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, i32, f32, P, P, P]
     lib.mla_prefill_paged.restype = i32
     lib.mla_prefill_paged.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, i64, i32, i32, f32, P, P, P]
+    lib.mla_kv_append.restype = i32
+    lib.mla_kv_append.argtypes = [P, i64, i64, P, i64, i64, i32, i32, P, P, i64, P, f32, P, i32, P, P, i32, i32, P, i64,
+                                  i32, f32, P]
+    lib.mla_kv_evict.restype = i32
+    lib.mla_kv_evict.argtypes = [P, i64, i32, i32, P, i32, P, P, P, i64, P, i32, i32, i32, i32, i32, i32, P, i64, P, P,
+                                 i64, P]
     lib.mla_get_status.restype = i32
     lib.mla_get_status.argtypes = [P]
     lib.mla_status_string.restype = ctypes.c_char_p
@@ -107,6 +113,43 @@ def _stream_handle(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+_POOL_DTYPE = {MLA_KV_BF16: (torch.bfloat16,), MLA_KV_E4M3: (torch.uint8, torch.float8_e4m3fn),
+               MLA_KV_INT8: (torch.int8,), MLA_KV_INT8_PAGE: (torch.int8,)}
+
+
+def _refuse(what: str, why: str):
+    raise MlaError(MLA_ERR_INVALID_ARG, f"{what} ({why})")
+
+
+def _want(what, device, tensors):
+    """Argument checks of one call: (name, tensor, dtypes, shape or None) each on `device`, contiguous."""
+    for name, t, dtypes, shape in tensors:
+        if t.device != device or device.type != "cuda":
+            _refuse(what, f"{name} is on {t.device}")
+        if t.dtype not in dtypes:
+            _refuse(what, f"{name} is {t.dtype}")
+        if shape is not None and tuple(t.shape) != shape:
+            _refuse(what, f"{name} has shape {tuple(t.shape)}, not {shape}")
+        if not t.is_contiguous():
+            _refuse(what, f"{name} is not contiguous")
+
+
+def _want_pool(what, kv_pages, kv_dtype):
+    if kv_dtype not in _POOL_DTYPE:
+        _refuse(what, f"kv_dtype {kv_dtype}")
+    if kv_pages.dim() != 3 or kv_pages.shape[2] != 576:
+        _refuse(what, f"kv_pages has shape {tuple(kv_pages.shape)}")
+    _want(what, kv_pages.device, [("kv_pages", kv_pages, _POOL_DTYPE[kv_dtype], None)])
+
+
+def _call(what, device, stream, fn, *args):
+    """fn(*args, stream) on the tensors' own device: its current stream unless one is given."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(what, device, stream, fn, *args)
+    _check(fn(*args, _stream_handle(stream)), what)
 
 
 def decode_plan(seq_lens_host, q_len: int, num_heads: int, page_size: int, max_pages_per_seq: int,
@@ -248,6 +291,86 @@ def prefill_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                                _stream_handle(stream))
     _check(rc, "mla_prefill_paged")
     return out, lse
+
+
+def kv_append(q: torch.Tensor | None, kv: torch.Tensor | None, positions: torch.Tensor, slots: torch.Tensor | None,
+              cos_sin: torch.Tensor, kv_pages: torch.Tensor | None, kv_weight=None, q_weight=None, eps: float = 1e-6,
+              interleaved: bool = True, kv_dtype: int = MLA_KV_BF16, kv_scale: float = 1.0, q_out=None, stream=None):
+    """mla_kv_append through the C ABI: norm and rotate a step's queries [N,H,q_dim] and latent
+    keys [N,576], and write the keys into pool rows ``slots`` [N] int64 (negative: not stored).
+    q (and q_out) may be strided views with a dense last dimension; q None: keys only, kv None:
+    queries only.  Returns q_out (allocated when not given)."""
+    what = "mla_kv_append"
+    some = q if q is not None else kv
+    if some is None:
+        _refuse(what, "neither q nor kv")
+    dev = some.device
+    n = int(some.shape[0])
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != 64:
+        _refuse(what, f"cos_sin has shape {tuple(cos_sin.shape)}")
+    _want(what, dev, [("positions", positions, (torch.int32,), (n,)), ("cos_sin", cos_sin, (torch.float32,), None)])
+    bf16 = torch.bfloat16
+    qa = (None, 0, 0, None, 0, 0, 0, 0, None)
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=bf16, device=dev)
+        for name, t in (("q", q), ("q_out", q_out)):
+            if t.device != dev or dev.type != "cuda" or t.dtype != bf16 or t.dim() != 3 or t.shape != q.shape:
+                _refuse(what, f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}")
+            if t.shape[2] > 1 and t.stride(2) != 1:
+                _refuse(what, f"the last dimension of {name} is not dense")
+        H, D = int(q.shape[1]), int(q.shape[2])
+        if q_weight is not None:
+            _want(what, dev, [("q_weight", q_weight, (bf16,), (D,))])
+        qa = (_ptr(q), q.stride(0), q.stride(1), _ptr(q_out), q_out.stride(0), q_out.stride(1), H, D, _ptr(q_weight))
+    ka, pool, rows = (None, 0, None), None, 0
+    if kv is not None:
+        if kv_pages is None or slots is None:
+            _refuse(what, "kv without kv_pages and slots")
+        _want_pool(what, kv_pages, kv_dtype)
+        if kv.device != dev or kv_pages.device != dev or kv.dtype != bf16 or tuple(kv.shape) != (n, 576) or kv.stride(1) != 1:
+            _refuse(what, f"kv is {kv.dtype} {tuple(kv.shape)} on {kv.device}")
+        _want(what, dev, [("slots", slots, (torch.int64,), (n,))])
+        if kv_weight is not None:
+            _want(what, dev, [("kv_weight", kv_weight, (bf16,), (512,))])
+        ka = (_ptr(kv), kv.stride(0), _ptr(kv_weight))
+        pool, rows = _ptr(kv_pages), kv_pages.shape[0] * kv_pages.shape[1]
+    _call(what, dev, stream, lib.mla_kv_append, *qa, *ka, float(eps), _ptr(cos_sin), int(cos_sin.shape[0]), _ptr(positions),
+          _ptr(slots) if kv is not None else None, n, int(bool(interleaved)), pool, int(rows), int(kv_dtype), float(kv_scale))
+    return q_out
+
+
+def kv_evict(kv_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch.Tensor,
+             mass: torch.Tensor, dst_page_table: torch.Tensor, sink: int, recent: int, max_seq_len: int, max_keep: int,
+             kv_dtype: int = MLA_KV_BF16, kept=None, new_lens=None, mass_out=None, stream=None):
+    """mla_kv_evict through the C ABI: keep the heaviest keys of each request (its first ``sink``
+    and last ``recent`` always) and copy their rows, in order, into the pages of
+    ``dst_page_table``.  mass [B, >= max_seq_len] fp32.  Returns (kept [B,max_keep] int32, new_lens
+    [B] int32, mass_out [B, >= max_keep] fp32)."""
+    what = "mla_kv_evict"
+    _want_pool(what, kv_pages, kv_dtype)
+    dev = kv_pages.device
+    B = int(seq_lens.numel())
+    i32, f32 = (torch.int32,), (torch.float32,)
+    if kept is None:
+        kept = torch.zeros(B, max_keep, dtype=torch.int32, device=dev)
+    if new_lens is None:
+        new_lens = torch.zeros(B, dtype=torch.int32, device=dev)
+    if mass_out is None:
+        mass_out = torch.zeros(B, max_keep, dtype=torch.float32, device=dev)
+    _want(what, dev, [("page_table", page_table, i32, None), ("seq_lens", seq_lens, i32, (B,)),
+                      ("keep_lens", keep_lens, i32, (B,)), ("mass", mass, f32, None),
+                      ("dst_page_table", dst_page_table, i32, None), ("kept", kept, i32, None),
+                      ("new_lens", new_lens, i32, (B,)), ("mass_out", mass_out, f32, None)])
+    for name, t in (("page_table", page_table), ("mass", mass), ("dst_page_table", dst_page_table), ("kept", kept),
+                    ("mass_out", mass_out)):
+        if t.dim() != 2 or t.shape[0] != B:
+            _refuse(what, f"{name} has shape {tuple(t.shape)}")
+    _call(what, dev, stream, lib.mla_kv_evict, _ptr(kv_pages), int(kv_pages.shape[0]), int(kv_pages.shape[1]), int(kv_dtype),
+          _ptr(page_table), int(page_table.shape[1]), _ptr(seq_lens), _ptr(keep_lens), _ptr(mass), int(mass.shape[1]),
+          _ptr(dst_page_table), int(dst_page_table.shape[1]), B, int(sink), int(recent), int(max_seq_len), int(max_keep),
+          _ptr(kept), int(kept.shape[1]), _ptr(new_lens), _ptr(mass_out), int(mass_out.shape[1]))
+    return kept, new_lens, mass_out
 
 
 def set_profile_events(start=None, stop=None) -> None:

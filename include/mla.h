@@ -174,6 +174,28 @@ int mla_decode_int8_paged(const mla_decode_plan_t* plan, const void* q, const vo
                           int q_len, int num_heads, float scale, float kv_scale, void* out, float* lse,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* Decode of a TREE of drafted tokens: as mla_decode, but the drafts do not follow one another;
+ * draft t of request b sees the whole prefix (keys 0 .. L_b - T - 1) and, of the T drafts at the
+ * request's last positions, those whose bit is set in its mask word.
+ *   plan        : from mla_decode_tree_plan: mla_decode_plan with q_len = T <= 64 and a workspace for
+ *                 fp32 split partials (mla_decode_plan's own plans run too, given a workspace of
+ *                 that size).
+ *   page_scales : as mla_decode_int8_paged for an MLA_KV_INT8_PAGE plan, else NULL.
+ *   tree_mask   : [B, T] uint64, 8-byte aligned: bit u of word (b, t) = draft t sees draft u (usually
+ *                 its ancestors and itself; any word is accepted, bits from T on are ignored).
+ *   out, lse    : as mla_decode; a draft that sees no key at all (an empty mask over an empty
+ *                 prefix) gets out 0 and lse -infinity.
+ * An infinity or NaN in a draft's latent row reaches only the drafts that see it.  Launches,
+ * workspace rules and every other argument and error as mla_decode; also MLA_ERR_UNSUPPORTED for
+ * more than 64 drafts. */
+int mla_decode_tree_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads,
+                         int page_size, int max_pages_per_seq, int64_t num_pages, int kv_dtype,
+                         int num_sms, mla_decode_plan_t* plan_out);
+int mla_decode_tree(const mla_decode_plan_t* plan, const void* q, const void* kv_pages, const float* page_scales,
+                    const int32_t* page_table, const int32_t* seq_lens, const uint64_t* tree_mask,
+                    int q_len, int num_heads, float scale, float kv_scale, void* out, float* lse,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* The two stages of mla_decode, for callers that schedule them apart (e.g. to put other
  * work between them, or to time the split-KV partial kernel on its own).  The TokenSpeed
  * talk ("构建面向 Agentic 推理的下一代 LLM 推理引擎", section "Kernel：让 MLA 真正跑满 GPU")

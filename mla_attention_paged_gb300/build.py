@@ -18,7 +18,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmla.so")
 SOURCES = ["mla_api.cu", "mla_decode_sm103a.cu", "mla_decode_e4m3_sm103a.cu", "mla_decode_narrow_sm103a.cu",
            "mla_prefill_sm103a.cu", "mla_noalloc.cu", "mla_cache_api.cu", "mla_append_sm103a.cu", "mla_evict_sm103a.cu"]
-HEADERS = ["mla_internal.h", "sm103a_ptx.cuh", "kv8_decode.cuh", os.path.join("..", "..", "include", "mla.h")]
+HEADERS = ["mla_internal.h", "sm103a_ptx.cuh", "kv8_decode.cuh", "tree_mask.cuh", os.path.join("..", "..", "include", "mla.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -273,9 +273,20 @@ const char* mla_status_string(int status) {
   }
 }
 
-int mla_decode_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads, int page_size,
-                    int max_pages_per_seq, int64_t num_pages, int kv_dtype, int num_sms,
-                    mla_decode_plan_t* plan_out) {
+}  // extern "C"
+
+namespace {
+
+// Scratch of the split partials: one normalised output row (bf16; a tree's stays fp32) and one
+// log-sum-exp per (request, split, folded row).
+size_t partial_bytes(const mla_decode_plan_t& pl, bool tree) {
+  if (pl.max_splits <= 1) return 0;
+  const size_t parts = static_cast<size_t>(pl.batch) * pl.max_splits * pl.rows;
+  return 256 + parts * kValueDim * (tree ? sizeof(float) : sizeof(__nv_bfloat16)) + parts * sizeof(float);
+}
+
+int make_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads, int page_size, int max_pages_per_seq,
+              int64_t num_pages, int kv_dtype, int num_sms, bool tree, mla_decode_plan_t* plan_out) {
   if (!seq_lens_host || !plan_out || batch < 1 || q_len < 1 || num_heads < 1 || max_pages_per_seq < 1 ||
       num_pages < 1)
     return MLA_ERR_INVALID_ARG;
@@ -301,8 +312,8 @@ int mla_decode_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_
   std::string key;
   key.reserve(64 + 4 * lens.size());
   char head[160];
-  snprintf(head, sizeof head, "%d,%d,%d,%d,%d,%lld,%d,%d|", batch, q_len, num_heads, page_size, max_pages_per_seq,
-           static_cast<long long>(num_pages), kv_dtype, num_sms);
+  snprintf(head, sizeof head, "%d,%d,%d,%d,%d,%lld,%d,%d,%d|", batch, q_len, num_heads, page_size, max_pages_per_seq,
+           static_cast<long long>(num_pages), kv_dtype, num_sms, tree ? 1 : 0);
   key += head;
   key.append(reinterpret_cast<const char*>(lens.data()), lens.size() * sizeof(int));
   {
@@ -336,12 +347,7 @@ int mla_decode_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_
     for (int L : lens) n_ctas += (L + pl.chunk_tokens - 1) / pl.chunk_tokens;
     pl.split_major = (n_ctas * pl.head_groups > num_sms && split_major_order(pl.head_groups)) ? 1 : 0;
   }
-  if (pl.max_splits > 1) {
-    const size_t parts = static_cast<size_t>(batch) * pl.max_splits * pl.rows;
-    pl.workspace_bytes = 256 + parts * kValueDim * sizeof(__nv_bfloat16) + parts * sizeof(float);
-  } else {
-    pl.workspace_bytes = 0;
-  }
+  pl.workspace_bytes = partial_bytes(pl, tree);
   {
     std::lock_guard<std::mutex> lock(g_plan_mu);
     if (g_plan_cache.size() > 4096) g_plan_cache.clear();
@@ -349,6 +355,25 @@ int mla_decode_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_
   }
   *plan_out = pl;
   return MLA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mla_decode_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads, int page_size,
+                    int max_pages_per_seq, int64_t num_pages, int kv_dtype, int num_sms,
+                    mla_decode_plan_t* plan_out) {
+  return make_plan(batch, seq_lens_host, q_len, num_heads, page_size, max_pages_per_seq, num_pages, kv_dtype, num_sms,
+                   false, plan_out);
+}
+
+int mla_decode_tree_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads, int page_size,
+                         int max_pages_per_seq, int64_t num_pages, int kv_dtype, int num_sms,
+                         mla_decode_plan_t* plan_out) {
+  if (q_len > kMaxTreeDrafts) return MLA_ERR_UNSUPPORTED;
+  return make_plan(batch, seq_lens_host, q_len, num_heads, page_size, max_pages_per_seq, num_pages, kv_dtype, num_sms,
+                   true, plan_out);
 }
 
 }  // extern "C"
@@ -363,7 +388,8 @@ constexpr int kStageCombine = 2;
 int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_pages, const float* page_scales,
                   const int32_t* page_table,
                   const int32_t* seq_lens, int q_len, int num_heads, float scale, float kv_scale, void* out,
-                  float* lse, void* workspace, size_t workspace_bytes, void* stream, int stages) {
+                  float* lse, void* workspace, size_t workspace_bytes, void* stream, int stages,
+                  const uint64_t* tree_mask = nullptr) {
   const bool partial = (stages & kStagePartial) != 0;
   if (!plan || !seq_lens || !out || !lse) return MLA_ERR_INVALID_ARG;
   if (partial && (!q || !kv_pages || !page_table)) return MLA_ERR_INVALID_ARG;
@@ -375,9 +401,11 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
   if (!aligned(out, 16) || !aligned(lse, 4)) return MLA_ERR_INVALID_ARG;
   if (partial && (!aligned(q, 16) || !aligned(kv_pages, 16))) return MLA_ERR_INVALID_ARG;
   if (partial && (!(scale > 0.f) || !(kv_scale > 0.f))) return MLA_ERR_INVALID_ARG;
-  if (plan->workspace_bytes > 0) {
+  // (a tree's need is its own, whichever call made the plan)
+  const size_t need = tree_mask ? partial_bytes(*plan, true) : plan->workspace_bytes;
+  if (need > 0) {
     if (!workspace) return MLA_ERR_INVALID_ARG;
-    if (workspace_bytes < plan->workspace_bytes) return MLA_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
   }
   unsigned* status = status_ptr();
@@ -454,9 +482,15 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
   p.lse = lse;
   if (plan->max_splits > 1) {
     const size_t parts = static_cast<size_t>(plan->batch) * plan->max_splits * plan->rows;
-    p.ws_o = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + 256);
-    p.ws_lse = reinterpret_cast<float*>(p.ws_o + parts * kValueDim);
+    if (tree_mask) {
+      p.ws_of = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+      p.ws_lse = p.ws_of + parts * kValueDim;
+    } else {
+      p.ws_o = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + 256);
+      p.ws_lse = reinterpret_cast<float*>(p.ws_o + parts * kValueDim);
+    }
   }
+  p.tree_mask = tree_mask;
   p.status = status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (partial) {
@@ -488,6 +522,16 @@ int mla_decode_int8_paged(const mla_decode_plan_t* plan, const void* q, const vo
   if (!plan || plan->kv_dtype != MLA_KV_INT8_PAGE || !page_scales) return MLA_ERR_INVALID_ARG;
   return decode_stages(plan, q, kv_pages, page_scales, page_table, seq_lens, q_len, num_heads, scale, kv_scale, out,
                        lse, workspace, workspace_bytes, stream, kStagePartial | kStageCombine);
+}
+
+int mla_decode_tree(const mla_decode_plan_t* plan, const void* q, const void* kv_pages, const float* page_scales,
+                    const int32_t* page_table, const int32_t* seq_lens, const uint64_t* tree_mask, int q_len,
+                    int num_heads, float scale, float kv_scale, void* out, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (!plan || !tree_mask || !aligned(tree_mask, 8)) return MLA_ERR_INVALID_ARG;
+  if (plan->q_len > kMaxTreeDrafts) return MLA_ERR_UNSUPPORTED;
+  return decode_stages(plan, q, kv_pages, page_scales, page_table, seq_lens, q_len, num_heads, scale, kv_scale, out,
+                       lse, workspace, workspace_bytes, stream, kStagePartial | kStageCombine, tree_mask);
 }
 
 int mla_decode_partial(const mla_decode_plan_t* plan, const void* q, const void* kv_pages,

@@ -65,6 +65,7 @@
 
 #include "mla_internal.h"
 #include "sm103a_ptx.cuh"
+#include "tree_mask.cuh"
 
 namespace mla {
 namespace {
@@ -213,7 +214,8 @@ __device__ __forceinline__ void p_split16(const float (&x)[16], int lim, float s
 // kMayIdle: q_len * heads is not a multiple of 64, so a row group may hold 48 rows or fewer
 // and a softmax warp may own no row; such warps then skip their S reads and P writes.  (A
 // compile-time choice: the check alone measured 1.2 % slower on full 64-row groups.)
-template <bool kMayIdle>
+// kTree: drafts see each other by p.tree_mask instead of in order, and partials are fp32.
+template <bool kMayIdle, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                            const DecodeParams p) {
@@ -578,6 +580,8 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
     const float v_scale = p.v_scale;
     int lim_abs[2];
     bool row_active[2];
+    const int p0 = L - p.T;        // first draft
+    uint64_t drafts[2] = {0, 0};   // kTree: the drafts each row sees
     float scale_log2[2];
     // S holds (q 2^s) . k_code: the row's 2^-s and kv_scale (in p.scale_log2) return here;
     // P carries 2^kPShift, which cancels in O / l and returns in the LSE.
@@ -586,6 +590,8 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
       const int r = rr0 + 8 * h;
       row_active[h] = r < nrows;
       lim_abs[h] = L - p.T + (row0 + r) / p.H;  // last visible key of the row
+      if (kTree && row_active[h])
+        drafts[h] = p.tree_mask[static_cast<int64_t>(b) * p.T + (row0 + r) / p.H] & draft_bits(p.T);
       scale_log2[h] = failed ? 0.f : p.scale_log2 * ctrl->q_unscale[r];
     }
     float m_w[2] = {-INFINITY, -INFINITY};  // reference max of this warp's last tile
@@ -639,6 +645,17 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
         for (int h = 0; h < 2; ++h) {
           // the row's last visible key in this tile, counted from this thread's first key 2c
           lim[h] = row_active[h] ? (min(kv_end - 1, lim_abs[h]) - k0 - 2 * cq) : -1;
+          if constexpr (kTree) {
+            lim[h] = row_active[h] ? 63 : -1;
+            if (k0 + kTileKeys > p0) {
+              const uint64_t seen = tree_tile_bits(drafts[h], p0, k0) >> (2 * cq);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (!((seen >> (8 * i)) & 1)) x[h][2 * i] = -INFINITY;  // weight 0
+                if (!((seen >> (8 * i + 1)) & 1)) x[h][2 * i + 1] = -INFINITY;
+              }
+            }
+          }
           if (lim[h] >= 57) {
 #pragma unroll
             for (int k = 0; k < 16; ++k) mx[h] = fmaxf(mx[h], x[h][k]);
@@ -741,6 +758,13 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
             st_shared_v4(stage + blk * kRawBlock + row * 64 + piece * 16, 0u, 0u, 0u, 0u);
           }
         }
+        if (kTree && k0 + kTileKeys > p0) {
+          // this tile's drafts: some rows give them weight 0
+          const uint32_t stage = smem_u32(smem + kOffRaw + s * kRawTile);
+          const int d0 = max(p0 - k0, 0), n = (min(valid_rows, kTileKeys) - d0) * 4;
+          for (int i = quad * 32 + lane; i < n * (kValueDim / 64); i += kSoftmaxThreads / 2)
+            make_finite<true>(stage + (i / n) * kRawBlock + d0 * 64 + (i % n) * 16);
+        }
       }
       fence_proxy_async_smem();
       if (bar_or(bar_par, kSoftmaxThreads / 2, fail || (*abort_flag != 0))) {
@@ -816,9 +840,10 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
           const float fb = (mb == -INFINITY) ? 0.f : ex2_approx(mb - m);
           const float ls = ctrl->fin[0][1][r] * fa + ctrl->fin[1][1][r] * fb;
           const float lu = ctrl->fin[0][2][r] * fa + ctrl->fin[1][2][r] * fb;
-          const float lse2 = (ls > 0.f) ? (m + __log2f(ls) - kPShift) : -INFINITY;
+          // (a row that sees nothing has sums of 0; kTree passes a NaN on)
+          const float lse2 = (kTree ? ls != 0.f : ls > 0.f) ? (m + __log2f(ls) - kPShift) : -INFINITY;
           const float lse_nat = lse2 * 0.69314718055994530942f;
-          ctrl->row_scale[r] = (lu > 0.f) ? (v_scale / lu) : 0.f;
+          ctrl->row_scale[r] = (kTree ? lu != 0.f : lu > 0.f) ? (v_scale / lu) : 0.f;
           if (row_active[h]) {
             const int64_t grow = static_cast<int64_t>(b) * p.R + row0 + r;
             if (final_out)
@@ -851,6 +876,10 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
+          if (kTree && !final_out) {  // a tree's partials stay fp32: [64][512] in stages 0-3
+            st_shared_f32(stage_s + ((kh * 32 + i) * kValueDim + dim) * 4, __uint_as_float(v[i]) * rs[i]);
+            continue;
+          }
           const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(v[i]) * rs[i]);
           asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage_s + ((kh * 32 + i) * kValueDim + dim) * 2),
                        "h"(*reinterpret_cast<const uint16_t*>(&o)));
@@ -858,6 +887,13 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
       }
       const __nv_bfloat16* stage_h = reinterpret_cast<const __nv_bfloat16*>(smem + kOffOStage);
       named_bar_sync(1, kSoftmaxThreads);
+      if (kTree && !final_out) {
+        static_assert(kGroupRows * kValueDim * 4 <= kStages * kRawTile, "fp32 staging");
+        const uint4* const src = reinterpret_cast<const uint4*>(smem + kOffOStage);
+        uint4* const dst = reinterpret_cast<uint4*>(
+            p.ws_of + ((static_cast<int64_t>(b) * p.max_splits + split) * p.R + row0) * kValueDim);
+        for (int c = threadIdx.x; c < nrows * (kValueDim / 4); c += kSoftmaxThreads) dst[c] = src[c];
+      } else {
       constexpr int kChunksPerRow = kValueDim * 2 / 16;
       __nv_bfloat16* dst = final_out
                                ? p.out + (static_cast<int64_t>(b) * p.R + row0) * kValueDim
@@ -866,6 +902,7 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
         const int rr = c / kChunksPerRow, cc = c % kChunksPerRow;
         const uint4 v = *reinterpret_cast<const uint4*>(stage_h + rr * kValueDim + cc * 8);
         *reinterpret_cast<uint4*>(dst + rr * kValueDim + cc * 8) = v;
+      }
       }
     }
   }
@@ -885,17 +922,19 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
 
 cudaError_t launch_decode_partial_e4m3(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv,
                                        int head_groups, cudaStream_t stream) {
+  // [tree][a row group may hold idle warps]
+  static constexpr decltype(&decode_partial_e4m3_kernel<false, false>) kernels[4] = {
+      decode_partial_e4m3_kernel<false, false>, decode_partial_e4m3_kernel<true, false>,
+      decode_partial_e4m3_kernel<false, true>, decode_partial_e4m3_kernel<true, true>};
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(decode_partial_e4m3_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemBytes);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(decode_partial_e4m3_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemBytes);
-    if (e != cudaSuccess) return e;
+    for (auto kernel : kernels) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+      if (e != cudaSuccess) return e;
+    }
     configured_device = dev;
   }
   cudaLaunchConfig_t cfg = {};
@@ -909,8 +948,7 @@ cudaError_t launch_decode_partial_e4m3(const DecodeParams& p, const CUtensorMap&
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // a group of 48 rows or fewer exists when R is not a multiple of 64
-  return (p.R % kGroupRows != 0) ? cudaLaunchKernelEx(&cfg, decode_partial_e4m3_kernel<true>, tm_q, tm_kv, p)
-                                 : cudaLaunchKernelEx(&cfg, decode_partial_e4m3_kernel<false>, tm_q, tm_kv, p);
+  return cudaLaunchKernelEx(&cfg, kernels[(p.tree_mask ? 2 : 0) + (p.R % kGroupRows != 0 ? 1 : 0)], tm_q, tm_kv, p);
 }
 
 }  // namespace mla

@@ -24,6 +24,7 @@
 // issuer.
 #include "mla_internal.h"
 #include "sm103a_ptx.cuh"
+#include "tree_mask.cuh"
 
 namespace mla {
 namespace {
@@ -73,6 +74,8 @@ constexpr uint32_t kTmemQ = 192;  // Q: column block c (64 dims) at 192 + 32c, 2
 static_assert(kTmemQ + kDimBlocks * 32 <= kTmemCols, "TMEM budget");
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
+// kTree: drafts see each other by p.tree_mask instead of in order, and partials are fp32.
+template <bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_partial_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                              const DecodeParams p) {
@@ -322,6 +325,9 @@ decode_partial_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __g
     const bool row_active = r < nrows;
     const int t = r / p.H;
     const int lim_abs = L - p.T + t;  // last visible key of this row
+    const int p0 = L - p.T;           // first draft
+    uint64_t drafts = 0;              // kTree: the drafts this row sees
+    if (kTree && owns_rows && row_active) drafts = p.tree_mask[static_cast<int64_t>(b) * p.T + t] & draft_bits(p.T);
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     float m_used = -INFINITY;
     float l_sum = 0.f;
@@ -373,7 +379,16 @@ decode_partial_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __g
         tc_fence_before();
         mbar_arrive(&ctrl->s_free);
         // keys i <= lim of this lane's 32-key half are visible
-        const int lim = (owns_rows && row_active) ? (min(kv_end - 1, lim_abs) - k0 - 32 * half) : -1;
+        int lim = (owns_rows && row_active) ? (min(kv_end - 1, lim_abs) - k0 - 32 * half) : -1;
+        if constexpr (kTree) {
+          lim = (owns_rows && row_active) ? 31 : -1;
+          if (k0 + kTileKeys > p0) {
+            const uint32_t seen = static_cast<uint32_t>(tree_tile_bits(drafts, p0, k0) >> (32 * half));
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((seen >> i) & 1u)) sr[i] = 0xff800000u;  // -inf: weight 0
+          }
+        }
         online_softmax_step<32, true>(sr, lim, scale_log2, kRescaleThreshold, m_used, l_sum, packed, alpha,
                                       need_rescale);
       }
@@ -413,6 +428,14 @@ decode_partial_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __g
             const int row = valid_rows + rem / 8;
             st_shared_v4(smem_u32(stage + blk * kBlockBytes + row * 128 + (rem % 8) * 16), 0u, 0u, 0u, 0u);
           }
+          fence_proxy_async_smem();
+        }
+        if (kTree && k0 + kTileKeys > p0) {
+          // this tile's drafts: some rows give them weight 0
+          const uint32_t stage = smem_u32(smem + kOffStages + (j % kStages) * kTileBytes);
+          const int d0 = max(p0 - k0, 0), n = (min(valid_rows, kTileKeys) - d0) * 8;
+          for (int idx = threadIdx.x; idx < n * 8; idx += 128)
+            make_finite<false>(stage + (idx / n) * kBlockBytes + d0 * 128 + (idx % n) * 16);
           fence_proxy_async_smem();
         }
       }
@@ -455,9 +478,11 @@ decode_partial_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __g
       const bool final_out = (nsplit_b == 1);
       l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 16);  // the two halves' partial row sums
       if (owns_rows && row_lane) {
-        const float lse2 = (l_sum > 0.f) ? (m_used + __log2f(l_sum)) : -INFINITY;
+        // (a row that sees nothing has l_sum 0; kTree passes a NaN on)
+        const bool some = kTree ? l_sum != 0.f : l_sum > 0.f;
+        const float lse2 = some ? (m_used + __log2f(l_sum)) : -INFINITY;
         const float lse_nat = lse2 * 0.69314718055994530942f;
-        ctrl->row_scale[r] = (l_sum > 0.f) ? (p.v_scale / l_sum) : 0.f;
+        ctrl->row_scale[r] = some ? (p.v_scale / l_sum) : 0.f;
         if (row_active) {
           const int64_t grow = static_cast<int64_t>(b) * p.R + r;
           if (final_out)
@@ -487,6 +512,10 @@ decode_partial_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __g
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
+          if (kTree && !final_out) {  // a tree's partials stay fp32: [32][512] in stage 0
+            st_shared_f32(stage_s + (i * kValueDim + dim) * 4, __uint_as_float(v[i]) * rs[i]);
+            continue;
+          }
           const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(v[i]) * rs[i]);
           asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage_s + (i * kValueDim + dim) * 2),
                        "h"(*reinterpret_cast<const uint16_t*>(&o)));
@@ -494,6 +523,13 @@ decode_partial_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __g
       }
       const __nv_bfloat16* stage_h = reinterpret_cast<const __nv_bfloat16*>(smem + kOffStages);
       named_bar_sync(1, 128);
+      if (kTree && !final_out) {
+        static_assert(kNarrowRows * kValueDim * 4 <= kTileBytes, "fp32 staging");
+        const uint4* const src = reinterpret_cast<const uint4*>(smem + kOffStages);
+        uint4* const dst =
+            reinterpret_cast<uint4*>(p.ws_of + (static_cast<int64_t>(b) * p.max_splits + split) * p.R * kValueDim);
+        for (int c = threadIdx.x; c < nrows * (kValueDim / 4); c += 128) dst[c] = src[c];
+      } else {
       constexpr int kChunksPerRow = kValueDim * 2 / 16;
       __nv_bfloat16* dst = final_out ? p.out + static_cast<int64_t>(b) * p.R * kValueDim
                                      : p.ws_o + (static_cast<int64_t>(b) * p.max_splits + split) * p.R * kValueDim;
@@ -501,6 +537,7 @@ decode_partial_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __g
         const int rr = c / kChunksPerRow, cc = c % kChunksPerRow;
         const uint4 v = *reinterpret_cast<const uint4*>(stage_h + rr * kValueDim + cc * 8);
         *reinterpret_cast<uint4*>(dst + rr * kValueDim + cc * 8) = v;
+      }
       }
     }
   }
@@ -526,7 +563,9 @@ cudaError_t launch_decode_partial_narrow(const DecodeParams& p, const CUtensorMa
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(decode_partial_narrow_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    e = cudaFuncSetAttribute(decode_partial_narrow_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(decode_partial_narrow_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
@@ -541,7 +580,8 @@ cudaError_t launch_decode_partial_narrow(const DecodeParams& p, const CUtensorMa
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_partial_narrow_kernel, tm_q, tm_kv, p);
+  return p.tree_mask ? cudaLaunchKernelEx(&cfg, decode_partial_narrow_kernel<true>, tm_q, tm_kv, p)
+                     : cudaLaunchKernelEx(&cfg, decode_partial_narrow_kernel<false>, tm_q, tm_kv, p);
 }
 
 }  // namespace mla

@@ -32,6 +32,7 @@
 #include "kv8_decode.cuh"
 #include "mla_internal.h"
 #include "sm103a_ptx.cuh"
+#include "tree_mask.cuh"
 
 namespace mla {
 namespace {
@@ -96,7 +97,8 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // and f16 GEMMs of the int8 paths, kPageScales the per-key scales of kKvInt8Page).
 // kSplitMajor: the grid's launch order (a compile-time choice: a run-time select of the
 // block-index mapping measured 1.4 % slower on 128-head decode).
-template <int kKv, bool kSplitMajor>
+// kTree: drafts see each other by p.tree_mask instead of in order, and partials are fp32.
+template <int kKv, bool kSplitMajor, bool kTree>
 __global__ void __launch_bounds__(threads_for(kKv != kKvBf16), 1)
 decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                       const DecodeParams p) {
@@ -580,6 +582,9 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     const bool row_active = r < nrows;
     const int t = (row0 + r) / p.H;
     const int lim_abs = L - p.T + t;  // last visible key of this row
+    const int p0 = L - p.T;           // first draft
+    uint64_t drafts = 0;              // kTree: the drafts this row sees
+    if (kTree && row_active) drafts = p.tree_mask[static_cast<int64_t>(b) * p.T + t] & draft_bits(p.T);
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     float m_used = -INFINITY;
     float l_sum = 0.f;
@@ -604,7 +609,17 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         tc_fence_before();
         mbar_arrive(&ctrl->s_free[sb]);
         // keys i <= lim of this lane's 32-key half are visible
-        const int lim = row_active ? (min(kv_end - 1, lim_abs) - k0 - 32 * half) : -1;
+        int lim = row_active ? (min(kv_end - 1, lim_abs) - k0 - 32 * half) : -1;
+        uint32_t seen = 0xffffffffu;  // kTree: a bit per key of this lane's half
+        if constexpr (kTree) {
+          lim = row_active ? 31 : -1;
+          if (k0 + kTileKeys > p0) {
+            seen = static_cast<uint32_t>(tree_tile_bits(drafts, p0, k0) >> (32 * half));
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((seen >> i) & 1u)) sr[i] = 0xff800000u;  // -inf: weight 0
+          }
+        }
         if constexpr (kPageScales) {
           // the keys' scales relative to kv_scale (written by the decode warps before they
           // released the tile: waiting on that release orders their writes before the reads)
@@ -617,6 +632,11 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             ks[i + 1] = f.y;
             ks[i + 2] = f.z;
             ks[i + 3] = f.w;
+          }
+          if constexpr (kTree) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((seen >> i) & 1u)) ks[i] = 1.f;  // -inf stays -inf under a scale of 0
           }
           online_softmax_step<32, true, true, true>(sr, lim, scale_log2, kRescaleThreshold, m_used, l_sum, packed,
                                                     alpha, need_rescale, ks);
@@ -662,6 +682,14 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             const int row = valid_rows + rem / 8;
             st_shared_v4(smem_u32(stage + blk * kBlockBytes + row * 128 + (rem % 8) * 16), 0u, 0u, 0u, 0u);
           }
+          fence_proxy_async_smem();
+        }
+        if (kTree && k0 + kTileKeys > p0) {
+          // this tile's drafts: some rows give them weight 0
+          const uint32_t stage = smem_u32(smem + kOffStages + (j % kStages) * kTileBytes);
+          const int d0 = max(p0 - k0, 0), n = (min(valid_rows, kTileKeys) - d0) * 8;
+          for (int idx = threadIdx.x; idx < n * 8; idx += 128)
+            make_finite<false>(stage + (idx / n) * kBlockBytes + d0 * 128 + (idx % n) * 16);
           fence_proxy_async_smem();
         }
       }
@@ -725,9 +753,11 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       const bool final_out = (nsplit_b == 1);
       l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 16);  // the two halves' partial row sums
       if (row_lane) {
-        const float lse2 = (l_sum > 0.f) ? (m_used + __log2f(l_sum)) : -INFINITY;
+        // (a row that sees nothing has l_sum 0; kTree passes a NaN on)
+        const bool some = kTree ? l_sum != 0.f : l_sum > 0.f;
+        const float lse2 = some ? (m_used + __log2f(l_sum)) : -INFINITY;
         const float lse_nat = lse2 * 0.69314718055994530942f;
-        ctrl->row_scale[r] = (l_sum > 0.f) ? (v_scale / l_sum) : 0.f;
+        ctrl->row_scale[r] = some ? (v_scale / l_sum) : 0.f;
         if (row_active) {
           const int64_t grow = static_cast<int64_t>(b) * p.R + row0 + r;
           if (final_out)
@@ -744,7 +774,21 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       // The 64 row scales go to registers first: shared-memory loads interleaved with the
       // staging stores below would each have to wait for the stores before them.
       const uint32_t stage_s = smem_u32(smem + kOffStages);  // [64][512] bf16
-      if constexpr (kInt8) {
+      if (kTree && !final_out) {
+        // A tree's partials stay fp32 ([64][512] in both stages): a second bf16 rounding would
+        // add as much error as the output's own.
+        static_assert(kGroupRows * kValueDim * 4 <= kStages * kTileBytes, "fp32 staging");
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          const int dim = (c >> 1) * 128 + warp * 32 + lane, hh = c & 1;
+          uint32_t v[32];
+          tmem_ld32(tmem + lane_base + (c >> 1) * 64 + hh * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            st_shared_f32(stage_s + ((hh * 32 + i) * kValueDim + dim) * 4, __uint_as_float(v[i]) * ctrl->row_scale[hh * 32 + i]);
+        }
+      } else if constexpr (kInt8) {
         // (the int8 kernels run at a lower register cap: rows 32hh .. 32hh+31 at a time,
         // their 32 scales in registers)
 #pragma unroll 1
@@ -802,6 +846,12 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       }
       __nv_bfloat16* stage_h = reinterpret_cast<__nv_bfloat16*>(smem + kOffStages);
       named_bar_sync(1, 128);
+      if (kTree && !final_out) {
+        const uint4* const src = reinterpret_cast<const uint4*>(smem + kOffStages);
+        uint4* const dst = reinterpret_cast<uint4*>(
+            p.ws_of + ((static_cast<int64_t>(b) * p.max_splits + split) * p.R + row0) * kValueDim);
+        for (int c = threadIdx.x; c < nrows * (kValueDim / 4); c += 128) dst[c] = src[c];
+      } else {
       constexpr int kChunksPerRow = kValueDim * 2 / 16;
       __nv_bfloat16* dst = final_out
                                ? p.out + (static_cast<int64_t>(b) * p.R + row0) * kValueDim
@@ -810,6 +860,7 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const int rr = c / kChunksPerRow, cc = c % kChunksPerRow;
         const uint4 v = *reinterpret_cast<const uint4*>(stage_h + rr * kValueDim + cc * 8);
         *reinterpret_cast<uint4*>(dst + rr * kValueDim + cc * 8) = v;
+      }
       }
     }
   }
@@ -840,8 +891,12 @@ constexpr int kCombineThreads = 64 * kCombineRows;
 constexpr int kCombineBatch = 32;  // splits staged per round (lane l holds split s0 + l)
 constexpr int kCombineRowBytes = kValueDim * 2;
 
+// kTree: the partials are fp32 (half as many splits a batch in the same shared memory).
+template <bool kTree>
 __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const DecodeParams p) {
-  extern __shared__ __align__(128) uint8_t cs[];  // [split][row][512] bf16
+  constexpr int kBatch = kTree ? kCombineBatch / 2 : kCombineBatch;
+  constexpr int kRowBytes = kTree ? 2 * kCombineRowBytes : kCombineRowBytes;
+  extern __shared__ __align__(128) uint8_t cs[];  // [split][row][512] bf16 or fp32
   __shared__ uint64_t bar;
   __shared__ int abort_flag;
   const int row0 = blockIdx.x * kCombineRows;
@@ -874,14 +929,16 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const D
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
   bool ok = true;
   uint32_t phase = 0;
-  for (int s0 = 0; s0 < ns && ok; s0 += kCombineBatch) {
-    const int nb = min(kCombineBatch, ns - s0);
+  for (int s0 = 0; s0 < ns && ok; s0 += kBatch) {
+    const int nb = min(kBatch, ns - s0);
     if (tid == 0) {
-      mbar_arrive_expect_tx(&bar, static_cast<uint32_t>(nb * nr * kCombineRowBytes));
+      mbar_arrive_expect_tx(&bar, static_cast<uint32_t>(nb * nr * kRowBytes));
       const uint64_t pol = policy_evict_first();
       for (int s = 0; s < nb; ++s)
-        bulk_load(cs + s * nr * kCombineRowBytes, p.ws_o + ((base + s0 + s) * p.R + row0) * kValueDim,
-                  static_cast<uint32_t>(nr * kCombineRowBytes), &bar, pol);
+        bulk_load(cs + s * nr * kRowBytes,
+                  kTree ? static_cast<const void*>(p.ws_of + ((base + s0 + s) * p.R + row0) * kValueDim)
+                        : static_cast<const void*>(p.ws_o + ((base + s0 + s) * p.R + row0) * kValueDim),
+                  static_cast<uint32_t>(nr * kRowBytes), &bar, pol);
     }
     const float l = (lane < nb) ? __ldg(lse_s + static_cast<int64_t>(s0 + lane) * p.R) : -INFINITY;
     float bm = l;
@@ -895,7 +952,8 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const D
       w_run *= c;
       m_run = m_new;
     }
-    const float w = (m_new == -INFINITY) ? 0.f : __expf(l - m_new);
+    float w = (m_new == -INFINITY) ? 0.f : __expf(l - m_new);
+    if (kTree && l != l) w = l;  // (a NaN stays one where every split's is)
     float ws = w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
@@ -903,13 +961,21 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const D
     ok = mbar_wait(&bar, phase, &abort_flag);
     phase ^= 1u;
     if (ok) {
-      const uint32_t src = smem_u32(cs) + (active ? r : 0) * kCombineRowBytes + c8 * 16;
+      const uint32_t src = smem_u32(cs) + (active ? r : 0) * kRowBytes + c8 * (kTree ? 32 : 16);
       for (int s = 0; s < nb; ++s) {
         const float ws_s = __shfl_sync(0xffffffffu, w, s);
+        if constexpr (kTree) {
+          if (ws_s == 0.f) continue;  // (a split none of whose keys this row sees; uniform over the row's threads)
+          const uint4 lo = ld_shared_v4(src + s * nr * kRowBytes), hi = ld_shared_v4(src + s * nr * kRowBytes + 16);
+          const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] += ws_s * __uint_as_float(u[i]);
+          continue;
+        }
         uint32_t v0, v1, v2, v3;
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(v0), "=r"(v1), "=r"(v2), "=r"(v3)
-                     : "r"(src + s * nr * kCombineRowBytes));
+                     : "r"(src + s * nr * kRowBytes));
         const uint32_t vv[4] = {v0, v1, v2, v3};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -929,7 +995,8 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const D
     return;
   }
   if (active) {
-    const float inv = w_run > 0.f ? 1.f / w_run : 0.f;
+    const bool some = kTree ? w_run != 0.f : w_run > 0.f;  // (kTree passes a NaN on)
+    const float inv = some ? 1.f / w_run : 0.f;
     uint4 pk;
     pk.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
     pk.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
@@ -937,7 +1004,7 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const D
     pk.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
     const int64_t orow = static_cast<int64_t>(b) * p.R + row0 + r;
     *reinterpret_cast<uint4*>(p.out + orow * kValueDim + c8 * 8) = pk;
-    if (c8 == 0) p.lse[orow] = (w_run > 0.f) ? (m_run + __logf(w_run)) : -INFINITY;
+    if (c8 == 0) p.lse[orow] = some ? (m_run + __logf(w_run)) : -INFINITY;
   }
 }
 
@@ -957,7 +1024,7 @@ __global__ void selftest_timeout_kernel(unsigned* status) {
   if (threadIdx.x == 0 && (!ok || abort_flag)) atomicOr(status, kStatusTimeout);
 }
 
-template <int kKv>
+template <int kKv, bool kTree>
 cudaError_t launch_partial_impl(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv,
                                 int head_groups, cudaStream_t stream) {
   static thread_local int configured_device = -1;
@@ -965,10 +1032,10 @@ cudaError_t launch_partial_impl(const DecodeParams& p, const CUtensorMap& tm_q, 
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(decode_partial_kernel<kKv, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(decode_partial_kernel<kKv, false, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(decode_partial_kernel<kKv, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(decode_partial_kernel<kKv, true, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes);
     if (e != cudaSuccess) return e;
     configured_device = dev;
@@ -985,8 +1052,8 @@ cudaError_t launch_partial_impl(const DecodeParams& p, const CUtensorMap& tm_q, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.split_major ? cudaLaunchKernelEx(&cfg, decode_partial_kernel<kKv, true>, tm_q, tm_kv, p)
-                       : cudaLaunchKernelEx(&cfg, decode_partial_kernel<kKv, false>, tm_q, tm_kv, p);
+  return p.split_major ? cudaLaunchKernelEx(&cfg, decode_partial_kernel<kKv, true, kTree>, tm_q, tm_kv, p)
+                       : cudaLaunchKernelEx(&cfg, decode_partial_kernel<kKv, false, kTree>, tm_q, tm_kv, p);
 }
 
 }  // namespace
@@ -995,12 +1062,17 @@ cudaError_t launch_decode_partial(const DecodeParams& p, const CUtensorMap& tm_q
                                   int head_groups, cudaStream_t stream) {
   switch (p.kv_dtype) {
     case kKvE4m3: return launch_decode_partial_e4m3(p, tm_q, tm_kv, head_groups, stream);
-    case kKvInt8: return launch_partial_impl<kKvInt8>(p, tm_q, tm_kv, head_groups, stream);
-    case kKvInt8Page: return launch_partial_impl<kKvInt8Page>(p, tm_q, tm_kv, head_groups, stream);
+    case kKvInt8:
+      return p.tree_mask ? launch_partial_impl<kKvInt8, true>(p, tm_q, tm_kv, head_groups, stream)
+                         : launch_partial_impl<kKvInt8, false>(p, tm_q, tm_kv, head_groups, stream);
+    case kKvInt8Page:
+      return p.tree_mask ? launch_partial_impl<kKvInt8Page, true>(p, tm_q, tm_kv, head_groups, stream)
+                         : launch_partial_impl<kKvInt8Page, false>(p, tm_q, tm_kv, head_groups, stream);
     default:
       // at most 32 folded rows: Q fits in tensor memory, and shared memory takes three tiles
       if (p.R <= 32) return launch_decode_partial_narrow(p, tm_q, tm_kv, stream);
-      return launch_partial_impl<kKvBf16>(p, tm_q, tm_kv, head_groups, stream);
+      return p.tree_mask ? launch_partial_impl<kKvBf16, true>(p, tm_q, tm_kv, head_groups, stream)
+                         : launch_partial_impl<kKvBf16, false>(p, tm_q, tm_kv, head_groups, stream);
   }
 }
 
@@ -1011,14 +1083,19 @@ cudaError_t launch_selftest_timeout(unsigned* status, cudaStream_t stream) {
 
 cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t stream) {
   const dim3 grid((p.R + kCombineRows - 1) / kCombineRows, p.B);
-  const int smem = min(p.max_splits, kCombineBatch) * kCombineRows * kCombineRowBytes;
+  const bool tree = p.tree_mask != nullptr;
+  const int smem = (tree ? 2 * min(p.max_splits, kCombineBatch / 2) : min(p.max_splits, kCombineBatch)) * kCombineRows *
+                   kCombineRowBytes;
   // the shared-memory limit is a per-device attribute: set it once per device and thread
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(decode_combine_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(decode_combine_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kCombineBatch * kCombineRows * kCombineRowBytes);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(decode_combine_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kCombineBatch * kCombineRows * kCombineRowBytes);
     if (e != cudaSuccess) return e;
     configured_device = dev;
@@ -1033,7 +1110,8 @@ cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_combine_kernel, p);
+  return tree ? cudaLaunchKernelEx(&cfg, decode_combine_kernel<true>, p)
+              : cudaLaunchKernelEx(&cfg, decode_combine_kernel<false>, p);
 }
 
 }  // namespace mla

@@ -1,0 +1,58 @@
+// tree_mask.cuh -- what the decode kernels share for trees of drafted tokens: which keys of a
+// 64-key tile a row sees, and draft rows made safe to multiply by a zero weight.
+#pragma once
+
+#include "sm103a_ptx.cuh"
+
+namespace mla {
+
+// Keys of the tile k0 .. k0 + 63 that a row sees, as a bit per key: every key before the
+// first draft (position p0), and draft u where bit u of `mask` (cut to the T drafts) is set.
+__device__ __forceinline__ uint64_t tree_tile_bits(uint64_t mask, int p0, int k0) {
+  const int d = p0 - k0;  // prefix keys in (or past) this tile
+  if (d >= 64) return ~0ull;
+  if (d > 0) return ((1ull << d) - 1) | (mask << d);
+  return d > -64 ? mask >> (-d) : 0ull;
+}
+
+// The T low bits.
+__device__ __forceinline__ uint64_t draft_bits(int T) { return T >= 64 ? ~0ull : (1ull << T) - 1; }
+
+// bf16 pairs with infinities and NaNs replaced by zero.  A draft that a row does not see
+// has weight 0 there, but 0 times an infinity or NaN is NaN; rows that do see it have a
+// score that is not finite already, so its value row no longer matters to them.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+  return w;
+}
+
+// e4m3 codes (four in a word) with the NaN codes 0x7F and 0xFF replaced by zero.
+__device__ __forceinline__ uint32_t finite_e4m3x4(uint32_t w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (((w >> (8 * i)) & 0x7Fu) == 0x7Fu) w &= ~(0xFFu << (8 * i));
+  return w;
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t saddr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(saddr));
+  return v;
+}
+
+// Rewrite a 16-byte piece of a draft's value row without infinities or NaNs.
+template <bool kE4m3>
+__device__ __forceinline__ void make_finite(uint32_t saddr) {
+  const uint4 v = ld_shared_v4(saddr);
+  uint4 f;
+  f.x = kE4m3 ? finite_e4m3x4(v.x) : finite_bf16x2(v.x);
+  f.y = kE4m3 ? finite_e4m3x4(v.y) : finite_bf16x2(v.y);
+  f.z = kE4m3 ? finite_e4m3x4(v.z) : finite_bf16x2(v.z);
+  f.w = kE4m3 ? finite_e4m3x4(v.w) : finite_bf16x2(v.w);
+  if ((f.x ^ v.x) | (f.y ^ v.y) | (f.z ^ v.z) | (f.w ^ v.w)) st_shared_v4(saddr, f.x, f.y, f.z, f.w);
+}
+
+}  // namespace mla

@@ -30,7 +30,8 @@ MLA_KV_INT8_PAGE = 3
 EXPORTED = ["mla_decode_plan", "mla_decode", "mla_decode_partial", "mla_decode_combine", "mla_decode_noalloc",
             "mla_decode_int8_paged",
             "mla_prefill_varlen", "mla_prefill_paged", "mla_get_status", "mla_status_string", "mla_version", "mla_set_profile_events",
-            "mla_profile_elapsed_ms", "mla_selftest_wait_timeout", "mla_kv_append", "mla_kv_evict"]
+            "mla_profile_elapsed_ms", "mla_selftest_wait_timeout", "mla_kv_append", "mla_kv_evict",
+            "mla_decode_tree_plan", "mla_decode_tree"]
 
 
 class MlaError(RuntimeError):
@@ -73,6 +74,10 @@ def _load() -> ctypes.CDLL:
     lib.mla_prefill_varlen.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, i32, f32, P, P, P]
     lib.mla_prefill_paged.restype = i32
     lib.mla_prefill_paged.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, i64, i32, i32, f32, P, P, P]
+    lib.mla_decode_tree_plan.restype = i32
+    lib.mla_decode_tree_plan.argtypes = lib.mla_decode_plan.argtypes
+    lib.mla_decode_tree.restype = i32
+    lib.mla_decode_tree.argtypes = [ctypes.POINTER(DecodePlan), P, P, P, P, P, P, i32, i32, f32, f32, P, P, P, sz, P]
     lib.mla_kv_append.restype = i32
     lib.mla_kv_append.argtypes = [P, i64, i64, P, i64, i64, i32, i32, P, P, i64, P, f32, P, i32, P, P, i32, i32, P, i64,
                                   i32, f32, P]
@@ -161,6 +166,18 @@ def decode_plan(seq_lens_host, q_len: int, num_heads: int, page_size: int, max_p
                              int(page_size), int(max_pages_per_seq), int(num_pages), int(kv_dtype), int(num_sms),
                              ctypes.byref(plan))
     _check(rc, "mla_decode_plan")
+    return plan
+
+
+def decode_tree_plan(seq_lens_host, q_len: int, num_heads: int, page_size: int, max_pages_per_seq: int,
+                     num_pages: int, kv_dtype: int = MLA_KV_BF16, num_sms: int = 0) -> DecodePlan:
+    """Plan a decode_tree launch (q_len <= 64 drafts) from HOST sequence lengths (drafts included)."""
+    lens = torch.as_tensor(seq_lens_host, dtype=torch.int32).cpu().contiguous()
+    plan = DecodePlan()
+    rc = lib.mla_decode_tree_plan(int(lens.numel()), ctypes.c_void_p(lens.data_ptr()), int(q_len), int(num_heads),
+                                  int(page_size), int(max_pages_per_seq), int(num_pages), int(kv_dtype), int(num_sms),
+                                  ctypes.byref(plan))
+    _check(rc, "mla_decode_tree_plan")
     return plan
 
 
@@ -290,6 +307,39 @@ def prefill_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                                int(num_pages), int(max_seqlen_q), int(Nq), float(scale), _ptr(out), _ptr(lse),
                                _stream_handle(stream))
     _check(rc, "mla_prefill_paged")
+    return out, lse
+
+
+def decode_tree(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_table: torch.Tensor,
+                seq_lens: torch.Tensor, tree_mask: torch.Tensor, scale: float, kv_scale: float = 1.0, page_scales=None,
+                out=None, lse=None, workspace=None, stream=None):
+    """mla_decode_tree through the C ABI: decode of a tree of drafts.  tree_mask [B,T] int64 (its 64
+    bits): bit u of [b, t] = draft t sees draft u.  Returns (out [B,T,H,512] bf16, lse [B,T,H] fp32)."""
+    what = "mla_decode_tree"
+    _want_pool(what, kv_pages, plan.kv_dtype)
+    dev = kv_pages.device
+    B, T, H = plan.batch, plan.q_len, plan.num_heads
+    if out is None:
+        out = torch.empty(B, T, H, 512, dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty(B, T, H, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = workspace_for(plan, dev)
+    i32 = (torch.int32,)
+    _want(what, dev, [("q", q, (torch.bfloat16,), (B, T, H, 576)), ("page_table", page_table, i32, (B, plan.max_pages_per_seq)),
+                      ("seq_lens", seq_lens, i32, (B,)), ("tree_mask", tree_mask, (torch.int64,), (B, T)),
+                      ("out", out, (torch.bfloat16,), (B, T, H, 512)), ("lse", lse, (torch.float32,), (B, T, H))])
+    if kv_pages.shape[0] != plan.num_pages or kv_pages.shape[1] != plan.page_size:
+        _refuse(what, f"kv_pages has shape {tuple(kv_pages.shape)}, not the plan's")
+    if page_scales is not None:
+        _want(what, dev, [("page_scales", page_scales, (torch.float32,), (plan.num_pages,))])
+    ws_bytes = 0
+    if workspace is not None:
+        _want(what, dev, [("workspace", workspace, (workspace.dtype,), None)])
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _call(what, dev, stream, lib.mla_decode_tree, ctypes.byref(plan), _ptr(q), _ptr(kv_pages), _ptr(page_scales),
+          _ptr(page_table), _ptr(seq_lens), _ptr(tree_mask), T, H, float(scale), float(kv_scale), _ptr(out), _ptr(lse),
+          _ptr(workspace), ws_bytes)
     return out, lse
 
 

@@ -344,6 +344,32 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
                   const int64_t* slots, int num_tokens, int interleaved, void* kv_pages, int64_t num_slots,
                   int kv_dtype, float kv_scale, void* stream);
 
+/* The attention weight that each cached key received in a decode step, accumulated over steps:
+ *   mass[b, j] = decay * mass[b, j] + sum over rows (t, h) that see key j of
+ *                exp(scale q[b,t,h] . k_j - lse[b,t,h]),   j < L_b
+ * Call it after the step's mla_decode / mla_decode_tree, with that call's arguments and lse; each
+ * row then adds a total weight of 1.  Sums are fp32, in a fixed order.
+ *   plan        : from mla_decode_plan or mla_decode_tree_plan.
+ *   q, kv_pages, page_table, seq_lens, scale, kv_scale : as mla_decode.
+ *   page_scales : as mla_decode_int8_paged for an MLA_KV_INT8_PAGE plan, else NULL.
+ *   tree_mask   : as mla_decode_tree, or NULL: draft t sees keys 0 .. L_b - T + t.
+ *   lse         : [B, T, H] fp32; a row whose lse is not finite adds nothing.
+ *   decay       : >= 0; 0 overwrites mass without reading it.
+ *   mass        : fp32, row b at mass + b * mass_stride (elements; >= plan->max_seq_len); entries from
+ *                 L_b on are left as they were.
+ *   workspace   : device scratch of the size mla_key_mass_workspace gives for the plan, 256-byte
+ *                 aligned (NULL when that is 0); overwritten; calls that share one are stream-ordered.
+ * Launched as a programmatic dependent like mla_decode.  Errors: MLA_ERR_INVALID_ARG,
+ * MLA_ERR_UNSUPPORTED (tree_mask with more than 64 drafts), MLA_ERR_WORKSPACE_TOO_SMALL,
+ * MLA_ERR_CUDA.  Device-side, recorded as MLA_ERR_DEVICE_ARG: a length below q_len or beyond the
+ * plan (that request's row is left as it was) and a page id outside [0, num_pages) (its rows count
+ * as zeros). */
+int mla_key_mass_workspace(const mla_decode_plan_t* plan, size_t* bytes_out);
+int mla_key_mass(const mla_decode_plan_t* plan, const void* q, const void* kv_pages, const float* page_scales,
+                 const int32_t* page_table, const int32_t* seq_lens, const uint64_t* tree_mask,
+                 const float* lse, int q_len, int num_heads, float scale, float kv_scale, float decay,
+                 float* mass, int64_t mass_stride, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Eviction by accumulated attention weight: choose the keys that each request keeps and copy their
  * latent rows, in order, into new pages of the same pool.  Request b with L = seq_lens[b] cached
  * keys keeps K = min(keep_lens[b], L): the first s = min(sink, K), the last r = min(recent, K - s),

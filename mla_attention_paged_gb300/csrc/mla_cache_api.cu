@@ -1,5 +1,6 @@
 // mla_cache_api.cu -- host side of the entry points that keep the paged latent cache
-// (include/mla.h): mla_kv_append writes it and mla_kv_evict shrinks it.
+// (include/mla.h): mla_kv_append writes it, mla_key_mass weighs its keys and mla_kv_evict
+// shrinks it.
 // Argument checks run before anything is enqueued; nothing is allocated and no stream is
 // synchronised.
 #include <cstring>
@@ -102,6 +103,58 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
   p.kv_dtype = kv_dtype;
   p.kv_scale = kv_scale;
   return launch_kv_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_key_mass_workspace(const mla_decode_plan_t* plan, size_t* bytes_out) {
+  if (!plan || !bytes_out) return MLA_ERR_INVALID_ARG;
+  *bytes_out = 0;
+  return MLA_OK;
+}
+
+int mla_key_mass(const mla_decode_plan_t* plan, const void* q, const void* kv_pages, const float* page_scales,
+                 const int32_t* page_table, const int32_t* seq_lens, const uint64_t* tree_mask, const float* lse,
+                 int q_len, int num_heads, float scale, float kv_scale, float decay, float* mass, int64_t mass_stride,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!plan || !q || !kv_pages || !page_table || !seq_lens || !lse || !mass) return MLA_ERR_INVALID_ARG;
+  if ((plan->kv_dtype == MLA_KV_INT8_PAGE) != (page_scales != nullptr)) return MLA_ERR_INVALID_ARG;
+  if (q_len != plan->q_len || num_heads != plan->num_heads || plan->rows != q_len * num_heads) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_pages, 16) || !aligned(page_scales, 4) || !aligned(page_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(tree_mask, 8) || !aligned(lse, 4) || !aligned(mass, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(kv_scale > 0.f) || !(decay >= 0.f) || mass_stride < plan->max_seq_len) return MLA_ERR_INVALID_ARG;
+  if (tree_mask && q_len > kMaxTreeDrafts) return MLA_ERR_UNSUPPORTED;
+  size_t need = 0;
+  mla_key_mass_workspace(plan, &need);
+  if (need > 0) {
+    if (!workspace || !aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  }
+  KeyMassParams p;
+  memset(&p, 0, sizeof p);
+  p.status = status_ptr();
+  if (!p.status) return MLA_ERR_CUDA;
+  p.B = plan->batch;
+  p.T = q_len;
+  p.H = num_heads;
+  p.R = plan->rows;
+  p.page_size = plan->page_size;
+  p.max_pages = plan->max_pages_per_seq;
+  p.max_seq = plan->max_seq_len;
+  p.kv_dtype = plan->kv_dtype;
+  p.num_pages = plan->num_pages;
+  p.scale_log2 = scale * 1.4426950408889634f * (plan->kv_dtype != MLA_KV_BF16 ? kv_scale : 1.f);
+  p.decay = decay;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.kv_pool = static_cast<const uint8_t*>(kv_pages);
+  p.page_scales = page_scales;
+  p.inv_ref_scale = 1.f / kv_scale;
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.tree_mask = tree_mask;
+  p.lse = lse;
+  p.mass = mass;
+  p.mass_stride = mass_stride;
+  return launch_key_mass(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 int mla_kv_evict(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype, const int32_t* page_table,

@@ -116,6 +116,27 @@ struct EvictParams {
   unsigned* status;
 };
 
+// Attention weight of each key of a decode step, accumulated.
+struct KeyMassParams {
+  int B, T, H, R;               // R = T*H folded rows per request
+  int page_size, max_pages, max_seq;
+  int kv_dtype;
+  int64_t num_pages;
+  float scale_log2;             // softmax scale * log2(e) (* kv_scale for an 8-bit pool)
+  float decay;
+  const __nv_bfloat16* q;       // [B, T, H, 576]
+  const uint8_t* kv_pool;
+  const float* page_scales;     // kKvInt8Page: [num_pages]
+  float inv_ref_scale;          // kKvInt8Page: 1 / kv_scale
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const uint64_t* tree_mask;    // [B, T], or null: drafts in order
+  const float* lse;             // [B, T, H]
+  float* mass;                  // row b at b * mass_stride
+  int64_t mass_stride;
+  unsigned* status;
+};
+
 // Host helpers of mla_api.cu that every entry point uses.
 unsigned* status_ptr();  // device address of the current device's status word
 // Tiled tensor map (128-byte swizzle unless given).  dims/strides innermost first; strides
@@ -127,6 +148,7 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 inline bool page_size_ok(int P) { return P == 8 || P == 16 || P == 32 || P == 64 || P == 128 || P == 256; }
 
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_key_mass(const KeyMassParams& p, cudaStream_t stream);
 cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t stream);
 
 // Decode: split-KV partial kernel (tensor maps over q and the latent pool).

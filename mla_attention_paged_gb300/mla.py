@@ -31,7 +31,7 @@ EXPORTED = ["mla_decode_plan", "mla_decode", "mla_decode_partial", "mla_decode_c
             "mla_decode_int8_paged",
             "mla_prefill_varlen", "mla_prefill_paged", "mla_get_status", "mla_status_string", "mla_version", "mla_set_profile_events",
             "mla_profile_elapsed_ms", "mla_selftest_wait_timeout", "mla_kv_append", "mla_kv_evict",
-            "mla_decode_tree_plan", "mla_decode_tree"]
+            "mla_decode_tree_plan", "mla_decode_tree", "mla_key_mass_workspace", "mla_key_mass"]
 
 
 class MlaError(RuntimeError):
@@ -78,6 +78,10 @@ def _load() -> ctypes.CDLL:
     lib.mla_decode_tree_plan.argtypes = lib.mla_decode_plan.argtypes
     lib.mla_decode_tree.restype = i32
     lib.mla_decode_tree.argtypes = [ctypes.POINTER(DecodePlan), P, P, P, P, P, P, i32, i32, f32, f32, P, P, P, sz, P]
+    lib.mla_key_mass_workspace.restype = i32
+    lib.mla_key_mass_workspace.argtypes = [ctypes.POINTER(DecodePlan), ctypes.POINTER(sz)]
+    lib.mla_key_mass.restype = i32
+    lib.mla_key_mass.argtypes = [ctypes.POINTER(DecodePlan), P, P, P, P, P, P, P, i32, i32, f32, f32, f32, P, i64, P, sz, P]
     lib.mla_kv_append.restype = i32
     lib.mla_kv_append.argtypes = [P, i64, i64, P, i64, i64, i32, i32, P, P, i64, P, f32, P, i32, P, P, i32, i32, P, i64,
                                   i32, f32, P]
@@ -388,6 +392,45 @@ def kv_append(q: torch.Tensor | None, kv: torch.Tensor | None, positions: torch.
     _call(what, dev, stream, lib.mla_kv_append, *qa, *ka, float(eps), _ptr(cos_sin), int(cos_sin.shape[0]), _ptr(positions),
           _ptr(slots) if kv is not None else None, n, int(bool(interleaved)), pool, int(rows), int(kv_dtype), float(kv_scale))
     return q_out
+
+
+def key_mass_workspace_for(plan: DecodePlan, device) -> torch.Tensor | None:
+    """Allocate (with torch) a workspace of the size key_mass needs under this plan."""
+    need = ctypes.c_size_t()
+    _check(lib.mla_key_mass_workspace(ctypes.byref(plan), ctypes.byref(need)), "mla_key_mass_workspace")
+    return torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
+
+
+def key_mass(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+             lse: torch.Tensor, mass: torch.Tensor, scale: float, kv_scale: float = 1.0, tree_mask=None, page_scales=None,
+             decay: float = 1.0, workspace=None, stream=None) -> torch.Tensor:
+    """mla_key_mass through the C ABI: mass [B, >= max_seq_len] fp32 becomes decay * mass + the
+    attention weight each key received in the step whose lse [B,T,H] this is.  Returns mass."""
+    what = "mla_key_mass"
+    _want_pool(what, kv_pages, plan.kv_dtype)
+    dev = kv_pages.device
+    B, T, H = plan.batch, plan.q_len, plan.num_heads
+    if workspace is None:
+        workspace = key_mass_workspace_for(plan, dev)
+    i32, f32 = (torch.int32,), (torch.float32,)
+    _want(what, dev, [("q", q, (torch.bfloat16,), (B, T, H, 576)), ("page_table", page_table, i32, (B, plan.max_pages_per_seq)),
+                      ("seq_lens", seq_lens, i32, (B,)), ("lse", lse, f32, (B, T, H)), ("mass", mass, f32, None)])
+    if mass.dim() != 2 or mass.shape[0] != B:
+        _refuse(what, f"mass has shape {tuple(mass.shape)}")
+    if kv_pages.shape[0] != plan.num_pages or kv_pages.shape[1] != plan.page_size:
+        _refuse(what, f"kv_pages has shape {tuple(kv_pages.shape)}, not the plan's")
+    if tree_mask is not None:
+        _want(what, dev, [("tree_mask", tree_mask, (torch.int64,), (B, T))])
+    if page_scales is not None:
+        _want(what, dev, [("page_scales", page_scales, f32, (plan.num_pages,))])
+    ws_bytes = 0
+    if workspace is not None:
+        _want(what, dev, [("workspace", workspace, (workspace.dtype,), None)])
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _call(what, dev, stream, lib.mla_key_mass, ctypes.byref(plan), _ptr(q), _ptr(kv_pages), _ptr(page_scales), _ptr(page_table),
+          _ptr(seq_lens), _ptr(tree_mask), _ptr(lse), T, H, float(scale), float(kv_scale), float(decay), _ptr(mass),
+          int(mass.shape[1]), _ptr(workspace), ws_bytes)
+    return mass
 
 
 def kv_evict(kv_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch.Tensor,

@@ -107,7 +107,7 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
 
 int mla_key_mass_workspace(const mla_decode_plan_t* plan, size_t* bytes_out) {
   if (!plan || !bytes_out) return MLA_ERR_INVALID_ARG;
-  *bytes_out = 0;
+  *bytes_out = key_mass_part_bytes(plan->kv_dtype, plan->batch, plan->rows, plan->max_seq_len);
   return MLA_OK;
 }
 
@@ -154,7 +154,31 @@ int mla_key_mass(const mla_decode_plan_t* plan, const void* q, const void* kv_pa
   p.lse = lse;
   p.mass = mass;
   p.mass_stride = mass_stride;
-  return launch_key_mass(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  p.part = static_cast<float*>(workspace);
+  // Queries as nine 128-byte-swizzled blocks of 64 columns; the pool as boxes of 64 columns by
+  // a page's share of a 128-key tile.
+  CUtensorMap tm_q, tm_kv;
+  memset(&tm_q, 0, sizeof tm_q);
+  memset(&tm_kv, 0, sizeof tm_kv);
+  const uint64_t pool_rows = static_cast<uint64_t>(plan->num_pages) * plan->page_size;
+  const uint32_t box_kv[2] = {64, static_cast<uint32_t>(plan->page_size < 128 ? plan->page_size : 128)};
+  if (plan->kv_dtype == MLA_KV_BF16) {
+    const uint64_t dims[3] = {64, static_cast<uint64_t>(plan->batch) * plan->rows, kLatentDim / 64};
+    const uint64_t strides[2] = {kLatentDim * 2, 128};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(key_mass_group_rows(plan->rows)), kLatentDim / 64};
+    const uint64_t kv_dims[2] = {kLatentDim, pool_rows};
+    const uint64_t kv_strides[1] = {kLatentDim * 2};
+    if (!make_map(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box) ||
+        !make_map(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_pages, kv_dims, kv_strides, box_kv))
+      return MLA_ERR_CUDA;
+  } else if (plan->kv_dtype == MLA_KV_E4M3) {
+    const uint64_t kv_dims[2] = {kLatentDim, pool_rows};
+    const uint64_t kv_strides[1] = {kLatentDim};
+    if (!make_map(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, kv_pages, kv_dims, kv_strides, box_kv, CU_TENSOR_MAP_SWIZZLE_64B))
+      return MLA_ERR_CUDA;
+  }
+  return launch_key_mass(p, tm_q, tm_kv, plan->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK
+                                                                                                           : MLA_ERR_CUDA;
 }
 
 int mla_kv_evict(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype, const int32_t* page_table,

@@ -7,10 +7,28 @@
 // with the visibility of mla_decode (draft t sees keys 0 .. L_b - T + t) or, with tree masks,
 // of mla_decode_tree.  A row whose lse is not finite adds nothing.
 //
-// This kernel: one CTA per (32 keys, request), the keys decoded to fp32 in shared memory,
-// 16 query rows at a time beside them; a thread owns one key and every fourth row, and the
-// four threads of a key add their sums in a fixed order.
+// bf16 and e4m3 pools: key_mass_mma_kernel.  What has to be read is the keys, once; so it is
+// bound by memory while a request has few rows, and by the first product with many.
+//  * S^T = K . Q^T on the tensor cores (tcgen05, M = 128 keys, N = up to 128 query rows): a
+//    key is a TMEM lane, so its weights lie in one thread's columns and their sum needs no
+//    exchange between threads; the result is stored without atomics, in a fixed order.
+//  * K streams by TMA (128 keys x 64 columns a piece) through a ring that takes what shared
+//    memory the resident Q leaves.  An e4m3 pool is multiplied as its raw codes (kind::f8f6f4)
+//    with Q split in two e4m3 parts (as mla_decode_e4m3_sm103a.cu), the two parts side by
+//    side along N.
+//  * The grid is one CTA per SM; every CTA takes an equal run of the batch's 128-key tiles,
+//    across requests (keys are independent, so nothing is joined afterwards).  Requests of
+//    more than 128 rows run in row groups side by side, whose sums a second kernel adds up.
+//  * Two groups of four warps take alternate tiles from two S buffers, so exponentials
+//    (R per key) run beside the next tile's product.
+//
+// int8 pools: key_mass_kernel, one CTA per (32 keys, request), the keys decoded to fp32 in
+// shared memory, 16 query rows at a time beside them; a thread owns one key and every fourth
+// row, and the four threads of a key add their sums in a fixed order.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "mla_internal.h"
 #include "sm103a_ptx.cuh"
@@ -25,16 +43,6 @@ constexpr int kThreads = 128;
 constexpr int kPitch = kLatentDim + 1;  // odd: a warp's 32 keys fall in 32 banks
 constexpr int kSmemBytes = (kKeys * kPitch + kRows * kLatentDim + kThreads) * 4;
 
-template <int kKv>
-__device__ __forceinline__ float element(const uint8_t* row, int c) {
-  if constexpr (kKv == kKvBf16) {
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[c]);
-  } else if constexpr (kKv == kKvE4m3) {
-    return static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(row)[c]);
-  } else {
-    return static_cast<float>(reinterpret_cast<const int8_t*>(row)[c]);
-  }
-}
 
 template <int kKv>
 __global__ void __launch_bounds__(kThreads) key_mass_kernel(const KeyMassParams p) {
@@ -52,7 +60,6 @@ __global__ void __launch_bounds__(kThreads) key_mass_kernel(const KeyMassParams 
   }
   if (k0 >= L) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int elem = kKv == kKvBf16 ? 2 : 1;
   for (int i = warp; i < kKeys; i += kThreads / 32) {
     const int j = k0 + i;
     const uint8_t* row = nullptr;
@@ -62,11 +69,11 @@ __global__ void __launch_bounds__(kThreads) key_mass_kernel(const KeyMassParams 
       if (page < 0 || page >= p.num_pages) {
         if (lane == 0) atomicOr(p.status, kStatusDeviceArg);
       } else {
-        row = p.kv_pool + (page * p.page_size + j % p.page_size) * kLatentDim * elem;
+        row = p.kv_pool + (page * p.page_size + j % p.page_size) * kLatentDim;
         if (kKv == kKvInt8Page) mult = p.page_scales[page] * p.inv_ref_scale;
       }
     }
-    for (int c = lane; c < kLatentDim; c += 32) ks[i * kPitch + c] = row ? element<kKv>(row, c) * mult : 0.f;
+    for (int c = lane; c < kLatentDim; c += 32) ks[i * kPitch + c] = row ? static_cast<float>(static_cast<int8_t>(row[c])) * mult : 0.f;
   }
   const int key = k0 + lane;
   const int u = key - (L - p.T);  // draft index of this key (negative: prefix)
@@ -105,8 +112,488 @@ __global__ void __launch_bounds__(kThreads) key_mass_kernel(const KeyMassParams 
   }
 }
 
+// ----------------------------------------------------------------------------------------
+// bf16 and e4m3 pools
+// ----------------------------------------------------------------------------------------
+constexpr int kTile = 128;                        // keys per tile (MMA M, TMEM lanes)
+constexpr int kDimBlocks = kLatentDim / 64;       // 9 blocks of 64 columns
+constexpr int kMaxRows = 128;                     // query rows a CTA holds (MMA N; e4m3: 2 x)
+constexpr int kMaxStages = 12;
+constexpr int kGroupWarps = 4;                    // warps that read one S buffer
+constexpr int kEpiWarps = 2 * kGroupWarps;
+constexpr int kEpiThreads = 32 * kEpiWarps;
+constexpr int kLoadWarp = kEpiWarps;
+constexpr int kMmaWarp = kEpiWarps + 1;
+constexpr int kMmaThreads = 32 * (kEpiWarps + 2);
+constexpr uint32_t kTmemCols = 512;               // two S buffers of up to 256 columns
+constexpr int kNeverSees = -2147483647 - 1;       // draft index of a row that adds nothing
+
+// Column blocks per ring stage: one bf16 block is 16 KB; e4m3 blocks are 8 KB and two MMAs
+// each, so three share a barrier.
+template <bool kE4m3>
+constexpr int kStageBlocks = kE4m3 ? 3 : 1;
+template <bool kE4m3>
+constexpr int kStageBytes = kTile * 64 * (kE4m3 ? 1 : 2) * kStageBlocks<kE4m3>;
+
+struct MassCtrl {
+  uint64_t q_full;
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
+  uint64_t s_full[2];
+  uint64_t s_free[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int first_b, first_tile;   // where this CTA's run of tiles begins
+  int64_t tiles;             // and its length
+  int any_dead;              // some of the segment's rows add nothing
+  alignas(16) float2 row[kMaxRows];      // scale of the row's scores and its -lse, log2 domain
+  alignas(16) uint64_t mask[kMaxRows];   // trees: the drafts the row sees
+  int draft[kMaxRows];                   // the row's draft, or kNeverSees
+};
+constexpr int kCtrlBytes = 4096;
+static_assert(sizeof(MassCtrl) <= kCtrlBytes, "control block");
+constexpr int kMaxSmem = 232448;
+
+// The shared memory a launch takes: alignment slack, control, Q (N rows x 1152 bytes in either
+// format), and as many ring stages as fit.
+struct MassShape {
+  int rows, groups, stages, smem;
+};
+template <bool kE4m3>
+MassShape mass_shape(int R) {
+  MassShape s;
+  s.groups = (R + kMaxRows - 1) / kMaxRows;
+  s.rows = ((R + s.groups - 1) / s.groups + 15) / 16 * 16;  // even groups, a multiple of the MMA's N step
+  s.groups = (R + s.rows - 1) / s.rows;
+  const int left = kMaxSmem - 1024 - kCtrlBytes - s.rows * kLatentDim * 2;
+  s.stages = left / kStageBytes<kE4m3> < kMaxStages ? left / kStageBytes<kE4m3> : kMaxStages;
+  s.smem = 1024 + kCtrlBytes + s.rows * kLatentDim * 2 + s.stages * kStageBytes<kE4m3>;
+  return s;
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// One query row of an e4m3 launch: q 2^s = hi + lo with its largest element in [128, 256), as
+// K-major 64-byte-swizzled rows `row` (hi) and `row + rows` (lo) of nine blocks of 2 x rows
+// rows.  The whole warp works on it; returns 2^-s.
+__device__ __forceinline__ float split_row(const __nv_bfloat16* q, uint32_t q_smem, int row, int rows, int lane) {
+  uint4 w[3];
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int c = lane + 32 * i;  // chunk of eight columns, 72 in all
+    w[i] = c < kLatentDim / 8 ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  // 2^s from the exponent field, kept where both 2^s and 2^-s are normal numbers
+  int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
+  e = max(-110, min(e, 120));
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
+  const float down = __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int c = lane + 32 * i;
+    if (c >= kLatentDim / 8) break;
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = make_float2(__uint_as_float(u[k] << 16) * up, __uint_as_float(u[k] & 0xFFFF0000u) * up);
+      const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+      const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+      const __nv_fp8x2_storage_t l =
+          __nv_cvt_float2_to_fp8x2(make_float2(x.x - hf.x, x.y - hf.y), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t sh = 16 * (k & 1);
+      hi[k >> 1] = (k & 1 ? hi[k >> 1] : 0u) | static_cast<uint32_t>(h) << sh;
+      lo[k >> 1] = (k & 1 ? lo[k >> 1] : 0u) | static_cast<uint32_t>(l) << sh;
+    }
+    const int blk = c >> 3, x = (c & 7) * 8;  // byte x of the block's 64-byte row
+    auto at = [&](int r) {
+      return q_smem + blk * (2 * rows * 64) + r * 64 + ((((x >> 4) ^ (r >> 1)) & 3) << 4) + (x & 8);
+    };
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at(row)), "r"(hi[0]), "r"(hi[1]) : "memory");
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at(row + rows)), "r"(lo[0]), "r"(lo[1]) : "memory");
+  }
+  return down;
+}
+
+template <bool kE4m3>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                    const KeyMassParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int N = p.group_rows;
+  MassCtrl* ctrl = reinterpret_cast<MassCtrl*>(smem);
+  uint8_t* q_s = smem + kCtrlBytes;                    // [9][N (e4m3: 2 N)][128 (64) bytes]
+  uint8_t* ring = q_s + N * kLatentDim * 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = blockIdx.x % p.groups, set = blockIdx.x / p.groups;
+  const int row0 = group * N, nrows = min(N, p.R - row0);
+
+  if (threadIdx.x == 0) {
+    mbar_init(&ctrl->q_full, kE4m3 ? kEpiWarps : 1);
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctrl->s_full[i], 1);
+      mbar_init(&ctrl->s_free[i], kGroupWarps);
+    }
+    mbar_init(&ctrl->drain, 1);
+    ctrl->abort_flag = 0;
+    ctrl->any_dead = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&ctrl->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    if (!kE4m3) tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_kv);
+  }
+  // programmatic dependent launch: no input is read before the previous kernel has completed
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  auto bad_len = [&](int L) {
+    return L < p.T || L > p.max_seq || L > static_cast<int64_t>(p.max_pages) * p.page_size;
+  };
+  auto tiles_of = [&](int b) -> int {
+    const int L = p.seq_lens[b];
+    return bad_len(L) ? 0 : (L + kTile - 1) / kTile;
+  };
+  if (warp == 0) {
+    // this CTA's run: tiles [total set / sets, total (set + 1) / sets) of the batch
+    int64_t total = 0;
+    for (int b = lane; b < p.B; b += 32) {
+      total += tiles_of(b);
+      if (blockIdx.x == 0 && bad_len(p.seq_lens[b])) atomicOr(p.status, kStatusDeviceArg);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const int64_t begin = total * set / p.sets, end = total * (set + 1) / p.sets;
+    int64_t before = 0;
+    int fb = 0, ft = 0;
+    bool found = begin >= end;
+    for (int b0 = 0; !found && b0 < p.B; b0 += 32) {
+      const int n = b0 + lane < p.B ? tiles_of(b0 + lane) : 0;
+      int64_t incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, before + incl > begin);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        const int64_t at = __shfl_sync(0xffffffffu, before + incl - n, l);
+        fb = b0 + l;
+        ft = static_cast<int>(begin - at);
+        found = true;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      ctrl->first_b = fb;
+      ctrl->first_tile = ft;
+      ctrl->tiles = end - begin;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem_base;
+  volatile int* abort_flag = &ctrl->abort_flag;
+  constexpr int kBlocksPerStage = kStageBlocks<kE4m3>;
+  constexpr int kStageB = kStageBytes<kE4m3>;
+  constexpr int kBlockB = kStageB / kBlocksPerStage;
+  const uint32_t s_cols = kE4m3 ? 2 * N : N;
+
+  // Every role walks the same segments: the run's tiles of one request.
+  int b = ctrl->first_b, it = ctrl->first_tile;
+  int64_t left = ctrl->tiles;
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------------ TMA producer: lanes
+    // share the pieces (page part, column block) of a stage
+    const int P = p.page_size;
+    const int parts = P >= kTile ? 1 : kTile / P, part_rows = kTile / parts;
+    const uint64_t pol = p.groups == 1 ? policy_evict_first() : policy_evict_normal();
+    const unsigned n_pages = static_cast<unsigned>(min(p.num_pages, static_cast<int64_t>(0x7fffffff)));
+    bool bad_pid = false, ok = true;
+    int slot = 0, phase = 0, issued = 0;
+    while (ok && left > 0) {
+      const int nt = tiles_of(b);
+      if (it >= nt) {
+        ++b;
+        it = 0;
+        continue;
+      }
+      const int n = static_cast<int>(min(static_cast<int64_t>(nt - it), left));
+      const int L = p.seq_lens[b];
+      const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+      // pool row of this lane's page part of tile i; a part past the end, and an id outside the
+      // pool (reported), lie before the first row, which TMA fills with zeros
+      auto part_row = [&](int i) -> int {
+        const int k = i * kTile + lane * part_rows;
+        if (lane >= parts || k >= L) return -part_rows;
+        const int pid = __ldg(pt + k / P);
+        if (static_cast<unsigned>(pid) >= n_pages) {
+          bad_pid = true;
+          return -part_rows;
+        }
+        return pid * P + k % P;
+      };
+      int row = part_row(it);
+      for (int i = 0; ok && i < n; ++i) {
+        const int next = i + 1 < n ? part_row(it + i + 1) : 0;
+#pragma unroll 1
+        for (int c = 0; c < kDimBlocks; c += kBlocksPerStage) {
+          bool w = true;
+          if (lane == 0 && issued >= p.stages) w = mbar_wait(&ctrl->empty[slot], phase ^ 1, abort_flag);
+          ok = __shfl_sync(0xffffffffu, w, 0);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&ctrl->full[slot], kStageB);
+          __syncwarp();
+          if (lane < parts) {
+            uint8_t* dst = ring + slot * kStageB + lane * part_rows * (kBlockB / kTile);
+#pragma unroll
+            for (int k = 0; k < kBlocksPerStage; ++k)
+              tma_load_2d(dst + k * kBlockB, &tm_kv, &ctrl->full[slot], (c + k) * 64, row, pol);
+          }
+          ++issued;
+          if (++slot == p.stages) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+        row = next;
+      }
+      left -= n;
+      it += n;
+    }
+    if (__any_sync(0xffffffffu, bad_pid) && lane == 0) atomicOr(p.status, kStatusDeviceArg);
+    if (!ok && lane == 0) {
+      // copies still in flight land before the CTA exits: the last use of every stage
+      for (int u = max(0, issued - p.stages); u < issued; ++u) drain_wait(&ctrl->full[u % p.stages], (u / p.stages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------ MMA issuer
+    const uint32_t idesc = kE4m3 ? make_idesc_e4m3(kTile, 2 * N) : make_idesc_bf16(kTile, N, false, false);
+    const uint32_t q_block = N * 128;  // bytes of a column block of Q in either format
+    bool ok = true;
+    int slot = 0, phase = 0, t = 0, seg = 0;
+    while (ok && left > 0) {
+      const int nt = tiles_of(b);
+      if (it >= nt) {
+        ++b;
+        it = 0;
+        continue;
+      }
+      const int n = static_cast<int>(min(static_cast<int64_t>(nt - it), left));
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctrl->q_full, seg & 1, abort_flag));
+      for (int i = 0; ok && i < n; ++i, ++t) {
+        const int buf = t & 1;
+        if (t >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&ctrl->s_free[buf], ((t >> 1) - 1) & 1, abort_flag));
+        const uint32_t d = tmem + buf * s_cols;
+#pragma unroll 1
+        for (int c = 0; ok && c < kDimBlocks; c += kBlocksPerStage) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&ctrl->full[slot], phase, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kBlocksPerStage; ++k) {
+              const uint32_t ka = smem_u32(ring + slot * kStageB + k * kBlockB), qa = smem_u32(q_s) + (c + k) * q_block;
+              if constexpr (kE4m3) {
+                const uint64_t kd = make_smem_desc_sw64(ka), qd = make_smem_desc_sw64(qa);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) umma_f8(d, kd + 2 * x, qd + 2 * x, idesc, (c | k | x) != 0);
+              } else {
+                const uint64_t kd = make_smem_desc(ka, 16, 1024), qd = make_smem_desc(qa, 16, 1024);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) umma_bf16(d, kd + 2 * x, qd + 2 * x, idesc, (c | k | x) != 0);
+              }
+            }
+            umma_commit(&ctrl->empty[slot]);
+            if (c + kBlocksPerStage >= kDimBlocks) umma_commit(&ctrl->s_full[buf]);
+          }
+          __syncwarp();
+          if (++slot == p.stages) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      left -= n;
+      it += n;
+      ++seg;
+    }
+    if (elect_one()) {
+      umma_commit(&ctrl->drain);
+      drain_wait(&ctrl->drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ weights and sums (warps
+    // 0-7): warps 0-3 take even tiles, 4-7 odd ones; a thread owns the key of its TMEM lane
+    const int mine = warp >> 2;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const int key_in_tile = 32 * (warp & 3) + lane;
+    bool fail = false;
+    int t = 0, seg = 0;
+    while (left > 0) {
+      const int nt = tiles_of(b);
+      if (it >= nt) {
+        ++b;
+        it = 0;
+        continue;
+      }
+      const int n = static_cast<int>(min(static_cast<int64_t>(nt - it), left));
+      const int L = p.seq_lens[b];
+      const int p0 = L - p.T;
+      // both groups have read every S of the segment before: its products are complete, and
+      // Q and the rows' data may be replaced
+      if (bar_or(1, kEpiThreads, fail || *abort_flag != 0)) break;
+      if (threadIdx.x == 0) ctrl->any_dead = 0;
+      if (!kE4m3 && threadIdx.x == 0) {
+        mbar_arrive_expect_tx(&ctrl->q_full, N * kLatentDim * 2);
+        tma_load_3d(q_s, &tm_q, &ctrl->q_full, 0, b * p.R + row0, 0, policy_evict_last());
+      }
+      named_bar_sync(1, kEpiThreads);
+      for (int r = threadIdx.x; r < N; r += kEpiThreads) {
+        const bool real = r < nrows;
+        const int64_t at = static_cast<int64_t>(b) * p.R + row0 + r;
+        const float lse = real ? p.lse[at] : INFINITY;
+        const bool live = fabsf(lse) < INFINITY;  // (false for NaN)
+        const int draft = (row0 + r) / p.H;
+        if (!live) ctrl->any_dead = 1;
+        ctrl->draft[r] = live ? draft : kNeverSees;
+        ctrl->mask[r] = live && p.tree_mask ? p.tree_mask[static_cast<int64_t>(b) * p.T + draft] & draft_bits(p.T) : 0;
+        if (!kE4m3) ctrl->row[r] = make_float2(p.scale_log2, live ? -lse * 1.4426950408889634f : 0.f);
+        else ctrl->row[r].y = live ? -lse * 1.4426950408889634f : 0.f;
+      }
+      if (kE4m3) {
+        for (int r = warp; r < N; r += kEpiWarps) {
+          // (rows past the group's end repeat its last one; they add nothing)
+          const __nv_bfloat16* q = p.q + (static_cast<int64_t>(b) * p.R + row0 + min(r, nrows - 1)) * kLatentDim;
+          const float down = split_row(q, smem_u32(q_s), r, N, lane);
+          if (lane == 0) ctrl->row[r].x = p.scale_log2 * down;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->q_full);
+      }
+      named_bar_sync(1, kEpiThreads);
+      const bool any_dead = ctrl->any_dead != 0;
+      for (int i = 0; i < n; ++i, ++t) {
+        if ((t & 1) != mine || fail) continue;
+        const int k0 = (it + i) * kTile;
+        const int key = k0 + key_in_tile;
+        float* out = p.groups == 1 ? p.mass + static_cast<int64_t>(b) * p.mass_stride + key
+                                   : p.part + (static_cast<int64_t>(group) * p.B + b) * p.max_seq + key;
+        const bool accumulate = p.groups == 1 && p.decay != 0.f && key < L;
+        const float old = accumulate ? *out : 0.f;
+        fail = __any_sync(0xffffffffu, !mbar_wait(&ctrl->s_full[mine], (t >> 1) & 1, abort_flag));
+        if (fail) continue;
+        tc_fence_after();
+        const uint32_t s_tmem = tmem + lane_base + mine * s_cols;
+        const int u = key - p0;  // draft index of this key (negative: prefix)
+        const bool all = !any_dead && k0 + kTile <= p0;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int c = 0; c < N; c += 16) {
+          uint32_t v[16], w[16];
+          tmem_ld16(s_tmem + c, v);
+          if (kE4m3) tmem_ld16(s_tmem + N + c, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            const float4 rc = *reinterpret_cast<const float4*>(&ctrl->row[c + k]);
+            float s0 = __uint_as_float(v[k]), s1 = __uint_as_float(v[k + 1]);
+            if (kE4m3) {
+              s0 += __uint_as_float(w[k]);
+              s1 += __uint_as_float(w[k + 1]);
+            }
+            float e0 = ex2_approx(fmaf(s0, rc.x, rc.y)), e1 = ex2_approx(fmaf(s1, rc.z, rc.w));
+            if (!all) {
+              const int d0 = ctrl->draft[c + k], d1 = ctrl->draft[c + k + 1];
+              bool v0 = u <= d0, v1 = u <= d1;  // (a prefix key is seen by every row that adds anything)
+              if (p.tree_mask && u >= 0) {
+                v0 = u < 64 && ((ctrl->mask[c + k] >> u) & 1);
+                v1 = u < 64 && ((ctrl->mask[c + k + 1] >> u) & 1);
+              }
+              e0 = v0 ? e0 : 0.f;
+              e1 = v1 ? e1 : 0.f;
+            }
+            acc[(k >> 1) & 1] += e0;
+            acc[2 + ((k >> 1) & 1)] += e1;
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->s_free[mine]);
+        const float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        if (key < L) *out = accumulate ? fmaf(p.decay, old, sum) : sum;
+      }
+      left -= n;
+      it += n;
+      ++seg;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && ctrl->abort_flag) atomicOr(p.status, kStatusTimeout);
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Row groups' sums into the mass, in the groups' order.
+__global__ void __launch_bounds__(256) key_mass_join_kernel(const KeyMassParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = blockIdx.y, key = blockIdx.x * 256 + threadIdx.x;
+  const int L = p.seq_lens[b];
+  if (L < p.T || L > p.max_seq || L > static_cast<int64_t>(p.max_pages) * p.page_size || key >= L) return;
+  float sum = 0.f;
+  for (int g = 0; g < p.groups; ++g) sum += p.part[(static_cast<int64_t>(g) * p.B + b) * p.max_seq + key];
+  float* m = p.mass + static_cast<int64_t>(b) * p.mass_stride + key;
+  *m = p.decay == 0.f ? sum : fmaf(p.decay, *m, sum);
+}
+
+template <typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int kKv>
-cudaError_t launch(const KeyMassParams& p, cudaStream_t stream) {
+cudaError_t launch_simple(const KeyMassParams& p, cudaStream_t stream) {
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -116,27 +603,50 @@ cudaError_t launch(const KeyMassParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.max_seq + kKeys - 1) / kKeys, p.B);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, key_mass_kernel<kKv>, p);
+  return launch_dependent(key_mass_kernel<kKv>, dim3((p.max_seq + kKeys - 1) / kKeys, p.B), kThreads, kSmemBytes, stream, p);
+}
+
+template <bool kE4m3>
+cudaError_t launch_mma(KeyMassParams p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv, int num_sms,
+                       cudaStream_t stream) {
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_device != dev) {
+    e = cudaFuncSetAttribute(key_mass_mma_kernel<kE4m3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
+  const MassShape s = mass_shape<kE4m3>(p.R);
+  p.group_rows = s.rows;
+  p.groups = s.groups;
+  p.stages = s.stages;
+  // one CTA per SM, and no more sets than tiles
+  const int64_t tiles = static_cast<int64_t>(p.B) * ((p.max_seq + kTile - 1) / kTile);
+  p.sets = static_cast<int>(std::min(static_cast<int64_t>(std::max(1, num_sms / s.groups)), tiles));
+  e = launch_dependent(key_mass_mma_kernel<kE4m3>, dim3(p.sets * s.groups), kMmaThreads, s.smem, stream, tm_q, tm_kv, p);
+  if (e != cudaSuccess || s.groups == 1) return e;
+  return launch_dependent(key_mass_join_kernel, dim3((p.max_seq + 255) / 256, p.B), 256, 0, stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_key_mass(const KeyMassParams& p, cudaStream_t stream) {
+int key_mass_group_rows(int R) { return mass_shape<false>(R).rows; }
+
+size_t key_mass_part_bytes(int kv_dtype, int B, int R, int max_seq) {
+  if (kv_dtype != kKvBf16 && kv_dtype != kKvE4m3) return 0;
+  const int groups = mass_shape<false>(R).groups;
+  return groups == 1 ? 0 : static_cast<size_t>(groups) * B * max_seq * sizeof(float);
+}
+
+cudaError_t launch_key_mass(const KeyMassParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv, int num_sms,
+                            cudaStream_t stream) {
   switch (p.kv_dtype) {
-    case kKvE4m3: return launch<kKvE4m3>(p, stream);
-    case kKvInt8: return launch<kKvInt8>(p, stream);
-    case kKvInt8Page: return launch<kKvInt8Page>(p, stream);
-    default: return launch<kKvBf16>(p, stream);
+    case kKvE4m3: return launch_mma<true>(p, tm_q, tm_kv, num_sms, stream);
+    case kKvInt8: return launch_simple<kKvInt8>(p, stream);
+    case kKvInt8Page: return launch_simple<kKvInt8Page>(p, stream);
+    default: return launch_mma<false>(p, tm_q, tm_kv, num_sms, stream);
   }
 }
 

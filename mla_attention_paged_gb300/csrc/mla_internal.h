@@ -113,6 +113,7 @@ struct EvictParams {
   int32_t* new_lens;
   float* mass_out;
   int64_t mass_out_stride;
+  int cached;                   // images a CTA keeps in shared memory (launch_kv_evict)
   unsigned* status;
 };
 

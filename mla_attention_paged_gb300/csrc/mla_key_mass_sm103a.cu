@@ -181,52 +181,70 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-// One query row of an e4m3 launch: q 2^s = hi + lo with its largest element in [128, 256), as
-// K-major 64-byte-swizzled rows `row` (hi) and `row + rows` (lo) of nine blocks of 2 x rows
-// rows.  The whole warp works on it; returns 2^-s.
-__device__ __forceinline__ float split_row(const __nv_bfloat16* q, uint32_t q_smem, int row, int rows, int lane) {
-  uint4 w[3];
-  float mx = 0.f;
+// Query rows of an e4m3 launch: q 2^s = hi + lo with each row's largest element in [128, 256),
+// as K-major 64-byte-swizzled rows r (hi) and r + rows (lo) of nine blocks of 2 x rows rows.
+// The warp takes rows warp, warp + 8, ..., kSplitRows at a time with all their loads in flight
+// (one at a time, 80 rows took 10 us of load latency); rows past `real` repeat the last one.
+// scale[r] becomes scale_log2 2^-s.
+constexpr int kSplitRows = 4;
+
+__device__ __forceinline__ void split_rows(const __nv_bfloat16* q, uint32_t q_smem, int rows, int real, int warp, int lane,
+                                           float scale_log2, float2* scale) {
+  for (int r0 = warp; r0 < rows; r0 += kSplitRows * kEpiWarps) {
+    uint4 w[kSplitRows][3];
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int c = lane + 32 * i;  // chunk of eight columns, 72 in all
-    w[i] = c < kLatentDim / 8 ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    for (int m = 0; m < kSplitRows; ++m) {
+      const int r = min(r0 + m * kEpiWarps, real - 1);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  // 2^s from the exponent field, kept where both 2^s and 2^-s are normal numbers
-  int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-  e = max(-110, min(e, 120));
-  const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
-  const float down = __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int c = lane + 32 * i;
-    if (c >= kLatentDim / 8) break;
-    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-    uint32_t hi[2], lo[2];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 x = make_float2(__uint_as_float(u[k] << 16) * up, __uint_as_float(u[k] & 0xFFFF0000u) * up);
-      const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
-      const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-      const __nv_fp8x2_storage_t l =
-          __nv_cvt_float2_to_fp8x2(make_float2(x.x - hf.x, x.y - hf.y), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t sh = 16 * (k & 1);
-      hi[k >> 1] = (k & 1 ? hi[k >> 1] : 0u) | static_cast<uint32_t>(h) << sh;
-      lo[k >> 1] = (k & 1 ? lo[k >> 1] : 0u) | static_cast<uint32_t>(l) << sh;
+      for (int i = 0; i < 3; ++i) {
+        const int c = lane + 32 * i;  // chunk of eight columns, 72 in all
+        w[m][i] = c < kLatentDim / 8 ? __ldg(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(r) * kLatentDim) + c)
+                                     : make_uint4(0u, 0u, 0u, 0u);
+      }
     }
-    const int blk = c >> 3, x = (c & 7) * 8;  // byte x of the block's 64-byte row
-    auto at = [&](int r) {
-      return q_smem + blk * (2 * rows * 64) + r * 64 + ((((x >> 4) ^ (r >> 1)) & 3) << 4) + (x & 8);
-    };
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at(row)), "r"(hi[0]), "r"(hi[1]) : "memory");
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at(row + rows)), "r"(lo[0]), "r"(lo[1]) : "memory");
+#pragma unroll
+    for (int m = 0; m < kSplitRows; ++m) {
+      const int r = r0 + m * kEpiWarps;
+      if (r >= rows) break;
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint32_t u[4] = {w[m][i].x, w[m][i].y, w[m][i].z, w[m][i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // 2^s from the exponent field, kept where both 2^s and 2^-s are normal numbers
+      const int e = max(-110, min(static_cast<int>(__float_as_uint(mx) >> 23) - 127, 120));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
+      if (lane == 0) scale[r].x = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int c = lane + 32 * i;
+        if (c >= kLatentDim / 8) break;
+        const uint32_t u[4] = {w[m][i].x, w[m][i].y, w[m][i].z, w[m][i].w};
+        uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = make_float2(__uint_as_float(u[k] << 16) * up, __uint_as_float(u[k] & 0xFFFF0000u) * up);
+          const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+          const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+          const __nv_fp8x2_storage_t l =
+              __nv_cvt_float2_to_fp8x2(make_float2(x.x - hf.x, x.y - hf.y), __NV_SATFINITE, __NV_E4M3);
+          hi[k >> 1] |= static_cast<uint32_t>(h) << (16 * (k & 1));
+          lo[k >> 1] |= static_cast<uint32_t>(l) << (16 * (k & 1));
+        }
+        const int blk = c >> 3, x = (c & 7) * 8;  // byte x of the block's 64-byte row
+        auto at = [&](int row) {
+          return q_smem + blk * (2 * rows * 64) + row * 64 + ((((x >> 4) ^ (row >> 1)) & 3) << 4) + (x & 8);
+        };
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at(r)), "r"(hi[0]), "r"(hi[1]) : "memory");
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at(r + rows)), "r"(lo[0]), "r"(lo[1]) : "memory");
+      }
+    }
   }
-  return down;
 }
 
 template <bool kE4m3>
@@ -488,12 +506,8 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         else ctrl->row[r].y = live ? -lse * 1.4426950408889634f : 0.f;
       }
       if (kE4m3) {
-        for (int r = warp; r < N; r += kEpiWarps) {
-          // (rows past the group's end repeat its last one; they add nothing)
-          const __nv_bfloat16* q = p.q + (static_cast<int64_t>(b) * p.R + row0 + min(r, nrows - 1)) * kLatentDim;
-          const float down = split_row(q, smem_u32(q_s), r, N, lane);
-          if (lane == 0) ctrl->row[r].x = p.scale_log2 * down;
-        }
+        split_rows(p.q + (static_cast<int64_t>(b) * p.R + row0) * kLatentDim, smem_u32(q_s), N, nrows, warp, lane,
+                   p.scale_log2, ctrl->row);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctrl->q_full);

@@ -11,11 +11,14 @@
 // Everything is held in fp32 from the load to the one rounding at the store (bf16, or the
 // value over kv_scale rounded to the nearest e4m3 or int8 code, saturated).
 //
-// Bound by memory: each input is read once and each output written once.  One warp per
-// (token, head) or per token's key; a lane holds 16-byte chunks (8 columns) in registers, so
-// the norm is one shuffle reduction and nothing passes through shared memory.  The 64
-// rotated columns always sit in lanes 24-31 (chunk k of 8 in lane 24 + k), which puts a
-// half-split pair's two chunks in lanes that differ in bit 2.
+// Bound by memory: each input is read once and each output written once.  Eight lanes share a
+// row (a head's query or a token's key) and hold it in registers, 16-byte chunk l, l + 8, ... in
+// lane l, so the norm is three shuffles and nothing passes through shared memory.  The 64
+// rotated columns are one chunk per lane, which puts the two chunks of a half-split pair in
+// lanes that differ in bit 2.  A warp takes four rows at a time: for queries four heads of one
+// token, kSteps times with all loads in flight, so positions, cosines and weights are read once
+// per warp; for keys four tokens.  (A warp per row, two loads in flight, took 72 us where
+// this takes APPEND_US for 8191 tokens of 16 normed 192-wide heads and their keys.)
 #include <cuda_fp8.h>
 
 #include "mla_internal.h"
@@ -26,7 +29,11 @@ namespace {
 
 constexpr int kRope = 64;
 constexpr int kWarps = 4;
-constexpr int kRopeLane = 24;  // lanes 24-31 hold the rotated columns' eight chunks
+#ifndef MANY
+#define MANY 4
+#endif
+constexpr int kManySteps = MANY;
+constexpr int64_t kFewRows = 16384;
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -50,45 +57,51 @@ __device__ __forceinline__ float sum_sq(const float (&f)[8]) {
   return s;
 }
 
-__device__ __forceinline__ float warp_sum(float s) {
+// Sum over the kLanes lanes of a row.
+template <int kLanes>
+__device__ __forceinline__ float row_sum(float s) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
 
-__device__ __forceinline__ void scale8(float (&f)[8], float inv, const __nv_bfloat16* w) {
-  float g[8];
-  unpack8(__ldg(reinterpret_cast<const uint4*>(w)), g);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * g[i];
+// A lane's cosines and sines: interleaved, pairs 4l .. 4l+3 of its chunk l; half-split, pairs
+// 8 (l % 4) .. + 7.
+struct Turn {
+  float c[8], s[8];
+};
+
+__device__ __forceinline__ void load_turn(Turn& t, const float* cs, int l, bool interleaved) {
+  const float4* cp = reinterpret_cast<const float4*>(cs) + (interleaved ? l : 2 * (l & 3));
+  const float4 c0 = __ldg(cp), s0 = __ldg(cp + 8);
+  const float4 c1 = interleaved ? c0 : __ldg(cp + 1), s1 = interleaved ? s0 : __ldg(cp + 9);
+  t.c[0] = c0.x, t.c[1] = c0.y, t.c[2] = c0.z, t.c[3] = c0.w, t.c[4] = c1.x, t.c[5] = c1.y, t.c[6] = c1.z, t.c[7] = c1.w;
+  t.s[0] = s0.x, t.s[1] = s0.y, t.s[2] = s0.z, t.s[3] = s0.w, t.s[4] = s1.x, t.s[5] = s1.y, t.s[6] = s1.z, t.s[7] = s1.w;
 }
 
-// Rotate this lane's chunk k = lane - 24 (lanes 24-31; the others take part in the shuffles).
-__device__ __forceinline__ void rotate(float (&f)[8], const float* cs, int lane, bool interleaved) {
-  const int k = lane & 7;
+__device__ __forceinline__ void rotate(float (&f)[8], const Turn& t, int l, bool interleaved) {
   if (interleaved) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(cs) + k);
-    const float4 s = __ldg(reinterpret_cast<const float4*>(cs + 32) + k);
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float a = f[2 * i], b = f[2 * i + 1];
-      f[2 * i] = a * cc[i] - b * ss[i];
-      f[2 * i + 1] = b * cc[i] + a * ss[i];
+      f[2 * i] = a * t.c[i] - b * t.s[i];
+      f[2 * i + 1] = b * t.c[i] + a * t.s[i];
     }
   } else {
-    const float4* cp = reinterpret_cast<const float4*>(cs) + 2 * (k & 3);
-    const float4* sp = reinterpret_cast<const float4*>(cs + 32) + 2 * (k & 3);
-    const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
-    const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-    const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-    const float sign = k < 4 ? -1.f : 1.f;  // first half: a cos - b sin; second: b cos + a sin
+    const float sign = l < 4 ? -1.f : 1.f;  // first half: a cos - b sin; second: b cos + a sin
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float other = __shfl_xor_sync(0xffffffffu, f[i], 4);
-      f[i] = f[i] * cc[i] + sign * (other * ss[i]);
+      f[i] = f[i] * t.c[i] + sign * (other * t.s[i]);
     }
   }
+}
+
+__device__ __forceinline__ void scale8(float (&f)[8], float inv, const uint4& w) {
+  float g[8];
+  unpack8(w, g);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * g[i];
 }
 
 // Eight values as 8-bit codes of x / scale.
@@ -117,76 +130,143 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale, bool i
   return make_uint2(w[0], w[1]);
 }
 
-__global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendParams p) {
+// kChunks: most chunks of a query lane that are not rotated, ceil((q_dim - 64) / 64).
+// kSteps: four heads a step.  kKeyLanes: lanes that share a key's row (8, or all 32).
+// The first k_warps warps of the grid take keys, the others queries.
+template <int kChunks, int kSteps, int kKeyLanes>
+__global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendParams p, int64_t k_warps, int warps_per_token) {
   // programmatic dependent launch: no input is read before the previous kernel has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int per_token = p.heads + (p.kv_in ? 1 : 0);
+  const int lane = threadIdx.x & 31, sub = lane >> 3, l = lane & 7;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (unit >= static_cast<int64_t>(p.tokens) * per_token) return;
-  const int n = static_cast<int>(unit / per_token);
-  const int h = static_cast<int>(unit % per_token);  // == heads: the token's key
-  const int pos = __ldg(p.positions + n);
-  const bool is_key = h == p.heads;
-  int64_t slot = 0;
-  if (is_key) {
-    slot = __ldg(p.slots + n);
-    if (slot < 0) return;  // a padded token has no place in the cache
-  }
-  if (static_cast<unsigned>(pos) >= static_cast<unsigned>(p.max_positions) || (is_key && slot >= p.num_slots)) {
-    if (lane == 0) atomicOr(p.status, kStatusDeviceArg);
+  const bool inter = p.interleaved != 0;
+  if (unit >= k_warps) {
+    // ------------------------------------------------------------------ queries of one token
+    if (unit - k_warps >= static_cast<int64_t>(p.tokens) * warps_per_token) return;
+    const int n = static_cast<int>((unit - k_warps) / warps_per_token);
+    const int h0 = static_cast<int>((unit - k_warps) % warps_per_token) * 4 * kSteps + sub;
+    const int pos = __ldg(p.positions + n);
+    if (static_cast<unsigned>(pos) >= static_cast<unsigned>(p.max_positions)) {
+      if (lane == 0) atomicOr(p.status, kStatusDeviceArg);
+      return;
+    }
+    const int chunks = (p.q_dim - kRope) / 8;
+    const __nv_bfloat16* src = p.q_in + static_cast<int64_t>(n) * p.q_in_token;
+    __nv_bfloat16* dst = p.q_out + static_cast<int64_t>(n) * p.q_out_token;
+    // (wide rows go one step at a time: their chunks fill the registers)
+    constexpr int kTogether = kChunks <= 2 ? kSteps : 1;
+    Turn turn;
+    uint4 wt[kChunks + 1];
+#pragma unroll 1
+    for (int s0 = 0; s0 < kSteps; s0 += kTogether) {
+      uint4 w[kTogether][kChunks + 1];
+#pragma unroll
+      for (int s = 0; s < kTogether; ++s) {
+        const int h = h0 + 4 * (s0 + s);
+        const uint4* row = reinterpret_cast<const uint4*>(src + static_cast<int64_t>(h) * p.q_in_head);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+          w[s][i] = h < p.heads && l + 8 * i < chunks ? row[l + 8 * i] : make_uint4(0u, 0u, 0u, 0u);
+        w[s][kChunks] = h < p.heads ? row[chunks + l] : make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (s0 == 0) {
+        load_turn(turn, p.cos_sin + static_cast<int64_t>(pos) * kRope, l, inter);
+        if (p.q_weight) {
+          const uint4* g = reinterpret_cast<const uint4*>(p.q_weight);
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) wt[i] = l + 8 * i < chunks ? __ldg(g + l + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+          wt[kChunks] = __ldg(g + chunks + l);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < kTogether; ++s) {
+        const int h = h0 + 4 * (s0 + s);
+        float f[kChunks + 1][8];
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i <= kChunks; ++i) {
+          unpack8(w[s][i], f[i]);
+          ss += sum_sq(f[i]);
+        }
+        if (p.q_weight) {
+          const float inv = 1.f / sqrtf(row_sum<8>(ss) / static_cast<float>(p.q_dim) + p.eps);
+#pragma unroll
+          for (int i = 0; i <= kChunks; ++i) scale8(f[i], inv, wt[i]);
+        }
+        rotate(f[kChunks], turn, l, inter);
+        if (h < p.heads) {
+          uint4* out = reinterpret_cast<uint4*>(dst + static_cast<int64_t>(h) * p.q_out_head);
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i)
+            if (l + 8 * i < chunks) out[l + 8 * i] = pack8(f[i]);
+          out[chunks + l] = pack8(f[kChunks]);
+        }
+      }
+    }
     return;
   }
-  const float* cs = p.cos_sin + static_cast<int64_t>(pos) * kRope;
-  const __nv_bfloat16* src = is_key ? p.kv_in + static_cast<int64_t>(n) * p.kv_in_token
-                                    : p.q_in + static_cast<int64_t>(n) * p.q_in_token + static_cast<int64_t>(h) * p.q_in_head;
-  const int plain = (is_key ? kLatentDim : p.q_dim) - kRope;  // columns that are not rotated
-  const __nv_bfloat16* weight = is_key ? p.kv_weight : p.q_weight;
-  const int chunks = plain / 8;                               // at most 64: two per lane
-  const bool has0 = lane < chunks, has1 = lane + 32 < chunks, has_r = lane >= kRopeLane;
-  float f0[8] = {}, f1[8] = {}, fr[8] = {};
-  {
-    const uint4* s4 = reinterpret_cast<const uint4*>(src);
-    uint4 w0 = {}, w1 = {}, wr = {};
-    if (has0) w0 = s4[lane];
-    if (has1) w1 = s4[lane + 32];
-    if (has_r) wr = s4[chunks + lane - kRopeLane];
-    unpack8(w0, f0);
-    unpack8(w1, f1);
-    unpack8(wr, fr);
+  // -------------------------------------------------------------------- keys, kKeyLanes a row
+  constexpr int kLatentChunks = kValueDim / 8 / kKeyLanes;  // per lane; lanes 0-7 also rotate one
+  const int kl = lane % kKeyLanes;
+  const int64_t n = unit * (32 / kKeyLanes) + lane / kKeyLanes;
+  int64_t slot = -1;
+  int pos = 0;
+  if (n < p.tokens) {
+    slot = __ldg(p.slots + n);  // (a padded token has no place in the cache)
+    pos = __ldg(p.positions + n);
+    if (slot >= 0 && (slot >= p.num_slots || static_cast<unsigned>(pos) >= static_cast<unsigned>(p.max_positions))) {
+      if (kl == 0) atomicOr(p.status, kStatusDeviceArg);
+      slot = -1;
+    }
   }
-  if (weight) {
-    // a key's norm covers its 512 latent columns, a query's its whole width
-    const float ss = warp_sum(sum_sq(f0) + sum_sq(f1) + (is_key ? 0.f : sum_sq(fr)));
-    const int width = is_key ? kValueDim : p.q_dim;
-    const float inv = 1.f / sqrtf(ss / static_cast<float>(width) + p.eps);
-    if (has0) scale8(f0, inv, weight + lane * 8);
-    if (has1) scale8(f1, inv, weight + (lane + 32) * 8);
-    if (has_r && !is_key) scale8(fr, inv, weight + plain + (lane - kRopeLane) * 8);
+  const bool live = slot >= 0;  // (the others still take part in the shuffles)
+  uint4 w[kLatentChunks + 1];
+  const uint4* row = reinterpret_cast<const uint4*>(p.kv_in + n * p.kv_in_token);
+#pragma unroll
+  for (int i = 0; i < kLatentChunks; ++i) w[i] = live ? row[kl + kKeyLanes * i] : make_uint4(0u, 0u, 0u, 0u);
+  w[kLatentChunks] = live && kl < 8 ? row[kValueDim / 8 + kl] : make_uint4(0u, 0u, 0u, 0u);
+  Turn turn;
+  load_turn(turn, p.cos_sin + (live ? static_cast<int64_t>(pos) * kRope : 0), l, inter);
+  float inv = 1.f;
+  if (p.kv_weight) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kLatentChunks; ++i) {
+      float f[8];
+      unpack8(w[i], f);
+      ss += sum_sq(f);
+    }
+    inv = 1.f / sqrtf(row_sum<kKeyLanes>(ss) / static_cast<float>(kValueDim) + p.eps);
   }
-  rotate(fr, cs, lane, p.interleaved != 0);
-  if (!is_key || p.kv_dtype == kKvBf16) {
-    uint4* dst = reinterpret_cast<uint4*>(
-        is_key ? reinterpret_cast<__nv_bfloat16*>(p.kv_pages) + slot * kLatentDim
-               : p.q_out + static_cast<int64_t>(n) * p.q_out_token + static_cast<int64_t>(h) * p.q_out_head);
-    if (has0) dst[lane] = pack8(f0);
-    if (has1) dst[lane + 32] = pack8(f1);
-    if (has_r) dst[chunks + lane - kRopeLane] = pack8(fr);
-  } else {
-    const bool int8 = p.kv_dtype == kKvInt8;
-    uint2* dst = reinterpret_cast<uint2*>(p.kv_pages + slot * kLatentDim);
-    if (has0) dst[lane] = codes8(f0, p.kv_scale, int8);
-    if (has1) dst[lane + 32] = codes8(f1, p.kv_scale, int8);
-    if (has_r) dst[chunks + lane - kRopeLane] = codes8(fr, p.kv_scale, int8);
+#pragma unroll
+  for (int i = 0; i <= kLatentChunks; ++i) {
+    const int c = i < kLatentChunks ? kl + kKeyLanes * i : kValueDim / 8 + kl;
+    float f[8];
+    unpack8(w[i], f);
+    if (i == kLatentChunks)
+      rotate(f, turn, l, inter);
+    else if (p.kv_weight)
+      scale8(f, inv, __ldg(reinterpret_cast<const uint4*>(p.kv_weight) + c));
+    if (!live || (i == kLatentChunks && kl >= 8)) continue;
+    const int64_t at = slot * (kLatentDim / 8) + c;
+    if (p.kv_dtype == kKvBf16)
+      reinterpret_cast<uint4*>(p.kv_pages)[at] = pack8(f);
+    else
+      reinterpret_cast<uint2*>(p.kv_pages)[at] = codes8(f, p.kv_scale, p.kv_dtype == kKvInt8);
   }
 }
 
-}  // namespace
-
-cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(p.tokens) * (p.heads + (p.kv_in ? 1 : 0));
+template <int kChunks>
+cudaError_t launch_chunks(const AppendParams& p, cudaStream_t stream) {
+  // Few rows: one step and a warp per key, for the shortest chain; many: more bytes in flight
+  // per warp.
+  const bool few = static_cast<int64_t>(p.tokens) * (p.heads > 0 ? p.heads : 16) <= kFewRows;
+  const int steps = few ? 1 : kManySteps, key_rows = few ? 1 : 4;
+  const int per_token = (p.heads + 4 * steps - 1) / (4 * steps);
+  const int64_t k_warps = p.kv_in ? (p.tokens + key_rows - 1) / key_rows : 0;
+  const int64_t warps = k_warps + static_cast<int64_t>(p.tokens) * per_token;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((units + kWarps - 1) / kWarps));
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps));
   cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -194,7 +274,17 @@ cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_append_kernel, p);
+  return few ? cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, 1, 32>, p, k_warps, per_token)
+             : cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, kManySteps, 8>, p, k_warps, per_token);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream) {
+  const int chunks = p.q_in ? (p.q_dim - kRope + 63) / 64 : 0;
+  if (chunks == 0) return launch_chunks<0>(p, stream);
+  if (chunks <= 2) return launch_chunks<2>(p, stream);
+  return launch_chunks<8>(p, stream);
 }
 
 }  // namespace mla

@@ -15,12 +15,13 @@
 // passes of 11, 11 and 10 bits, counted in shared memory), then one pass that emits the kept
 // indices in order.  Bound by latency (a few hundred KB per request): a request of many keys
 // is spread over a cluster of CTAs, each keeping the images of its share in shared memory;
-// they read each other's counts there, one cluster barrier a pass.
+// one warp of each reads the cluster's counts through distributed shared memory in two steps
+// (64 sums of 32 bins, then the bins of one), one cluster barrier a pass.  The loops are left
+// rolled: the kernel runs once through its code, and fully unrolled it waited 2,300 cycles
+// a pass for instructions, whatever the number of keys.
 // Copy: bound by memory.  A warp copies a few consecutive rows with all their loads in
 // flight before the first store.
 #include <cooperative_groups.h>
-
-#include <algorithm>
 
 #include "mla_internal.h"
 #include "sm103a_ptx.cuh"
@@ -34,6 +35,8 @@ constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kCluster = 8;            // CTAs per request
+constexpr int kCoarse = kBins / 32;    // sums of 32 bins
+constexpr int kRound = 128;            // keys of a warp's round: four consecutive ones a lane
 constexpr int kMaxCached = 48 * 1024;  // images a CTA keeps in shared memory; longer shares are read again
 constexpr int kOneCtaKeys = 8192;      // up to this length a request has one CTA
 constexpr int kCopyWarps = 8;
@@ -55,23 +58,47 @@ __device__ __forceinline__ int keep_count(const EvictParams& p, int b, int& L) {
   return K;
 }
 
-// Keys of a CTA's share: whole rounds of 32 lanes for each of the 32 warps.
+// Keys of a CTA's share: whole rounds for each of its warps.
 __host__ __device__ inline int share_of(int span, int ctas) {
-  const int per_warp = (span + ctas * kSelectThreads - 1) / (ctas * kSelectThreads) * 32;
-  return per_warp * kSelectWarps;
+  const int step = ctas * kSelectWarps * kRound;
+  return (span + step - 1) / step * kSelectWarps * kRound;
 }
 
+// Sum over the warps before `warp` of one value per warp (in shared memory), and over all.
+__device__ __forceinline__ int warps_before(const int* v, int warp, int lane, int& total) {
+  const int own = v[lane];
+  total = __reduce_add_sync(0xffffffffu, own);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? own : 0);
+}
+
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ int scan32(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
+
+// kCtas: CTAs per request (the cluster).
+template <int kCtas>
 __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const EvictParams p) {
-  extern __shared__ uint32_t images[];  // p.cached of them
-  __shared__ int hist[3][kBins];
-  __shared__ int warp_sum[kSelectWarps];
+  extern __shared__ __align__(16) uint32_t images[];  // p.cached of them
+  __shared__ __align__(16) int hist[3][kBins];
+  __shared__ __align__(16) int coarse[3][kCoarse];
   __shared__ int s_digit, s_need;
-  __shared__ int2 warp_count[kSelectWarps];
+  __shared__ int warp_gt[kSelectWarps], warp_eq[kSelectWarps];
   __shared__ int2 cta_count;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   cg::cluster_group cluster = cg::this_cluster();
-  const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-  const int b = blockIdx.x / ctas;
+  const int rank = kCtas == 1 ? 0 : static_cast<int>(cluster.block_rank());
+  auto of = [&](int* x, int r) -> const int* { return kCtas == 1 ? x : cluster.map_shared_rank(x, r); };
+  auto meet = [&]() {
+    if (kCtas == 1) __syncthreads();
+    else cluster.sync();
+  };
+  const int b = blockIdx.x / kCtas;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int L;
   const int K = keep_count(p, b, L);
@@ -85,101 +112,141 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const EvictPa
   const int m = K - lo - tail;  // to choose from [lo, hi)
   int32_t* kept = p.kept + static_cast<int64_t>(b) * p.kept_stride;
   if (tid == 0 && rank == 0) p.new_lens[b] = K;
-  for (int i = rank * kSelectThreads + tid; i < lo; i += ctas * kSelectThreads) kept[i] = i;
-  for (int i = rank * kSelectThreads + tid; i < tail; i += ctas * kSelectThreads) kept[K - tail + i] = hi + i;
+  for (int i = rank * kSelectThreads + tid; i < lo; i += kCtas * kSelectThreads) kept[i] = i;
+  for (int i = rank * kSelectThreads + tid; i < tail; i += kCtas * kSelectThreads) kept[K - tail + i] = hi + i;
   if (m == 0) return;
-  const int share = share_of(hi - lo, ctas);
+  const int share = share_of(hi - lo, kCtas);
   const int first = lo + static_cast<int>(min(static_cast<int64_t>(rank) * share, static_cast<int64_t>(hi - lo)));
   const int n = min(share, hi - first);
   const float* mass = p.mass + static_cast<int64_t>(b) * p.mass_stride + first;
   const bool cached = share <= p.cached;
-  auto image = [&](int i) -> uint32_t { return cached ? images[i] : mass_key(mass[i]); };
+  const int rounds = share / (kSelectWarps * kRound);
+  const int at0 = warp * rounds * kRound + 4 * lane;  // this lane's four keys of its warp's first round
+  const int todo = min(rounds, max(0, (n - warp * rounds * kRound + kRound - 1) / kRound));  // rounds that hold keys
+  auto fetch = [&](int i) -> uint4 {
+    return make_uint4(i < n ? mass_key(mass[i]) : 0u, i + 1 < n ? mass_key(mass[i + 1]) : 0u,
+                      i + 2 < n ? mass_key(mass[i + 2]) : 0u, i + 3 < n ? mass_key(mass[i + 3]) : 0u);
+  };
+  auto image4 = [&](int i) -> uint4 { return cached ? *reinterpret_cast<const uint4*>(images + i) : fetch(i); };
 
-  // threshold: the m-th largest image; `need` of the images equal to it are kept
   for (int i = tid; i < 3 * kBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
+  if (cached) {
+#pragma unroll 4
+    for (int r = 0; r < todo; ++r) *reinterpret_cast<uint4*>(images + at0 + r * kRound) = fetch(at0 + r * kRound);
+  }
   __syncthreads();
+  // threshold: the m-th largest image; `need` of the images equal to it are kept
   uint32_t prefix = 0;
   int need = m;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    if (pass == 0) {
-#pragma unroll 8
-      for (int i = tid; i < n; i += kSelectThreads) {
-        const uint32_t k = mass_key(mass[i]);
-        if (cached) images[i] = k;
-        atomicAdd(&hist[0][k >> 21], 1);
-      }
-    } else {
-      const int known = pass == 1 ? 21 : 10;  // the bits above are the prefix
-      const uint32_t mask = pass == 1 ? kBins - 1 : 1023;
-      for (int i = tid; i < n; i += kSelectThreads) {
-        const uint32_t k = image(i);
-        if (((k ^ prefix) >> known) == 0) atomicAdd(&hist[pass][(k >> shift) & mask], 1);
-      }
-    }
-    cluster.sync();
-    // every CTA sums the cluster's counts and scans them from the largest digit down
-    int c[2] = {0, 0};
-    const int bin = kBins - 1 - 2 * tid;  // this thread: bins bin and bin - 1
-    for (int r = 0; r < ctas; ++r) {
-      const int* h = cluster.map_shared_rank(&hist[pass][0], r);
-      c[0] += h[bin];
-      c[1] += h[bin - 1];
-    }
-    int incl = c[0] + c[1];
+    const uint32_t digit_mask = pass == 2 ? 1023 : kBins - 1;
+    const uint32_t known = pass == 0 ? 0u : 0xffffffffu << (pass == 1 ? 21 : 10);  // the bits of the prefix
+    int* h = hist[pass];
+#pragma unroll 1
+    for (int r = 0; r < todo; ++r) {
+      const int i = at0 + r * kRound;
+      const uint4 k4 = image4(i);
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      for (int e = 0; e < 4; ++e)
+        if (i + e < n && ((k[e] ^ prefix) & known) == 0) atomicAdd(&h[(k[e] >> shift) & digit_mask], 1);
     }
-    if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int before = incl - c[0] - c[1];
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    if (before < need && need <= before + c[0] + c[1]) {  // (one thread)
-      const bool up = need <= before + c[0];
-      s_digit = up ? bin : bin - 1;
-      s_need = up ? need - before : need - before - c[0];
+    {
+      const int2 two = *reinterpret_cast<const int2*>(h + 2 * tid);
+      int s = two.x + two.y;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if ((lane & 15) == 0) coarse[pass][tid / 16] = s;
+    }
+    meet();
+    if (warp == 0) {
+      // from the largest digit down: the sum, then the bin, in which the m-th key falls
+      const int c0 = kCoarse - 1 - 2 * lane;  // this lane's sums: c0 and c0 - 1
+      int up = 0, down = 0;
+#pragma unroll
+      for (int r = 0; r < kCtas; ++r) {
+        const int2 v = *reinterpret_cast<const int2*>(of(coarse[pass], r) + c0 - 1);
+        up += v.y;
+        down += v.x;
+      }
+      int before = scan32(up + down, lane) - up - down;
+      bool mine = before < need && need <= before + up + down;
+      int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+      const bool first_of_two = need <= before + up;
+      const int c = __shfl_sync(0xffffffffu, first_of_two ? c0 : c0 - 1, src);
+      const int above = __shfl_sync(0xffffffffu, first_of_two ? before : before + up, src);
+      const int bin = 32 * c + 31 - lane;
+      int count = 0;
+#pragma unroll
+      for (int r = 0; r < kCtas; ++r) count += of(h, r)[bin];
+      before = above + scan32(count, lane) - count;
+      if (before < need && need <= before + count) {  // (one lane)
+        s_digit = bin;
+        s_need = need - before;
+      }
     }
     __syncthreads();
     prefix |= static_cast<uint32_t>(s_digit) << shift;
     need = s_need;
   }
   // emission in order: heavier and equal keys before this warp, then round by round
-  const int per_warp = share / kSelectWarps, w0 = warp * per_warp;
   int gt = 0, eq = 0;
-  for (int i = w0 + lane; i < w0 + per_warp; i += 32) {
-    const uint32_t k = i < n ? image(i) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, i < n && k > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, i < n && k == prefix));
+#pragma unroll 1
+  for (int r = 0; r < todo; ++r) {
+    const int i = at0 + r * kRound;
+    const uint4 k4 = image4(i);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      gt += i + e < n && k[e] > prefix;
+      eq += i + e < n && k[e] == prefix;
+    }
   }
-  if (lane == 0) warp_count[warp] = make_int2(gt, eq);
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) {
+    warp_gt[warp] = gt;
+    warp_eq[warp] = eq;
+  }
   __syncthreads();
-  int2 at = make_int2(0, 0), all = make_int2(0, 0);
-  for (int w = 0; w < kSelectWarps; ++w) {
-    if (w == warp) at = all;
-    all.x += warp_count[w].x;
-    all.y += warp_count[w].y;
+  int all_gt, all_eq;
+  gt = warps_before(warp_gt, warp, lane, all_gt);
+  eq = warps_before(warp_eq, warp, lane, all_eq);
+  if (kCtas > 1) {
+    if (tid == 0) cta_count = make_int2(all_gt, all_eq);
+    cluster.sync();
+    const int2 v = lane < rank ? *cluster.map_shared_rank(&cta_count, lane) : make_int2(0, 0);
+    gt += __reduce_add_sync(0xffffffffu, v.x);
+    eq += __reduce_add_sync(0xffffffffu, v.y);
   }
-  if (tid == 0) cta_count = all;
-  cluster.sync();
-  for (int r = 0; r < rank; ++r) {
-    const int2 v = *cluster.map_shared_rank(&cta_count, r);
-    at.x += v.x;
-    at.y += v.y;
+#pragma unroll 1
+  for (int r = 0; r < todo; ++r) {
+    const int i = at0 + r * kRound;
+    const uint4 k4 = image4(i);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    int own = 0;  // heavier, and equal << 16, of this lane
+#pragma unroll
+    for (int e = 0; e < 4; ++e) own += i + e < n ? (k[e] > prefix ? 1 : k[e] == prefix ? 1 << 16 : 0) : 0;
+    const int incl = scan32(own, lane), all = __shfl_sync(0xffffffffu, incl, 31);
+    int g = gt + ((incl - own) & 0xffff), q = eq + ((incl - own) >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (i + e >= n) continue;
+      if (k[e] > prefix) {
+        kept[lo + g + min(q, need)] = first + i + e;
+        ++g;
+      } else if (k[e] == prefix) {
+        if (q < need) kept[lo + g + q] = first + i + e;
+        ++q;
+      }
+    }
+    gt += all & 0xffff;
+    eq += all >> 16;
   }
-  for (int i = w0 + lane; i < w0 + per_warp; i += 32) {
-    const uint32_t k = i < n ? image(i) : 0u;
-    const bool g = i < n && k > prefix, e = i < n && k == prefix;
-    const unsigned bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
-    const unsigned below = (1u << lane) - 1u;
-    const int gr = at.x + __popc(bg & below), er = at.y + __popc(be & below);
-    if (g || (e && er < need)) kept[lo + gr + min(er, need)] = first + i;
-    at.x += __popc(bg);
-    at.y += __popc(be);
-  }
-  cluster.sync();  // no CTA leaves while another may read its counts
+  if (kCtas > 1) cluster.sync();  // no CTA leaves while another may read its counts
 }
 
 // kChunks: 16-byte pieces of a row (72 of bf16, 36 of 8-bit codes).
@@ -251,15 +318,20 @@ cudaError_t launch_kv_evict(const EvictParams& params, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(kv_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4);
+    e = cudaFuncSetAttribute(kv_select_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kv_select_kernel<kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
   EvictParams p = params;
   // one CTA walks a short request faster than a cluster meets
   const int ctas = p.max_seq <= kOneCtaKeys ? 1 : kCluster;
-  p.cached = std::min(share_of(std::max(p.max_seq, 1), ctas), kMaxCached);
-  e = launch_dependent(kv_select_kernel, dim3(p.B * ctas), kSelectThreads, p.cached * 4, ctas, p, stream);
+  const int share = share_of(p.max_seq > 0 ? p.max_seq : 1, ctas);
+  p.cached = share < kMaxCached ? share : kMaxCached;
+  e = ctas == 1 ? launch_dependent(kv_select_kernel<1>, dim3(p.B), kSelectThreads, p.cached * 4, 1, p, stream)
+                : launch_dependent(kv_select_kernel<kCluster>, dim3(p.B * kCluster), kSelectThreads, p.cached * 4, kCluster,
+                                   p, stream);
   if (e != cudaSuccess || p.max_keep == 0) return e;
   const int rows = (p.row_bytes == 2 * kLatentDim ? 4 : 8) * kCopyWarps;
   const dim3 grid((p.max_keep + rows - 1) / rows, p.B);

@@ -132,33 +132,50 @@ def _refuse(what: str, why: str):
     raise MlaError(MLA_ERR_INVALID_ARG, f"{what} ({why})")
 
 
-def _want(what, device, tensors):
-    """Argument checks of one call: (name, tensor, dtypes, shape or None) each on `device`, contiguous."""
-    for name, t, dtypes, shape in tensors:
-        if t.device != device or device.type != "cuda":
-            _refuse(what, f"{name} is on {t.device}")
-        if t.dtype not in dtypes:
-            _refuse(what, f"{name} is {t.dtype}")
-        if shape is not None and tuple(t.shape) != shape:
-            _refuse(what, f"{name} has shape {tuple(t.shape)}, not {shape}")
-        if not t.is_contiguous():
-            _refuse(what, f"{name} is not contiguous")
+def _want(what, dev, name, t, dtype, shape=None):
+    """One tensor argument: on CUDA device number `dev`, contiguous, of `dtype` and (unless None) `shape`."""
+    if t.get_device() != dev or dev < 0:
+        _refuse(what, f"{name} is on {t.device}")
+    if t.dtype is not dtype:
+        _refuse(what, f"{name} is {t.dtype}")
+    if shape is not None and t.shape != shape:
+        _refuse(what, f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if not t.is_contiguous():
+        _refuse(what, f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+def _want_rows(what, dev, name, t, dtype, rows):
+    """A contiguous [rows, any] tensor: its address and row length."""
+    if t.dim() != 2 or t.shape[0] != rows:
+        _refuse(what, f"{name} has shape {tuple(t.shape)}")
+    return _want(what, dev, name, t, dtype), t.shape[1]
 
 
 def _want_pool(what, kv_pages, kv_dtype):
-    if kv_dtype not in _POOL_DTYPE:
-        _refuse(what, f"kv_dtype {kv_dtype}")
+    """The latent pool: its device number and address."""
+    dev = kv_pages.get_device()
     if kv_pages.dim() != 3 or kv_pages.shape[2] != 576:
         _refuse(what, f"kv_pages has shape {tuple(kv_pages.shape)}")
-    _want(what, kv_pages.device, [("kv_pages", kv_pages, _POOL_DTYPE[kv_dtype], None)])
+    if kv_pages.dtype not in _POOL_DTYPE.get(kv_dtype, ()):
+        _refuse(what, f"kv_pages is {kv_pages.dtype} for kv_dtype {kv_dtype}")
+    return dev, _want(what, dev, "kv_pages", kv_pages, kv_pages.dtype)
 
 
-def _call(what, device, stream, fn, *args):
-    """fn(*args, stream) on the tensors' own device: its current stream unless one is given."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call(what, device, stream, fn, *args)
-    _check(fn(*args, _stream_handle(stream)), what)
+def _want_workspace(what, dev, workspace):
+    if workspace is None:
+        return None, 0
+    return _want(what, dev, "workspace", workspace, workspace.dtype), workspace.numel() * workspace.element_size()
+
+
+def _call(what, dev, stream, fn, *args):
+    """fn(*args, stream) on CUDA device number `dev`: its current stream unless one is given."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(what, dev, stream, fn, *args)
+    rc = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    if rc != MLA_OK:
+        raise MlaError(rc, what)
 
 
 def decode_plan(seq_lens_host, q_len: int, num_heads: int, page_size: int, max_pages_per_seq: int,
@@ -320,30 +337,24 @@ def decode_tree(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_
     """mla_decode_tree through the C ABI: decode of a tree of drafts.  tree_mask [B,T] int64 (its 64
     bits): bit u of [b, t] = draft t sees draft u.  Returns (out [B,T,H,512] bf16, lse [B,T,H] fp32)."""
     what = "mla_decode_tree"
-    _want_pool(what, kv_pages, plan.kv_dtype)
-    dev = kv_pages.device
+    dev, pool = _want_pool(what, kv_pages, plan.kv_dtype)
     B, T, H = plan.batch, plan.q_len, plan.num_heads
-    if out is None:
-        out = torch.empty(B, T, H, 512, dtype=torch.bfloat16, device=dev)
-    if lse is None:
-        lse = torch.empty(B, T, H, dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = workspace_for(plan, dev)
-    i32 = (torch.int32,)
-    _want(what, dev, [("q", q, (torch.bfloat16,), (B, T, H, 576)), ("page_table", page_table, i32, (B, plan.max_pages_per_seq)),
-                      ("seq_lens", seq_lens, i32, (B,)), ("tree_mask", tree_mask, (torch.int64,), (B, T)),
-                      ("out", out, (torch.bfloat16,), (B, T, H, 512)), ("lse", lse, (torch.float32,), (B, T, H))])
     if kv_pages.shape[0] != plan.num_pages or kv_pages.shape[1] != plan.page_size:
         _refuse(what, f"kv_pages has shape {tuple(kv_pages.shape)}, not the plan's")
-    if page_scales is not None:
-        _want(what, dev, [("page_scales", page_scales, (torch.float32,), (plan.num_pages,))])
-    ws_bytes = 0
-    if workspace is not None:
-        _want(what, dev, [("workspace", workspace, (workspace.dtype,), None)])
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _call(what, dev, stream, lib.mla_decode_tree, ctypes.byref(plan), _ptr(q), _ptr(kv_pages), _ptr(page_scales),
-          _ptr(page_table), _ptr(seq_lens), _ptr(tree_mask), T, H, float(scale), float(kv_scale), _ptr(out), _ptr(lse),
-          _ptr(workspace), ws_bytes)
+    if out is None:
+        out = torch.empty(B, T, H, 512, dtype=torch.bfloat16, device=kv_pages.device)
+    if lse is None:
+        lse = torch.empty(B, T, H, dtype=torch.float32, device=kv_pages.device)
+    if workspace is None:
+        workspace = workspace_for(plan, kv_pages.device)
+    ws, ws_bytes = _want_workspace(what, dev, workspace)
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    _call(what, dev, stream, lib.mla_decode_tree, plan, _want(what, dev, "q", q, bf16, (B, T, H, 576)), pool,
+          None if page_scales is None else _want(what, dev, "page_scales", page_scales, f32, (plan.num_pages,)),
+          _want(what, dev, "page_table", page_table, i32, (B, plan.max_pages_per_seq)),
+          _want(what, dev, "seq_lens", seq_lens, i32, (B,)),
+          _want(what, dev, "tree_mask", tree_mask, torch.int64, (B, T)), T, H, scale, kv_scale,
+          _want(what, dev, "out", out, bf16, (B, T, H, 512)), _want(what, dev, "lse", lse, f32, (B, T, H)), ws, ws_bytes)
     return out, lse
 
 
@@ -358,39 +369,35 @@ def kv_append(q: torch.Tensor | None, kv: torch.Tensor | None, positions: torch.
     some = q if q is not None else kv
     if some is None:
         _refuse(what, "neither q nor kv")
-    dev = some.device
-    n = int(some.shape[0])
+    dev, n = some.get_device(), some.shape[0]
+    bf16 = torch.bfloat16
     if cos_sin.dim() != 2 or cos_sin.shape[1] != 64:
         _refuse(what, f"cos_sin has shape {tuple(cos_sin.shape)}")
-    _want(what, dev, [("positions", positions, (torch.int32,), (n,)), ("cos_sin", cos_sin, (torch.float32,), None)])
-    bf16 = torch.bfloat16
+    table, pos = _want(what, dev, "cos_sin", cos_sin, torch.float32), _want(what, dev, "positions", positions, torch.int32, (n,))
     qa = (None, 0, 0, None, 0, 0, 0, 0, None)
     if q is not None:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=bf16, device=dev)
+            q_out = torch.empty(q.shape, dtype=bf16, device=q.device)
         for name, t in (("q", q), ("q_out", q_out)):
-            if t.device != dev or dev.type != "cuda" or t.dtype != bf16 or t.dim() != 3 or t.shape != q.shape:
+            if t.get_device() != dev or dev < 0 or t.dtype is not bf16 or t.dim() != 3 or t.shape != q.shape:
                 _refuse(what, f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}")
-            if t.shape[2] > 1 and t.stride(2) != 1:
+            if t.stride(2) != 1:
                 _refuse(what, f"the last dimension of {name} is not dense")
-        H, D = int(q.shape[1]), int(q.shape[2])
-        if q_weight is not None:
-            _want(what, dev, [("q_weight", q_weight, (bf16,), (D,))])
-        qa = (_ptr(q), q.stride(0), q.stride(1), _ptr(q_out), q_out.stride(0), q_out.stride(1), H, D, _ptr(q_weight))
-    ka, pool, rows = (None, 0, None), None, 0
+        H, D = q.shape[1], q.shape[2]
+        qa = (q.data_ptr(), q.stride(0), q.stride(1), q_out.data_ptr(), q_out.stride(0), q_out.stride(1), H, D,
+              None if q_weight is None else _want(what, dev, "q_weight", q_weight, bf16, (D,)))
+    ka, pool, rows, slot = (None, 0, None), None, 0, None
     if kv is not None:
         if kv_pages is None or slots is None:
             _refuse(what, "kv without kv_pages and slots")
-        _want_pool(what, kv_pages, kv_dtype)
-        if kv.device != dev or kv_pages.device != dev or kv.dtype != bf16 or tuple(kv.shape) != (n, 576) or kv.stride(1) != 1:
+        pool_dev, pool = _want_pool(what, kv_pages, kv_dtype)
+        if kv.get_device() != dev or pool_dev != dev or kv.dtype is not bf16 or kv.shape != (n, 576) or kv.stride(1) != 1:
             _refuse(what, f"kv is {kv.dtype} {tuple(kv.shape)} on {kv.device}")
-        _want(what, dev, [("slots", slots, (torch.int64,), (n,))])
-        if kv_weight is not None:
-            _want(what, dev, [("kv_weight", kv_weight, (bf16,), (512,))])
-        ka = (_ptr(kv), kv.stride(0), _ptr(kv_weight))
-        pool, rows = _ptr(kv_pages), kv_pages.shape[0] * kv_pages.shape[1]
-    _call(what, dev, stream, lib.mla_kv_append, *qa, *ka, float(eps), _ptr(cos_sin), int(cos_sin.shape[0]), _ptr(positions),
-          _ptr(slots) if kv is not None else None, n, int(bool(interleaved)), pool, int(rows), int(kv_dtype), float(kv_scale))
+        slot = _want(what, dev, "slots", slots, torch.int64, (n,))
+        ka = (kv.data_ptr(), kv.stride(0), None if kv_weight is None else _want(what, dev, "kv_weight", kv_weight, bf16, (512,)))
+        rows = kv_pages.shape[0] * kv_pages.shape[1]
+    _call(what, dev, stream, lib.mla_kv_append, *qa, *ka, eps, table, cos_sin.shape[0], pos, slot, n, 1 if interleaved else 0,
+          pool, rows, kv_dtype, kv_scale)
     return q_out
 
 
@@ -407,29 +414,21 @@ def key_mass(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_tab
     """mla_key_mass through the C ABI: mass [B, >= max_seq_len] fp32 becomes decay * mass + the
     attention weight each key received in the step whose lse [B,T,H] this is.  Returns mass."""
     what = "mla_key_mass"
-    _want_pool(what, kv_pages, plan.kv_dtype)
-    dev = kv_pages.device
+    dev, pool = _want_pool(what, kv_pages, plan.kv_dtype)
     B, T, H = plan.batch, plan.q_len, plan.num_heads
-    if workspace is None:
-        workspace = key_mass_workspace_for(plan, dev)
-    i32, f32 = (torch.int32,), (torch.float32,)
-    _want(what, dev, [("q", q, (torch.bfloat16,), (B, T, H, 576)), ("page_table", page_table, i32, (B, plan.max_pages_per_seq)),
-                      ("seq_lens", seq_lens, i32, (B,)), ("lse", lse, f32, (B, T, H)), ("mass", mass, f32, None)])
-    if mass.dim() != 2 or mass.shape[0] != B:
-        _refuse(what, f"mass has shape {tuple(mass.shape)}")
     if kv_pages.shape[0] != plan.num_pages or kv_pages.shape[1] != plan.page_size:
         _refuse(what, f"kv_pages has shape {tuple(kv_pages.shape)}, not the plan's")
-    if tree_mask is not None:
-        _want(what, dev, [("tree_mask", tree_mask, (torch.int64,), (B, T))])
-    if page_scales is not None:
-        _want(what, dev, [("page_scales", page_scales, f32, (plan.num_pages,))])
-    ws_bytes = 0
-    if workspace is not None:
-        _want(what, dev, [("workspace", workspace, (workspace.dtype,), None)])
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _call(what, dev, stream, lib.mla_key_mass, ctypes.byref(plan), _ptr(q), _ptr(kv_pages), _ptr(page_scales), _ptr(page_table),
-          _ptr(seq_lens), _ptr(tree_mask), _ptr(lse), T, H, float(scale), float(kv_scale), float(decay), _ptr(mass),
-          int(mass.shape[1]), _ptr(workspace), ws_bytes)
+    if workspace is None:
+        workspace = key_mass_workspace_for(plan, kv_pages.device)
+    ws, ws_bytes = _want_workspace(what, dev, workspace)
+    i32, f32 = torch.int32, torch.float32
+    mass_ptr, stride = _want_rows(what, dev, "mass", mass, f32, B)
+    _call(what, dev, stream, lib.mla_key_mass, plan, _want(what, dev, "q", q, torch.bfloat16, (B, T, H, 576)), pool,
+          None if page_scales is None else _want(what, dev, "page_scales", page_scales, f32, (plan.num_pages,)),
+          _want(what, dev, "page_table", page_table, i32, (B, plan.max_pages_per_seq)),
+          _want(what, dev, "seq_lens", seq_lens, i32, (B,)),
+          None if tree_mask is None else _want(what, dev, "tree_mask", tree_mask, torch.int64, (B, T)),
+          _want(what, dev, "lse", lse, f32, (B, T, H)), T, H, scale, kv_scale, decay, mass_ptr, stride, ws, ws_bytes)
     return mass
 
 
@@ -441,28 +440,21 @@ def kv_evict(kv_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.T
     ``dst_page_table``.  mass [B, >= max_seq_len] fp32.  Returns (kept [B,max_keep] int32, new_lens
     [B] int32, mass_out [B, >= max_keep] fp32)."""
     what = "mla_kv_evict"
-    _want_pool(what, kv_pages, kv_dtype)
-    dev = kv_pages.device
-    B = int(seq_lens.numel())
-    i32, f32 = (torch.int32,), (torch.float32,)
+    dev, pool = _want_pool(what, kv_pages, kv_dtype)
+    B = seq_lens.numel()
+    i32, f32 = torch.int32, torch.float32
     if kept is None:
-        kept = torch.zeros(B, max_keep, dtype=torch.int32, device=dev)
+        kept = torch.zeros(B, max_keep, dtype=i32, device=kv_pages.device)
     if new_lens is None:
-        new_lens = torch.zeros(B, dtype=torch.int32, device=dev)
+        new_lens = torch.zeros(B, dtype=i32, device=kv_pages.device)
     if mass_out is None:
-        mass_out = torch.zeros(B, max_keep, dtype=torch.float32, device=dev)
-    _want(what, dev, [("page_table", page_table, i32, None), ("seq_lens", seq_lens, i32, (B,)),
-                      ("keep_lens", keep_lens, i32, (B,)), ("mass", mass, f32, None),
-                      ("dst_page_table", dst_page_table, i32, None), ("kept", kept, i32, None),
-                      ("new_lens", new_lens, i32, (B,)), ("mass_out", mass_out, f32, None)])
-    for name, t in (("page_table", page_table), ("mass", mass), ("dst_page_table", dst_page_table), ("kept", kept),
-                    ("mass_out", mass_out)):
-        if t.dim() != 2 or t.shape[0] != B:
-            _refuse(what, f"{name} has shape {tuple(t.shape)}")
-    _call(what, dev, stream, lib.mla_kv_evict, _ptr(kv_pages), int(kv_pages.shape[0]), int(kv_pages.shape[1]), int(kv_dtype),
-          _ptr(page_table), int(page_table.shape[1]), _ptr(seq_lens), _ptr(keep_lens), _ptr(mass), int(mass.shape[1]),
-          _ptr(dst_page_table), int(dst_page_table.shape[1]), B, int(sink), int(recent), int(max_seq_len), int(max_keep),
-          _ptr(kept), int(kept.shape[1]), _ptr(new_lens), _ptr(mass_out), int(mass_out.shape[1]))
+        mass_out = torch.zeros(B, max_keep, dtype=f32, device=kv_pages.device)
+    table, dst = _want_rows(what, dev, "page_table", page_table, i32, B), _want_rows(what, dev, "dst_page_table", dst_page_table, i32, B)
+    _call(what, dev, stream, lib.mla_kv_evict, pool, kv_pages.shape[0], kv_pages.shape[1], kv_dtype, *table,
+          _want(what, dev, "seq_lens", seq_lens, i32, (B,)), _want(what, dev, "keep_lens", keep_lens, i32, (B,)),
+          *_want_rows(what, dev, "mass", mass, f32, B), *dst, B, sink, recent, max_seq_len, max_keep,
+          *_want_rows(what, dev, "kept", kept, i32, B), _want(what, dev, "new_lens", new_lens, i32, (B,)),
+          *_want_rows(what, dev, "mass_out", mass_out, f32, B))
     return kept, new_lens, mass_out
 
 

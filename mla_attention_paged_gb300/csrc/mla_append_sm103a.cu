@@ -17,8 +17,8 @@
 // rotated columns are one chunk per lane, which puts the two chunks of a half-split pair in
 // lanes that differ in bit 2.  A warp takes four rows at a time: for queries four heads of one
 // token, kSteps times with all loads in flight, so positions, cosines and weights are read once
-// per warp; for keys four tokens.  (A warp per row, two loads in flight, took 72 us where
-// this takes APPEND_US for 8191 tokens of 16 normed 192-wide heads and their keys.)
+// per warp; keys 16 lanes a row.  (A warp per row, two loads in flight, took 72 us where this
+// takes 22.8 for 8191 tokens of 16 normed 192-wide heads and their keys: 5.3 TB/s.)
 #include <cuda_fp8.h>
 
 #include "mla_internal.h"
@@ -29,11 +29,9 @@ namespace {
 
 constexpr int kRope = 64;
 constexpr int kWarps = 4;
-#ifndef MANY
-#define MANY 4
-#endif
-constexpr int kManySteps = MANY;
-constexpr int64_t kFewRows = 16384;
+constexpr int kManySteps = 2;
+constexpr int kManyKeyLanes = 16;
+constexpr int64_t kFewRows = 12288;
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -131,10 +129,12 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale, bool i
 }
 
 // kChunks: most chunks of a query lane that are not rotated, ceil((q_dim - 64) / 64).
-// kSteps: four heads a step.  kKeyLanes: lanes that share a key's row (8, or all 32).
+// kSteps: four heads a step.  kKeyLanes: lanes that share a key's row.  Five CTAs an SM (102
+// registers) measured 22.8 us on 8191 tokens of 16 normed 192-wide heads against 25.0 at four and
+// 29 spilling at six; streaming loads and stores (nothing is read again) 24.6 against 26.8.
 // The first k_warps warps of the grid take keys, the others queries.
 template <int kChunks, int kSteps, int kKeyLanes>
-__global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendParams p, int64_t k_warps, int warps_per_token) {
+__global__ void __launch_bounds__(32 * kWarps, kChunks <= 2 ? 5 : 1) kv_append_kernel(const AppendParams p, int64_t k_warps, int warps_per_token) {
   // programmatic dependent launch: no input is read before the previous kernel has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, sub = lane >> 3, l = lane & 7;
@@ -145,11 +145,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendPara
     if (unit - k_warps >= static_cast<int64_t>(p.tokens) * warps_per_token) return;
     const int n = static_cast<int>((unit - k_warps) / warps_per_token);
     const int h0 = static_cast<int>((unit - k_warps) % warps_per_token) * 4 * kSteps + sub;
-    const int pos = __ldg(p.positions + n);
-    if (static_cast<unsigned>(pos) >= static_cast<unsigned>(p.max_positions)) {
-      if (lane == 0) atomicOr(p.status, kStatusDeviceArg);
-      return;
-    }
+    const int pos = __ldg(p.positions + n);  // (checked once the rows' loads are in flight)
     const int chunks = (p.q_dim - kRope) / 8;
     const __nv_bfloat16* src = p.q_in + static_cast<int64_t>(n) * p.q_in_token;
     __nv_bfloat16* dst = p.q_out + static_cast<int64_t>(n) * p.q_out_token;
@@ -166,10 +162,14 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendPara
         const uint4* row = reinterpret_cast<const uint4*>(src + static_cast<int64_t>(h) * p.q_in_head);
 #pragma unroll
         for (int i = 0; i < kChunks; ++i)
-          w[s][i] = h < p.heads && l + 8 * i < chunks ? row[l + 8 * i] : make_uint4(0u, 0u, 0u, 0u);
-        w[s][kChunks] = h < p.heads ? row[chunks + l] : make_uint4(0u, 0u, 0u, 0u);
+          w[s][i] = h < p.heads && l + 8 * i < chunks ? __ldcs(row + l + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        w[s][kChunks] = h < p.heads ? __ldcs(row + chunks + l) : make_uint4(0u, 0u, 0u, 0u);
       }
       if (s0 == 0) {
+        if (static_cast<unsigned>(pos) >= static_cast<unsigned>(p.max_positions)) {
+          if (lane == 0) atomicOr(p.status, kStatusDeviceArg);
+          return;
+        }
         load_turn(turn, p.cos_sin + static_cast<int64_t>(pos) * kRope, l, inter);
         if (p.q_weight) {
           const uint4* g = reinterpret_cast<const uint4*>(p.q_weight);
@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendPara
           uint4* out = reinterpret_cast<uint4*>(dst + static_cast<int64_t>(h) * p.q_out_head);
 #pragma unroll
           for (int i = 0; i < kChunks; ++i)
-            if (l + 8 * i < chunks) out[l + 8 * i] = pack8(f[i]);
-          out[chunks + l] = pack8(f[kChunks]);
+            if (l + 8 * i < chunks) __stcs(out + l + 8 * i, pack8(f[i]));
+          __stcs(out + chunks + l, pack8(f[kChunks]));
         }
       }
     }
@@ -209,22 +209,19 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendPara
   constexpr int kLatentChunks = kValueDim / 8 / kKeyLanes;  // per lane; lanes 0-7 also rotate one
   const int kl = lane % kKeyLanes;
   const int64_t n = unit * (32 / kKeyLanes) + lane / kKeyLanes;
-  int64_t slot = -1;
-  int pos = 0;
-  if (n < p.tokens) {
-    slot = __ldg(p.slots + n);  // (a padded token has no place in the cache)
-    pos = __ldg(p.positions + n);
-    if (slot >= 0 && (slot >= p.num_slots || static_cast<unsigned>(pos) >= static_cast<unsigned>(p.max_positions))) {
-      if (kl == 0) atomicOr(p.status, kStatusDeviceArg);
-      slot = -1;
-    }
-  }
-  const bool live = slot >= 0;  // (the others still take part in the shuffles)
+  const bool real = n < p.tokens;
+  int64_t slot = real ? __ldg(p.slots + n) : -1;  // (negative: a padded token has no place in the cache)
+  const int pos = real ? __ldg(p.positions + n) : 0;
   uint4 w[kLatentChunks + 1];
   const uint4* row = reinterpret_cast<const uint4*>(p.kv_in + n * p.kv_in_token);
 #pragma unroll
-  for (int i = 0; i < kLatentChunks; ++i) w[i] = live ? row[kl + kKeyLanes * i] : make_uint4(0u, 0u, 0u, 0u);
-  w[kLatentChunks] = live && kl < 8 ? row[kValueDim / 8 + kl] : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < kLatentChunks; ++i) w[i] = real ? __ldcs(row + kl + kKeyLanes * i) : make_uint4(0u, 0u, 0u, 0u);
+  w[kLatentChunks] = real && kl < 8 ? __ldcs(row + kValueDim / 8 + kl) : make_uint4(0u, 0u, 0u, 0u);
+  if (slot >= 0 && (slot >= p.num_slots || static_cast<unsigned>(pos) >= static_cast<unsigned>(p.max_positions))) {
+    if (kl == 0) atomicOr(p.status, kStatusDeviceArg);
+    slot = -1;
+  }
+  const bool live = slot >= 0;  // (the others still take part in the shuffles)
   Turn turn;
   load_turn(turn, p.cos_sin + (live ? static_cast<int64_t>(pos) * kRope : 0), l, inter);
   float inv = 1.f;
@@ -258,10 +255,11 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const AppendPara
 
 template <int kChunks>
 cudaError_t launch_chunks(const AppendParams& p, cudaStream_t stream) {
-  // Few rows: one step and a warp per key, for the shortest chain; many: more bytes in flight
-  // per warp.
+  // Few rows: one step and a warp per key, for the shortest chain (4 tokens of 16 heads 2.1
+  // against 2.6 us, 512 normed 192-wide 3.05 against 3.18); many: more bytes in flight per warp
+  // (2048 tokens 7.1 against 8.2 us).
   const bool few = static_cast<int64_t>(p.tokens) * (p.heads > 0 ? p.heads : 16) <= kFewRows;
-  const int steps = few ? 1 : kManySteps, key_rows = few ? 1 : 4;
+  const int steps = few ? 1 : kManySteps, key_rows = few ? 1 : 32 / kManyKeyLanes;
   const int per_token = (p.heads + 4 * steps - 1) / (4 * steps);
   const int64_t k_warps = p.kv_in ? (p.tokens + key_rows - 1) / key_rows : 0;
   const int64_t warps = k_warps + static_cast<int64_t>(p.tokens) * per_token;
@@ -275,7 +273,7 @@ cudaError_t launch_chunks(const AppendParams& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return few ? cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, 1, 32>, p, k_warps, per_token)
-             : cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, kManySteps, 8>, p, k_warps, per_token);
+             : cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, kManySteps, kManyKeyLanes>, p, k_warps, per_token);
 }
 
 }  // namespace

@@ -168,12 +168,16 @@ def _want_workspace(what, dev, workspace):
     return _want(what, dev, "workspace", workspace, workspace.dtype), workspace.numel() * workspace.element_size()
 
 
+# The current stream's handle without a Stream object around it (2.8 us a call; this 0.1).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _call(what, dev, stream, fn, *args):
     """fn(*args, stream) on CUDA device number `dev`: its current stream unless one is given."""
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _call(what, dev, stream, fn, *args)
-    rc = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    rc = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc != MLA_OK:
         raise MlaError(rc, what)
 
@@ -378,13 +382,15 @@ def kv_append(q: torch.Tensor | None, kv: torch.Tensor | None, positions: torch.
     if q is not None:
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=bf16, device=q.device)
-        for name, t in (("q", q), ("q_out", q_out)):
-            if t.get_device() != dev or dev < 0 or t.dtype is not bf16 or t.dim() != 3 or t.shape != q.shape:
-                _refuse(what, f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}")
-            if t.stride(2) != 1:
-                _refuse(what, f"the last dimension of {name} is not dense")
-        H, D = q.shape[1], q.shape[2]
-        qa = (q.data_ptr(), q.stride(0), q.stride(1), q_out.data_ptr(), q_out.stride(0), q_out.stride(1), H, D,
+        shape = q.shape
+        if q_out.get_device() != dev or dev < 0 or q.dtype is not bf16 or q_out.dtype is not bf16 or len(shape) != 3 or q_out.shape != shape:
+            _refuse(what, f"q is {q.dtype} {tuple(shape)} on {q.device}, q_out {q_out.dtype} {tuple(q_out.shape)} on {q_out.device}")
+        qt, qh, dense = q.stride()
+        ot, oh, out_dense = q_out.stride()
+        if dense != 1 or out_dense != 1:
+            _refuse(what, "the last dimension of q or q_out is not dense")
+        H, D = shape[1], shape[2]
+        qa = (q.data_ptr(), qt, qh, q_out.data_ptr(), ot, oh, H, D,
               None if q_weight is None else _want(what, dev, "q_weight", q_weight, bf16, (D,)))
     ka, pool, rows, slot = (None, 0, None), None, 0, None
     if kv is not None:

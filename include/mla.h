@@ -178,8 +178,8 @@ int mla_decode_int8_paged(const mla_decode_plan_t* plan, const void* q, const vo
  * draft t of request b sees the whole prefix (keys 0 .. L_b - T - 1) and, of the T drafts at the
  * request's last positions, those whose bit is set in its mask word.
  *   plan        : from mla_decode_tree_plan: mla_decode_plan with q_len = T <= 64 and a workspace for
- *                 fp32 split partials (mla_decode_plan's own plans run too, given a workspace of
- *                 that size).
+ *                 a tree's split partials (fp32 over a bf16 pool; mla_decode_plan's own plans run
+ *                 too, given a workspace of that size).
  *   page_scales : as mla_decode_int8_paged for an MLA_KV_INT8_PAGE plan, else NULL.
  *   tree_mask   : [B, T] uint64, 8-byte aligned: bit u of word (b, t) = draft t sees draft u (usually
  *                 its ancestors and itself; any word is accepted, bits from T on are ignored).
@@ -360,8 +360,8 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
  *   workspace   : device scratch of the size mla_key_mass_workspace gives for the plan, 256-byte
  *                 aligned (NULL when that is 0); overwritten; calls that share one are stream-ordered.
  * Launched as a programmatic dependent like mla_decode.  Errors: MLA_ERR_INVALID_ARG,
- * MLA_ERR_UNSUPPORTED (tree_mask with more than 64 drafts), MLA_ERR_WORKSPACE_TOO_SMALL,
- * MLA_ERR_CUDA.  Device-side, recorded as MLA_ERR_DEVICE_ARG: a length below q_len or beyond the
+ * MLA_ERR_UNSUPPORTED (tree_mask with more than 64 drafts; batch times the longest request beyond
+ * 2^38 keys), MLA_ERR_WORKSPACE_TOO_SMALL, MLA_ERR_CUDA.  Device-side, recorded as MLA_ERR_DEVICE_ARG: a length below q_len or beyond the
  * plan (that request's row is left as it was) and a page id outside [0, num_pages) (its rows count
  * as zeros). */
 int mla_key_mass_workspace(const mla_decode_plan_t* plan, size_t* bytes_out);

@@ -277,12 +277,12 @@ const char* mla_status_string(int status) {
 
 namespace {
 
-// Scratch of the split partials: one normalised output row (bf16; a tree's stays fp32) and one
-// log-sum-exp per (request, split, folded row).
+// Scratch of the split partials: one normalised output row (16 bits; a tree's over a bf16 pool
+// stays fp32) and one log-sum-exp per (request, split, folded row).
 size_t partial_bytes(const mla_decode_plan_t& pl, bool tree) {
   if (pl.max_splits <= 1) return 0;
   const size_t parts = static_cast<size_t>(pl.batch) * pl.max_splits * pl.rows;
-  return 256 + parts * kValueDim * (tree ? sizeof(float) : sizeof(__nv_bfloat16)) + parts * sizeof(float);
+  return 256 + parts * kValueDim * (tree && pl.kv_dtype == MLA_KV_BF16 ? sizeof(float) : sizeof(__nv_bfloat16)) + parts * sizeof(float);
 }
 
 int make_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads, int page_size, int max_pages_per_seq,
@@ -482,7 +482,7 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
   p.lse = lse;
   if (plan->max_splits > 1) {
     const size_t parts = static_cast<size_t>(plan->batch) * plan->max_splits * plan->rows;
-    if (tree_mask) {
+    if (tree_mask && !kv8) {
       p.ws_of = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
       p.ws_lse = p.ws_of + parts * kValueDim;
     } else {

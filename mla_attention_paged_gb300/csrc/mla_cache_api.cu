@@ -123,6 +123,7 @@ int mla_key_mass(const mla_decode_plan_t* plan, const void* q, const void* kv_pa
     return MLA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !(kv_scale > 0.f) || !(decay >= 0.f) || mass_stride < plan->max_seq_len) return MLA_ERR_INVALID_ARG;
   if (tree_mask && q_len > kMaxTreeDrafts) return MLA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(plan->batch) * (plan->max_seq_len / 128 + 1) >= (int64_t(1) << 31)) return MLA_ERR_UNSUPPORTED;
   size_t need = 0;
   mla_key_mass_workspace(plan, &need);
   if (need > 0) {

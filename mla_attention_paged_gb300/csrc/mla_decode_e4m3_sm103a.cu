@@ -214,7 +214,7 @@ __device__ __forceinline__ void p_split16(const float (&x)[16], int lim, float s
 // kMayIdle: q_len * heads is not a multiple of 64, so a row group may hold 48 rows or fewer
 // and a softmax warp may own no row; such warps then skip their S reads and P writes.  (A
 // compile-time choice: the check alone measured 1.2 % slower on full 64-row groups.)
-// kTree: drafts see each other by p.tree_mask instead of in order, and partials are fp32.
+// kTree: drafts see each other by p.tree_mask instead of in order, and partials are f16.
 template <bool kMayIdle, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
@@ -526,28 +526,37 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
       const float mult = ctrl->q_mult[r];
       const uint32_t qb = qb0 + r * 128;
       const uint32_t lane_q = static_cast<uint32_t>(quad_q * 32) << 16;
+      // Lanes l and l + 8 hold a row's hi and lo TMEM lanes.  Each splits every other chunk
+      // of eight columns into both parts and hands its partner the one the partner stores: the
+      // conversions, which bound this, are done once (each lane for itself took 9,400 cycles of
+      // a CTA's start).
 #pragma unroll 1
       for (int cb = 0; cb < 4; ++cb) {
         const int c = 4 * kh_q + cb;
         uint32_t codes[16];  // 64 codes of block c, four per word, column order
 #pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {  // bf16 chunk ch = columns 8ch .. 8ch+7
-          uint32_t w[4];
+        for (int ch2 = 0; ch2 < 4; ++ch2) {  // bf16 chunk ch = columns 8ch .. 8ch+7
+          const int ch = 2 * ch2 + (lo_part ? 1 : 0);
+          uint32_t w[4], hi[4], lo[4];
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                        : "r"(qb + c * kF16Block + ((ch ^ (r & 7)) << 4)));
 #pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            const float x0 = __uint_as_float(w[i] << 16) * mult, x1 = __uint_as_float(w[i] & 0xFFFF0000u) * mult;
-            const float x2 = __uint_as_float(w[i + 1] << 16) * mult;
-            const float x3 = __uint_as_float(w[i + 1] & 0xFFFF0000u) * mult;
-            uint32_t c01 = f32x2_to_e4m3x2(x0, x1), c23 = f32x2_to_e4m3x2(x2, x3);
-            if (lo_part) {
-              const float2 v01 = e4m3x2_to_f32x2(c01), v23 = e4m3x2_to_f32x2(c23);
-              c01 = f32x2_to_e4m3x2(x0 - v01.x, x1 - v01.y);
-              c23 = f32x2_to_e4m3x2(x2 - v23.x, x3 - v23.y);
-            }
-            codes[2 * ch + (i >> 1)] = c01 | (c23 << 16);
+          for (int i = 0; i < 4; ++i) {
+            // (the scaled value has 8 significant bits and lies below 256: f16 holds it, and the
+            // residual, exactly down to where both codes are zero)
+            const uint32_t x = pack_f16x2(__uint_as_float(w[i] << 16) * mult, __uint_as_float(w[i] & 0xFFFF0000u) * mult);
+            hi[i] = f16x2_to_e4m3x2(x);
+            uint32_t d;
+            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(e4m3x2_to_f16x2(hi[i])));
+            lo[i] = f16x2_to_e4m3x2(d);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t h = hi[2 * k] | (hi[2 * k + 1] << 16), l = lo[2 * k] | (lo[2 * k + 1] << 16);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, lo_part ? h : l, 8);
+            codes[4 * ch2 + k] = lo_part ? got : h;      // chunk 2 ch2
+            codes[4 * ch2 + 2 + k] = lo_part ? l : got;  // chunk 2 ch2 + 1
           }
         }
         tmem_st16(tmem + lane_q + kTmemQ + c * 16, codes);
@@ -843,7 +852,8 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
           // (a row that sees nothing has sums of 0; kTree passes a NaN on)
           const float lse2 = (kTree ? ls != 0.f : ls > 0.f) ? (m + __log2f(ls) - kPShift) : -INFINITY;
           const float lse_nat = lse2 * 0.69314718055994530942f;
-          ctrl->row_scale[r] = (kTree ? lu != 0.f : lu > 0.f) ? (v_scale / lu) : 0.f;
+          // (a tree's partials are f16 in units of the codes; the combine scales them)
+          ctrl->row_scale[r] = (kTree ? lu != 0.f : lu > 0.f) ? ((kTree && !final_out ? 1.f : v_scale) / lu) : 0.f;
           if (row_active[h]) {
             const int64_t grow = static_cast<int64_t>(b) * p.R + row0 + r;
             if (final_out)
@@ -876,24 +886,12 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          if (kTree && !final_out) {  // a tree's partials stay fp32: [64][512] in stages 0-3
-            st_shared_f32(stage_s + ((kh * 32 + i) * kValueDim + dim) * 4, __uint_as_float(v[i]) * rs[i]);
-            continue;
-          }
-          const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(v[i]) * rs[i]);
-          asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage_s + ((kh * 32 + i) * kValueDim + dim) * 2),
-                       "h"(*reinterpret_cast<const uint16_t*>(&o)));
+          st_shared_u16(stage_s + ((kh * 32 + i) * kValueDim + dim) * 2,
+                        out_bits<kTree>(__uint_as_float(v[i]) * rs[i], final_out));
         }
       }
       const __nv_bfloat16* stage_h = reinterpret_cast<const __nv_bfloat16*>(smem + kOffOStage);
       named_bar_sync(1, kSoftmaxThreads);
-      if (kTree && !final_out) {
-        static_assert(kGroupRows * kValueDim * 4 <= kStages * kRawTile, "fp32 staging");
-        const uint4* const src = reinterpret_cast<const uint4*>(smem + kOffOStage);
-        uint4* const dst = reinterpret_cast<uint4*>(
-            p.ws_of + ((static_cast<int64_t>(b) * p.max_splits + split) * p.R + row0) * kValueDim);
-        for (int c = threadIdx.x; c < nrows * (kValueDim / 4); c += kSoftmaxThreads) dst[c] = src[c];
-      } else {
       constexpr int kChunksPerRow = kValueDim * 2 / 16;
       __nv_bfloat16* dst = final_out
                                ? p.out + (static_cast<int64_t>(b) * p.R + row0) * kValueDim
@@ -902,7 +900,6 @@ decode_partial_e4m3_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
         const int rr = c / kChunksPerRow, cc = c % kChunksPerRow;
         const uint4 v = *reinterpret_cast<const uint4*>(stage_h + rr * kValueDim + cc * 8);
         *reinterpret_cast<uint4*>(dst + rr * kValueDim + cc * 8) = v;
-      }
       }
     }
   }

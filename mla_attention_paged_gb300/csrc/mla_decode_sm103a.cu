@@ -757,7 +757,8 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const bool some = kTree ? l_sum != 0.f : l_sum > 0.f;
         const float lse2 = some ? (m_used + __log2f(l_sum)) : -INFINITY;
         const float lse_nat = lse2 * 0.69314718055994530942f;
-        ctrl->row_scale[r] = some ? (v_scale / l_sum) : 0.f;
+        // (an int8 pool's partials of a tree are f16 in units of its codes; the combine scales them)
+        ctrl->row_scale[r] = some ? ((kTree && kInt8 && !final_out ? 1.f : v_scale) / l_sum) : 0.f;
         if (row_active) {
           const int64_t grow = static_cast<int64_t>(b) * p.R + row0 + r;
           if (final_out)
@@ -774,19 +775,32 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       // The 64 row scales go to registers first: shared-memory loads interleaved with the
       // staging stores below would each have to wait for the stores before them.
       const uint32_t stage_s = smem_u32(smem + kOffStages);  // [64][512] bf16
-      if (kTree && !final_out) {
-        // A tree's partials stay fp32 ([64][512] in both stages): a second bf16 rounding would
-        // add as much error as the output's own.
+      if (kTree && !kInt8 && !final_out) {
+        // A bf16 pool's partials of a tree stay fp32 ([64][512] in both stages): a second bf16
+        // rounding would add as much error as the output's own.  The scales of 32 rows at a
+        // time go to registers first (loaded between the stores they cost 7,800 cycles).
         static_assert(kGroupRows * kValueDim * 4 <= kStages * kTileBytes, "fp32 staging");
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          const int dim = (c >> 1) * 128 + warp * 32 + lane, hh = c & 1;
-          uint32_t v[32];
-          tmem_ld32(tmem + lane_base + (c >> 1) * 64 + hh * 32, v);
-          tmem_ld_wait();
+        for (int hh = 0; hh < 2; ++hh) {
+          float rs[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            st_shared_f32(stage_s + ((hh * 32 + i) * kValueDim + dim) * 4, __uint_as_float(v[i]) * ctrl->row_scale[hh * 32 + i]);
+          for (int i = 0; i < 32; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&ctrl->row_scale[hh * 32 + i]);
+            rs[i] = f.x;
+            rs[i + 1] = f.y;
+            rs[i + 2] = f.z;
+            rs[i + 3] = f.w;
+          }
+#pragma unroll 1
+          for (int qc = 0; qc < 4; ++qc) {
+            const int dim = qc * 128 + warp * 32 + lane;
+            uint32_t v[32];
+            tmem_ld32(tmem + lane_base + qc * 64 + hh * 32, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              st_shared_f32(stage_s + ((hh * 32 + i) * kValueDim + dim) * 4, __uint_as_float(v[i]) * rs[i]);
+          }
         }
       } else if constexpr (kInt8) {
         // (the int8 kernels run at a lower register cap: rows 32hh .. 32hh+31 at a time,
@@ -810,9 +824,8 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(v[i]) * rs[i]);
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage_s + ((hh * 32 + i) * kValueDim + dim) * 2),
-                           "h"(*reinterpret_cast<const uint16_t*>(&o)));
+              st_shared_u16(stage_s + ((hh * 32 + i) * kValueDim + dim) * 2,
+                            out_bits<kTree>(__uint_as_float(v[i]) * rs[i], final_out));
             }
           }
         }
@@ -846,7 +859,7 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       }
       __nv_bfloat16* stage_h = reinterpret_cast<__nv_bfloat16*>(smem + kOffStages);
       named_bar_sync(1, 128);
-      if (kTree && !final_out) {
+      if (kTree && !kInt8 && !final_out) {
         const uint4* const src = reinterpret_cast<const uint4*>(smem + kOffStages);
         uint4* const dst = reinterpret_cast<uint4*>(
             p.ws_of + ((static_cast<int64_t>(b) * p.max_splits + split) * p.R + row0) * kValueDim);
@@ -891,11 +904,14 @@ constexpr int kCombineThreads = 64 * kCombineRows;
 constexpr int kCombineBatch = 32;  // splits staged per round (lane l holds split s0 + l)
 constexpr int kCombineRowBytes = kValueDim * 2;
 
-// kTree: the partials are fp32 (half as many splits a batch in the same shared memory).
-template <bool kTree>
+// kPart: the partials' format, bf16, or for a tree fp32 (bf16 pools; half as many splits a batch
+// in the same shared memory) or f16 in units of the codes (8-bit pools, whose values stay
+// inside f16's range: p.v_scale makes them the output's).
+template <int kPart>
 __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const DecodeParams p) {
-  constexpr int kBatch = kTree ? kCombineBatch / 2 : kCombineBatch;
-  constexpr int kRowBytes = kTree ? 2 * kCombineRowBytes : kCombineRowBytes;
+  constexpr bool kTree = kPart != kPartBf16, kWide = kPart == kPartF32;
+  constexpr int kBatch = kWide ? kCombineBatch / 2 : kCombineBatch;
+  constexpr int kRowBytes = kWide ? 2 * kCombineRowBytes : kCombineRowBytes;
   extern __shared__ __align__(128) uint8_t cs[];  // [split][row][512] bf16 or fp32
   __shared__ uint64_t bar;
   __shared__ int abort_flag;
@@ -936,7 +952,7 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const D
       const uint64_t pol = policy_evict_first();
       for (int s = 0; s < nb; ++s)
         bulk_load(cs + s * nr * kRowBytes,
-                  kTree ? static_cast<const void*>(p.ws_of + ((base + s0 + s) * p.R + row0) * kValueDim)
+                  kWide ? static_cast<const void*>(p.ws_of + ((base + s0 + s) * p.R + row0) * kValueDim)
                         : static_cast<const void*>(p.ws_o + ((base + s0 + s) * p.R + row0) * kValueDim),
                   static_cast<uint32_t>(nr * kRowBytes), &bar, pol);
     }
@@ -961,11 +977,11 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const D
     ok = mbar_wait(&bar, phase, &abort_flag);
     phase ^= 1u;
     if (ok) {
-      const uint32_t src = smem_u32(cs) + (active ? r : 0) * kRowBytes + c8 * (kTree ? 32 : 16);
+      const uint32_t src = smem_u32(cs) + (active ? r : 0) * kRowBytes + c8 * (kWide ? 32 : 16);
       for (int s = 0; s < nb; ++s) {
         const float ws_s = __shfl_sync(0xffffffffu, w, s);
-        if constexpr (kTree) {
-          if (ws_s == 0.f) continue;  // (a split none of whose keys this row sees; uniform over the row's threads)
+        if (kTree && ws_s == 0.f) continue;  // (a split none of whose keys this row sees; uniform over the row's threads)
+        if constexpr (kWide) {
           const uint4 lo = ld_shared_v4(src + s * nr * kRowBytes), hi = ld_shared_v4(src + s * nr * kRowBytes + 16);
           const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
@@ -979,7 +995,8 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const D
         const uint32_t vv[4] = {v0, v1, v2, v3};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&vv[i]));
+          const float2 f = kPart == kPartF16 ? __half22float2(*reinterpret_cast<const __half2*>(&vv[i]))
+                                             : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&vv[i]));
           acc[2 * i] += ws_s * f.x;
           acc[2 * i + 1] += ws_s * f.y;
         }
@@ -996,7 +1013,7 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const D
   }
   if (active) {
     const bool some = kTree ? w_run != 0.f : w_run > 0.f;  // (kTree passes a NaN on)
-    const float inv = some ? 1.f / w_run : 0.f;
+    const float inv = some ? (kPart == kPartF16 ? p.v_scale : 1.f) / w_run : 0.f;
     uint4 pk;
     pk.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
     pk.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
@@ -1083,21 +1100,22 @@ cudaError_t launch_selftest_timeout(unsigned* status, cudaStream_t stream) {
 
 cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t stream) {
   const dim3 grid((p.R + kCombineRows - 1) / kCombineRows, p.B);
-  const bool tree = p.tree_mask != nullptr;
-  const int smem = (tree ? 2 * min(p.max_splits, kCombineBatch / 2) : min(p.max_splits, kCombineBatch)) * kCombineRows *
+  const bool wide = p.ws_of != nullptr;
+  const int smem = (wide ? 2 * min(p.max_splits, kCombineBatch / 2) : min(p.max_splits, kCombineBatch)) * kCombineRows *
                    kCombineRowBytes;
+  static constexpr decltype(&decode_combine_kernel<kPartBf16>) kernels[3] = {
+      decode_combine_kernel<kPartBf16>, decode_combine_kernel<kPartF32>, decode_combine_kernel<kPartF16>};
   // the shared-memory limit is a per-device attribute: set it once per device and thread
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(decode_combine_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kCombineBatch * kCombineRows * kCombineRowBytes);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(decode_combine_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kCombineBatch * kCombineRows * kCombineRowBytes);
-    if (e != cudaSuccess) return e;
+    for (auto kernel : kernels) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kCombineBatch * kCombineRows * kCombineRowBytes);
+      if (e != cudaSuccess) return e;
+    }
     configured_device = dev;
   }
   cudaLaunchConfig_t cfg = {};
@@ -1110,8 +1128,7 @@ cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return tree ? cudaLaunchKernelEx(&cfg, decode_combine_kernel<true>, p)
-              : cudaLaunchKernelEx(&cfg, decode_combine_kernel<false>, p);
+  return cudaLaunchKernelEx(&cfg, kernels[wide ? kPartF32 : p.tree_mask ? kPartF16 : kPartBf16], p);
 }
 
 }  // namespace mla

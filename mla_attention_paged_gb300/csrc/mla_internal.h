@@ -14,6 +14,11 @@ constexpr int kValueDim = 512;   // value = first 512 latent columns
 constexpr int kTileKeys = 64;    // keys per decode tile
 constexpr int kGroupRows = 64;   // folded query rows per decode CTA
 
+// Formats of the split partials (see DecodeParams).
+constexpr int kPartBf16 = 0;
+constexpr int kPartF32 = 1;
+constexpr int kPartF16 = 2;
+
 constexpr int kMaxTreeDrafts = 64;  // drafts of a tree: one bit each of a 64-bit word
 
 // Pool formats of the decode kernel (the values of mla_kv_dtype_t).
@@ -46,9 +51,9 @@ struct DecodeParams {
   float* ws_lse;                // [B, max_splits, R] partial log-sum-exp (natural log)
   unsigned* status;             // device status word
   // tree decode (tree_mask non-null): [B, T] bit u of word (b, t) = draft t sees draft u; the
-  // split partials are fp32
+  // split partials are f16 in units of the codes in ws_o (8-bit pools), or fp32 in ws_of
   const uint64_t* tree_mask;
-  float* ws_of;                 // [B, max_splits, R, 512] partial outputs of a tree decode (normalised, fp32)
+  float* ws_of;                 // [B, max_splits, R, 512] partial outputs of a tree decode over a bf16 pool
 };
 
 struct PrefillParams {
@@ -168,8 +173,7 @@ cudaError_t launch_decode_partial_e4m3(const DecodeParams& p, const CUtensorMap&
 // tensor memory, a three-tile ring (mla_decode_narrow_sm103a.cu).
 cudaError_t launch_decode_partial_narrow(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv,
                                          cudaStream_t stream);
-// Decode: LSE-merge of the split partials for requests with more than one split (fp32 partials
-// when p.tree_mask is set).
+// Decode: LSE-merge of the split partials for requests with more than one split.
 cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t stream);
 // Watchdog self-test kernel (a wait nothing satisfies; must time out and report).
 cudaError_t launch_selftest_timeout(unsigned* status, cudaStream_t stream);

@@ -145,7 +145,7 @@ struct MassCtrl {
   uint32_t tmem_base;
   int abort_flag;
   int first_b, first_tile;   // where this CTA's run of tiles begins
-  int64_t tiles;             // and its length
+  int tiles;                 // and its length
   int any_dead;              // some of the segment's rows add nothing
   alignas(16) float2 row[kMaxRows];      // scale of the row's scores and its -lse, log2 domain
   alignas(16) uint64_t mask[kMaxRows];   // trees: the drafts the row sees
@@ -228,11 +228,12 @@ __device__ __forceinline__ void split_rows(const __nv_bfloat16* q, uint32_t q_sm
         uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 x = make_float2(__uint_as_float(u[k] << 16) * up, __uint_as_float(u[k] & 0xFFFF0000u) * up);
-          const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
-          const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-          const __nv_fp8x2_storage_t l =
-              __nv_cvt_float2_to_fp8x2(make_float2(x.x - hf.x, x.y - hf.y), __NV_SATFINITE, __NV_E4M3);
+          // (8 significant bits below 256: exact in f16, and the residual too)
+          const uint32_t x = pack_f16x2(__uint_as_float(u[k] << 16) * up, __uint_as_float(u[k] & 0xFFFF0000u) * up);
+          const __half2 xh = *reinterpret_cast<const __half2*>(&x);
+          const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(xh), __NV_SATFINITE, __NV_E4M3);
+          const __half2 d = __hsub2(xh, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+          const __nv_fp8x2_storage_t l = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(d), __NV_SATFINITE, __NV_E4M3);
           hi[k >> 1] |= static_cast<uint32_t>(h) << (16 * (k & 1));
           lo[k >> 1] |= static_cast<uint32_t>(l) << (16 * (k & 1));
         }
@@ -294,40 +295,57 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     return bad_len(L) ? 0 : (L + kTile - 1) / kTile;
   };
   if (warp == 0) {
-    // this CTA's run: tiles [total set / sets, total (set + 1) / sets) of the batch
-    int64_t total = 0;
-    for (int b = lane; b < p.B; b += 32) {
-      total += tiles_of(b);
-      if (blockIdx.x == 0 && bad_len(p.seq_lens[b])) atomicOr(p.status, kStatusDeviceArg);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const int64_t begin = total * set / p.sets, end = total * (set + 1) / p.sets;
-    int64_t before = 0;
-    int fb = 0, ft = 0;
-    bool found = begin >= end;
-    for (int b0 = 0; !found && b0 < p.B; b0 += 32) {
-      const int n = b0 + lane < p.B ? tiles_of(b0 + lane) : 0;
-      int64_t incl = n;
+    // This CTA's run.  Equal runs, tiles [total set / sets, total (set + 1) / sets) of the batch,
+    // may cross from one request into the next, which costs a CTA the new queries and a drained
+    // pipe (10 us on an e4m3 pool, whose queries are split); runs of whole shares of one
+    // request, c tiles each, are taken instead where they are at most two tiles longer.
+    const int mine = lane < p.B ? tiles_of(lane) : 0;  // (the first 32 requests stay in registers)
+    auto tiles = [&](int b0) { return b0 == 0 ? mine : (b0 + lane < p.B ? tiles_of(b0 + lane) : 0); };
+    auto sum_of = [&](auto&& f) {
+      int s = 0;
+      for (int b0 = 0; b0 < p.B; b0 += 32) s += f(tiles(b0));
+      return __reduce_add_sync(0xffffffffu, s);
+    };
+    if (blockIdx.x == 0)
+      for (int b = lane; b < p.B; b += 32)
+        if (bad_len(p.seq_lens[b])) atomicOr(p.status, kStatusDeviceArg);
+    const int total = sum_of([](int n) { return n; });
+    const int even = (total + p.sets - 1) / p.sets;
+    int share = 0;  // tiles of a whole share, or 0: equal runs
+    for (int c = even; c > 0 && c <= even + 2; ++c)
+      if (sum_of([c](int n) { return (n + c - 1) / c; }) <= p.sets) {
+        share = c;
+        break;
+      }
+    // units (tiles or shares) before each request locate this CTA's first one
+    auto units = [&](int n) { return share ? (n + share - 1) / share : n; };
+    auto cut = [&](int s) { return static_cast<int>(static_cast<int64_t>(total) * s / p.sets); };
+    const int begin = share ? set : cut(set);
+    int fb = 0, ft = 0, count = share ? 0 : cut(set + 1) - begin, before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int nt = tiles(b0), n = units(nt);
+      int incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
       const unsigned hit = __ballot_sync(0xffffffffu, before + incl > begin);
       if (hit) {
         const int l = __ffs(hit) - 1;
-        const int64_t at = __shfl_sync(0xffffffffu, before + incl - n, l);
+        const int at = __shfl_sync(0xffffffffu, before + incl - n, l);
+        const int its = __shfl_sync(0xffffffffu, nt, l);
         fb = b0 + l;
-        ft = static_cast<int>(begin - at);
-        found = true;
+        ft = (begin - at) * (share ? share : 1);
+        if (share) count = min(share, its - ft);
+        break;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) {
       ctrl->first_b = fb;
       ctrl->first_tile = ft;
-      ctrl->tiles = end - begin;
+      ctrl->tiles = count;
     }
   }
   tc_fence_before();
@@ -342,7 +360,7 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
   // Every role walks the same segments: the run's tiles of one request.
   int b = ctrl->first_b, it = ctrl->first_tile;
-  int64_t left = ctrl->tiles;
+  int left = ctrl->tiles;
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------------ TMA producer: lanes
@@ -360,7 +378,7 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         it = 0;
         continue;
       }
-      const int n = static_cast<int>(min(static_cast<int64_t>(nt - it), left));
+      const int n = min(nt - it, left);
       const int L = p.seq_lens[b];
       const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
       // pool row of this lane's page part of tile i; a part past the end, and an id outside the
@@ -422,7 +440,7 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         it = 0;
         continue;
       }
-      const int n = static_cast<int>(min(static_cast<int64_t>(nt - it), left));
+      const int n = min(nt - it, left);
       ok = __all_sync(0xffffffffu, mbar_wait(&ctrl->q_full, seg & 1, abort_flag));
       for (int i = 0; ok && i < n; ++i, ++t) {
         const int buf = t & 1;
@@ -481,7 +499,7 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         it = 0;
         continue;
       }
-      const int n = static_cast<int>(min(static_cast<int64_t>(nt - it), left));
+      const int n = min(nt - it, left);
       const int L = p.seq_lens[b];
       const int p0 = L - p.T;
       // both groups have read every S of the segment before: its products are complete, and
@@ -529,12 +547,7 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const int u = key - p0;  // draft index of this key (negative: prefix)
         const bool all = !any_dead && k0 + kTile <= p0;
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int c = 0; c < N; c += 16) {
-          uint32_t v[16], w[16];
-          tmem_ld16(s_tmem + c, v);
-          if (kE4m3) tmem_ld16(s_tmem + N + c, w);
-          tmem_ld_wait();
+        auto add16 = [&](int c, const uint32_t(&v)[16], const uint32_t(&w)[16]) {
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
             const float4 rc = *reinterpret_cast<const float4*>(&ctrl->row[c + k]);
@@ -557,6 +570,18 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             acc[(k >> 1) & 1] += e0;
             acc[2 + ((k >> 1) & 1)] += e1;
           }
+        };
+#pragma unroll 1
+        for (int c = 0; c < N; c += 32) {  // two loads of 16 columns a wait
+          uint32_t v[2][16], w[2][16];
+          const bool two = c + 16 < N;
+          tmem_ld16(s_tmem + c, v[0]);
+          if (kE4m3) tmem_ld16(s_tmem + N + c, w[0]);
+          if (two) tmem_ld16(s_tmem + c + 16, v[1]);
+          if (kE4m3 && two) tmem_ld16(s_tmem + N + c + 16, w[1]);
+          tmem_ld_wait();
+          add16(c, v[0], w[0]);
+          if (two) add16(c + 16, v[1], w[1]);
         }
         tc_fence_before();
         __syncwarp();
@@ -637,7 +662,7 @@ cudaError_t launch_mma(KeyMassParams p, const CUtensorMap& tm_q, const CUtensorM
   p.groups = s.groups;
   p.stages = s.stages;
   // one CTA per SM, and no more sets than tiles
-  const int64_t tiles = static_cast<int64_t>(p.B) * ((p.max_seq + kTile - 1) / kTile);
+  const int64_t tiles = static_cast<int64_t>(p.B) * ((p.max_seq + kTile - 1) / kTile);  // (below 2^31: the caller)
   p.sets = static_cast<int>(std::min(static_cast<int64_t>(std::max(1, num_sms / s.groups)), tiles));
   e = launch_dependent(key_mass_mma_kernel<kE4m3>, dim3(p.sets * s.groups), kMmaThreads, s.smem, stream, tm_q, tm_kv, p);
   if (e != cudaSuccess || s.groups == 1) return e;

@@ -18,6 +18,14 @@ __device__ __forceinline__ uint64_t tree_tile_bits(uint64_t mask, int p0, int k0
 // The T low bits.
 __device__ __forceinline__ uint64_t draft_bits(int T) { return T >= 64 ? ~0ull : (1ull << T) - 1; }
 
+// An output value as the bits it is staged in: bf16, or f16 for a split partial of a tree
+// (an 8-bit pool's, in units of its codes).
+template <bool kTree>
+__device__ __forceinline__ uint32_t out_bits(float v, bool final_out) {
+  if (kTree && !final_out) return __half_as_ushort(__float2half_rn(v));
+  return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
 // bf16 pairs with infinities and NaNs replaced by zero.  A draft that a row does not see
 // has weight 0 there, but 0 times an infinity or NaN is NaN; rows that do see it have a
 // score that is not finite already, so its value row no longer matters to them.

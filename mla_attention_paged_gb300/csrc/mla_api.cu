@@ -106,6 +106,7 @@ std::unordered_map<std::string, mla_decode_plan_t> g_plan_cache;
 // first tiles' latency) and the epilogue take about as long.
 constexpr long long kCombineTiles = 2;
 long long cta_fixed_tiles(int kv_dtype) { return kv_dtype == MLA_KV_E4M3 ? 10 : 3; }
+constexpr long long kPairFixedTiles = 8;  // (a pair takes about half as long for a tile)
 
 // Launch order of a multi-wave plan: split by split (every request's split s before any
 // split s + 1, so that short remainders go last) for one row group; request by request
@@ -336,7 +337,11 @@ int make_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads,
   pl.num_sms = num_sms;
   pl.rows = q_len * num_heads;
   pl.head_groups = (pl.rows + kGroupRows - 1) / kGroupRows;
-  const int ct = choose_chunk_tiles(lens, pl.head_groups, num_sms, cta_fixed_tiles(kv_dtype));
+  // a tree over a bf16 pool with more than 32 rows runs on pairs of CTAs (and SMs)
+  const bool pairs = tree && kv_dtype == MLA_KV_BF16 && pl.rows > 32;
+  const int groups = pairs ? tree_pair_groups(pl.rows) : pl.head_groups;
+  const int units = pairs ? std::max(1, num_sms / 2) : num_sms;
+  const int ct = choose_chunk_tiles(lens, groups, units, pairs ? kPairFixedTiles : cta_fixed_tiles(kv_dtype));
   pl.chunk_tokens = ct * kTileKeys;
   pl.max_seq_len = max_len;
   pl.max_splits = (max_len + pl.chunk_tokens - 1) / pl.chunk_tokens;
@@ -345,7 +350,7 @@ int make_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads,
     // more CTAs with work than SMs, one row group: launch split by split, as the cost model assumed
     long long n_ctas = 0;
     for (int L : lens) n_ctas += (L + pl.chunk_tokens - 1) / pl.chunk_tokens;
-    pl.split_major = (n_ctas * pl.head_groups > num_sms && split_major_order(pl.head_groups)) ? 1 : 0;
+    pl.split_major = (n_ctas * groups > units && split_major_order(groups)) ? 1 : 0;
   }
   pl.workspace_bytes = partial_bytes(pl, tree);
   {
@@ -411,6 +416,7 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
   unsigned* status = status_ptr();
   if (!status) return MLA_ERR_CUDA;
 
+  const bool pairs = tree_mask && plan->kv_dtype == MLA_KV_BF16 && plan->rows > 32;
   const uint64_t row_bytes = kLatentDim * 2;
   // Latent rows are viewed as [rows][9 blocks][64 columns] (block stride 128 bytes), so one
   // 3-D box {64 columns, n rows, 9 blocks} lands a whole row range as the nine 128-byte
@@ -420,7 +426,7 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
   if (partial) {
     const uint64_t dims[3] = {64, static_cast<uint64_t>(plan->batch) * plan->rows, kLatentDim / 64};
     const uint64_t strides[2] = {row_bytes, 128};
-    const uint32_t box[3] = {64, static_cast<uint32_t>(kGroupRows), kLatentDim / 64};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(pairs ? tree_pair_rows(plan->rows) : kGroupRows), kLatentDim / 64};
     if (!make_map(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box)) return MLA_ERR_CUDA;
   }
   memset(&tm_kv, 0, sizeof tm_kv);
@@ -442,7 +448,27 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
         return MLA_ERR_CUDA;
     }
   }
-  if (partial && plan->kv_dtype == MLA_KV_BF16) {  // int8 pages are read row by row by the decode warps
+  CUtensorMap tm_v;
+  memset(&tm_v, 0, sizeof tm_v);
+  if (partial && pairs) {
+    // K boxes: half a tile's keys, all nine column blocks; V boxes: a tile's keys, the four
+    // blocks of one CTA's value columns; pages below 64 keys: one (page part, block) at a time
+    const uint64_t rows = static_cast<uint64_t>(plan->num_pages) * plan->page_size;
+    if (plan->page_size >= kTileKeys) {
+      const uint64_t dims[3] = {64, rows, kLatentDim / 64};
+      const uint64_t strides[2] = {row_bytes, 128};
+      const uint32_t box_k[3] = {64, kTileKeys / 2, kLatentDim / 64}, box_v[3] = {64, kTileKeys, kValueDim / 128};
+      if (!make_map(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, kv_pages, dims, strides, box_k) ||
+          !make_map(&tm_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, kv_pages, dims, strides, box_v))
+        return MLA_ERR_CUDA;
+    } else {
+      const uint64_t dims[2] = {static_cast<uint64_t>(kLatentDim), rows};
+      const uint64_t strides[1] = {row_bytes};
+      const uint32_t box[2] = {64, static_cast<uint32_t>(std::min(plan->page_size, kTileKeys / 2))};
+      if (!make_map(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_pages, dims, strides, box)) return MLA_ERR_CUDA;
+      tm_v = tm_kv;
+    }
+  } else if (partial && plan->kv_dtype == MLA_KV_BF16) {  // int8 pages are read row by row by the decode warps
     const uint64_t rows = static_cast<uint64_t>(plan->num_pages) * plan->page_size;
     if (plan->page_size >= kTileKeys) {  // a 64-key tile is one row range of one page
       const uint64_t dims[3] = {64, rows, kLatentDim / 64};
@@ -495,7 +521,9 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (partial) {
     if (g_prof_start && record_event(g_prof_start, s) != cudaSuccess) return MLA_ERR_CUDA;
-    if (launch_decode_partial(p, tm_q, tm_kv, plan->head_groups, s) != cudaSuccess) return MLA_ERR_CUDA;
+    if ((pairs ? launch_decode_tree_pair(p, tm_q, tm_kv, tm_v, s)
+               : launch_decode_partial(p, tm_q, tm_kv, plan->head_groups, s)) != cudaSuccess)
+      return MLA_ERR_CUDA;
     if (g_prof_stop && record_event(g_prof_stop, s) != cudaSuccess) return MLA_ERR_CUDA;
   }
   if ((stages & kStageCombine) && plan->max_splits > 1) {

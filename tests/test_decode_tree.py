@@ -42,12 +42,16 @@ def _raw(mla, plan, **kw):
     return mla.lib.mla_decode_tree(ctypes.byref(plan), *a.values(), None)
 
 
-def test_tree_plan_sizes_fp32_partials(mla):
-    tree, chain = _plan(mla), mla.decode_plan([9000, 300], 4, 16, 64, 200, 400, 0, 152)
-    assert tree.max_splits == chain.max_splits > 1 and tree.chunk_tokens == chain.chunk_tokens
-    parts = 2 * tree.max_splits * 64
-    assert tree.workspace_bytes == 256 + parts * 512 * 4 + parts * 4
-    assert chain.workspace_bytes == 256 + parts * 512 * 2 + parts * 4
+@pytest.mark.parametrize("kv,width", [(0, 4), (1, 2), (2, 2), (3, 2)])
+@pytest.mark.parametrize("T", [1, 2, 4, 20])
+def test_tree_plan_sizes_its_partials(mla, kv, width, T):
+    """fp32 rows over a bf16 pool, 16-bit rows over 8-bit ones; narrow trees split as mla_decode."""
+    tree, chain = _plan(mla, T=T, kv=kv), mla.decode_plan([9000, 300], T, 16, 64, 200, 400, kv, 152)
+    assert tree.max_splits > 1 and tree.rows == 16 * T
+    parts = 2 * tree.max_splits * 16 * T
+    assert tree.workspace_bytes == 256 + parts * 512 * width + parts * 4
+    if kv or T <= 2:
+        assert (tree.max_splits, tree.chunk_tokens) == (chain.max_splits, chain.chunk_tokens)
 
 
 @pytest.mark.parametrize("bad,code", [

@@ -40,6 +40,7 @@ constexpr int kRound = 128;            // keys of a warp's round: four consecuti
 constexpr int kMaxCached = 48 * 1024;  // images a CTA keeps in shared memory; longer shares are read again
 constexpr int kOneCtaKeys = 8192;      // up to this length a request has one CTA
 constexpr int kCopyWarps = 8;
+constexpr int kLanePieces = 9;         // 16-byte pieces a lane copies
 
 // Order-preserving image of a mass: larger mass, larger image; NaN below everything.
 __device__ __forceinline__ uint32_t mass_key(float m) {
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const EvictPa
 // kChunks: 16-byte pieces of a row (72 of bf16, 36 of 8-bit codes).
 template <int kChunks>
 __global__ void __launch_bounds__(32 * kCopyWarps) kv_copy_kernel(const EvictParams p) {
-  constexpr int kRows = 288 / kChunks;  // rows a warp copies: 9 pieces a lane
+  constexpr int kRows = 32 * kLanePieces / kChunks;  // rows a warp copies
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.y;
   const int lane = threadIdx.x & 31;
@@ -276,18 +277,18 @@ __global__ void __launch_bounds__(32 * kCopyWarps) kv_copy_kernel(const EvictPar
     }
   }
   uint4* pool = reinterpret_cast<uint4*>(p.kv_pages);
-  uint4 v[9];
+  uint4 v[kLanePieces];
 #pragma unroll
-  for (int k = 0; k < 9; ++k) {
+  for (int k = 0; k < kLanePieces; ++k) {
     const int c = lane + 32 * k;
     const int64_t s = __shfl_sync(0xffffffffu, src, c / kChunks);
     if (s >= 0) v[k] = __ldcs(pool + s + c % kChunks);
   }
 #pragma unroll
-  for (int k = 0; k < 9; ++k) {
+  for (int k = 0; k < kLanePieces; ++k) {
     const int c = lane + 32 * k;
     const int64_t d = __shfl_sync(0xffffffffu, dst, c / kChunks);
-    if (d >= 0) pool[d + c % kChunks] = v[k];
+    if (d >= 0) __stcs(pool + d + c % kChunks, v[k]);
   }
 }
 
@@ -333,7 +334,7 @@ cudaError_t launch_kv_evict(const EvictParams& params, cudaStream_t stream) {
                 : launch_dependent(kv_select_kernel<kCluster>, dim3(p.B * kCluster), kSelectThreads, p.cached * 4, kCluster,
                                    p, stream);
   if (e != cudaSuccess || p.max_keep == 0) return e;
-  const int rows = (p.row_bytes == 2 * kLatentDim ? 4 : 8) * kCopyWarps;
+  const int rows = 32 * kLanePieces / (p.row_bytes / 16) * kCopyWarps;
   const dim3 grid((p.max_keep + rows - 1) / rows, p.B);
   return p.row_bytes == 2 * kLatentDim ? launch_dependent(kv_copy_kernel<72>, grid, 32 * kCopyWarps, 0, 1, p, stream)
                                        : launch_dependent(kv_copy_kernel<36>, grid, 32 * kCopyWarps, 0, 1, p, stream);

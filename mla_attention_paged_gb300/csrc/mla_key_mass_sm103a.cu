@@ -126,7 +126,6 @@ constexpr int kLoadWarp = kEpiWarps;
 constexpr int kMmaWarp = kEpiWarps + 1;
 constexpr int kMmaThreads = 32 * (kEpiWarps + 2);
 constexpr uint32_t kTmemCols = 512;               // two S buffers of up to 256 columns
-constexpr int kNeverSees = -2147483647 - 1;       // draft index of a row that adds nothing
 
 // Column blocks per ring stage: one bf16 block is 16 KB; e4m3 blocks are 8 KB and two MMAs
 // each, so three share a barrier.
@@ -146,10 +145,10 @@ struct MassCtrl {
   int abort_flag;
   int first_b, first_tile;   // where this CTA's run of tiles begins
   int tiles;                 // and its length
-  int any_dead;              // some of the segment's rows add nothing
   alignas(16) float2 row[kMaxRows];      // scale of the row's scores and its -lse, log2 domain
-  alignas(16) uint64_t mask[kMaxRows];   // trees: the drafts the row sees
-  int draft[kMaxRows];                   // the row's draft, or kNeverSees
+  uint64_t mask[kMaxTreeDrafts];         // trees: what each of the group's drafts sees
+  alignas(16) int draft[kMaxRows];       // the row's draft (trees: from the group's first on)
+  uint32_t live[kMaxRows / 32];          // a bit per row that adds something
 };
 constexpr int kCtrlBytes = 4096;
 static_assert(sizeof(MassCtrl) <= kCtrlBytes, "control block");
@@ -274,7 +273,6 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     }
     mbar_init(&ctrl->drain, 1);
     ctrl->abort_flag = 0;
-    ctrl->any_dead = 0;
     fence_mbarrier_init();
   }
   if (warp == kMmaWarp) {
@@ -297,8 +295,10 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   if (warp == 0) {
     // This CTA's run.  Equal runs, tiles [total set / sets, total (set + 1) / sets) of the batch,
     // may cross from one request into the next, which costs a CTA the new queries and a drained
-    // pipe (10 us on an e4m3 pool, whose queries are split); runs of whole shares of one
-    // request, c tiles each, are taken instead where they are at most two tiles longer.
+    // pipe: about a tile's time, on an e4m3 pool, whose queries are split, three.  Runs of whole
+    // shares of one request, c tiles each, are taken instead where they are no longer than that
+    // (8 requests of 2K-16K e4m3 keys: 24.7 -> 19.0 us; 16 of 8K-131K bf16 keys keep equal
+    // runs: 191 us against 199).
     const int mine = lane < p.B ? tiles_of(lane) : 0;  // (the first 32 requests stay in registers)
     auto tiles = [&](int b0) { return b0 == 0 ? mine : (b0 + lane < p.B ? tiles_of(b0 + lane) : 0); };
     auto sum_of = [&](auto&& f) {
@@ -312,7 +312,7 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const int total = sum_of([](int n) { return n; });
     const int even = (total + p.sets - 1) / p.sets;
     int share = 0;  // tiles of a whole share, or 0: equal runs
-    for (int c = even; c > 0 && c <= even + 2; ++c)
+    for (int c = even; c > 0 && c <= even + (kE4m3 ? 3 : 1); ++c)
       if (sum_of([c](int n) { return (n + c - 1) / c; }) <= p.sets) {
         share = c;
         break;
@@ -505,23 +505,23 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       // both groups have read every S of the segment before: its products are complete, and
       // Q and the rows' data may be replaced
       if (bar_or(1, kEpiThreads, fail || *abort_flag != 0)) break;
-      if (threadIdx.x == 0) ctrl->any_dead = 0;
       if (!kE4m3 && threadIdx.x == 0) {
         mbar_arrive_expect_tx(&ctrl->q_full, N * kLatentDim * 2);
         tma_load_3d(q_s, &tm_q, &ctrl->q_full, 0, b * p.R + row0, 0, policy_evict_last());
       }
-      named_bar_sync(1, kEpiThreads);
-      for (int r = threadIdx.x; r < N; r += kEpiThreads) {
-        const bool real = r < nrows;
-        const int64_t at = static_cast<int64_t>(b) * p.R + row0 + r;
-        const float lse = real ? p.lse[at] : INFINITY;
+      if (warp < kMaxRows / 32) {  // a thread per row
+        const int r = threadIdx.x;
+        const float lse = r < nrows ? p.lse[static_cast<int64_t>(b) * p.R + row0 + r] : INFINITY;
         const bool live = fabsf(lse) < INFINITY;  // (false for NaN)
-        const int draft = (row0 + r) / p.H;
-        if (!live) ctrl->any_dead = 1;
-        ctrl->draft[r] = live ? draft : kNeverSees;
-        ctrl->mask[r] = live && p.tree_mask ? p.tree_mask[static_cast<int64_t>(b) * p.T + draft] & draft_bits(p.T) : 0;
-        if (!kE4m3) ctrl->row[r] = make_float2(p.scale_log2, live ? -lse * 1.4426950408889634f : 0.f);
-        else ctrl->row[r].y = live ? -lse * 1.4426950408889634f : 0.f;
+        const unsigned word = __ballot_sync(0xffffffffu, live);
+        if (lane == 0) ctrl->live[warp] = word;
+        ctrl->draft[r] = (row0 + r) / p.H - (p.tree_mask ? row0 / p.H : 0);
+        const float neg_lse = live ? -lse * 1.4426950408889634f : 0.f;
+        if (kE4m3) ctrl->row[r].y = neg_lse;
+        else ctrl->row[r] = make_float2(p.scale_log2, neg_lse);
+      } else if (p.tree_mask) {  // a thread per draft of the group
+        const int t = row0 / p.H + threadIdx.x - kMaxRows;
+        if (t * p.H < row0 + nrows) ctrl->mask[t - row0 / p.H] = p.tree_mask[static_cast<int64_t>(b) * p.T + t] & draft_bits(p.T);
       }
       if (kE4m3) {
         split_rows(p.q + (static_cast<int64_t>(b) * p.R + row0) * kLatentDim, smem_u32(q_s), N, nrows, warp, lane,
@@ -531,7 +531,8 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         if (lane == 0) mbar_arrive(&ctrl->q_full);
       }
       named_bar_sync(1, kEpiThreads);
-      const bool any_dead = ctrl->any_dead != 0;
+      bool all_live = true;
+      for (int r = 0; r < N; r += 16) all_live &= ((ctrl->live[r >> 5] >> (r & 31)) & 0xffffu) == 0xffffu;
       for (int i = 0; i < n; ++i, ++t) {
         if ((t & 1) != mine || fail) continue;
         const int k0 = (it + i) * kTile;
@@ -545,30 +546,47 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         tc_fence_after();
         const uint32_t s_tmem = tmem + lane_base + mine * s_cols;
         const int u = key - p0;  // draft index of this key (negative: prefix)
-        const bool all = !any_dead && k0 + kTile <= p0;
+        const bool all = all_live && k0 + kTile <= p0;
+        // trees: the group's drafts that see this key, a bit each
+        uint64_t seers = ~0ull;
+        if (!all && p.tree_mask && u >= 0) {
+          seers = 0;
+          const int drafts = (row0 + nrows - 1) / p.H - row0 / p.H + 1;
+          if (u < p.T)
+            for (int d = 0; d < drafts; ++d) seers |= ((ctrl->mask[d] >> u) & 1ull) << d;
+        }
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
         auto add16 = [&](int c, const uint32_t(&v)[16], const uint32_t(&w)[16]) {
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
+          auto weights = [&](int k, float& e0, float& e1) {
             const float4 rc = *reinterpret_cast<const float4*>(&ctrl->row[c + k]);
             float s0 = __uint_as_float(v[k]), s1 = __uint_as_float(v[k + 1]);
             if (kE4m3) {
               s0 += __uint_as_float(w[k]);
               s1 += __uint_as_float(w[k + 1]);
             }
-            float e0 = ex2_approx(fmaf(s0, rc.x, rc.y)), e1 = ex2_approx(fmaf(s1, rc.z, rc.w));
-            if (!all) {
-              const int d0 = ctrl->draft[c + k], d1 = ctrl->draft[c + k + 1];
-              bool v0 = u <= d0, v1 = u <= d1;  // (a prefix key is seen by every row that adds anything)
-              if (p.tree_mask && u >= 0) {
-                v0 = u < 64 && ((ctrl->mask[c + k] >> u) & 1);
-                v1 = u < 64 && ((ctrl->mask[c + k + 1] >> u) & 1);
-              }
-              e0 = v0 ? e0 : 0.f;
-              e1 = v1 ? e1 : 0.f;
+            e0 = ex2_approx(fmaf(s0, rc.x, rc.y));
+            e1 = ex2_approx(fmaf(s1, rc.z, rc.w));
+          };
+          if (all) {
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float e0, e1;
+              weights(k, e0, e1);
+              acc[(k >> 1) & 1] += e0;
+              acc[2 + ((k >> 1) & 1)] += e1;
             }
-            acc[(k >> 1) & 1] += e0;
-            acc[2 + ((k >> 1) & 1)] += e1;
+          } else {
+            const uint32_t live = ctrl->live[c >> 5] >> (c & 31);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float e0, e1;
+              weights(k, e0, e1);
+              const int2 d = *reinterpret_cast<const int2*>(&ctrl->draft[c + k]);
+              const bool see0 = p.tree_mask ? (seers >> (d.x & 63)) & 1 : u <= d.x;
+              const bool see1 = p.tree_mask ? (seers >> (d.y & 63)) & 1 : u <= d.y;
+              acc[(k >> 1) & 1] += see0 && ((live >> k) & 1) ? e0 : 0.f;
+              acc[2 + ((k >> 1) & 1)] += see1 && ((live >> (k + 1)) & 1) ? e1 : 0.f;
+            }
           }
         };
 #pragma unroll 1

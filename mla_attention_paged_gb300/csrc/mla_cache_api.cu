@@ -107,7 +107,7 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
 
 int mla_key_mass_workspace(const mla_decode_plan_t* plan, size_t* bytes_out) {
   if (!plan || !bytes_out) return MLA_ERR_INVALID_ARG;
-  *bytes_out = key_mass_part_bytes(plan->kv_dtype, plan->batch, plan->rows, plan->max_seq_len);
+  *bytes_out = key_mass_part_bytes(plan->batch, plan->rows, plan->max_seq_len);
   return MLA_OK;
 }
 
@@ -172,10 +172,11 @@ int mla_key_mass(const mla_decode_plan_t* plan, const void* q, const void* kv_pa
     if (!make_map(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box) ||
         !make_map(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_pages, kv_dims, kv_strides, box_kv))
       return MLA_ERR_CUDA;
-  } else if (plan->kv_dtype == MLA_KV_E4M3) {
+  } else {
     const uint64_t kv_dims[2] = {kLatentDim, pool_rows};
     const uint64_t kv_strides[1] = {kLatentDim};
-    if (!make_map(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, kv_pages, kv_dims, kv_strides, box_kv, CU_TENSOR_MAP_SWIZZLE_64B))
+    if (!make_map(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, kv_pages, kv_dims, kv_strides, box_kv,
+                  plan->kv_dtype == MLA_KV_E4M3 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE))
       return MLA_ERR_CUDA;
   }
   return launch_key_mass(p, tm_q, tm_kv, plan->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK

@@ -141,7 +141,7 @@ struct KeyMassParams {
   float* mass;                  // row b at b * mass_stride
   int64_t mass_stride;
   float* part;                  // row groups' sums [groups, B, max_seq] (more than one group)
-  int group_rows, groups, sets, stages;  // launch shape (launch_key_mass)
+  int group_rows, groups, sets, stages, raw_stages;  // launch shape (launch_key_mass)
   unsigned* status;
 };
 
@@ -156,11 +156,11 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 inline bool page_size_ok(int P) { return P == 8 || P == 16 || P == 32 || P == 64 || P == 128 || P == 256; }
 
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
-// tm_q / tm_kv: bf16 and e4m3 pools only.
+// tm_q: bf16 pools only.
 cudaError_t launch_key_mass(const KeyMassParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv, int num_sms,
                             cudaStream_t stream);
 int key_mass_group_rows(int R);  // query rows a CTA holds: the height of tm_q's box
-size_t key_mass_part_bytes(int kv_dtype, int B, int R, int max_seq);  // scratch of KeyMassParams::part
+size_t key_mass_part_bytes(int B, int R, int max_seq);  // scratch of KeyMassParams::part
 cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t stream);
 
 // Decode: split-KV partial kernel (tensor maps over q and the latent pool).

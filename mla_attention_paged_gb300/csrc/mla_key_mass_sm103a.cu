@@ -7,8 +7,8 @@
 // with the visibility of mla_decode (draft t sees keys 0 .. L_b - T + t) or, with tree masks,
 // of mla_decode_tree.  A row whose lse is not finite adds nothing.
 //
-// bf16 and e4m3 pools: key_mass_mma_kernel.  What has to be read is the keys, once; so it is
-// bound by memory while a request has few rows, and by the first product with many.
+// What has to be read is the keys, once; so it is bound by memory while a request has few rows,
+// and by the product with many.
 //  * S^T = K . Q^T on the tensor cores (tcgen05, M = 128 keys, N = up to 128 query rows): a
 //    key is a TMEM lane, so its weights lie in one thread's columns and their sum needs no
 //    exchange between threads; the result is stored without atomics, in a fixed order.
@@ -21,15 +21,14 @@
 //    more than 128 rows run in row groups side by side, whose sums a second kernel adds up.
 //  * Two groups of four warps take alternate tiles from two S buffers, so exponentials
 //    (R per key) run beside the next tile's product.
-//
-// int8 pools: key_mass_kernel, one CTA per (32 keys, request), the keys decoded to fp32 in
-// shared memory, 16 query rows at a time beside them; a thread owns one key and every fourth
-// row, and the four threads of a key add their sums in a fixed order.
+//  * int8 pools: the codes arrive by TMA in a ring of their own; six warps write them into the
+//    K ring as f16, exactly; Q is converted to f16.  A page's scale multiplies its keys' scores.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
 
+#include "kv8_decode.cuh"
 #include "mla_internal.h"
 #include "sm103a_ptx.cuh"
 #include "tree_mask.cuh"
@@ -37,84 +36,6 @@
 namespace mla {
 namespace {
 
-constexpr int kKeys = 32;
-constexpr int kRows = 16;
-constexpr int kThreads = 128;
-constexpr int kPitch = kLatentDim + 1;  // odd: a warp's 32 keys fall in 32 banks
-constexpr int kSmemBytes = (kKeys * kPitch + kRows * kLatentDim + kThreads) * 4;
-
-
-template <int kKv>
-__global__ void __launch_bounds__(kThreads) key_mass_kernel(const KeyMassParams p) {
-  extern __shared__ float sm[];
-  float* ks = sm;                       // [32][577]
-  float* qs = ks + kKeys * kPitch;      // [16][576]
-  float* part = qs + kRows * kLatentDim;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int b = blockIdx.y;
-  const int L = p.seq_lens[b];
-  const int k0 = blockIdx.x * kKeys;
-  if (L < p.T || L > p.max_seq || L > static_cast<int64_t>(p.max_pages) * p.page_size) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(p.status, kStatusDeviceArg);
-    return;
-  }
-  if (k0 >= L) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = warp; i < kKeys; i += kThreads / 32) {
-    const int j = k0 + i;
-    const uint8_t* row = nullptr;
-    float mult = 1.f;
-    if (j < L) {
-      const int64_t page = p.page_table[static_cast<int64_t>(b) * p.max_pages + j / p.page_size];
-      if (page < 0 || page >= p.num_pages) {
-        if (lane == 0) atomicOr(p.status, kStatusDeviceArg);
-      } else {
-        row = p.kv_pool + (page * p.page_size + j % p.page_size) * kLatentDim;
-        if (kKv == kKvInt8Page) mult = p.page_scales[page] * p.inv_ref_scale;
-      }
-    }
-    for (int c = lane; c < kLatentDim; c += 32) ks[i * kPitch + c] = row ? static_cast<float>(static_cast<int8_t>(row[c])) * mult : 0.f;
-  }
-  const int key = k0 + lane;
-  const int u = key - (L - p.T);  // draft index of this key (negative: prefix)
-  float total = 0.f;
-  for (int r0 = 0; r0 < p.R; r0 += kRows) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kRows * kLatentDim; i += kThreads) {
-      const int r = r0 + i / kLatentDim;
-      qs[i] = r < p.R ? __bfloat162float(p.q[(static_cast<int64_t>(b) * p.R + r) * kLatentDim + i % kLatentDim]) : 0.f;
-    }
-    __syncthreads();
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    const float* kr = ks + lane * kPitch;
-    for (int c = 0; c < kLatentDim; ++c) {
-      const float k = kr[c];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = fmaf(k, qs[(warp + 4 * i) * kLatentDim + c], s[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + warp + 4 * i;
-      if (r >= p.R) continue;
-      const int t = r / p.H;
-      const bool seen = u < 0 || (p.tree_mask ? (u < p.T && ((p.tree_mask[static_cast<int64_t>(b) * p.T + t] >> u) & 1))
-                                              : u <= t);
-      const float lse = p.lse[static_cast<int64_t>(b) * p.R + r];
-      if (seen && fabsf(lse) < INFINITY) total += ex2_approx(fmaf(s[i], p.scale_log2, -lse * 1.4426950408889634f));
-    }
-  }
-  part[threadIdx.x] = total;
-  __syncthreads();
-  if (warp == 0 && key < L) {
-    const float sum = (part[lane] + part[32 + lane]) + (part[64 + lane] + part[96 + lane]);
-    float* m = p.mass + static_cast<int64_t>(b) * p.mass_stride + key;
-    *m = p.decay == 0.f ? sum : fmaf(p.decay, *m, sum);
-  }
-}
-
-// ----------------------------------------------------------------------------------------
-// bf16 and e4m3 pools
-// ----------------------------------------------------------------------------------------
 constexpr int kTile = 128;                        // keys per tile (MMA M, TMEM lanes)
 constexpr int kDimBlocks = kLatentDim / 64;       // 9 blocks of 64 columns
 constexpr int kMaxRows = 128;                     // query rows a CTA holds (MMA N; e4m3: 2 x)
@@ -124,20 +45,24 @@ constexpr int kEpiWarps = 2 * kGroupWarps;
 constexpr int kEpiThreads = 32 * kEpiWarps;
 constexpr int kLoadWarp = kEpiWarps;
 constexpr int kMmaWarp = kEpiWarps + 1;
-constexpr int kMmaThreads = 32 * (kEpiWarps + 2);
+constexpr int kDecodeWarps = 6;                   // int8: the warps after kMmaWarp
+constexpr int threads_for(int kv) { return 32 * (kEpiWarps + 2 + (kv >= kKvInt8 ? kDecodeWarps : 0)); }
+constexpr int kRawBytes = kTile * 64;             // int8: one column block of a tile as codes
 constexpr uint32_t kTmemCols = 512;               // two S buffers of up to 256 columns
 
-// Column blocks per ring stage: one bf16 block is 16 KB; e4m3 blocks are 8 KB and two MMAs
+// Column blocks per ring stage: a 16-bit block is 16 KB; e4m3 blocks are 8 KB and two MMAs
 // each, so three share a barrier.
-template <bool kE4m3>
-constexpr int kStageBlocks = kE4m3 ? 3 : 1;
-template <bool kE4m3>
-constexpr int kStageBytes = kTile * 64 * (kE4m3 ? 1 : 2) * kStageBlocks<kE4m3>;
+template <int kKv>
+constexpr int kStageBlocks = kKv == kKvE4m3 ? 3 : 1;
+template <int kKv>
+constexpr int kStageBytes = kTile * 64 * (kKv == kKvE4m3 ? 1 : 2) * kStageBlocks<kKv>;
 
 struct MassCtrl {
   uint64_t q_full;
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
+  uint64_t raw_full[kMaxStages];   // int8: codes landed
+  uint64_t raw_empty[kMaxStages];  // int8: codes written to the K ring
   uint64_t s_full[2];
   uint64_t s_free[2];
   uint64_t drain;
@@ -157,17 +82,23 @@ constexpr int kMaxSmem = 232448;
 // The shared memory a launch takes: alignment slack, control, Q (N rows x 1152 bytes in either
 // format), and as many ring stages as fit.
 struct MassShape {
-  int rows, groups, stages, smem;
+  int rows, groups, stages, raw_stages, smem;
 };
-template <bool kE4m3>
+template <int kKv>
 MassShape mass_shape(int R) {
   MassShape s;
   s.groups = (R + kMaxRows - 1) / kMaxRows;
   s.rows = ((R + s.groups - 1) / s.groups + 15) / 16 * 16;  // even groups, a multiple of the MMA's N step
   s.groups = (R + s.rows - 1) / s.rows;
   const int left = kMaxSmem - 1024 - kCtrlBytes - s.rows * kLatentDim * 2;
-  s.stages = left / kStageBytes<kE4m3> < kMaxStages ? left / kStageBytes<kE4m3> : kMaxStages;
-  s.smem = 1024 + kCtrlBytes + s.rows * kLatentDim * 2 + s.stages * kStageBytes<kE4m3>;
+  s.raw_stages = 0;
+  if (kKv >= kKvInt8) {  // of what is left, somewhat less than half for the K ring
+    s.stages = std::min(6, left / (kStageBytes<kKv> + 5 * kRawBytes / 2));
+    s.raw_stages = std::min(kMaxStages, (left - s.stages * kStageBytes<kKv>) / kRawBytes);
+  } else {
+    s.stages = std::min(kMaxStages, left / kStageBytes<kKv>);
+  }
+  s.smem = 1024 + kCtrlBytes + s.rows * kLatentDim * 2 + s.stages * kStageBytes<kKv> + s.raw_stages * kRawBytes;
   return s;
 }
 
@@ -247,25 +178,46 @@ __device__ __forceinline__ void split_rows(const __nv_bfloat16* q, uint32_t q_sm
   }
 }
 
-template <bool kE4m3>
-__global__ void __launch_bounds__(kMmaThreads, 1)
-key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
-                    const KeyMassParams p) {
+// Query rows of an int8 launch as f16 (rows past `real` repeat the last one).
+__device__ __forceinline__ void half_rows(const __nv_bfloat16* q, uint32_t q_smem, int rows, int real, int warp, int lane) {
+  for (int r = warp; r < rows; r += kEpiWarps) {
+    const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<int64_t>(min(r, real - 1)) * kLatentDim);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int c = lane + 32 * i;  // chunk of eight columns, 72 in all
+      if (c >= kLatentDim / 8) break;
+      const uint4 w = __ldg(src + c);
+      st_shared_v4(q_smem + (c >> 3) * (rows * 128) + r * 128 + (((c ^ r) & 7) << 4), bf16x2_to_f16x2(w.x),
+                   bf16x2_to_f16x2(w.y), bf16x2_to_f16x2(w.z), bf16x2_to_f16x2(w.w));
+    }
+  }
+}
+
+template <int kKv>
+__global__ void __launch_bounds__(threads_for(kKv), 1)
+key_mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                const KeyMassParams p) {
+  constexpr bool kE4m3 = kKv == kKvE4m3, kInt8 = kKv == kKvInt8 || kKv == kKvInt8Page, kBf16 = kKv == kKvBf16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int N = p.group_rows;
   MassCtrl* ctrl = reinterpret_cast<MassCtrl*>(smem);
   uint8_t* q_s = smem + kCtrlBytes;                    // [9][N (e4m3: 2 N)][128 (64) bytes]
   uint8_t* ring = q_s + N * kLatentDim * 2;
+  uint8_t* raw = ring + p.stages * kStageBytes<kKv>;   // int8: codes, [128][64] a slot
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = blockIdx.x % p.groups, set = blockIdx.x / p.groups;
   const int row0 = group * N, nrows = min(N, p.R - row0);
 
   if (threadIdx.x == 0) {
-    mbar_init(&ctrl->q_full, kE4m3 ? kEpiWarps : 1);
+    mbar_init(&ctrl->q_full, kBf16 ? 1 : kEpiWarps);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&ctrl->full[s], 1);
       mbar_init(&ctrl->empty[s], 1);
+    }
+    for (int s = 0; s < p.raw_stages; ++s) {
+      mbar_init(&ctrl->raw_full[s], 1);
+      mbar_init(&ctrl->raw_empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctrl->s_full[i], 1);
@@ -280,7 +232,7 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     tmem_relinquish();
   }
   if (warp == kLoadWarp && lane == 0) {
-    if (!kE4m3) tma_prefetch_desc(&tm_q);
+    if (kBf16) tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_kv);
   }
   // programmatic dependent launch: no input is read before the previous kernel has completed
@@ -353,8 +305,8 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem_base;
   volatile int* abort_flag = &ctrl->abort_flag;
-  constexpr int kBlocksPerStage = kStageBlocks<kE4m3>;
-  constexpr int kStageB = kStageBytes<kE4m3>;
+  constexpr int kBlocksPerStage = kStageBlocks<kKv>;
+  constexpr int kStageB = kStageBytes<kKv>;
   constexpr int kBlockB = kStageB / kBlocksPerStage;
   const uint32_t s_cols = kE4m3 ? 2 * N : N;
 
@@ -365,6 +317,11 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------------ TMA producer: lanes
     // share the pieces (page part, column block) of a stage
+    uint64_t* const full = kInt8 ? ctrl->raw_full : ctrl->full;
+    uint64_t* const empty = kInt8 ? ctrl->raw_empty : ctrl->empty;
+    uint8_t* const into = kInt8 ? raw : ring;
+    const int stages = kInt8 ? p.raw_stages : p.stages;
+    constexpr int kLoadB = kInt8 ? kRawBytes : kStageB, kPieceB = kLoadB / kBlocksPerStage;
     const int P = p.page_size;
     const int parts = P >= kTile ? 1 : kTile / P, part_rows = kTile / parts;
     const uint64_t pol = p.groups == 1 ? policy_evict_first() : policy_evict_normal();
@@ -399,19 +356,19 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 #pragma unroll 1
         for (int c = 0; c < kDimBlocks; c += kBlocksPerStage) {
           bool w = true;
-          if (lane == 0 && issued >= p.stages) w = mbar_wait(&ctrl->empty[slot], phase ^ 1, abort_flag);
+          if (lane == 0 && issued >= stages) w = mbar_wait(&empty[slot], phase ^ 1, abort_flag);
           ok = __shfl_sync(0xffffffffu, w, 0);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&ctrl->full[slot], kStageB);
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], kLoadB);
           __syncwarp();
           if (lane < parts) {
-            uint8_t* dst = ring + slot * kStageB + lane * part_rows * (kBlockB / kTile);
+            uint8_t* dst = into + slot * kLoadB + lane * part_rows * (kPieceB / kTile);
 #pragma unroll
             for (int k = 0; k < kBlocksPerStage; ++k)
-              tma_load_2d(dst + k * kBlockB, &tm_kv, &ctrl->full[slot], (c + k) * 64, row, pol);
+              tma_load_2d(dst + k * kPieceB, &tm_kv, &full[slot], (c + k) * 64, row, pol);
           }
           ++issued;
-          if (++slot == p.stages) {
+          if (++slot == stages) {
             slot = 0;
             phase ^= 1;
           }
@@ -424,12 +381,54 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     if (__any_sync(0xffffffffu, bad_pid) && lane == 0) atomicOr(p.status, kStatusDeviceArg);
     if (!ok && lane == 0) {
       // copies still in flight land before the CTA exits: the last use of every stage
-      for (int u = max(0, issued - p.stages); u < issued; ++u) drain_wait(&ctrl->full[u % p.stages], (u / p.stages) & 1);
+      for (int u = max(0, issued - stages); u < issued; ++u) drain_wait(&full[u % stages], (u / stages) & 1);
+    }
+    __syncwarp();
+  } else if (kInt8 && warp > kMmaWarp) {
+    // ------------------------------------------------------------------ int8 codes into the K ring as
+    // f16: each warp takes every sixth (tile, column block).  (Reading the codes with loads
+    // instead, whole sectors from 64-byte pieces of rows, held the in-flight bytes to what L1
+    // can allocate: 313 us for 16 requests of 65536 keys and 32 rows where this takes 175.)
+    // No more warps than stages of either ring: a warp that starts block u has seen block u -
+    // warps filled and u - warps - stages consumed, so the parities it waits for are the right
+    // ones.
+    const int warps = min(kDecodeWarps, min(p.stages, p.raw_stages)), dw = warp - kMmaWarp - 1;
+    const int blocks = left * kDimBlocks;
+    bool ok = true;
+    for (int u = dw; ok && dw < warps && u < blocks; u += warps) {
+      const int rs = u % p.raw_stages, slot = u % p.stages, use = u / p.stages;
+      bool go = true;
+      if (lane == 0) {
+        go = mbar_wait(&ctrl->raw_full[rs], (u / p.raw_stages) & 1, abort_flag);
+        if (go && use > 0) go = mbar_wait(&ctrl->empty[slot], (use - 1) & 1, abort_flag);
+      }
+      ok = __shfl_sync(0xffffffffu, go, 0);
+      if (!ok) break;
+      // lane l: 16 codes, chunk l % 4 of rows l / 4 + 8 k
+      const uint32_t from = smem_u32(raw) + rs * kRawBytes + lane * 16;
+      const uint32_t to = smem_u32(ring) + slot * kStageB + (lane >> 2) * 128 + (lane & 3) * 32;
+      const int sw = (lane >> 2) << 4;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4 w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = ld_shared_v4(from + (8 * h + k) * 512);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) store_f16_chunk_int8(to + (8 * h + k) * 1024, sw, w[k]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctrl->full[slot]);
+        mbar_arrive(&ctrl->raw_empty[rs]);
+      }
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issuer
-    const uint32_t idesc = kE4m3 ? make_idesc_e4m3(kTile, 2 * N) : make_idesc_bf16(kTile, N, false, false);
+    const uint32_t idesc = kE4m3   ? make_idesc_e4m3(kTile, 2 * N)
+                           : kInt8 ? make_idesc_f16(kTile, N, false, false)
+                                   : make_idesc_bf16(kTile, N, false, false);
     const uint32_t q_block = N * 128;  // bytes of a column block of Q in either format
     bool ok = true;
     int slot = 0, phase = 0, t = 0, seg = 0;
@@ -505,7 +504,7 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       // both groups have read every S of the segment before: its products are complete, and
       // Q and the rows' data may be replaced
       if (bar_or(1, kEpiThreads, fail || *abort_flag != 0)) break;
-      if (!kE4m3 && threadIdx.x == 0) {
+      if (kBf16 && threadIdx.x == 0) {
         mbar_arrive_expect_tx(&ctrl->q_full, N * kLatentDim * 2);
         tma_load_3d(q_s, &tm_q, &ctrl->q_full, 0, b * p.R + row0, 0, policy_evict_last());
       }
@@ -522,6 +521,12 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       } else if (p.tree_mask) {  // a thread per draft of the group
         const int t = row0 / p.H + threadIdx.x - kMaxRows;
         if (t * p.H < row0 + nrows) ctrl->mask[t - row0 / p.H] = p.tree_mask[static_cast<int64_t>(b) * p.T + t] & draft_bits(p.T);
+      }
+      if (kInt8) {
+        half_rows(p.q + (static_cast<int64_t>(b) * p.R + row0) * kLatentDim, smem_u32(q_s), N, nrows, warp, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->q_full);
       }
       if (kE4m3) {
         split_rows(p.q + (static_cast<int64_t>(b) * p.R + row0) * kLatentDim, smem_u32(q_s), N, nrows, warp, lane,
@@ -541,6 +546,11 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                    : p.part + (static_cast<int64_t>(group) * p.B + b) * p.max_seq + key;
         const bool accumulate = p.groups == 1 && p.decay != 0.f && key < L;
         const float old = accumulate ? *out : 0.f;
+        float rel = 1.f;  // the scale of the key's page, relative to kv_scale
+        if (kKv == kKvInt8Page && key < L) {
+          const int pid = __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + key / p.page_size);
+          rel = pid >= 0 && pid < p.num_pages ? __ldg(p.page_scales + pid) * p.inv_ref_scale : 0.f;
+        }
         fail = __any_sync(0xffffffffu, !mbar_wait(&ctrl->s_full[mine], (t >> 1) & 1, abort_flag));
         if (fail) continue;
         tc_fence_after();
@@ -563,6 +573,10 @@ key_mass_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             if (kE4m3) {
               s0 += __uint_as_float(w[k]);
               s1 += __uint_as_float(w[k + 1]);
+            }
+            if (kKv == kKvInt8Page) {
+              s0 *= rel;
+              s1 *= rel;
             }
             e0 = ex2_approx(fmaf(s0, rc.x, rc.y));
             e1 = ex2_approx(fmaf(s1, rc.z, rc.w));
@@ -650,60 +664,45 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, in
 }
 
 template <int kKv>
-cudaError_t launch_simple(const KeyMassParams& p, cudaStream_t stream) {
+cudaError_t launch(KeyMassParams p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv, int num_sms, cudaStream_t stream) {
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(key_mass_kernel<kKv>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    e = cudaFuncSetAttribute(key_mass_kernel<kKv>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  return launch_dependent(key_mass_kernel<kKv>, dim3((p.max_seq + kKeys - 1) / kKeys, p.B), kThreads, kSmemBytes, stream, p);
-}
-
-template <bool kE4m3>
-cudaError_t launch_mma(KeyMassParams p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv, int num_sms,
-                       cudaStream_t stream) {
-  static thread_local int configured_device = -1;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (configured_device != dev) {
-    e = cudaFuncSetAttribute(key_mass_mma_kernel<kE4m3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e != cudaSuccess) return e;
-    configured_device = dev;
-  }
-  const MassShape s = mass_shape<kE4m3>(p.R);
+  const MassShape s = mass_shape<kKv>(p.R);
   p.group_rows = s.rows;
   p.groups = s.groups;
   p.stages = s.stages;
+  p.raw_stages = s.raw_stages;
   // one CTA per SM, and no more sets than tiles
   const int64_t tiles = static_cast<int64_t>(p.B) * ((p.max_seq + kTile - 1) / kTile);  // (below 2^31: the caller)
   p.sets = static_cast<int>(std::min(static_cast<int64_t>(std::max(1, num_sms / s.groups)), tiles));
-  e = launch_dependent(key_mass_mma_kernel<kE4m3>, dim3(p.sets * s.groups), kMmaThreads, s.smem, stream, tm_q, tm_kv, p);
+  e = launch_dependent(key_mass_kernel<kKv>, dim3(p.sets * s.groups), threads_for(kKv), s.smem, stream, tm_q, tm_kv, p);
   if (e != cudaSuccess || s.groups == 1) return e;
   return launch_dependent(key_mass_join_kernel, dim3((p.max_seq + 255) / 256, p.B), 256, 0, stream, p);
 }
 
 }  // namespace
 
-int key_mass_group_rows(int R) { return mass_shape<false>(R).rows; }
+int key_mass_group_rows(int R) { return mass_shape<kKvBf16>(R).rows; }
 
-size_t key_mass_part_bytes(int kv_dtype, int B, int R, int max_seq) {
-  if (kv_dtype != kKvBf16 && kv_dtype != kKvE4m3) return 0;
-  const int groups = mass_shape<false>(R).groups;
+size_t key_mass_part_bytes(int B, int R, int max_seq) {
+  const int groups = mass_shape<kKvBf16>(R).groups;
   return groups == 1 ? 0 : static_cast<size_t>(groups) * B * max_seq * sizeof(float);
 }
 
 cudaError_t launch_key_mass(const KeyMassParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv, int num_sms,
                             cudaStream_t stream) {
   switch (p.kv_dtype) {
-    case kKvE4m3: return launch_mma<true>(p, tm_q, tm_kv, num_sms, stream);
-    case kKvInt8: return launch_simple<kKvInt8>(p, stream);
-    case kKvInt8Page: return launch_simple<kKvInt8Page>(p, stream);
-    default: return launch_mma<false>(p, tm_q, tm_kv, num_sms, stream);
+    case kKvE4m3: return launch<kKvE4m3>(p, tm_q, tm_kv, num_sms, stream);
+    case kKvInt8: return launch<kKvInt8>(p, tm_q, tm_kv, num_sms, stream);
+    case kKvInt8Page: return launch<kKvInt8Page>(p, tm_q, tm_kv, num_sms, stream);
+    default: return launch<kKvBf16>(p, tm_q, tm_kv, num_sms, stream);
   }
 }
 

@@ -1,10 +1,13 @@
 // mla_decode_tree_sm103a.cu -- decode of a tree of drafted tokens over a paged bf16 latent
-// cache for requests of more than 32 folded rows, sm_103a.
+// cache for requests of more than 64 folded rows, sm_103a.
 //
 // What it computes (per request b, draft t, head h, folded row m = t*H + h):
 //   out[b,t,h,:] = sum_j softmax_j(scale * q[b,t,h,:] . k_j) * k_j[:512]
 // over the keys j < L - T and those drafts j = L - T + u whose bit u is set in the row's mask.
-// (At most 32 rows: decode_partial_narrow_kernel; 8-bit pools: the kernels of their formats.)
+// (Fewer rows: decode_partial_narrow_kernel and decode_partial_kernel, which are bound by reading
+// the cache; with half of its rows empty a pair spent twice the products and measured 272 us
+// against 262 on 16 requests of 8K-131K keys with 64 rows.  8-bit pools: the kernels of their
+// formats.)
 //
 // Why a kernel of its own.  An output row takes 512 fp32 accumulators, so an SM's tensor memory
 // (512 columns of 128 lanes) holds the output of 64 rows beside their scores.  One CTA with
@@ -24,8 +27,6 @@
 //  * Softmax: TMEM lane l holds row l % 64, keys 0-31 (l < 64) or 32-63 of the tile; warps w and
 //    w + 4 share a lane quadrant and take 16 of those keys each.  A row's four threads swap their
 //    maxima through shared memory (one barrier a tile).  Lazy rescale as in the other kernels.
-//  * Requests of 33-64 rows put up to 32 rows in each CTA; the shared memory that saves takes a
-//    third K stage.  They are bound by reading the cache.
 // Every wait is bounded; on expiry the CTA records a timeout, drains and returns.
 #include "mla_internal.h"
 #include "sm103a_ptx.cuh"
@@ -33,7 +34,6 @@
 
 namespace mla {
 
-int tree_pair_rows(int R) { return R <= 64 ? 32 : 64; }
 int tree_pair_groups(int R) { return (R + 127) / 128; }
 
 namespace {
@@ -46,8 +46,9 @@ constexpr int kVBlock = kTileKeys * 128;            // 8 KB
 constexpr int kVBlocks = kValueDim / 64 / 2;        // 4: a CTA's half of the value columns
 constexpr int kVBytes = kVBlocks * kVBlock;         // 32 KB
 constexpr int kPBytes = 64 * 128;                   // 64 rows x 64 keys
+constexpr int kKStages = 2;
 constexpr int kVStages = 2;
-constexpr int kMaxKStages = 3;
+constexpr int kRows = 64;                           // rows a CTA holds
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kLoadWarp = kSoftmaxWarps, kBmm1Warp = kLoadWarp + 1, kBmm2Warp = kLoadWarp + 2;
@@ -58,13 +59,13 @@ constexpr int kArrivals = 2 * kSoftmaxWarps;        // softmax warps of the pair
 struct PairCtrl {
   // counted in CTA 0 (loads and softmax warps of both CTAs)
   uint64_t q_full;
-  uint64_t k_full[kMaxKStages];
+  uint64_t k_full[kKStages];
   uint64_t v_full[kVStages];
   uint64_t s_free[2];
   uint64_t p_full;
   uint64_t drain1, drain2;
   // in both CTAs (commits arrive in both)
-  uint64_t k_empty[kMaxKStages];
+  uint64_t k_empty[kKStages];
   uint64_t v_empty[kVStages];
   uint64_t s_full[2];
   uint64_t o_done;
@@ -76,21 +77,15 @@ struct PairCtrl {
 constexpr int kCtrlBytes = 4096;
 static_assert(sizeof(PairCtrl) <= kCtrlBytes, "control block");
 
-// kRows: rows a CTA holds (64, or 32 for requests of at most 64 rows).
-template <int kRows>
-struct Shape {
-  static constexpr int kKStages = kRows == 64 ? 2 : 3;
-  static constexpr int kQBlock = kRows * 128;
-  static constexpr int kQBytes = kDimBlocks * kQBlock;
-  // Q | K ring | V ring | P | control.  (With 32 rows the MMA's other 32 A rows read what lies
-  // behind: their results are never used.)
-  static constexpr int kOffK = kQBytes;
-  static constexpr int kOffV = kOffK + kKStages * kKBytes;
-  static constexpr int kOffP = kOffV + kVStages * kVBytes;
-  static constexpr int kOffCtrl = kOffP + kPBytes;
-  static constexpr int kSmem = kOffCtrl + kCtrlBytes + 1024;
-  static_assert(kSmem <= 232448, "shared memory per block");
-};
+// Shared memory map: Q | K ring | V ring | P | control
+constexpr int kQBlock = kRows * 128;
+constexpr int kQBytes = kDimBlocks * kQBlock;
+constexpr int kOffK = kQBytes;
+constexpr int kOffV = kOffK + kKStages * kKBytes;
+constexpr int kOffP = kOffV + kVStages * kVBytes;
+constexpr int kOffCtrl = kOffP + kPBytes;
+constexpr int kSmemBytes = kOffCtrl + kCtrlBytes + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory per block");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // O: columns 0-255; S: 32 columns per buffer
@@ -167,26 +162,13 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar, uint16_t mask) {
       : "memory");
 }
 
-// 16 consecutive columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-
-template <int kRows>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const DecodeParams p, const int group_rows) {
-  using S = Shape<kRows>;
-  constexpr int kKStages = S::kKStages;
   extern __shared__ uint8_t smem_raw[];
   // (the same offset in both CTAs: their dynamic shared memory starts at the same address)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  PairCtrl* ctrl = reinterpret_cast<PairCtrl*>(smem + S::kOffCtrl);
+  PairCtrl* ctrl = reinterpret_cast<PairCtrl*>(smem + kOffCtrl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t rank;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -275,7 +257,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     uint64_t* const full = is_k ? ctrl->k_full : ctrl->v_full;
     uint64_t* const empty = is_k ? ctrl->k_empty : ctrl->v_empty;
     const CUtensorMap* const map = is_k ? &tm_k : &tm_v;
-    const uint32_t ring = smem_u32(smem + (is_k ? S::kOffK : S::kOffV));
+    const uint32_t ring = smem_u32(smem + (is_k ? kOffK : kOffV));
     const uint32_t stage_bytes = is_k ? kKBytes : kVBytes, block_bytes = is_k ? kKBlock : kVBlock;
     const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
     const unsigned n_pages = static_cast<unsigned>(min(p.num_pages, static_cast<int64_t>(0x7fffffff)));
@@ -293,7 +275,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     };
     if (lane == 0) {
       const uint32_t bar = map_rank(smem_u32(&ctrl->q_full), 0);
-      if (rank == 0) mbar_arrive_expect_tx(&ctrl->q_full, 2 * S::kQBytes);
+      if (rank == 0) mbar_arrive_expect_tx(&ctrl->q_full, 2 * kQBytes);
       load_pair_3d(smem_u32(smem), &tm_q, bar, 0, b * p.R + row0, 0, policy_evict_last());
     }
     int cur[3], nxt[3];
@@ -368,13 +350,13 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         ok = __all_sync(0xffffffffu, w);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t k_desc = make_smem_desc(smem_u32(smem + S::kOffK + slot * kKBytes), 16, 1024);
+        const uint64_t k_desc = make_smem_desc(smem_u32(smem + kOffK + slot * kKBytes), 16, 1024);
         if (elect_one()) {
 #pragma unroll
           for (int c = 0; c < kDimBlocks; ++c) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_pair(tmem + kTmemS + sb * 32, q_desc + static_cast<uint64_t>((c * S::kQBlock + k * 32) >> 4),
+              umma_pair(tmem + kTmemS + sb * 32, q_desc + static_cast<uint64_t>((c * kQBlock + k * 32) >> 4),
                         k_desc + static_cast<uint64_t>((c * kKBlock + k * 32) >> 4), idesc, (c | k) != 0);
           }
           commit_pair(&ctrl->s_full[sb], 3);
@@ -396,7 +378,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     // ------------------------------------------------------------------ BMM2 (CTA 0, for the pair)
     if (rank == 0) {
       const uint32_t idesc = make_idesc_bf16(128, 256, false, true);
-      const uint64_t p_desc = make_smem_desc(smem_u32(smem + S::kOffP), 16, 1024);
+      const uint64_t p_desc = make_smem_desc(smem_u32(smem + kOffP), 16, 1024);
       bool ok = true;
       for (int j = 0; ok && j < ntiles; ++j) {
         const int s = j % kVStages;
@@ -407,7 +389,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         tc_fence_after();
         // V: 16 keys (two 8-key groups, SBO apart) x 128 of this CTA's value columns (two
         // 64-column blocks, LBO apart), MN-major
-        const uint64_t v_desc = make_smem_desc(smem_u32(smem + S::kOffV + s * kVBytes), kVBlock, 1024);
+        const uint64_t v_desc = make_smem_desc(smem_u32(smem + kOffV + s * kVBytes), kVBlock, 1024);
         if (elect_one()) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -441,7 +423,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     if (row_active) drafts = p.tree_mask[static_cast<int64_t>(b) * p.T + (row0 + r) / p.H] & draft_bits(p.T);
     const uint32_t s_free0 = map_rank(smem_u32(&ctrl->s_free[0]), 0);
     const uint32_t p_full0 = map_rank(smem_u32(&ctrl->p_full), 0);
-    const uint32_t p_row = smem_u32(smem + S::kOffP) + r * 128;
+    const uint32_t p_row = smem_u32(smem + kOffP) + r * 128;
     float m_used = -INFINITY, l_sum = 0.f;
     bool failed = false, fail = false;
     for (int j = 0; j < ntiles; ++j) {
@@ -524,7 +506,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
       if (k0 + kTileKeys > p0) {
         // (BMM1 of such a tile waited for its V in both CTAs.)  Rows past the request's end become
         // zero, drafts' infinities and NaNs too: rows that do not see them give them weight 0.
-        const uint32_t stage = smem_u32(smem + S::kOffV + (j % kVStages) * kVBytes);
+        const uint32_t stage = smem_u32(smem + kOffV + (j % kVStages) * kVBytes);
         const int first = max(p0 - k0, 0), valid = min(L - k0, kTileKeys);
         for (int idx = threadIdx.x; idx < (kTileKeys - first) * 8 * kVBlocks; idx += kSoftmaxThreads) {
           const int row = first + idx / (8 * kVBlocks), rem = idx % (8 * kVBlocks);
@@ -564,7 +546,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
       const int dim = 256 * hi + 128 * hf;  // this thread's 128 output columns
       const int pitch = kValueDim * (final_out ? 2 : 4) + 16;
       static_assert(kRows * (kValueDim * 4 + 16) <= kKStages * kKBytes + kVStages * kVBytes, "output staging");
-      const uint32_t stage = smem_u32(smem + S::kOffK);
+      const uint32_t stage = smem_u32(smem + kOffK);
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t v[32];
@@ -608,25 +590,26 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
   release_tmem();
 }
 
-template <int kRows>
-cudaError_t launch_rows(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                        cudaStream_t stream) {
+}  // namespace
+
+cudaError_t launch_decode_tree_pair(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                    const CUtensorMap& tm_v, cudaStream_t stream) {
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(decode_tree_pair_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<kRows>::kSmem);
+    e = cudaFuncSetAttribute(decode_tree_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
   const int groups = tree_pair_groups(p.R);
-  const int group_rows = 2 * ((p.R + 2 * groups - 1) / (2 * groups));  // even groups, at most 2 kRows rows
+  const int group_rows = 2 * ((p.R + 2 * groups - 1) / (2 * groups));  // even groups, at most 128 rows
   const unsigned gx = static_cast<unsigned>(2 * groups);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = p.split_major ? dim3(gx, p.B, p.max_splits) : dim3(gx, p.max_splits, p.B);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Shape<kRows>::kSmem;
+  cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -636,15 +619,7 @@ cudaError_t launch_rows(const DecodeParams& p, const CUtensorMap& tm_q, const CU
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, decode_tree_pair_kernel<kRows>, tm_q, tm_k, tm_v, p, group_rows);
-}
-
-}  // namespace
-
-cudaError_t launch_decode_tree_pair(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                                    const CUtensorMap& tm_v, cudaStream_t stream) {
-  return tree_pair_rows(p.R) == 32 ? launch_rows<32>(p, tm_q, tm_k, tm_v, stream)
-                                   : launch_rows<64>(p, tm_q, tm_k, tm_v, stream);
+  return cudaLaunchKernelEx(&cfg, decode_tree_pair_kernel, tm_q, tm_k, tm_v, p, group_rows);
 }
 
 }  // namespace mla

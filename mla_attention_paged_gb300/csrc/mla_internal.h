@@ -169,15 +169,13 @@ cudaError_t launch_decode_partial(const DecodeParams& p, const CUtensorMap& tm_q
 // Decode over an e4m3 pool: the split-KV partial kernel that runs BMM1 on the raw codes.
 cudaError_t launch_decode_partial_e4m3(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv,
                                        int head_groups, cudaStream_t stream);
-// Decode over a bf16 pool for requests of at most 32 folded rows (R <= 32): Q held in
+// Decode over a bf16 pool for requests of at most 32 folded rows (trees: 48): Q held in
 // tensor memory, a three-tile ring (mla_decode_narrow_sm103a.cu).
 cudaError_t launch_decode_partial_narrow(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv,
                                          cudaStream_t stream);
-// Tree decode over a bf16 pool for requests of more than 32 folded rows (pairs of CTAs; tensor
-// maps: q boxes of tree_pair_rows(R) rows, K and V boxes as launch_decode_tree_pair's caller builds).
+// Tree decode over a bf16 pool for requests of more than 64 folded rows (pairs of CTAs).
 cudaError_t launch_decode_tree_pair(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                     const CUtensorMap& tm_v, cudaStream_t stream);
-int tree_pair_rows(int R);    // rows each CTA of a pair holds
 int tree_pair_groups(int R);  // pairs along the folded row axis
 // Decode: LSE-merge of the split partials for requests with more than one split.
 cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t stream);

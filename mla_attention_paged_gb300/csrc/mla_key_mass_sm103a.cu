@@ -102,15 +102,6 @@ MassShape mass_shape(int R) {
   return s;
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-
 // Query rows of an e4m3 launch: q 2^s = hi + lo with each row's largest element in [128, 256),
 // as K-major 64-byte-swizzled rows r (hi) and r + rows (lo) of nine blocks of 2 x rows rows.
 // The warp takes rows warp, warp + 8, ..., kSplitRows at a time with all their loads in flight

@@ -50,7 +50,7 @@ def test_tree_plan_sizes_its_partials(mla, kv, width, T):
     assert tree.max_splits > 1 and tree.rows == 16 * T
     parts = 2 * tree.max_splits * 16 * T
     assert tree.workspace_bytes == 256 + parts * 512 * width + parts * 4
-    if kv or T <= 2:
+    if kv or T <= 4:
         assert (tree.max_splits, tree.chunk_tokens) == (chain.max_splits, chain.chunk_tokens)
 
 
@@ -202,6 +202,13 @@ CASES = [  # lens, T, H, page, kind, SMs planned for (1: never split)
     ([300, 1000], 7, 7, 16, "bf16", 0),
     ([63, 640, 2000], 4, 16, 8, "bf16", 0),                    # 64 rows
     ([1500, 90], 3, 16, 128, "bf16", 0),                       # 48 rows
+    ([64, 65, 2500], 11, 3, 64, "bf16", 0),                    # 33 rows
+    ([700, 130, 5], 5, 8, 8, "bf16", 1),                       # 40 rows
+    ([47, 111, 3000], 47, 1, 32, "bf16", 0),
+    ([300, 2000], 4, 16, 64, "bf16", 0),                       # 64 rows
+    ([900, 5, 129], 5, 13, 16, "bf16", 0),                     # 65 rows
+    ([128, 1000], 8, 16, 64, "bf16", 1),                       # 128 rows
+    ([1000, 70], 43, 3, 64, "bf16", 0),                        # 129 rows
     ([777, 2100], 16, 16, 64, "bf16", 0),                      # 256 rows
     ([1025, 70, 129], 33, 8, 256, "bf16", 0),
     ([200, 1111], 64, 16, 64, "bf16", 0),                      # 1024 rows
@@ -259,7 +266,7 @@ def test_splits_agree_and_peaked_scores(mla, kind, H):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-@pytest.mark.parametrize("T,H", [(3, 8), (6, 16), (20, 16)])
+@pytest.mark.parametrize("T,H", [(3, 8), (3, 16), (4, 16), (6, 16), (20, 16)])
 def test_not_finite_drafts_reach_only_those_that_see_them(mla, kind, T, H):
     """NaN and infinite rows in drafts; NaN in every row behind the request's end."""
     lens = [64 + 2 + T, 500]
@@ -341,7 +348,8 @@ def test_bad_lengths_and_pages_are_reported(mla, kind):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind,T,H", [("bf16", 2, 16), ("bf16", 8, 16), ("bf16", 32, 16), ("e4m3", 8, 16)])
+@pytest.mark.parametrize("kind,T,H", [("bf16", 2, 16), ("bf16", 3, 16), ("bf16", 4, 16), ("bf16", 8, 16), ("bf16", 32, 16),
+                                       ("e4m3", 8, 16), ("int8", 4, 16)])
 def test_captured_calls_follow_the_device_inputs(mla, kind, T, H):
     """Two captured calls on one workspace, replayed with new masks, lengths and queries."""
     lens = [1000, 3000]

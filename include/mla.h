@@ -28,13 +28,15 @@
  *
  * Conventions shared by every call:
  *  - Every pointer argument that is not documented as host memory is DEVICE memory owned
- *    by the caller.  The library never allocates or frees device memory and never
- *    synchronises the stream in mla_decode / mla_prefill_varlen / mla_prefill_paged.
+ *    by the caller.  The library never allocates or frees device memory and, but for
+ *    mla_get_status, never synchronises the stream.
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *  - Tensors are dense and row-major (last index fastest), with the layouts given below.
  *  - Every call returns an mla_status_t code; no C++ exception crosses this ABI.
  *    Host-side argument checks run before anything is enqueued; on a non-zero return
  *    nothing was launched unless the code is MLA_ERR_CUDA.
+ *  - The first call of an entry point on each device and host thread sets its kernels up: make
+ *    it before a stream capture.
  *  - Device-side failures (a bounded wait that ran out, a length beyond the plan) are
  *    recorded in a per-device status word that mla_get_status() reads and clears.
  */

@@ -362,6 +362,16 @@ int make_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads,
   return MLA_OK;
 }
 
+// The planner's containers may run out of host memory; no exception leaves the library.
+template <typename... Args>
+int plan_no_throw(Args... args) {
+  try {
+    return make_plan(args...);
+  } catch (...) {
+    return MLA_ERR_CUDA;
+  }
+}
+
 }  // namespace
 
 extern "C" {
@@ -369,16 +379,16 @@ extern "C" {
 int mla_decode_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads, int page_size,
                     int max_pages_per_seq, int64_t num_pages, int kv_dtype, int num_sms,
                     mla_decode_plan_t* plan_out) {
-  return make_plan(batch, seq_lens_host, q_len, num_heads, page_size, max_pages_per_seq, num_pages, kv_dtype, num_sms,
-                   false, plan_out);
+  return plan_no_throw(batch, seq_lens_host, q_len, num_heads, page_size, max_pages_per_seq, num_pages, kv_dtype, num_sms,
+                       false, plan_out);
 }
 
 int mla_decode_tree_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads, int page_size,
                          int max_pages_per_seq, int64_t num_pages, int kv_dtype, int num_sms,
                          mla_decode_plan_t* plan_out) {
   if (q_len > kMaxTreeDrafts) return MLA_ERR_UNSUPPORTED;
-  return make_plan(batch, seq_lens_host, q_len, num_heads, page_size, max_pages_per_seq, num_pages, kv_dtype, num_sms,
-                   true, plan_out);
+  return plan_no_throw(batch, seq_lens_host, q_len, num_heads, page_size, max_pages_per_seq, num_pages, kv_dtype, num_sms,
+                       true, plan_out);
 }
 
 }  // extern "C"

@@ -218,6 +218,7 @@ CASES = [  # lens, T, H, page, kind, SMs planned for (1: never split)
     ([70, 2111], 2, 8, 16, "e4m3", 0),
     ([300, 129], 64, 5, 128, "e4m3", 0),
     ([900, 66], 31, 16, 32, "e4m3", 0),
+    ([100, 333], 9, 4, 8, "e4m3", 0),
     ([65, 700], 5, 16, 64, "int8", 0),
     ([64, 130], 64, 2, 16, "int8", 1),
     ([1200, 90], 9, 16, 128, "int8", 0),

@@ -141,6 +141,9 @@ CASES = [  # lens, T, H, page, kind, tree, decay, SMs planned for
     ([600, 77], 5, 16, 64, "e4m3", True, 0.97, 0),
     ([2000, 64], 2, 8, 16, "e4m3", False, 1.0, 0),
     ([300, 1300], 33, 16, 128, "e4m3", True, 0.5, 0),           # 528 rows
+    ([90, 777], 3, 5, 8, "e4m3", True, 1.0, 0),
+    ([400, 129] + [64 + 7 * i for i in range(60)], 2, 8, 64, "e4m3", False, 0.5, 0),  # more requests than a warp's lanes
+    ([64 + 3 * i for i in range(200)], 1, 16, 64, "bf16", False, 1.0, 0),             # more requests than SMs
     ([65, 700], 5, 16, 64, "int8", True, 1.0, 0),
     ([1200, 90], 9, 16, 8, "int8", False, 0.3, 0),
     ([65, 700], 5, 16, 64, "int8page", False, 0.9, 0),
@@ -233,7 +236,7 @@ def test_bad_lengths_and_pages_are_reported(mla, kind):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind,T", [("bf16", 2), ("bf16", 20), ("e4m3", 5)])
+@pytest.mark.parametrize("kind,T", [("bf16", 2), ("bf16", 20), ("e4m3", 5), ("int8", 3), ("int8", 20)])
 def test_captured_calls_follow_the_device_inputs(mla, kind, T):
     lens, H = [900, 2000], 16
     q, pool, table, scales, kv_scale, val = make(lens, T, H, 64, kind, 6)

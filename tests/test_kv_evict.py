@@ -180,6 +180,29 @@ def test_bad_lengths_and_pages_are_reported_and_skipped(mla):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("L,keep,m", [(393_216 + 5, 100_001, "ties"), (700_003, 699_000, "special")])
+def test_requests_longer_than_shared_memory_holds(mla, L, keep, m):
+    """More masses than a cluster keeps in shared memory; logical pages that share a few real ones."""
+    P, real, d = 64, 50, "cuda"
+    g = torch.Generator().manual_seed(L)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=d)
+    n_dst = -(-keep // P)
+    pool = torch.randint(0, 120, (real + n_dst, P, 576), generator=g, dtype=torch.uint8).to(d)
+    table = torch.randint(0, real, (1, -(-L // P)), generator=g).int()
+    mass = masses(1, L, 3, m)
+    kept, new_lens, mass_out = mla.kv_evict(pool, table.to(d), i32([L]), i32([keep]), mass.to(d),
+                                            torch.arange(real, real + n_dst, dtype=torch.int32, device=d)[None], 4, 100, L, keep,
+                                            mla.MLA_KV_E4M3)
+    assert mla.get_status() == mla.MLA_OK
+    ids = torch.tensor(chosen(mass[0], L, keep, 4, 100))
+    assert int(new_lens) == keep and torch.equal(kept[0].cpu().long(), ids)
+    assert torch.equal(mass_out[0].cpu().view(torch.int32), mass[0, ids].view(torch.int32))
+    ids = ids.to(d)
+    src = pool[table.to(d)[0].long()[ids // P], ids % P]
+    assert torch.equal(pool[real:].view(-1, 576)[:keep], src)
+
+
+@pytest.mark.gpu
 def test_captured_with_new_lengths_and_masses(mla):
     """A captured call follows the device's lengths and masses at replay."""
     d = "cuda"

@@ -206,3 +206,41 @@ def test_a_whole_step_in_one_graph(mla, kind):
         for a, b in zip(first, outs + [mass, c.pool]):
             assert torch.equal(a, b)
     assert mla.get_status() == mla.MLA_OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(mla, kind):
+    """Append, weights and eviction at the end of a pool of over 2^32 bytes."""
+    pages, B, L = (9_000_000_000 if kind == "bf16" else 4_700_000_000) // (PAGE * 576 * (2 if kind == "bf16" else 1)), 1, 100
+    g = torch.Generator().manual_seed(2)
+    c = Cache(mla, kind, B, 8)
+    c.pool = torch.zeros(pages, PAGE, 576, dtype=c.dtype, device=D)
+    kd = tree.KINDS[kind]
+    own = list(range(pages - 7, pages))
+    kv = torch.randn(L, 576, generator=g).bfloat16()
+    pos = torch.arange(L, dtype=torch.int32)
+    slots = torch.tensor([own[j // PAGE] * PAGE + j % PAGE for j in range(L)])
+    mla.kv_append(None, kv.to(D), pos.to(D), slots.to(D), c.cs.to(D), c.pool, kv_dtype=kd, kv_scale=c.scale)
+    rows = c.pool.view(-1, 576)[slots.to(D)].cpu()
+    want = append_reference(None, kv, pos, c.cs, None, None, True)[1]
+    if kind == "bf16":
+        check_bf16(rows, want)
+    else:
+        check_codes(rows, want, c.scale, kind)
+    c.rows = [rows]
+    q = torch.randn(B, 1, H, 576, generator=g).bfloat16()
+    tab = torch.tensor([own], dtype=torch.int32, device=D)
+    sl = torch.tensor([L], dtype=torch.int32, device=D)
+    plan = mla.decode_plan([L], 1, H, PAGE, 7, pages, kd)
+    val, vt = c.values()
+    lse = weight.true_lse(q, val, vt, [L], None)
+    mass = torch.zeros(1, L, device=D)
+    mla.key_mass(plan, q.to(D), c.pool, tab, sl, lse.to(D), mass, tree.SCALE, c.scale, decay=0.0)
+    new, tol = weight.reference(q, val, vt, [L], None, lse, torch.zeros(1, L), 0.0, kind)
+    assert ((mass.cpu().double() - new).abs() <= tol).all()
+    dst = torch.arange(pages - 12, pages - 7, dtype=torch.int32, device=D)[None]
+    kept, _, _ = mla.kv_evict(c.pool, tab, sl, torch.tensor([70], dtype=torch.int32, device=D), mass, dst, 2, 5, L, 70, kv_dtype=kd)
+    ids = chosen(mass[0].cpu(), L, 70, 2, 5)
+    assert kept[0].tolist() == ids
+    assert torch.equal(c.pool[pages - 12:pages - 7].view(-1, 576)[:70].cpu(), rows[torch.tensor(ids)])
+    assert mla.get_status() == mla.MLA_OK

@@ -38,7 +38,7 @@ constexpr int kCluster = 8;            // CTAs per request
 constexpr int kCoarse = kBins / 32;    // sums of 32 bins
 constexpr int kRound = 128;            // keys of a warp's round: four consecutive ones a lane
 constexpr int kMaxCached = 48 * 1024;  // images a CTA keeps in shared memory; longer shares are read again
-constexpr int kOneCtaKeys = 8192;      // up to this length a request has one CTA
+constexpr int kOneCtaKeys = 11264;      // up to this length a request has one CTA
 constexpr int kCopyWarps = 8;
 constexpr int kLanePieces = 9;         // 16-byte pieces a lane copies
 
@@ -235,14 +235,10 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const EvictPa
     int g = gt + ((incl - own) & 0xffff), q = eq + ((incl - own) >> 16);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (i + e >= n) continue;
-      if (k[e] > prefix) {
-        kept[lo + g + min(q, need)] = first + i + e;
-        ++g;
-      } else if (k[e] == prefix) {
-        if (q < need) kept[lo + g + q] = first + i + e;
-        ++q;
-      }
+      const bool heavy = i + e < n && k[e] > prefix, equal = i + e < n && k[e] == prefix;
+      if (heavy || (equal && q < need)) kept[lo + g + min(q, need)] = first + i + e;
+      g += heavy;
+      q += equal;
     }
     gt += all & 0xffff;
     eq += all >> 16;
@@ -326,7 +322,8 @@ cudaError_t launch_kv_evict(const EvictParams& params, cudaStream_t stream) {
     configured_device = dev;
   }
   EvictParams p = params;
-  // one CTA walks a short request faster than a cluster meets
+  // one CTA walks a short request faster than a cluster meets (four requests, whole call: of 8200
+  // keys 12.0 us against 13.2, of 12000 15.5 against 15.1)
   const int ctas = p.max_seq <= kOneCtaKeys ? 1 : kCluster;
   const int share = share_of(p.max_seq > 0 ? p.max_seq : 1, ctas);
   p.cached = share < kMaxCached ? share : kMaxCached;

@@ -133,6 +133,8 @@ CASES = [  # lens, keeps, page, kind, sink, recent, masses
     ([1025, 1024, 1023], [600, 1, 1000], 128, "e4m3", 0, 64, "equal"),
     ([2049, 4000], [2048, 1999], 256, "int8", 600, 700, "special"),
     ([9000, 30000, 17], [4000, 29999, 17], 64, "bf16", 4, 128, "heavy"),
+    ([11264, 9999], [5000, 9000], 64, "e4m3", 4, 30, "ties"),      # the longest that one CTA selects
+    ([11265, 300], [5000, 299], 64, "e4m3", 4, 30, "special"),
     ([70001], [33333], 64, "e4m3", 0, 0, "ties"),
 ]
 

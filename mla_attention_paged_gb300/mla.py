@@ -7,6 +7,7 @@ been built, importing this module raises; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -172,8 +173,22 @@ def _want_workspace(what, dev, workspace):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+def _on_stream(fn):
+    """Run a call whose ``stream`` is given with that stream current, so that what the call allocates
+    belongs to the stream that uses it."""
+    @functools.wraps(fn)
+    def on_stream(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, stream=stream, **kw)
+    return on_stream
+
+
 def _call(what, dev, stream, fn, *args):
     """fn(*args, stream) on CUDA device number `dev`: its current stream unless one is given."""
+    if stream is not None and stream.device_index != dev:
+        _refuse(what, f"the stream is on device {stream.device_index}")
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _call(what, dev, stream, fn, *args)
@@ -335,9 +350,10 @@ def prefill_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     return out, lse
 
 
+@_on_stream
 def decode_tree(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_table: torch.Tensor,
                 seq_lens: torch.Tensor, tree_mask: torch.Tensor, scale: float, kv_scale: float = 1.0, page_scales=None,
-                out=None, lse=None, workspace=None, stream=None):
+                out=None, lse=None, workspace=None, *, stream=None):
     """mla_decode_tree through the C ABI: decode of a tree of drafts.  tree_mask [B,T] int64 (its 64
     bits): bit u of [b, t] = draft t sees draft u.  Returns (out [B,T,H,512] bf16, lse [B,T,H] fp32)."""
     what = "mla_decode_tree"
@@ -362,9 +378,10 @@ def decode_tree(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_
     return out, lse
 
 
+@_on_stream
 def kv_append(q: torch.Tensor | None, kv: torch.Tensor | None, positions: torch.Tensor, slots: torch.Tensor | None,
               cos_sin: torch.Tensor, kv_pages: torch.Tensor | None, kv_weight=None, q_weight=None, eps: float = 1e-6,
-              interleaved: bool = True, kv_dtype: int = MLA_KV_BF16, kv_scale: float = 1.0, q_out=None, stream=None):
+              interleaved: bool = True, kv_dtype: int = MLA_KV_BF16, kv_scale: float = 1.0, q_out=None, *, stream=None):
     """mla_kv_append through the C ABI: norm and rotate a step's queries [N,H,q_dim] and latent
     keys [N,576], and write the keys into pool rows ``slots`` [N] int64 (negative: not stored).
     q (and q_out) may be strided views with a dense last dimension; q None: keys only, kv None:
@@ -414,9 +431,10 @@ def key_mass_workspace_for(plan: DecodePlan, device) -> torch.Tensor | None:
     return torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
 
 
+@_on_stream
 def key_mass(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
              lse: torch.Tensor, mass: torch.Tensor, scale: float, kv_scale: float = 1.0, tree_mask=None, page_scales=None,
-             decay: float = 1.0, workspace=None, stream=None) -> torch.Tensor:
+             decay: float = 1.0, workspace=None, *, stream=None) -> torch.Tensor:
     """mla_key_mass through the C ABI: mass [B, >= max_seq_len] fp32 becomes decay * mass + the
     attention weight each key received in the step whose lse [B,T,H] this is.  Returns mass."""
     what = "mla_key_mass"
@@ -438,9 +456,10 @@ def key_mass(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_tab
     return mass
 
 
+@_on_stream
 def kv_evict(kv_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch.Tensor,
              mass: torch.Tensor, dst_page_table: torch.Tensor, sink: int, recent: int, max_seq_len: int, max_keep: int,
-             kv_dtype: int = MLA_KV_BF16, kept=None, new_lens=None, mass_out=None, stream=None):
+             kv_dtype: int = MLA_KV_BF16, kept=None, new_lens=None, mass_out=None, *, stream=None):
     """mla_kv_evict through the C ABI: keep the heaviest keys of each request (its first ``sink``
     and last ``recent`` always) and copy their rows, in order, into the pages of
     ``dst_page_table``.  mass [B, >= max_seq_len] fp32.  Returns (kept [B,max_keep] int32, new_lens

@@ -208,6 +208,44 @@ def test_a_whole_step_in_one_graph(mla, kind):
     assert mla.get_status() == mla.MLA_OK
 
 
+def test_a_given_stream_owns_what_a_call_allocates(mla):
+    """Calls on a given stream while the current one is busy with memory it has just given back:
+    nothing of the results waits for the current stream or is overwritten by it."""
+    g = torch.Generator().manual_seed(5)
+    B, L = 2, 300
+    c = Cache(mla, "bf16", B, 100)
+    c.append(g, [L] * B, list(range(L)) * B)
+    tab, sl = c.table().to(D), torch.tensor([L] * B, dtype=torch.int32, device=D)
+    plan = mla.decode_tree_plan([L] * B, T, H, PAGE, tab.shape[1], c.pool.shape[0], 0)
+    q = torch.randn(B, T, H, 576, generator=g).bfloat16().to(D)
+    words = tree.random_tree(g, B, T).to(D)
+    pos, cs = torch.arange(B * T, dtype=torch.int32, device=D), c.cs.to(D)
+    keeps, mass = torch.tensor([90, 50], dtype=torch.int32, device=D), torch.rand(B, L, generator=g).to(D)
+    dst = torch.tensor([[c.free.pop() for _ in range(6)] for _ in range(B)], dtype=torch.int32, device=D)
+
+    def calls(stream):
+        yield lambda: mla.decode_tree(plan, q, c.pool, tab, sl, words, tree.SCALE, stream=stream)
+        yield lambda: (mla.kv_append(q.view(B * T, H, 576), None, pos, None, cs, None, stream=stream),)
+        yield lambda: mla.kv_evict(c.pool, tab, sl, keeps, mass, dst, 4, 16, L, 90, stream=stream)
+
+    want = [[o.clone() for o in call()] for call in calls(None)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for call, outs in zip(calls(side), want):
+        busy = [torch.empty_like(o) for o in outs]
+        torch.cuda._sleep(20_000_000)  # (some 10 ms)
+        for o in busy:
+            o.fill_(7)
+        del o, busy
+        got = call()
+        side.synchronize()
+        got = [o.clone() for o in got]
+        torch.cuda.synchronize()
+        for a, b in zip(got, outs):
+            assert torch.equal(a, b)
+    assert mla.get_status() == mla.MLA_OK
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_offsets_past_32_bits(mla, kind):
     """Append, weights and eviction at the end of a pool of over 2^32 bytes."""

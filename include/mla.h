@@ -332,8 +332,8 @@ int mla_prefill_paged(const void* q, const void* k_pages, const void* v_pages, c
  *                 not negative must differ: a row that two tokens name holds bytes of either.
  *   kv_pages    : the pool, num_slots = num_pages * page_size rows of 576 elements of kv_dtype.
  *   kv_scale    : scale of an e4m3 or int8 pool (ignored for bf16).
- * Pointers are 16-byte aligned (positions 4, slots 8).  Rows that no token names are left as
- * they were.  num_tokens 0 does nothing.  Launched as a programmatic dependent like mla_decode.
+ * Pointers are 16-byte aligned (positions 4, slots 8).  kv_in lies outside the pool.
+ * Rows that no token names are left as they were.  num_tokens 0 does nothing.  Launched as a programmatic dependent like mla_decode.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (num_heads > 1024, another q_dim, num_tokens >
  * 2^20, an MLA_KV_INT8_PAGE pool, whose page scales cannot follow new rows), MLA_ERR_CUDA.
  * Device-side, recorded as MLA_ERR_DEVICE_ARG: a position outside [0, max_positions) (the token's
@@ -363,9 +363,9 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
  *                 aligned (NULL when that is 0); overwritten; calls that share one are stream-ordered.
  * Launched as a programmatic dependent like mla_decode.  Errors: MLA_ERR_INVALID_ARG,
  * MLA_ERR_UNSUPPORTED (tree_mask with more than 64 drafts; batch times the longest request beyond
- * 2^38 keys), MLA_ERR_WORKSPACE_TOO_SMALL, MLA_ERR_CUDA.  Device-side, recorded as MLA_ERR_DEVICE_ARG: a length below q_len or beyond the
- * plan (that request's row is left as it was) and a page id outside [0, num_pages) (its rows count
- * as zeros). */
+ * 2^38 keys), MLA_ERR_WORKSPACE_TOO_SMALL, MLA_ERR_CUDA.  Device-side, recorded as
+ * MLA_ERR_DEVICE_ARG: a length below q_len or beyond the plan (that request's row is left as it
+ * was) and a page id outside [0, num_pages) (its rows count as zeros). */
 int mla_key_mass_workspace(const mla_decode_plan_t* plan, size_t* bytes_out);
 int mla_key_mass(const mla_decode_plan_t* plan, const void* q, const void* kv_pages, const float* page_scales,
                  const int32_t* page_table, const int32_t* seq_lens, const uint64_t* tree_mask,
@@ -388,7 +388,7 @@ int mla_key_mass(const mla_decode_plan_t* plan, const void* q, const void* kv_pa
  *   mass           : fp32, row b at mass + b * mass_stride (elements; >= max_seq_len).
  *   dst_page_table : [batch, max_dst_pages] int32 destination pages, which must be distinct and no
  *                    source page of any request of the call.
- *   max_seq_len, max_keep : host bounds on the lengths and on K.
+ *   max_seq_len, max_keep : host bounds on the lengths and on K (0: mass, or kept and mass_out, may be NULL).
  *   kept, mass_out : row b at b * kept_stride / b * mass_out_stride (elements; >= max_keep).
  *                    mass_out may not overlap mass, new_lens neither seq_lens nor keep_lens.
  * Two kernels on `stream` (selection, copy), programmatic dependents like mla_decode.

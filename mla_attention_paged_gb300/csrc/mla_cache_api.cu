@@ -70,6 +70,10 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
         (kv_weight && !aligned(kv_weight, 16)) || kv_in_token_stride < 0 || kv_in_token_stride % 8 != 0)
       return MLA_ERR_INVALID_ARG;
     if (kv_dtype != MLA_KV_BF16 && !(kv_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+    // a row may be written while another of the pool's is still to be read
+    if (overlap(kv_in, static_cast<size_t>((num_tokens - 1) * kv_in_token_stride + kLatentDim) * 2, kv_pages,
+                static_cast<size_t>(num_slots) * kLatentDim * (kv_dtype == MLA_KV_BF16 ? 2 : 1)))
+      return MLA_ERR_INVALID_ARG;
   }
   AppendParams p;
   memset(&p, 0, sizeof p);
@@ -196,7 +200,8 @@ int mla_kv_evict(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype,
   // a row's codes mean something else under another page's scale
   if (kv_dtype == MLA_KV_INT8_PAGE) return MLA_ERR_UNSUPPORTED;
   if (!page_size_ok(page_size) || batch > 65535 || max_seq_len > (1 << 24)) return MLA_ERR_UNSUPPORTED;
-  if (!kv_pages || !page_table || !seq_lens || !keep_lens || !mass || !dst_page_table || !kept || !new_lens || !mass_out)
+  if (!kv_pages || !page_table || !seq_lens || !keep_lens || !dst_page_table || !new_lens || (!mass && max_seq_len > 0) ||
+      ((!kept || !mass_out) && max_keep > 0))
     return MLA_ERR_INVALID_ARG;
   if (!aligned(kv_pages, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(keep_lens, 4) ||
       !aligned(mass, 4) || !aligned(dst_page_table, 4) || !aligned(kept, 4) || !aligned(new_lens, 4) ||

@@ -56,6 +56,11 @@ def test_unsupported_shapes_are_refused(mla, bad):
     assert _raw(mla, **bad) == mla.MLA_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("kv", [(1 << 30) - 1152, (1 << 30) + 64 * 1152 - 16, (1 << 30) + 16, (1 << 30) - 2 * 1152 + 16])
+def test_keys_inside_the_pool_are_refused(mla, kv):
+    assert _raw(mla, kv=kv) == mla.MLA_ERR_INVALID_ARG
+
+
 def test_no_tokens_is_no_work(mla):
     assert _raw(mla, n=0) == mla.MLA_OK
     assert _raw(mla, n=0, q_in=None, kv=None, pool=None) == mla.MLA_OK

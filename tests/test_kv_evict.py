@@ -146,6 +146,22 @@ def test_against_the_definition(mla, lens, keeps, page, kind, sink, recent, m):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,keeps,max_keep", [([5, 70], [0, 0], 0), ([0, 0], [3, 0], 0), ([0], [9], 4)])
+def test_nothing_kept(mla, lens, keeps, max_keep):
+    """Bounds of zero: empty outputs, and masses that nobody reads."""
+    d = "cuda"
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=d)
+    pool = torch.randint(0, 99, (8, 64, 576)).bfloat16().to(d)
+    was = pool.clone()
+    B = len(lens)
+    table, dst = torch.zeros(B, 2, dtype=torch.int32, device=d), torch.full((B, 1), 7, dtype=torch.int32, device=d)
+    kept, new_lens, mass_out = mla.kv_evict(pool, table, i32(lens), i32(keeps), torch.rand(B, max(lens), device=d), dst, 2, 2,
+                                            max(lens), max_keep, new_lens=i32([-3] * B))
+    assert mla.get_status() == mla.MLA_OK
+    assert new_lens.tolist() == [0] * B and kept.shape == mass_out.shape == (B, max_keep) and torch.equal(pool, was)
+
+
+@pytest.mark.gpu
 def test_a_long_request_among_many_short_ones(mla):
     lens = [150000] + [64 + 3 * i for i in range(40)]
     run(mla, lens, [70000] + [50] * 40, masses(41, 150000, 5), 64, "e4m3", 4, 32)

@@ -462,22 +462,15 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
   memset(&tm_v, 0, sizeof tm_v);
   if (partial && pairs) {
     // K boxes: half a tile's keys, all nine column blocks; V boxes: a tile's keys, the four
-    // blocks of one CTA's value columns; pages below 64 keys: one (page part, block) at a time
-    const uint64_t rows = static_cast<uint64_t>(plan->num_pages) * plan->page_size;
-    if (plan->page_size >= kTileKeys) {
-      const uint64_t dims[3] = {64, rows, kLatentDim / 64};
-      const uint64_t strides[2] = {row_bytes, 128};
-      const uint32_t box_k[3] = {64, kTileKeys / 2, kLatentDim / 64}, box_v[3] = {64, kTileKeys, kValueDim / 128};
-      if (!make_map(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, kv_pages, dims, strides, box_k) ||
-          !make_map(&tm_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, kv_pages, dims, strides, box_v))
-        return MLA_ERR_CUDA;
-    } else {
-      const uint64_t dims[2] = {static_cast<uint64_t>(kLatentDim), rows};
-      const uint64_t strides[1] = {row_bytes};
-      const uint32_t box[2] = {64, static_cast<uint32_t>(std::min(plan->page_size, kTileKeys / 2))};
-      if (!make_map(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_pages, dims, strides, box)) return MLA_ERR_CUDA;
-      tm_v = tm_kv;
-    }
+    // blocks of one CTA's value columns; pages below 64 keys: eight keys at a time
+    const bool whole = plan->page_size >= kTileKeys;
+    const uint64_t dims[3] = {64, static_cast<uint64_t>(plan->num_pages) * plan->page_size, kLatentDim / 64};
+    const uint64_t strides[2] = {row_bytes, 128};
+    const uint32_t box_k[3] = {64, whole ? kTileKeys / 2 : 8u, kLatentDim / 64};
+    const uint32_t box_v[3] = {64, whole ? kTileKeys : 8u, kValueDim / 128};
+    if (!make_map(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, kv_pages, dims, strides, box_k) ||
+        !make_map(&tm_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, kv_pages, dims, strides, box_v))
+      return MLA_ERR_CUDA;
   } else if (partial && plan->kv_dtype == MLA_KV_BF16) {  // int8 pages are read row by row by the decode warps
     const uint64_t rows = static_cast<uint64_t>(plan->num_pages) * plan->page_size;
     if (plan->page_size >= kTileKeys) {  // a 64-key tile is one row range of one page

@@ -22,8 +22,8 @@
 //  * BMM2, O += P . V (N = 256 twice, K = 64 keys): CTA r holds all 64 keys' columns 256r ..
 //    256r+255.  (The operand of one MMA lies at one address in both CTAs, so K and V are two
 //    copies: 68 KB a CTA and tile, the V one from L2.)  K and V have rings of their own.
-//  * Warps: 0-7 softmax and epilogue, 8 TMA producer, 9 and 10 issue BMM1 and BMM2 (CTA 0's, for
-//    the pair).  Loads of both CTAs count on barriers of CTA 0; commits arrive in both.
+//  * Warps: 0-7 softmax and epilogue, 8 and 9 load the K and the V ring, 10 and 11 issue BMM1 and
+//    BMM2 (CTA 0's, for the pair).  Loads of both CTAs count on barriers of CTA 0; commits arrive in both.
 //  * Softmax: TMEM lane l holds row l % 64, keys 0-31 (l < 64) or 32-63 of the tile; warps w and
 //    w + 4 share a lane quadrant and take 16 of those keys each.  A row's four threads swap their
 //    maxima through shared memory (one barrier a tile).  Lazy rescale as in the other kernels.
@@ -51,9 +51,9 @@ constexpr int kVStages = 2;
 constexpr int kRows = 64;                           // rows a CTA holds
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-constexpr int kLoadWarp = kSoftmaxWarps, kBmm1Warp = kLoadWarp + 1, kBmm2Warp = kLoadWarp + 2;
-constexpr int kAhead = 6;  // tiles that the L2 prefetch runs ahead of the loads
-constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
+constexpr int kLoadKWarp = kSoftmaxWarps, kLoadVWarp = kLoadKWarp + 1, kBmm1Warp = kLoadKWarp + 2, kBmm2Warp = kLoadKWarp + 3;
+constexpr int kAhead = 2;  // tiles that the L2 prefetch runs ahead of the loads
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kArrivals = 2 * kSoftmaxWarps;        // softmax warps of the pair
 
 struct PairCtrl {
@@ -130,13 +130,6 @@ __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, volati
   }
 }
 // TMA loads into this CTA's shared memory that count on a barrier of either CTA.
-__device__ __forceinline__ void load_pair_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, uint64_t pol) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(pol)
-      : "memory");
-}
 __device__ __forceinline__ void load_pair_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
                                              uint64_t pol) {
   asm volatile(
@@ -203,7 +196,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  if (warp == kLoadWarp && lane == 0) {
+  if (warp == kLoadKWarp && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -237,99 +230,87 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
   const int row0 = group * group_rows + static_cast<int>(rank) * half_rows;
   const int nrows = max(0, min(half_rows, p.R - row0));
   volatile int* abort_flag = &ctrl->abort_flag;
+  // Shared memory of a tile: from a page of at least 64 keys [column block][key], else [8 keys][block]
+  const bool whole = p.page_size >= kTileKeys;
+  const uint32_t k_block = whole ? kKBlock : 1024, k_eight = whole ? 1024 : kDimBlocks * 1024;
+  const uint32_t v_block = whole ? kVBlock : 1024, v_eight = whole ? 1024 : kVBlocks * 1024;
 
-  if (warp == kLoadWarp) {
-    // ------------------------------------------------------------------ TMA producer: lanes 0-15
-    // stream the K ring, lanes 16-31 the V ring.  Pages of 64 keys or more: one box per
-    // operand; smaller pages: one box per (page part, column block), shared by the lanes.  A
-    // part past the request's end, and a page id outside the pool (reported), lie before
-    // the first row, which TMA fills with zeros.
-    const bool is_k = lane < 16;
-    const int gl = lane & 15, leader = is_k ? 0 : 16;
-    const unsigned gmask = is_k ? 0x0000FFFFu : 0xFFFF0000u;
-    const int P = p.page_size;
-    const bool whole = P >= kTileKeys;
-    const int part = whole ? (is_k ? kHalfKeys : kTileKeys) : min(P, kHalfKeys);  // keys of a box
-    const int nblk = is_k ? kDimBlocks : kVBlocks;
-    const int nbox = whole ? 1 : (is_k ? kHalfKeys : kTileKeys) / part * nblk;    // at most 36: three per lane
-    const int first_key = is_k ? static_cast<int>(rank) * kHalfKeys : 0;
+  if (warp == kLoadKWarp || warp == kLoadVWarp) {
+    // ------------------------------------------------------------------ TMA producers, one per
+    // ring (as two halves of one warp they held each other up: 304 against 268 us on 8 requests of
+    // 20K-65K keys with 32 x 16 rows).  Pages of 64 keys or more: one box per operand and
+    // tile; smaller pages: one box per 8 keys (a lane each).  A box past the request's end, and
+    // a page id outside the pool (reported), lie before the first row, which TMA fills with zeros.
+    const bool is_k = warp == kLoadKWarp;
+    const int page_log2 = __ffs(p.page_size) - 1;  // (a power of two)
+    const int keys = is_k ? kHalfKeys : kTileKeys;
+    const int nbox = whole ? 1 : keys / 8;
+    const int first_key = (is_k ? static_cast<int>(rank) * kHalfKeys : 0) + 8 * lane;
+    const int first_blk = is_k ? 0 : static_cast<int>(rank) * kVBlocks;
     const int stages = is_k ? kKStages : kVStages;
     uint64_t* const full = is_k ? ctrl->k_full : ctrl->v_full;
     uint64_t* const empty = is_k ? ctrl->k_empty : ctrl->v_empty;
     const CUtensorMap* const map = is_k ? &tm_k : &tm_v;
-    const uint32_t ring = smem_u32(smem + (is_k ? kOffK : kOffV));
-    const uint32_t stage_bytes = is_k ? kKBytes : kVBytes, block_bytes = is_k ? kKBlock : kVBlock;
+    const uint32_t stage_bytes = is_k ? kKBytes : kVBytes;
+    const uint32_t ring = smem_u32(smem + (is_k ? kOffK : kOffV)) + lane * (stage_bytes / (keys / 8));
     const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
     const unsigned n_pages = static_cast<unsigned>(min(p.num_pages, static_cast<int64_t>(0x7fffffff)));
     const uint64_t pol = policy_evict_normal();  // (every byte of a value column is read by both CTAs)
     bool bad_pid = false;
-    auto row_of = [&](int j, int bx) -> int {  // pool row of box bx of tile j
-      const int k = kv_start + j * kTileKeys + first_key + (whole ? 0 : bx / nblk * part);
-      if (bx >= nbox || j >= ntiles || k >= L) return -kTileKeys;
-      const int pid = __ldg(pt + k / P);
+    auto has_keys = [&](int j) { return lane < nbox && j < ntiles && kv_start + j * kTileKeys + first_key < L; };
+    auto page_of = [&](int j) -> int {  // page of this lane's box of tile j (looked at tiles later)
+      return has_keys(j) ? __ldg(pt + ((kv_start + j * kTileKeys + first_key) >> page_log2)) : 0;
+    };
+    auto row_of = [&](int j, int pid) -> int {  // and its pool row
+      if (!has_keys(j)) return -kTileKeys;
       if (static_cast<unsigned>(pid) >= n_pages) {
         bad_pid = true;
         return -kTileKeys;
       }
-      return pid * P + k % P;
+      return (pid << page_log2) + ((kv_start + j * kTileKeys + first_key) & (p.page_size - 1));
     };
-    if (lane == 0) {
+    if (is_k && lane == 0) {
       const uint32_t bar = map_rank(smem_u32(&ctrl->q_full), 0);
       if (rank == 0) mbar_arrive_expect_tx(&ctrl->q_full, 2 * kQBytes);
       load_pair_3d(smem_u32(smem), &tm_q, bar, 0, b * p.R + row0, 0, policy_evict_last());
     }
-    int cur[3], nxt[3];
+    int page[kAhead + 1];  // of the next tiles
 #pragma unroll
-    for (int i = 0; i < 3; ++i) cur[i] = row_of(0, gl + 16 * i);
+    for (int i = 0; i <= kAhead; ++i) page[i] = page_of(i);
     int slot = 0, phase = 0, issued = 0;
     bool ok = true;
     for (int j = 0; j < ntiles; ++j) {
-#pragma unroll
-      for (int i = 0; i < 3; ++i) nxt[i] = row_of(j + 1, gl + 16 * i);
-      // Several pairs read each tile at about the same time: one of them asks L2 for it ahead (8
-      // requests of 20K-65K keys, four pairs a tile: 337 -> 320 us; a lone pair's own loads only
-      // got slower, 250 -> 265 us).
-      if (groups > 1 && whole && is_k && gl == 1 && j % groups == group && j + kAhead < ntiles) {
-        const int k = kv_start + (j + kAhead) * kTileKeys + first_key;
-        const int pid = k < L ? __ldg(pt + k / P) : -1;
-        if (static_cast<unsigned>(pid) < n_pages)
-          asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                           reinterpret_cast<uint64_t>(map)),
-                       "r"(0), "r"(pid * P + k % P), "r"(0)
-                       : "memory");
-      }
+      const int next = page_of(j + kAhead + 1);
+      const int row = row_of(j, page[0]);
       if (j >= stages) {
         bool w = true;
-        if (gl == 0) w = wait_pair(&empty[slot], phase ^ 1, abort_flag);
-        ok = __shfl_sync(gmask, w, leader);
+        if (lane == 0) w = wait_pair(&empty[slot], phase ^ 1, abort_flag);
+        ok = __shfl_sync(0xffffffffu, w, 0);
         if (!ok) break;
       }
-      if (rank == 0 && gl == 0) mbar_arrive_expect_tx(&full[slot], 2 * stage_bytes);
-      __syncwarp(gmask);
-      const uint32_t bar = map_rank(smem_u32(&full[slot]), 0), dst = ring + slot * stage_bytes;
-      if (whole) {
-        if (gl == 0) load_pair_3d(dst, map, bar, 0, cur[0], is_k ? 0 : static_cast<int>(rank) * kVBlocks, pol);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const int bx = gl + 16 * i;
-          if (bx < nbox) {
-            const int blk = bx % nblk;
-            load_pair_2d(dst + blk * block_bytes + bx / nblk * part * 128, map, bar,
-                         (blk + (is_k ? 0 : static_cast<int>(rank) * kVBlocks)) * 64, cur[i], pol);
-          }
-        }
-      }
+      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[slot], 2 * stage_bytes);
+      __syncwarp();
+      if (lane < nbox)
+        load_pair_3d(ring + slot * stage_bytes, map, map_rank(smem_u32(&full[slot]), 0), 0, row, first_blk, pol);
+      // Each key goes to two copies, and several pairs may read a tile at about the same time: one
+      // of them asks L2 for it ahead.  (Two tiles, against none: 304 -> 268 us with four pairs a
+      // tile, 287 -> 234 with one on 16 requests of 8K-131K keys; six tiles ahead 273 and 264.)
+      const int ahead = is_k && j % groups == group ? row_of(j + kAhead, page[kAhead]) : -1;
+      if (ahead >= 0)
+        asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                     "r"(0), "r"(ahead), "r"(0)
+                     : "memory");
       ++issued;
       if (++slot == stages) {
         slot = 0;
         phase ^= 1;
       }
 #pragma unroll
-      for (int i = 0; i < 3; ++i) cur[i] = nxt[i];
+      for (int i = 0; i < kAhead; ++i) page[i] = page[i + 1];
+      page[kAhead] = next;
     }
-    if (__any_sync(gmask, bad_pid) && gl == 0) atomicOr(p.status, kStatusDeviceArg);
-    if (!ok && gl == 0 && rank == 0) {
+    if (__any_sync(0xffffffffu, bad_pid) && lane == 0) atomicOr(p.status, kStatusDeviceArg);
+    if (!ok && lane == 0 && rank == 0) {
       // copies of the pair still in flight land before the CTAs leave
       if (is_k) drain_wait(&ctrl->q_full, 0);
       for (int u = max(0, issued - stages); u < issued; ++u) drain_wait(&full[u % stages], (u / stages) & 1);
@@ -350,14 +331,14 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         ok = __all_sync(0xffffffffu, w);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t k_desc = make_smem_desc(smem_u32(smem + kOffK + slot * kKBytes), 16, 1024);
+        const uint64_t k_desc = make_smem_desc(smem_u32(smem + kOffK + slot * kKBytes), 16, k_eight);
         if (elect_one()) {
 #pragma unroll
           for (int c = 0; c < kDimBlocks; ++c) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               umma_pair(tmem + kTmemS + sb * 32, q_desc + static_cast<uint64_t>((c * kQBlock + k * 32) >> 4),
-                        k_desc + static_cast<uint64_t>((c * kKBlock + k * 32) >> 4), idesc, (c | k) != 0);
+                        k_desc + static_cast<uint64_t>((c * k_block + k * 32) >> 4), idesc, (c | k) != 0);
           }
           commit_pair(&ctrl->s_full[sb], 3);
           commit_pair(&ctrl->k_empty[slot], 3);
@@ -389,14 +370,14 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         tc_fence_after();
         // V: 16 keys (two 8-key groups, SBO apart) x 128 of this CTA's value columns (two
         // 64-column blocks, LBO apart), MN-major
-        const uint64_t v_desc = make_smem_desc(smem_u32(smem + kOffV + s * kVBytes), kVBlock, 1024);
+        const uint64_t v_desc = make_smem_desc(smem_u32(smem + kOffV + s * kVBytes), v_block, v_eight);
         if (elect_one()) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               umma_pair(tmem + q * 128, p_desc + static_cast<uint64_t>((kk * 32) >> 4),
-                        v_desc + static_cast<uint64_t>((q * 2 * kVBlock + kk * 2048) >> 4), idesc,
+                        v_desc + static_cast<uint64_t>((q * 2 * v_block + kk * 2 * v_eight) >> 4), idesc,
                         (j > 0 || kk > 0) ? 1u : 0u);
           }
           commit_pair(&ctrl->o_done, 3);
@@ -510,7 +491,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int first = max(p0 - k0, 0), valid = min(L - k0, kTileKeys);
         for (int idx = threadIdx.x; idx < (kTileKeys - first) * 8 * kVBlocks; idx += kSoftmaxThreads) {
           const int row = first + idx / (8 * kVBlocks), rem = idx % (8 * kVBlocks);
-          const uint32_t at = stage + (rem >> 3) * kVBlock + row * 128 + (rem & 7) * 16;
+          const uint32_t at = stage + (rem >> 3) * v_block + (row >> 3) * v_eight + (row & 7) * 128 + (rem & 7) * 16;
           if (row < valid)
             make_finite<false>(at);
           else

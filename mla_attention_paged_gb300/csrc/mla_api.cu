@@ -337,8 +337,8 @@ int make_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads,
   pl.num_sms = num_sms;
   pl.rows = q_len * num_heads;
   pl.head_groups = (pl.rows + kGroupRows - 1) / kGroupRows;
-  // a tree over a bf16 pool with more than 64 rows runs on pairs of CTAs (and SMs)
-  const bool pairs = tree && kv_dtype == MLA_KV_BF16 && pl.rows > kGroupRows;
+  // a tree over a bf16 pool with more than 48 rows runs on pairs of CTAs (and SMs)
+  const bool pairs = tree && kv_dtype == MLA_KV_BF16 && pl.rows > kTreeNarrowRows;
   const int groups = pairs ? tree_pair_groups(pl.rows) : pl.head_groups;
   const int units = pairs ? std::max(1, num_sms / 2) : num_sms;
   const int ct = choose_chunk_tiles(lens, groups, units, pairs ? kPairFixedTiles : cta_fixed_tiles(kv_dtype));
@@ -426,7 +426,7 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
   unsigned* status = status_ptr();
   if (!status) return MLA_ERR_CUDA;
 
-  const bool pairs = tree_mask && plan->kv_dtype == MLA_KV_BF16 && plan->rows > kGroupRows;
+  const bool pairs = tree_mask && plan->kv_dtype == MLA_KV_BF16 && plan->rows > kTreeNarrowRows;
   const uint64_t row_bytes = kLatentDim * 2;
   // Latent rows are viewed as [rows][9 blocks][64 columns] (block stride 128 bytes), so one
   // 3-D box {64 columns, n rows, 9 blocks} lands a whole row range as the nine 128-byte

@@ -97,12 +97,13 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // and f16 GEMMs of the int8 paths, kPageScales the per-key scales of kKvInt8Page).
 // kSplitMajor: the grid's launch order (a compile-time choice: a run-time select of the
 // block-index mapping measured 1.4 % slower on 128-head decode).
-// kTree: drafts see each other by p.tree_mask instead of in order; partials are fp32 (bf16 pools) or f16.
+// kTree (int8 pools): drafts see each other by p.tree_mask instead of in order; partials are f16.
 template <int kKv, bool kSplitMajor, bool kTree>
 __global__ void __launch_bounds__(threads_for(kKv != kKvBf16), 1)
 decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                       const DecodeParams p) {
   constexpr bool kInt8 = kKv == kKvInt8 || kKv == kKvInt8Page;
+  static_assert(kInt8 || !kTree, "trees over bf16 pools run on the narrow and the pair kernel");
   constexpr bool kPageScales = kKv == kKvInt8Page;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -684,14 +685,6 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           }
           fence_proxy_async_smem();
         }
-        if (kTree && k0 + kTileKeys > p0) {
-          // this tile's drafts: some rows give them weight 0
-          const uint32_t stage = smem_u32(smem + kOffStages + (j % kStages) * kTileBytes);
-          const int d0 = max(p0 - k0, 0), n = (min(valid_rows, kTileKeys) - d0) * 8;
-          for (int idx = threadIdx.x; idx < n * 8; idx += 128)
-            make_finite<false>(stage + (idx / n) * kBlockBytes + d0 * 128 + (idx % n) * 16);
-          fence_proxy_async_smem();
-        }
       }
       if (ctrl->rescale_flag[0] | ctrl->rescale_flag[1] | ctrl->rescale_flag[2] | ctrl->rescale_flag[3]) {
         // O^T[dim, row] *= alpha[row] for all 512 value columns; this thread owns TMEM lane
@@ -758,7 +751,7 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const float lse2 = some ? (m_used + __log2f(l_sum)) : -INFINITY;
         const float lse_nat = lse2 * 0.69314718055994530942f;
         // (an int8 pool's partials of a tree are f16 in units of its codes; the combine scales them)
-        ctrl->row_scale[r] = some ? ((kTree && kInt8 && !final_out ? 1.f : v_scale) / l_sum) : 0.f;
+        ctrl->row_scale[r] = some ? ((kTree && !final_out ? 1.f : v_scale) / l_sum) : 0.f;
         if (row_active) {
           const int64_t grow = static_cast<int64_t>(b) * p.R + row0 + r;
           if (final_out)
@@ -775,34 +768,7 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       // The 64 row scales go to registers first: shared-memory loads interleaved with the
       // staging stores below would each have to wait for the stores before them.
       const uint32_t stage_s = smem_u32(smem + kOffStages);  // [64][512] bf16
-      if (kTree && !kInt8 && !final_out) {
-        // A bf16 pool's partials of a tree stay fp32 ([64][512] in both stages): a second bf16
-        // rounding would add as much error as the output's own.  The scales of 32 rows at a
-        // time go to registers first (loaded between the stores they cost 7,800 cycles).
-        static_assert(kGroupRows * kValueDim * 4 <= kStages * kTileBytes, "fp32 staging");
-#pragma unroll 1
-        for (int hh = 0; hh < 2; ++hh) {
-          float rs[32];
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&ctrl->row_scale[hh * 32 + i]);
-            rs[i] = f.x;
-            rs[i + 1] = f.y;
-            rs[i + 2] = f.z;
-            rs[i + 3] = f.w;
-          }
-#pragma unroll 1
-          for (int qc = 0; qc < 4; ++qc) {
-            const int dim = qc * 128 + warp * 32 + lane;
-            uint32_t v[32];
-            tmem_ld32(tmem + lane_base + qc * 64 + hh * 32, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              st_shared_f32(stage_s + ((hh * 32 + i) * kValueDim + dim) * 4, __uint_as_float(v[i]) * rs[i]);
-          }
-        }
-      } else if constexpr (kInt8) {
+      if constexpr (kInt8) {
         // (the int8 kernels run at a lower register cap: rows 32hh .. 32hh+31 at a time,
         // their 32 scales in registers)
 #pragma unroll 1
@@ -859,21 +825,14 @@ decode_partial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       }
       __nv_bfloat16* stage_h = reinterpret_cast<__nv_bfloat16*>(smem + kOffStages);
       named_bar_sync(1, 128);
-      if (kTree && !kInt8 && !final_out) {
-        const uint4* const src = reinterpret_cast<const uint4*>(smem + kOffStages);
-        uint4* const dst = reinterpret_cast<uint4*>(
-            p.ws_of + ((static_cast<int64_t>(b) * p.max_splits + split) * p.R + row0) * kValueDim);
-        for (int c = threadIdx.x; c < nrows * (kValueDim / 4); c += 128) dst[c] = src[c];
-      } else {
-        constexpr int kChunksPerRow = kValueDim * 2 / 16;
-        __nv_bfloat16* dst =
-            final_out ? p.out + (static_cast<int64_t>(b) * p.R + row0) * kValueDim
-                      : p.ws_o + ((static_cast<int64_t>(b) * p.max_splits + split) * p.R + row0) * kValueDim;
-        for (int c = threadIdx.x; c < nrows * kChunksPerRow; c += 128) {
-          const int rr = c / kChunksPerRow, cc = c % kChunksPerRow;
-          const uint4 v = *reinterpret_cast<const uint4*>(stage_h + rr * kValueDim + cc * 8);
-          *reinterpret_cast<uint4*>(dst + rr * kValueDim + cc * 8) = v;
-        }
+      constexpr int kChunksPerRow = kValueDim * 2 / 16;
+      __nv_bfloat16* dst = final_out
+                               ? p.out + (static_cast<int64_t>(b) * p.R + row0) * kValueDim
+                               : p.ws_o + ((static_cast<int64_t>(b) * p.max_splits + split) * p.R + row0) * kValueDim;
+      for (int c = threadIdx.x; c < nrows * kChunksPerRow; c += 128) {
+        const int rr = c / kChunksPerRow, cc = c % kChunksPerRow;
+        const uint4 v = *reinterpret_cast<const uint4*>(stage_h + rr * kValueDim + cc * 8);
+        *reinterpret_cast<uint4*>(dst + rr * kValueDim + cc * 8) = v;
       }
     }
   }
@@ -1088,9 +1047,8 @@ cudaError_t launch_decode_partial(const DecodeParams& p, const CUtensorMap& tm_q
     default:
       // at most 32 folded rows (48 of a tree): Q fits in tensor memory, and shared memory takes
       // three tiles
-      if (p.R <= (p.tree_mask ? 48 : 32)) return launch_decode_partial_narrow(p, tm_q, tm_kv, stream);
-      return p.tree_mask ? launch_partial_impl<kKvBf16, true>(p, tm_q, tm_kv, head_groups, stream)
-                         : launch_partial_impl<kKvBf16, false>(p, tm_q, tm_kv, head_groups, stream);
+      if (p.R <= (p.tree_mask ? kTreeNarrowRows : 32)) return launch_decode_partial_narrow(p, tm_q, tm_kv, stream);
+      return launch_partial_impl<kKvBf16, false>(p, tm_q, tm_kv, head_groups, stream);
   }
 }
 

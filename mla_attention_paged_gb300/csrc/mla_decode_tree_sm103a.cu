@@ -1,20 +1,21 @@
 // mla_decode_tree_sm103a.cu -- decode of a tree of drafted tokens over a paged bf16 latent
-// cache for requests of more than 64 folded rows, sm_103a.
+// cache for requests of more than 48 folded rows, sm_103a.
 //
 // What it computes (per request b, draft t, head h, folded row m = t*H + h):
 //   out[b,t,h,:] = sum_j softmax_j(scale * q[b,t,h,:] . k_j) * k_j[:512]
 // over the keys j < L - T and those drafts j = L - T + u whose bit u is set in the row's mask.
-// (Fewer rows: decode_partial_narrow_kernel and decode_partial_kernel, which are bound by reading
-// the cache; with half of its rows empty a pair spent twice the products and measured 272 us
-// against 262 on 16 requests of 8K-131K keys with 64 rows.  8-bit pools: the kernels of their
-// formats.)
+// (Fewer rows: decode_partial_narrow_kernel, which reads the cache faster, 214 us against 228 on 16
+// requests of 8K-131K keys with 48 rows.  8-bit pools: the kernels of their formats.)
 //
 // Why a kernel of its own.  An output row takes 512 fp32 accumulators, so an SM's tensor memory
 // (512 columns of 128 lanes) holds the output of 64 rows beside their scores.  One CTA with
-// 64 rows multiplies at M = 64, half the tensor rate (mla_decode_sm103a.cu reached 0.37 of
-// peak on wide trees).  Here two CTAs of a cluster multiply as a pair (cta_group::2): M = 128
-// rows, 64 in each SM, runs at the full rate (measured: N = 64 / 128 / 256 in 24.8 / 31.9 /
-// 63.9 cycles), and each SM fetches half of the B operand.
+// 64 rows multiplies at M = 64, half the tensor rate (such a kernel reached 0.37 of peak on wide
+// trees, and 262 us where this takes 225 on those requests with 64 rows).  Here two CTAs of a
+// cluster multiply as a pair (cta_group::2): M = 128 rows, 64 in each SM, runs at the full rate
+// (measured: N = 64 / 128 / 256 in 24.8 / 31.9 / 63.9 cycles), and each SM fetches half of the B
+// operand.  Bound by the products on wide trees (0.74 of the bf16 peak in a burst of 268 us on 8
+// requests of 20K-65K keys with 32 x 16 rows; 0.68 sustained, where the board's power is the
+// limit), by reading the cache with one pair a tile (0.84 of the copy rate at 64 rows).
 //  * CTA r of a pair holds rows 64r .. 64r+63 of the group: their Q (shared memory), their S (two
 //    buffers) and O (tensor memory; row i in lanes i and i + 64, which hold half of the
 //    columns each), their softmax and their output.

@@ -13,6 +13,7 @@ constexpr int kLatentDim = 576;  // 512 latent + 64 rope columns
 constexpr int kValueDim = 512;   // value = first 512 latent columns
 constexpr int kTileKeys = 64;    // keys per decode tile
 constexpr int kGroupRows = 64;   // folded query rows per decode CTA
+constexpr int kTreeNarrowRows = 48;  // most rows of a tree over a bf16 pool that one CTA takes
 
 // Formats of the split partials (see DecodeParams).
 constexpr int kPartBf16 = 0;
@@ -173,7 +174,7 @@ cudaError_t launch_decode_partial_e4m3(const DecodeParams& p, const CUtensorMap&
 // tensor memory, a three-tile ring (mla_decode_narrow_sm103a.cu).
 cudaError_t launch_decode_partial_narrow(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv,
                                          cudaStream_t stream);
-// Tree decode over a bf16 pool for requests of more than 64 folded rows (pairs of CTAs).
+// Tree decode over a bf16 pool for requests of more than kTreeNarrowRows folded rows (pairs of CTAs).
 cudaError_t launch_decode_tree_pair(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                     const CUtensorMap& tm_v, cudaStream_t stream);
 int tree_pair_groups(int R);  // pairs along the folded row axis

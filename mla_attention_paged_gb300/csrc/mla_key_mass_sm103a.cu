@@ -240,8 +240,8 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     // may cross from one request into the next, which costs a CTA the new queries and a drained
     // pipe: about a tile's time, on an e4m3 pool, whose queries are split, three.  Runs of whole
     // shares of one request, c tiles each, are taken instead where they are no longer than that
-    // (8 requests of 2K-16K e4m3 keys: 24.7 -> 19.0 us; 16 of 8K-131K bf16 keys keep equal
-    // runs: 191 us against 199).
+    // (8 requests of 2K-16K e4m3 keys: 24.7 -> 19.0 us; on 16 of 8K-131K bf16 keys neither is
+    // better by more than the runs' scatter).
     const int mine = lane < p.B ? tiles_of(lane) : 0;  // (the first 32 requests stay in registers)
     auto tiles = [&](int b0) { return b0 == 0 ? mine : (b0 + lane < p.B ? tiles_of(b0 + lane) : 0); };
     auto sum_of = [&](auto&& f) {

@@ -401,3 +401,56 @@ def test_offsets_past_32_bits(mla):
                                torch.tensor(lens, dtype=torch.int32, device=d), words.to(d), SCALE)
     assert mla.get_status() == mla.MLA_OK
     check(out, lse, reference(q, val, table, lens, words), "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,T,H", [("bf16", 3, 16), ("bf16", 6, 16), ("bf16", 20, 16), ("e4m3", 6, 16)])
+@pytest.mark.parametrize("page", [8, 16, 32, 128])
+def test_not_finite_rows_and_bad_pages_at_other_page_sizes(mla, kind, T, H, page):
+    """NaN drafts and NaN behind the requests' ends, and page ids outside the pool for one of them."""
+    lens = [64 + 2 + T, 500, 259]
+    g = torch.Generator().manual_seed(page)
+    words = random_tree(g, 3, T)
+    words[:, 2:] &= ~2  # only draft 1 sees draft 1
+    words[:, 0] &= ~2
+
+    def spoil(q, pool, table, val):
+        for b, L in enumerate(lens):
+            for j in [L - T + 1] + list(range(L, -(-L // page) * page)):
+                pool[table[b, j // page], j % page] = math.nan if kind == "bf16" else 0x7F
+                val[table[b, j // page], j % page] = 0.0
+
+    out, lse, ref, plan = run(mla, lens, T, H, page, kind, words, seed=5, tweak=spoil)
+    assert torch.isnan(out[:, 1]).all() and torch.isnan(lse[:, 1]).all()
+    keep = [t for t in range(T) if t != 1]
+    ref = tuple(x[:, keep] for x in ref)
+    check(out[:, keep], lse[:, keep], ref, kind)
+    q, pool, table, scales, kv_scale, val = make(lens, T, H, page, kind, 5)
+    spoil(q, pool, table, val)
+    table[0, 0], table[1, 2] = pool.shape[0] + 3, -1
+    d = "cuda"
+    out, lse = mla.decode_tree(plan, q.to(d), pool.to(d), table.to(d), torch.tensor(lens, dtype=torch.int32, device=d),
+                               words.to(d), SCALE, kv_scale)
+    assert mla.get_status() == mla.MLA_ERR_DEVICE_ARG
+    check(out[2:, keep], lse[2:, keep], tuple(x[2:] for x in ref), kind)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,T,H", [("bf16", 2, 16), ("bf16", 3, 16), ("bf16", 4, 16), ("bf16", 8, 16), ("e4m3", 8, 16),
+                                       ("int8", 4, 16)])
+def test_an_ordinary_plan_with_a_trees_workspace(mla, kind, T, H):
+    lens = [4000, 300, 77]
+    words = random_tree(torch.Generator().manual_seed(6), 3, T)
+    q, pool, table, scales, kv_scale, val = make(lens, T, H, 64, kind, 6)
+    d = "cuda"
+    plan = mla.decode_plan(lens, T, H, 64, table.shape[1], pool.shape[0], KINDS[kind])
+    rows = 3 * plan.max_splits * T * H
+    assert plan.max_splits > 1
+    ws = torch.empty(256 + rows * (512 * (4 if kind == "bf16" else 2) + 4), dtype=torch.uint8, device=d)
+    args = (q.to(d), pool.to(d), table.to(d), torch.tensor(lens, dtype=torch.int32, device=d), words.to(d), SCALE, kv_scale)
+    out, lse = mla.decode_tree(plan, *args, workspace=ws)
+    assert mla.get_status() == mla.MLA_OK
+    check(out, lse, reference(q, val, table, lens, words), kind)
+    with pytest.raises(mla.MlaError) as e:
+        mla.decode_tree(plan, *args, workspace=ws[:-256])
+    assert e.value.code == mla.MLA_ERR_WORKSPACE_TOO_SMALL

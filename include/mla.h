@@ -360,7 +360,8 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
  *   mass        : fp32, row b at mass + b * mass_stride (elements; >= plan->max_seq_len); entries from
  *                 L_b on are left as they were.
  *   workspace   : device scratch of the size mla_key_mass_workspace gives for the plan, 256-byte
- *                 aligned (NULL when that is 0); overwritten; calls that share one are stream-ordered.
+ *                 aligned (NULL when that is 0, as it is for at most 128 rows q_len * num_heads);
+ *                 overwritten; calls that share one are stream-ordered.
  * Launched as a programmatic dependent like mla_decode.  Errors: MLA_ERR_INVALID_ARG,
  * MLA_ERR_UNSUPPORTED (tree_mask with more than 64 drafts; batch times the longest request beyond
  * 2^38 keys), MLA_ERR_WORKSPACE_TOO_SMALL, MLA_ERR_CUDA.  Device-side, recorded as

@@ -6,8 +6,8 @@ been built, importing this module raises; there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
-import functools
 import os
 
 import torch
@@ -148,19 +148,20 @@ def _want(what, dev, name, t, dtype, shape=None):
 
 def _want_rows(what, dev, name, t, dtype, rows):
     """A contiguous [rows, any] tensor: its address and row length."""
-    if t.dim() != 2 or t.shape[0] != rows:
-        _refuse(what, f"{name} has shape {tuple(t.shape)}")
-    return _want(what, dev, name, t, dtype), t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows:
+        _refuse(what, f"{name} has shape {tuple(shape)}")
+    return _want(what, dev, name, t, dtype), shape[1]
 
 
 def _want_pool(what, kv_pages, kv_dtype):
-    """The latent pool: its device number and address."""
-    dev = kv_pages.get_device()
-    if kv_pages.dim() != 3 or kv_pages.shape[2] != 576:
-        _refuse(what, f"kv_pages has shape {tuple(kv_pages.shape)}")
-    if kv_pages.dtype not in _POOL_DTYPE.get(kv_dtype, ()):
-        _refuse(what, f"kv_pages is {kv_pages.dtype} for kv_dtype {kv_dtype}")
-    return dev, _want(what, dev, "kv_pages", kv_pages, kv_pages.dtype)
+    """The latent pool: its device number, address, pages and page size."""
+    dev, shape, dtype = kv_pages.get_device(), kv_pages.shape, kv_pages.dtype
+    if len(shape) != 3 or shape[2] != 576:
+        _refuse(what, f"kv_pages has shape {tuple(shape)}")
+    if dtype not in _POOL_DTYPE.get(kv_dtype, ()):
+        _refuse(what, f"kv_pages is {dtype} for kv_dtype {kv_dtype}")
+    return dev, _want(what, dev, "kv_pages", kv_pages, dtype), shape[0], shape[1]
 
 
 def _want_workspace(what, dev, workspace):
@@ -173,23 +174,20 @@ def _want_workspace(what, dev, workspace):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _on_stream(fn):
-    """Run a call whose ``stream`` is given with that stream current, so that what the call allocates
-    belongs to the stream that uses it."""
-    @functools.wraps(fn)
-    def on_stream(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, stream=stream, **kw)
-    return on_stream
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device  # (0.1 us against 0.2)
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(stream):
+    """The context in which a call allocates: what it makes belongs to the stream that uses it."""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
 
 
 def _call(what, dev, stream, fn, *args):
     """fn(*args, stream) on CUDA device number `dev`: its current stream unless one is given."""
     if stream is not None and stream.device_index != dev:
         _refuse(what, f"the stream is on device {stream.device_index}")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with torch.cuda.device(dev):
             return _call(what, dev, stream, fn, *args)
     rc = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
@@ -350,23 +348,24 @@ def prefill_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     return out, lse
 
 
-@_on_stream
 def decode_tree(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_table: torch.Tensor,
                 seq_lens: torch.Tensor, tree_mask: torch.Tensor, scale: float, kv_scale: float = 1.0, page_scales=None,
                 out=None, lse=None, workspace=None, *, stream=None):
     """mla_decode_tree through the C ABI: decode of a tree of drafts.  tree_mask [B,T] int64 (its 64
     bits): bit u of [b, t] = draft t sees draft u.  Returns (out [B,T,H,512] bf16, lse [B,T,H] fp32)."""
     what = "mla_decode_tree"
-    dev, pool = _want_pool(what, kv_pages, plan.kv_dtype)
+    dev, pool, pages, page_size = _want_pool(what, kv_pages, plan.kv_dtype)
     B, T, H = plan.batch, plan.q_len, plan.num_heads
-    if kv_pages.shape[0] != plan.num_pages or kv_pages.shape[1] != plan.page_size:
+    if pages != plan.num_pages or page_size != plan.page_size:
         _refuse(what, f"kv_pages has shape {tuple(kv_pages.shape)}, not the plan's")
-    if out is None:
-        out = torch.empty(B, T, H, 512, dtype=torch.bfloat16, device=kv_pages.device)
-    if lse is None:
-        lse = torch.empty(B, T, H, dtype=torch.float32, device=kv_pages.device)
-    if workspace is None:
-        workspace = workspace_for(plan, kv_pages.device)
+    if out is None or lse is None or workspace is None:
+        with _on(stream):
+            if out is None:
+                out = torch.empty(B, T, H, 512, dtype=torch.bfloat16, device=kv_pages.device)
+            if lse is None:
+                lse = torch.empty(B, T, H, dtype=torch.float32, device=kv_pages.device)
+            if workspace is None:
+                workspace = workspace_for(plan, kv_pages.device)
     ws, ws_bytes = _want_workspace(what, dev, workspace)
     bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     _call(what, dev, stream, lib.mla_decode_tree, plan, _want(what, dev, "q", q, bf16, (B, T, H, 576)), pool,
@@ -378,7 +377,6 @@ def decode_tree(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_
     return out, lse
 
 
-@_on_stream
 def kv_append(q: torch.Tensor | None, kv: torch.Tensor | None, positions: torch.Tensor, slots: torch.Tensor | None,
               cos_sin: torch.Tensor, kv_pages: torch.Tensor | None, kv_weight=None, q_weight=None, eps: float = 1e-6,
               interleaved: bool = True, kv_dtype: int = MLA_KV_BF16, kv_scale: float = 1.0, q_out=None, *, stream=None):
@@ -397,9 +395,10 @@ def kv_append(q: torch.Tensor | None, kv: torch.Tensor | None, positions: torch.
     table, pos = _want(what, dev, "cos_sin", cos_sin, torch.float32), _want(what, dev, "positions", positions, torch.int32, (n,))
     qa = (None, 0, 0, None, 0, 0, 0, 0, None)
     if q is not None:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=bf16, device=q.device)
         shape = q.shape
+        if q_out is None:
+            with _on(stream):
+                q_out = torch.empty(shape, dtype=bf16, device=q.device)
         if q_out.get_device() != dev or dev < 0 or q.dtype is not bf16 or q_out.dtype is not bf16 or len(shape) != 3 or q_out.shape != shape:
             _refuse(what, f"q is {q.dtype} {tuple(shape)} on {q.device}, q_out {q_out.dtype} {tuple(q_out.shape)} on {q_out.device}")
         qt, qh, dense = q.stride()
@@ -413,12 +412,12 @@ def kv_append(q: torch.Tensor | None, kv: torch.Tensor | None, positions: torch.
     if kv is not None:
         if kv_pages is None or slots is None:
             _refuse(what, "kv without kv_pages and slots")
-        pool_dev, pool = _want_pool(what, kv_pages, kv_dtype)
+        pool_dev, pool, pages, page_size = _want_pool(what, kv_pages, kv_dtype)
         if kv.get_device() != dev or pool_dev != dev or kv.dtype is not bf16 or kv.shape != (n, 576) or kv.stride(1) != 1:
             _refuse(what, f"kv is {kv.dtype} {tuple(kv.shape)} on {kv.device}")
         slot = _want(what, dev, "slots", slots, torch.int64, (n,))
         ka = (kv.data_ptr(), kv.stride(0), None if kv_weight is None else _want(what, dev, "kv_weight", kv_weight, bf16, (512,)))
-        rows = kv_pages.shape[0] * kv_pages.shape[1]
+        rows = pages * page_size
     _call(what, dev, stream, lib.mla_kv_append, *qa, *ka, eps, table, cos_sin.shape[0], pos, slot, n, 1 if interleaved else 0,
           pool, rows, kv_dtype, kv_scale)
     return q_out
@@ -431,19 +430,19 @@ def key_mass_workspace_for(plan: DecodePlan, device) -> torch.Tensor | None:
     return torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
 
 
-@_on_stream
 def key_mass(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
              lse: torch.Tensor, mass: torch.Tensor, scale: float, kv_scale: float = 1.0, tree_mask=None, page_scales=None,
              decay: float = 1.0, workspace=None, *, stream=None) -> torch.Tensor:
     """mla_key_mass through the C ABI: mass [B, >= max_seq_len] fp32 becomes decay * mass + the
     attention weight each key received in the step whose lse [B,T,H] this is.  Returns mass."""
     what = "mla_key_mass"
-    dev, pool = _want_pool(what, kv_pages, plan.kv_dtype)
+    dev, pool, pages, page_size = _want_pool(what, kv_pages, plan.kv_dtype)
     B, T, H = plan.batch, plan.q_len, plan.num_heads
-    if kv_pages.shape[0] != plan.num_pages or kv_pages.shape[1] != plan.page_size:
+    if pages != plan.num_pages or page_size != plan.page_size:
         _refuse(what, f"kv_pages has shape {tuple(kv_pages.shape)}, not the plan's")
-    if workspace is None:
-        workspace = key_mass_workspace_for(plan, kv_pages.device)
+    if workspace is None and plan.rows > 128:  # (fewer need none)
+        with _on(stream):
+            workspace = key_mass_workspace_for(plan, kv_pages.device)
     ws, ws_bytes = _want_workspace(what, dev, workspace)
     i32, f32 = torch.int32, torch.float32
     mass_ptr, stride = _want_rows(what, dev, "mass", mass, f32, B)
@@ -456,7 +455,6 @@ def key_mass(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_tab
     return mass
 
 
-@_on_stream
 def kv_evict(kv_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, keep_lens: torch.Tensor,
              mass: torch.Tensor, dst_page_table: torch.Tensor, sink: int, recent: int, max_seq_len: int, max_keep: int,
              kv_dtype: int = MLA_KV_BF16, kept=None, new_lens=None, mass_out=None, *, stream=None):
@@ -465,17 +463,18 @@ def kv_evict(kv_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.T
     ``dst_page_table``.  mass [B, >= max_seq_len] fp32.  Returns (kept [B,max_keep] int32, new_lens
     [B] int32, mass_out [B, >= max_keep] fp32)."""
     what = "mla_kv_evict"
-    dev, pool = _want_pool(what, kv_pages, kv_dtype)
+    dev, pool, pages, page_size = _want_pool(what, kv_pages, kv_dtype)
     B = seq_lens.numel()
     i32, f32 = torch.int32, torch.float32
-    if kept is None:
-        kept = torch.zeros(B, max_keep, dtype=i32, device=kv_pages.device)
-    if new_lens is None:
-        new_lens = torch.zeros(B, dtype=i32, device=kv_pages.device)
-    if mass_out is None:
-        mass_out = torch.zeros(B, max_keep, dtype=f32, device=kv_pages.device)
+    with _on(stream):
+        if kept is None:
+            kept = torch.zeros(B, max_keep, dtype=i32, device=kv_pages.device)
+        if new_lens is None:
+            new_lens = torch.zeros(B, dtype=i32, device=kv_pages.device)
+        if mass_out is None:
+            mass_out = torch.zeros(B, max_keep, dtype=f32, device=kv_pages.device)
     table, dst = _want_rows(what, dev, "page_table", page_table, i32, B), _want_rows(what, dev, "dst_page_table", dst_page_table, i32, B)
-    _call(what, dev, stream, lib.mla_kv_evict, pool, kv_pages.shape[0], kv_pages.shape[1], kv_dtype, *table,
+    _call(what, dev, stream, lib.mla_kv_evict, pool, pages, page_size, kv_dtype, *table,
           _want(what, dev, "seq_lens", seq_lens, i32, (B,)), _want(what, dev, "keep_lens", keep_lens, i32, (B,)),
           *_want_rows(what, dev, "mass", mass, f32, B), *dst, B, sink, recent, max_seq_len, max_keep,
           *_want_rows(what, dev, "kept", kept, i32, B), _want(what, dev, "new_lens", new_lens, i32, (B,)),

@@ -366,7 +366,9 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
  * MLA_ERR_UNSUPPORTED (tree_mask with more than 64 drafts; batch times the longest request beyond
  * 2^38 keys), MLA_ERR_WORKSPACE_TOO_SMALL, MLA_ERR_CUDA.  Device-side, recorded as
  * MLA_ERR_DEVICE_ARG: a length below q_len or beyond the plan (that request's row is left as it
- * was) and a page id outside [0, num_pages) (its rows count as zeros). */
+ * was), a page id outside [0, num_pages) (its rows count as zeros) and, on a page that a request
+ * reads, a page scale outside [0, 255 * kv_scale] or not finite (its keys get no weight: their mass
+ * only decays). */
 int mla_key_mass_workspace(const mla_decode_plan_t* plan, size_t* bytes_out);
 int mla_key_mass(const mla_decode_plan_t* plan, const void* q, const void* kv_pages, const float* page_scales,
                  const int32_t* page_table, const int32_t* seq_lens, const uint64_t* tree_mask,

@@ -22,7 +22,8 @@
 //  * Two groups of four warps take alternate tiles from two S buffers, so exponentials
 //    (R per key) run beside the next tile's product.
 //  * int8 pools: the codes arrive by TMA in a ring of their own; six warps write them into the
-//    K ring as f16, exactly; Q is converted to f16.  A page's scale multiplies its keys' scores.
+//    K ring as f16, exactly; Q is converted to f16.  A page's scale multiplies its keys' scores;
+//    keys of a page whose scale is out of range (reported) get no weight.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -528,9 +529,13 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const bool accumulate = p.groups == 1 && p.decay != 0.f && key < L;
         const float old = accumulate ? *out : 0.f;
         float rel = 1.f;  // the scale of the key's page, relative to kv_scale
+        bool bad_scale = false;
         if (kKv == kKvInt8Page && key < L) {
           const int pid = __ldg(p.page_table + static_cast<int64_t>(b) * p.max_pages + key / p.page_size);
           rel = pid >= 0 && pid < p.num_pages ? __ldg(p.page_scales + pid) * p.inv_ref_scale : 0.f;
+          // the decode's range; beyond it (or NaN) the key's weight would stay in the mass for good
+          bad_scale = !(rel >= 0.f && rel <= 255.f);
+          if (bad_scale) atomicOr(p.status, kStatusDeviceArg);
         }
         fail = __any_sync(0xffffffffu, !mbar_wait(&ctrl->s_full[mine], (t >> 1) & 1, abort_flag));
         if (fail) continue;
@@ -599,7 +604,7 @@ key_mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctrl->s_free[mine]);
-        const float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        const float sum = bad_scale ? 0.f : (acc[0] + acc[1]) + (acc[2] + acc[3]);
         if (key < L) *out = accumulate ? fmaf(p.decay, old, sum) : sum;
       }
       left -= n;

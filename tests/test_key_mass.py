@@ -271,3 +271,36 @@ def test_captured_calls_follow_the_device_inputs(mla, kind, T):
     torch.cuda.synchronize()
     assert torch.equal(md, first)  # the same sums, in the same order
     assert mla.get_status() == mla.MLA_OK
+
+
+# ------------------------------------------------------------------------------ page scales
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 20])  # 20 drafts of 16 heads: row groups, summed by a second kernel
+@pytest.mark.parametrize("decay", [0.0, 0.5])
+@pytest.mark.parametrize("factor", [math.nan, math.inf, -math.inf, -1e-3, 300.0])
+def test_page_scales_out_of_range_are_reported_and_add_nothing(mla, T, decay, factor):
+    """As mla_decode_int8_paged: a scale that is not finite or outside [0, 255 kv_scale] on a page that
+    is read.  Its keys get no weight; a page that no request reads may hold anything."""
+    lens, H, kind = [300, 200], 16, "int8page"
+    q, pool, table, scales, kv_scale, val = make(lens, T, H, 64, kind, 5)
+    lse = true_lse(q, val, table, lens, None)
+    mass = torch.rand(2, 300)
+    new, tol = reference(q, val, table, lens, None, lse, mass, decay, kind)
+    unread = (set(range(pool.shape[0])) - set(table[0, :5].tolist()) - set(table[1, :4].tolist())).pop()
+    d = "cuda"
+    plan = mla.decode_plan(lens, T, H, 64, table.shape[1], pool.shape[0], KINDS[kind])
+    call = lambda m: mla.key_mass(plan, q.to(d), pool.to(d), table.to(d), torch.tensor(lens, dtype=torch.int32, device=d), lse.to(d),
+                                  m, SCALE, kv_scale, page_scales=scales.to(d), decay=decay).cpu().double()
+    scales[unread] = factor
+    got = call(mass.to(d))
+    assert mla.get_status() == mla.MLA_OK
+    assert ((got - new).abs() <= tol).all()
+    # the second page of the first request, the last (partial) one of the other
+    scales[table[0, 1]] = scales[table[1, 3]] = factor * kv_scale
+    for b, j in ((0, slice(64, 128)), (1, slice(192, 200))):
+        new[b, j] = decay * mass[b, j].double()
+        tol[b, j] = 2.0 ** -23 * new[b, j]
+    got = call(mass.to(d))
+    assert mla.get_status() == mla.MLA_ERR_DEVICE_ARG
+    assert ((got - new).abs() <= tol).all()
+    assert mla.get_status() == mla.MLA_OK

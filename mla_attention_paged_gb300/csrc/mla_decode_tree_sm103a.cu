@@ -66,6 +66,8 @@ struct PairCtrl {
   uint64_t p_full;
   uint64_t drain1, drain2;
   // in both CTAs (commits arrive in both)
+  uint64_t v_here[2];  // V of the first or second tile that holds drafts has landed in both (BMM1's
+                       // warp arrives, up to two tiles ahead of the softmax: one barrier each, used once)
   uint64_t k_empty[kKStages];
   uint64_t v_empty[kVStages];
   uint64_t s_full[2];
@@ -103,26 +105,38 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// What one CTA hands the other crosses in shared memory (P, rewritten value rows) and tensor
+// memory (scores read, outputs rescaled; tcgen05 fences on either side).  So an arrival at the other
+// CTA releases, and a wait acquires, at cluster scope.  The release is a fence over the thread's
+// own CTA's shared memory alone: one of all memory took 607-614 us where this takes 297-306 (8 requests
+// of 20K-65K keys with 32 x 16 rows; without scopes 297-303).
+__device__ __forceinline__ void arrive_pair(uint32_t cluster_addr) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+      : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+// The same, passing on what this thread has itself acquired (copies that landed in either CTA).
+__device__ __forceinline__ void arrive_pair_all(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool try_wait_pair(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
 }
-// mbar_wait for barriers that the other CTA (or a commit of the pair) arrives on.
+// mbar_wait for barriers that the other CTA, a copy or a commit of the pair arrives on.
 __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (try_wait_cluster(bar, parity)) return true;
+  if (try_wait_pair(bar, parity)) return true;
   const unsigned long long t0 = global_timer_ns();
   while (true) {
-    if (try_wait_cluster(bar, parity)) return true;
+    if (try_wait_pair(bar, parity)) return true;
     if (*abort_flag) return false;
     if (global_timer_ns() - t0 > kWaitLimitNs) {
       *abort_flag = 1;
@@ -183,6 +197,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctrl->s_full[i], 1);
       mbar_init(&ctrl->s_free[i], kArrivals);
+      mbar_init(&ctrl->v_here[i], 1);
     }
     mbar_init(&ctrl->p_full, kArrivals);
     mbar_init(&ctrl->o_done, 1);
@@ -225,7 +240,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
   const int ntiles = (kv_end - kv_start + kTileKeys - 1) / kTileKeys;
   const int nsplit_b = (L + p.chunk - 1) / p.chunk;
   const int p0 = L - p.T;  // first draft
-  // tiles from here on hold drafts (or the end): their V is touched by the softmax
+  // tiles from here on hold drafts (or the end), two at most (64 drafts): their V is touched by the softmax
   const int tail_tile = max(0, p0 - kv_start) / kTileKeys;
   const int half_rows = group_rows / 2;
   const int row0 = group * group_rows + static_cast<int>(rank) * half_rows;
@@ -345,6 +360,10 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
           commit_pair(&ctrl->k_empty[slot], 3);
         }
         __syncwarp();
+        if (j >= tail_tile) {
+          if (lane < 2) arrive_pair_all(map_rank(smem_u32(&ctrl->v_here[j - tail_tile]), lane));
+          __syncwarp();
+        }
         if (++slot == kKStages) {
           slot = 0;
           phase ^= 1;
@@ -419,7 +438,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_remote(s_free0 + sb * 8);
+        if (lane == 0) arrive_pair(s_free0 + sb * 8);
         uint32_t seen = row_active ? 0xffffu : 0u;
         if (k0 + kTileKeys > p0) seen = row_active ? static_cast<uint32_t>(tree_tile_bits(drafts, p0, k0) >> kb) & 0xffffu : 0u;
         if (seen != 0xffffu) {
@@ -486,8 +505,11 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         tmem_st_wait();
       }
       if (k0 + kTileKeys > p0) {
-        // (BMM1 of such a tile waited for its V in both CTAs.)  Rows past the request's end become
-        // zero, drafts' infinities and NaNs too: rows that do not see them give them weight 0.
+        // V's copies count on barriers of CTA 0, whose BMM1 warp passes their arrival on to both CTAs.
+        // Rows past the request's end become zero, drafts' infinities and NaNs too: rows that do not
+        // see them give them weight 0.
+        fail = __any_sync(0xffffffffu, !wait_pair(&ctrl->v_here[j - tail_tile], 0, abort_flag));
+        if (fail) continue;
         const uint32_t stage = smem_u32(smem + kOffV + (j % kVStages) * kVBytes);
         const int first = max(p0 - k0, 0), valid = min(L - k0, kTileKeys);
         for (int idx = threadIdx.x; idx < (kTileKeys - first) * 8 * kVBlocks; idx += kSoftmaxThreads) {
@@ -502,7 +524,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_remote(p_full0);
+      if (lane == 0) arrive_pair(p_full0);
     }
     if (!failed && !fail) fail = !wait_pair(&ctrl->o_done, (ntiles - 1) & 1, abort_flag);
     if (!failed) ctrl->row_sum[mine][r] = l_sum;

@@ -187,7 +187,9 @@ int mla_decode_int8_paged(const mla_decode_plan_t* plan, const void* q, const vo
  *                 its ancestors and itself; any word is accepted, bits from T on are ignored).
  *   out, lse    : as mla_decode; a draft that sees no key at all (an empty mask over an empty
  *                 prefix) gets out 0 and lse -infinity.
- * An infinity or NaN in a draft's latent row reaches only the drafts that see it.  Launches,
+ * An infinity or NaN in a draft's latent row reaches only the drafts that see it: NaN everywhere, or,
+ * where the score is -infinity and so the weight 0, in the columns that hold it.  (A draft all of whose
+ * scores are -infinity counts as one that sees no key.)  Launches,
  * workspace rules and every other argument and error as mla_decode; also MLA_ERR_UNSUPPORTED for
  * more than 64 drafts. */
 int mla_decode_tree_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads,

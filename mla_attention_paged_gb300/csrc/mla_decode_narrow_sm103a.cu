@@ -54,6 +54,7 @@ struct NarrowCtrl {
   uint64_t p_full;
   uint64_t o_done;
   uint64_t mma_drain;
+  unsigned long long lost;  // trees: drafts that some row sees with a score of -infinity
   uint32_t tmem_base;
   int abort_flag;
   int rescale_flag[kMaxNarrowRows / 16];
@@ -124,6 +125,7 @@ decode_partial_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __g
     mbar_init(&ctrl->o_done, 1);
     mbar_init(&ctrl->mma_drain, 1);
     ctrl->abort_flag = 0;
+    if (kTree) ctrl->lost = 0;
     for (int w = 0; w < kRows / 16; ++w) ctrl->rescale_flag[w] = 0;
     fence_mbarrier_init();
   }
@@ -421,9 +423,13 @@ decode_partial_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __g
           lim = (owns_rows && row_active) ? 31 : -1;
           if (k0 + kTileKeys > p0) {
             const uint32_t seen = static_cast<uint32_t>(tree_tile_bits(drafts, p0, k0) >> (32 * half));
+            uint32_t minus = 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < 32; ++i) {
+              minus |= (sr[i] == 0xff800000u ? 1u : 0u) << i;
               if (!((seen >> i) & 1u)) sr[i] = 0xff800000u;  // -inf: weight 0
+            }
+            if (owns_rows && row_active && (minus & seen)) atomicOr(&ctrl->lost, draft_word(minus & seen, k0 + 32 * half, p0));
           }
         }
         online_softmax_step<32, true>(sr, lim, scale_log2, kRescaleThreshold, m_used, l_sum, packed, alpha,
@@ -568,6 +574,13 @@ decode_partial_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __g
       }
       const __nv_bfloat16* stage_h = reinterpret_cast<const __nv_bfloat16*>(smem + kOffStages);
       named_bar_sync(1, 128);
+      if (kTree && ctrl->lost != 0) {  // (the same in every thread: last changed before the barriers above)
+        pass_on_not_finite<128>(ctrl->lost, p.kv_pool, p.num_pages, p.page_size,
+                                p.page_table + static_cast<int64_t>(b) * p.max_pages, p0,
+                                p.tree_mask + static_cast<int64_t>(b) * p.T, 0, nrows, p.H, stage_s,
+                                kValueDim * (final_out ? 2 : 4), !final_out);
+        named_bar_sync(1, 128);
+      }
       if (kTree && !final_out) {
         static_assert(kRows * kValueDim * 4 <= kStages * kTileBytes, "fp32 staging");
         const uint4* const src = reinterpret_cast<const uint4*>(smem + kOffStages);

@@ -939,7 +939,9 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const D
       const uint32_t src = smem_u32(cs) + (active ? r : 0) * kRowBytes + c8 * (kWide ? 32 : 16);
       for (int s = 0; s < nb; ++s) {
         const float ws_s = __shfl_sync(0xffffffffu, w, s);
-        if (kTree && ws_s == 0.f) continue;  // (a split none of whose keys this row sees; uniform over the row's threads)
+        // (a split none of whose keys this row sees; uniform over the row's threads.  fp32 partials of
+        // such a split are 0, or NaN where a key of score -infinity has an infinite value: added)
+        if (kPart == kPartF16 && ws_s == 0.f) continue;
         if constexpr (kWide) {
           const uint4 lo = ld_shared_v4(src + s * nr * kRowBytes), hi = ld_shared_v4(src + s * nr * kRowBytes + 16);
           const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};

@@ -72,6 +72,7 @@ struct PairCtrl {
   uint64_t v_empty[kVStages];
   uint64_t s_full[2];
   uint64_t o_done;
+  unsigned long long lost;  // drafts that some row sees with a score of -infinity
   uint32_t tmem_base;
   int abort_flag;
   float row_max[2][4][64];  // by tile parity: the four partial maxima of each row
@@ -204,6 +205,7 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     mbar_init(&ctrl->drain1, 1);
     mbar_init(&ctrl->drain2, 1);
     ctrl->abort_flag = 0;
+    ctrl->lost = 0;
     fence_mbarrier_init();
   }
   if (warp == kBmm1Warp) {
@@ -440,7 +442,13 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         __syncwarp();
         if (lane == 0) arrive_pair(s_free0 + sb * 8);
         uint32_t seen = row_active ? 0xffffu : 0u;
-        if (k0 + kTileKeys > p0) seen = row_active ? static_cast<uint32_t>(tree_tile_bits(drafts, p0, k0) >> kb) & 0xffffu : 0u;
+        if (k0 + kTileKeys > p0) {
+          seen = row_active ? static_cast<uint32_t>(tree_tile_bits(drafts, p0, k0) >> kb) & 0xffffu : 0u;
+          uint32_t minus = 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) minus |= (s[i] == 0xff800000u ? 1u : 0u) << i;
+          if (minus & seen) atomicOr(&ctrl->lost, draft_word(minus & seen, k0 + kb, p0));
+        }
         if (seen != 0xffffu) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -575,6 +583,12 @@ decode_tree_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         }
       }
       named_bar_sync(1, kSoftmaxThreads);
+      if (ctrl->lost != 0) {  // (the same in every thread: last changed before the barriers above)
+        pass_on_not_finite<kSoftmaxThreads>(ctrl->lost, p.kv_pool, p.num_pages, p.page_size,
+                                            p.page_table + static_cast<int64_t>(b) * p.max_pages, p0,
+                                            p.tree_mask + static_cast<int64_t>(b) * p.T, row0, nrows, p.H, stage, pitch, !final_out);
+        named_bar_sync(1, kSoftmaxThreads);
+      }
       const int pieces = final_out ? kValueDim * 2 / 16 : kValueDim * 4 / 16;  // per row
       uint4* const dst = final_out ? reinterpret_cast<uint4*>(p.out + (grow - r) * kValueDim)
                                    : reinterpret_cast<uint4*>(p.ws_of + (prow - r) * kValueDim);

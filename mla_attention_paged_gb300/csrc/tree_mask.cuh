@@ -2,6 +2,7 @@
 // 64-key tile a row sees, and draft rows made safe to multiply by a zero weight.
 #pragma once
 
+#include "mla_internal.h"
 #include "sm103a_ptx.cuh"
 
 namespace mla {
@@ -27,8 +28,9 @@ __device__ __forceinline__ uint32_t out_bits(float v, bool final_out) {
 }
 
 // bf16 pairs with infinities and NaNs replaced by zero.  A draft that a row does not see
-// has weight 0 there, but 0 times an infinity or NaN is NaN; rows that do see it have a
-// score that is not finite already, so its value row no longer matters to them.
+// has weight 0 there, but 0 times an infinity or NaN is NaN.  Rows that do see it have a score
+// that is not finite: NaN or +infinity makes the whole row NaN without its values; -infinity
+// is a weight of 0, and pass_on_not_finite gives such rows the NaNs of 0 times infinity.
 __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
   if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
   if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
@@ -61,6 +63,38 @@ __device__ __forceinline__ void make_finite(uint32_t saddr) {
   f.z = kE4m3 ? finite_e4m3x4(v.z) : finite_bf16x2(v.z);
   f.w = kE4m3 ? finite_e4m3x4(v.w) : finite_bf16x2(v.w);
   if ((f.x ^ v.x) | (f.y ^ v.y) | (f.z ^ v.z) | (f.w ^ v.w)) st_shared_v4(saddr, f.x, f.y, f.z, f.w);
+}
+
+// A 32-bit word of keys first .. first + 31 of a request as a word of its drafts (p0: the first one).
+__device__ __forceinline__ uint64_t draft_word(uint32_t keys, int first, int p0) {
+  const int d = p0 - first;  // (below 64 for keys that may be drafts)
+  return d >= 0 ? static_cast<uint64_t>(keys) >> d : static_cast<uint64_t>(keys) << -d;
+}
+
+// Staged output rows (a row's 512 columns `pitch` bytes from the last one's, fp32 or bf16) become
+// NaN in the columns in which a draft of `lost` that they see holds an infinity or NaN in the
+// bf16 pool.  lost: the drafts that some row sees with a score of -infinity.  For all threads
+// 0 .. kThreads - 1, between barriers.
+template <int kThreads>
+__device__ __noinline__ void pass_on_not_finite(uint64_t lost, const uint8_t* pool, int64_t num_pages, int page_size,
+                                                const int32_t* pages, int p0, const uint64_t* masks, int row0, int nrows,
+                                                int heads, uint32_t stage, int pitch, bool fp32) {
+  for (; lost != 0; lost &= lost - 1) {
+    const int u = __ffsll(static_cast<long long>(lost)) - 1, j = p0 + u;
+    const int64_t pid = __ldg(pages + j / page_size);
+    if (pid < 0 || pid >= num_pages) continue;
+    const uint32_t* row = reinterpret_cast<const uint32_t*>(pool) + (pid * page_size + j % page_size) * (kLatentDim / 2);
+    for (int c = threadIdx.x; c < kValueDim / 2; c += kThreads) {
+      const uint32_t w = __ldg(row + c), gone = w ^ finite_bf16x2(w);
+      if (gone == 0) continue;
+      for (int r = 0; r < nrows; ++r) {
+        if (!((masks[(row0 + r) / heads] >> u) & 1)) continue;
+        const uint32_t at = stage + r * pitch + c * (fp32 ? 8 : 4);
+        if (gone & 0xFFFFu) fp32 ? st_shared_f32(at, NAN) : st_shared_u16(at, 0x7FFFu);
+        if (gone >> 16) fp32 ? st_shared_f32(at + 4, NAN) : st_shared_u16(at + 2, 0x7FFFu);
+      }
+    }
+  }
 }
 
 }  // namespace mla

@@ -454,3 +454,61 @@ def test_an_ordinary_plan_with_a_trees_workspace(mla, kind, T, H):
     with pytest.raises(mla.MlaError) as e:
         mla.decode_tree(plan, *args, workspace=ws[:-256])
     assert e.value.code == mla.MLA_ERR_WORKSPACE_TOO_SMALL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H", [(3, 8), (3, 16), (4, 16), (6, 16), (20, 16), (64, 2)])  # 24, 48, 64, 96, 320, 128 rows
+@pytest.mark.parametrize("page,sms", [(64, 1), (64, 0), (8, 0), (128, 0)])
+def test_one_infinity_in_a_draft_reaches_those_that_see_it(mla, T, H, page, sms):
+    """An infinite value whose score is -infinity has weight 0, and 0 x infinity is NaN in its column, in
+    the rows that see it and no other; in the rotated columns it is no value, and the key alone is lost."""
+    lens = [576 + T, 500, 130 + T, 64 + T]
+    words = random_tree(torch.Generator().manual_seed(T), 4, T)
+    words[:, 2:] &= ~2  # draft 1 is seen by itself and, where there is one, by the last draft alone
+    words[:, 0] &= ~2
+    words[:, T - 1] |= 2
+    # request: column and value of draft 1; the last request's infinity lies in its prefix, which all see
+    where = [(5, math.inf, None), (300, -math.inf, None), (540, math.inf, None), (511, math.inf, 10)]
+
+    def spoil(q, pool, table, val):
+        q[..., ::2, :] = q[..., ::2, :].abs()       # even heads: the score has the infinity's sign
+        q[..., 1::2, :] = -q[..., 1::2, :].abs()
+        q[q == 0] = 0.01
+        for b, (c, v, j) in enumerate(where):
+            j = lens[b] - T + 1 if j is None else j
+            pool[table[b, j // page], j % page, c] = v
+            val[table[b, j // page], j % page, c] = 0.0
+
+    q, pool, table, scales, kv_scale, val = make(lens, T, H, page, "bf16", 3)
+    spoil(q, pool, table, val)
+    plan = mla.decode_tree_plan(lens, T, H, page, table.shape[1], pool.shape[0], 0, sms)
+    d = "cuda"
+    out, lse = mla.decode_tree(plan, q.to(d), pool.to(d), table.to(d), torch.tensor(lens, dtype=torch.int32, device=d), words.to(d),
+                               SCALE)
+    assert mla.get_status() == mla.MLA_OK
+    out, lse = out.cpu(), lse.cpu()
+    # rows whose score is -infinity give the key no weight: the reference without it
+    ref = list(reference(q, val, table, lens, words & ~2))
+    for b, (c, v, j) in enumerate(where):
+        sees = ((words[b] >> 1) & 1).bool() if j is None else torch.ones(T, dtype=torch.bool)
+        up = torch.arange(H) % 2 == (0 if v > 0 else 1)
+        lost = sees[:, None] & up[None]             # a score of +infinity
+        some = sees[:, None] & ~up[None]            # a score of -infinity
+        assert torch.isnan(out[b][lost]).all() and not torch.isfinite(lse[b][lost]).any()
+        if j is not None:  # without the prefix key: its weight is exp(-infinity)
+            rows = rows_of(val, table, b, lens[b])
+            x = (q[b].double().reshape(T * H, 576) @ rows.T * SCALE).view(T, H, -1)
+            x[..., j] = -math.inf
+            for t in range(T):
+                for u in range(T):
+                    if not (int(words[b, t]) >> u) & 1:
+                        x[t, :, lens[b] - T + u] = -math.inf
+            ref[1][b] = torch.logsumexp(x, -1)
+            w = torch.exp(x - ref[1][b][..., None])
+            ref[0][b] = w @ rows[:, :512]
+            ref[2][b] = w @ rows[:, :512].abs()
+        if c < 512:
+            assert torch.isnan(out[b, :, :, c][some]).all()
+            out[b, :, :, c] = torch.where(some, ref[0][b, :, :, c].to(out.dtype), out[b, :, :, c])
+        keep = ~lost
+        check(out[b][keep], lse[b][keep], tuple(r[b][keep] for r in ref), "bf16")

@@ -26,6 +26,20 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   return x < y + bn && y < x + an;
 }
 
+// Whether two sets of `rows` rows (addresses, strides and lengths in bytes) share memory.  Rows of one
+// stride may lie side by side, as column ranges of one buffer; of two strides, the spans decide.
+bool rows_overlap(const void* a, int64_t a_stride, int64_t a_len, const void* b, int64_t b_stride, int64_t b_len, int64_t rows) {
+  if (a_len == 0 || b_len == 0) return false;
+  if (!overlap(a, (rows - 1) * a_stride + a_len, b, (rows - 1) * b_stride + b_len)) return false;
+  if (a_stride != b_stride || rows == 1) return true;
+  // row i + k of b lies at `off` + k strides from row i of a, k in (-rows, rows)
+  const int64_t off = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  const int64_t k0 = -off / a_stride;  // the rows of b that come near a's
+  for (int64_t k = k0 - 1; k <= k0 + 1; ++k)
+    if (k > -rows && k < rows && off + k * b_stride < a_len && off + k * b_stride + b_len > 0) return true;
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -210,8 +224,8 @@ int mla_kv_evict(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype,
   if (mass_stride < max_seq_len || kept_stride < max_keep || mass_out_stride < max_keep) return MLA_ERR_INVALID_ARG;
   // the copy reads mass while it writes mass_out, and lengths while it writes new ones
   const size_t B = static_cast<size_t>(batch);
-  if (overlap(mass, B * mass_stride * 4, mass_out, B * mass_out_stride * 4) || overlap(seq_lens, B * 4, new_lens, B * 4) ||
-      overlap(keep_lens, B * 4, new_lens, B * 4))
+  if (rows_overlap(mass, mass_stride * 4, int64_t(max_seq_len) * 4, mass_out, mass_out_stride * 4, int64_t(max_keep) * 4, batch) ||
+      overlap(seq_lens, B * 4, new_lens, B * 4) || overlap(keep_lens, B * 4, new_lens, B * 4))
     return MLA_ERR_INVALID_ARG;
   EvictParams p;
   memset(&p, 0, sizeof p);

@@ -251,3 +251,48 @@ def test_captured_with_new_lengths_and_masses(mla):
             ids = torch.tensor(ids, device=d)
             assert torch.equal(pool[dst[b].long()[i // 16], i % 16], pool[table[b].long()[ids // 16], ids % 16])
     assert mla.get_status() == mla.MLA_OK
+
+
+@pytest.mark.gpu
+def test_mass_and_mass_out_as_column_ranges_of_one_buffer(mla):
+    """Rows that lie side by side do not overlap; one column in common does."""
+    d = "cuda"
+    B, L, keep, P = 3, 200, 90, 64
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=d)
+    both = torch.rand(B, 320, device=d)
+    was = both.clone()
+    mass = both[:, 10:210].cpu()
+    pool = torch.randint(0, 99, (20, P, 576)).bfloat16().to(d)
+    table, dst = torch.arange(12, dtype=torch.int32, device=d).view(B, 4), torch.arange(12, 18, dtype=torch.int32, device=d).view(B, 2)
+    kept, new_lens = torch.zeros(B, keep, dtype=torch.int32, device=d), i32([0] * B)
+    lens, keeps = i32([L, 150, 97]), i32([keep, 60, 89])
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def call(at, out_stride=320, max_keep=keep):
+        return mla.lib.mla_kv_evict(pool.data_ptr(), 20, P, 0, table.data_ptr(), 4, lens.data_ptr(), keeps.data_ptr(),
+                                    both.data_ptr() + 40, 320, dst.data_ptr(), 2, B, 2, 3, L, max_keep, kept.data_ptr(), keep,
+                                    new_lens.data_ptr(), both.data_ptr() + 4 * at, out_stride, stream)
+
+    for at, stride in ((209, 320), (10 - keep + 1 + 320, 320), (0, 320), (60, 320), (210, 319)):
+        assert call(at, stride) == mla.MLA_ERR_INVALID_ARG
+    assert torch.equal(both, was)
+    assert call(210) == mla.MLA_OK and mla.get_status() == mla.MLA_OK
+    for b, (n, k) in enumerate(((L, keep), (150, 60), (97, 89))):
+        ids = chosen(mass[b], n, k, 2, 3)
+        assert kept[b, :k].tolist() == ids
+        assert torch.equal(both[b, 210:210 + k].cpu(), mass[b, ids])
+        assert torch.equal(both[b, 210 + k:], was[b, 210 + k:]) and torch.equal(both[b, :210], was[b, :210])
+
+
+def test_every_overlap_of_mass_and_mass_out_is_refused(mla):
+    """All offsets (elements) at which some row of one touches a row of the other, strides equal or not."""
+    base = 1 << 16
+    for B, stride, n, keep in ((1, 256, 100, 60), (2, 128, 100, 60), (3, 161, 100, 60), (3, 160, 160, 160)):
+        rows = {b * stride + i for b in range(B) for i in range(n)}
+        for out_stride in (stride, stride + 3):
+            for off in range(-keep - (B - 1) * out_stride - 2, B * stride + 2):
+                out = {off + b * out_stride + i for b in range(B) for i in (0, keep - 1)}
+                out |= {off + b * out_stride + i for b in range(B) for i in range(0, keep, 7)}
+                if rows & out:
+                    assert _raw(mla, batch=B, mass=base, mass_stride=stride, max_seq=n, max_keep=keep, kept_stride=keep,
+                                kept=1 << 24, mass_out=base + 4 * off, out_stride=out_stride) == mla.MLA_ERR_INVALID_ARG

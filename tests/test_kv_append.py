@@ -275,3 +275,31 @@ def test_captured_and_on_another_stream(mla):
     torch.cuda.synchronize()
     assert torch.equal(out, first) and torch.equal(pool, rows)
     assert mla.get_status() == mla.MLA_OK
+
+
+MANY = [  # tokens x heads above 12288: two steps of four heads a warp, 16 lanes a key
+    # n, heads, q_dim, kind, interleaved, q norm, kv norm, padded tokens
+    (129, 128, 64, "bf16", True, False, True, 9),        # 16512 rows, rotated columns alone
+    (1025, 13, 64, "e4m3", False, True, True, 100),      # 13325: a step that is partly past the heads
+    (769, 16, 192, "bf16", False, False, True, 0),       # 12304
+    (800, 16, 192, "int8", True, True, False, 33),
+    (2050, 7, 168, "e4m3", True, True, True, 1),         # 14350: chunks that do not fill the lanes
+    (999, 13, 576, "bf16", True, True, True, 17),        # wide rows: two turns of one step
+    (1300, 10, 320, "e4m3", False, False, True, 0),
+    (1541, 8, 264, "int8", False, True, True, 5),        # 12328
+    (12289, 1, 192, "bf16", True, True, True, 3),        # one head: three of a step's four rows are idle
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,heads,dim,kind,inter,qn,kn,pad", MANY)
+def test_many_rows_against_the_formulas(mla, n, heads, dim, kind, inter, qn, kn, pad):
+    test_against_the_formulas(mla, n, heads, dim, 64, kind, inter, qn, kn, pad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,dim", [(96, 192), (97, 192), (96, 576), (97, 576), (96, 64), (97, 64)])
+def test_both_sides_of_the_many_rows_border(mla, n, dim):
+    """12288 rows still run as few, 12416 as many."""
+    for inter in (True, False):
+        test_against_the_formulas(mla, n, 128, dim, 64, "bf16", inter, dim > 64, True, 2)

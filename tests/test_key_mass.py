@@ -304,3 +304,27 @@ def test_page_scales_out_of_range_are_reported_and_add_nothing(mla, T, decay, fa
     assert mla.get_status() == mla.MLA_ERR_DEVICE_ARG
     assert ((got - new).abs() <= tol).all()
     assert mla.get_status() == mla.MLA_OK
+
+
+# ------------------------------------------------------------------------------ workspace
+@pytest.mark.parametrize("T,groups", [(1, 1), (8, 1), (20, 3), (64, 8)])
+@pytest.mark.parametrize("kv", [0, 1, 2, 3])
+def test_workspace_holds_the_row_groups_sums(mla, kv, T, groups):
+    """One fp32 sum per row group, request and key; at most 128 rows are one group and need none."""
+    plan = mla.decode_plan([9000, 300], T, 16, 64, 200, 400, kv, 152)
+    need = ctypes.c_size_t(7)
+    assert mla.lib.mla_key_mass_workspace(ctypes.byref(plan), ctypes.byref(need)) == mla.MLA_OK
+    assert need.value == (0 if groups == 1 else groups * 2 * 9000 * 4)
+    ps = 1 << 9 if kv == 3 else None
+    if need.value:
+        assert _raw(mla, plan, ps=ps, ws=None) == mla.MLA_ERR_INVALID_ARG
+        assert _raw(mla, plan, ps=ps, ws=(1 << 26) + 8) == mla.MLA_ERR_INVALID_ARG
+        assert _raw(mla, plan, ps=ps, wsb=need.value - 1) == mla.MLA_ERR_WORKSPACE_TOO_SMALL
+
+
+def test_the_workspace_begins_at_129_rows(mla):
+    need = ctypes.c_size_t(7)
+    for T, bytes_ in ((128, 0), (129, 2 * 2 * 9000 * 4)):
+        plan = mla.decode_plan([9000, 300], T, 1, 64, 200, 400, 0, 152)
+        assert mla.lib.mla_key_mass_workspace(ctypes.byref(plan), ctypes.byref(need)) == mla.MLA_OK
+        assert need.value == bytes_

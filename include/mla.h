@@ -334,7 +334,8 @@ int mla_prefill_paged(const void* q, const void* k_pages, const void* v_pages, c
  *                 not negative must differ: a row that two tokens name holds bytes of either.
  *   kv_pages    : the pool, num_slots = num_pages * page_size rows of 576 elements of kv_dtype.
  *   kv_scale    : scale of an e4m3 or int8 pool (ignored for bf16).
- * Pointers are 16-byte aligned (positions 4, slots 8).  kv_in lies outside the pool.
+ * Pointers are 16-byte aligned (positions 4, slots 8).  kv_in, q_in and q_out lie outside the pool, and
+ * q_out holds no element of kv_in, the weights, cos_sin, positions or slots.
  * Rows that no token names are left as they were.  num_tokens 0 does nothing.  Launched as a programmatic dependent like mla_decode.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (num_heads > 1024, another q_dim, num_tokens >
  * 2^20, an MLA_KV_INT8_PAGE pool, whose page scales cannot follow new rows), MLA_ERR_CUDA.

@@ -64,6 +64,7 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
   if (num_tokens == 0) return MLA_OK;
   if (!has_q && !has_kv) return MLA_ERR_INVALID_ARG;
   if (!cos_sin || !positions || !aligned(cos_sin, 16) || !aligned(positions, 4)) return MLA_ERR_INVALID_ARG;
+  const size_t pool_bytes = num_slots < 1 ? 0 : static_cast<size_t>(num_slots) * kLatentDim * (kv_dtype == MLA_KV_BF16 ? 2 : 1);
   if (has_q) {
     if (!q_out || !aligned(q_in, 16) || !aligned(q_out, 16) || (q_weight && !aligned(q_weight, 16)))
       return MLA_ERR_INVALID_ARG;
@@ -76,7 +77,10 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
     const auto span = [&](int64_t token, int64_t head) {
       return static_cast<size_t>((num_tokens - 1) * token + (num_heads - 1) * head + q_dim) * 2;
     };
-    if (!in_place && overlap(q_in, span(q_in_token_stride, q_in_head_stride), q_out, span(q_out_token_stride, q_out_head_stride)))
+    const size_t in_span = span(q_in_token_stride, q_in_head_stride), out_span = span(q_out_token_stride, q_out_head_stride);
+    if (!in_place && overlap(q_in, in_span, q_out, out_span)) return MLA_ERR_INVALID_ARG;
+    // the same pass writes the pool's rows
+    if (has_kv && (overlap(q_in, in_span, kv_pages, pool_bytes) || overlap(q_out, out_span, kv_pages, pool_bytes)))
       return MLA_ERR_INVALID_ARG;
   }
   if (has_kv) {
@@ -85,8 +89,7 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
       return MLA_ERR_INVALID_ARG;
     if (kv_dtype != MLA_KV_BF16 && !(kv_scale > 0.f)) return MLA_ERR_INVALID_ARG;
     // a row may be written while another of the pool's is still to be read
-    if (overlap(kv_in, static_cast<size_t>((num_tokens - 1) * kv_in_token_stride + kLatentDim) * 2, kv_pages,
-                static_cast<size_t>(num_slots) * kLatentDim * (kv_dtype == MLA_KV_BF16 ? 2 : 1)))
+    if (overlap(kv_in, static_cast<size_t>((num_tokens - 1) * kv_in_token_stride + kLatentDim) * 2, kv_pages, pool_bytes))
       return MLA_ERR_INVALID_ARG;
   }
   AppendParams p;

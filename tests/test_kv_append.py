@@ -303,3 +303,10 @@ def test_both_sides_of_the_many_rows_border(mla, n, dim):
     """12288 rows still run as few, 12416 as many."""
     for inter in (True, False):
         test_against_the_formulas(mla, n, 128, dim, 64, "bf16", inter, dim > 64, True, 2)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q_out=(1 << 30) + 1152), dict(q_out=(1 << 30) - 384), dict(q_out=(1 << 30) + 64 * 1152 - 16),
+    dict(q_in=(1 << 30) + 64), dict(q_in=(1 << 30) - 16), dict(q_in=1 << 30, q_out=1 << 30)])
+def test_queries_inside_the_pool_are_refused(mla, bad):
+    assert _raw(mla, **bad) == mla.MLA_ERR_INVALID_ARG

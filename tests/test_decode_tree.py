@@ -512,3 +512,23 @@ def test_one_infinity_in_a_draft_reaches_those_that_see_it(mla, T, H, page, sms)
             out[b, :, :, c] = torch.where(some, ref[0][b, :, :, c].to(out.dtype), out[b, :, :, c])
         keep = ~lost
         check(out[b][keep], lse[b][keep], tuple(r[b][keep] for r in ref), "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,T,H", [("bf16", 2, 16), ("bf16", 3, 16), ("bf16", 5, 16), ("bf16", 8, 16), ("bf16", 12, 16),
+                                       ("e4m3", 8, 16), ("int8", 5, 16)])
+def test_an_ordinary_decode_on_a_trees_plan(mla, kind, T, H):
+    """mla_decode accepts the plan of a tree, whose chunks and launch order a pair's cost chose."""
+    lens = [9000, 300, 77 + T] + [500 + 64 * i for i in range(20)]
+    words = torch.tensor([[(2 << t) - 1 for t in range(T)]] * len(lens))
+    q, pool, table, scales, kv_scale, val = make(lens, T, H, 64, kind, 7)
+    d = "cuda"
+    for sms in (0, 8):
+        plan = mla.decode_tree_plan(lens, T, H, 64, table.shape[1], pool.shape[0], KINDS[kind], sms)
+        out, lse = mla.decode(plan, q.to(d), pool.to(d), table.to(d), torch.tensor(lens, dtype=torch.int32, device=d), SCALE, kv_scale)
+        assert mla.get_status() == mla.MLA_OK
+        ref = reference(q, val, table, lens, words)
+        # (bf16 partials of a split request: one more rounding, 2^-8 of the weighted values)
+        assert ((lse.cpu().double() - ref[1]).abs() <= 2.0 ** -17 * ref[3] + ref[4] + 2.0 ** -20 * (1 + ref[1].abs())).all()
+        tol = 2.0 ** -8 * ref[0].abs() + (2.0 ** -7 + 2 * (2.0 ** -17 * ref[3] + ref[4])[..., None] + 2.0 ** -17) * ref[2] + ref[5][..., None]
+        assert ((out.cpu().double() - ref[0]).abs() <= tol).all()

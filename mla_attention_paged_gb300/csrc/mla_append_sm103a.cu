@@ -129,7 +129,7 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale, bool i
 }
 
 // kChunks: most chunks of a query lane that are not rotated, ceil((q_dim - 64) / 64).
-// kSteps: four heads a step.  kKeyLanes: lanes that share a key's row.  Five CTAs an SM (102
+// kSteps: four heads a step.  kKeyLanes: lanes that share a key's row.  Five CTAs an SM (96
 // registers) measured 22.8 us on 8191 tokens of 16 normed 192-wide heads against 25.0 at four and
 // 29 spilling at six; streaming loads and stores (nothing is read again) 24.6 against 26.8.
 // The first k_warps warps of the grid take keys, the others queries.
@@ -255,9 +255,11 @@ __global__ void __launch_bounds__(32 * kWarps, kChunks <= 2 ? 5 : 1) kv_append_k
 
 template <int kChunks>
 cudaError_t launch_chunks(const AppendParams& p, cudaStream_t stream) {
-  // Few rows: one step and a warp per key, for the shortest chain (4 tokens of 16 heads 2.1
-  // against 2.6 us, 512 normed 192-wide 3.05 against 3.18); many: more bytes in flight per warp
-  // (2048 tokens 7.1 against 8.2 us).
+  // Few rows: one step and a warp per key, for the shortest chain; many: more bytes in flight per
+  // warp.  GPU us, few against many, by tokens x heads: 16 heads of 192 normed columns 2.8 / 3.1 at
+  // 8192, 4.2 / 3.6 at 12288, 4.7 / 4.3 at 16384, 11.6 / 10.1 at 49152; 64 columns 2.4 / 2.8, 2.5 / 2.9,
+  // 2.6 / 3.1, 6.1 / 5.3; 8 heads of 576 normed 7.9 / 6.9, 10.7 / 8.9, 13.0 / 11.2, 36.7 / 27.4.  (Wide
+  // rows cross at about 9000, 64 columns at about 20000: one border between them for all.)
   const bool few = static_cast<int64_t>(p.tokens) * (p.heads > 0 ? p.heads : 16) <= kFewRows;
   const int steps = few ? 1 : kManySteps, key_rows = few ? 1 : 32 / kManyKeyLanes;
   const int per_token = (p.heads + 4 * steps - 1) / (4 * steps);

@@ -39,3 +39,12 @@ def test_prefill_flops_by_enumeration(prefix, new, H):
         for i in range(n):
             pairs += sum(1 for j in range(p + n) if j <= p + i)
     assert bench.prefill_flops(wl) == 2 * H * (192 + 128) * pairs
+
+
+def test_the_headlines_traffic_record_belongs_to_the_sources():
+    """The DRAM bytes that the bench line quotes were measured on the kernel as it is now."""
+    import bench
+    record = bench._traffic_record(bench.WORKLOAD)
+    assert record is not None, "profiles/decode_partial_traffic.json was taken on other sources"
+    assert record["dram_bytes_per_launch"] == record["dram_bytes_read"] + record["dram_bytes_write"]
+    assert 1.0 <= record["dram_bytes_per_launch"] / record["algorithmic_bytes_per_launch"] < 1.02

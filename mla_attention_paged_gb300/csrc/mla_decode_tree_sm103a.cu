@@ -13,9 +13,9 @@
 // trees, and 262 us where this takes 225 on those requests with 64 rows).  Here two CTAs of a
 // cluster multiply as a pair (cta_group::2): M = 128 rows, 64 in each SM, runs at the full rate
 // (measured: N = 64 / 128 / 256 in 24.8 / 31.9 / 63.9 cycles), and each SM fetches half of the B
-// operand.  Bound by the products on wide trees (0.74 of the bf16 peak in a burst of 268 us on 8
-// requests of 20K-65K keys with 32 x 16 rows; 0.66 sustained, where the board's power is the
-// limit), by reading the cache with one pair a tile (0.84 of the copy rate at 64 rows).
+// operand.  Bound by shared memory and the products on wide trees (0.71 of the bf16 peak in a burst of
+// 279 us on 8 requests of 20K-65K keys with 32 x 16 rows; 0.65 sustained, where the board's power is
+// the limit), by reading the cache with one pair a tile (0.80-0.84 of the copy rate at 64 rows).
 //  * CTA r of a pair holds rows 64r .. 64r+63 of the group: their Q (shared memory), their S (two
 //    buffers) and O (tensor memory; row i in lanes i and i + 64, which hold half of the
 //    columns each), their softmax and their output.

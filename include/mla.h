@@ -70,6 +70,14 @@ typedef enum mla_kv_dtype_t {
   MLA_KV_INT8_PAGE = 3 /* int8 codes, each page with its own scale: a latent element is its
                         * code times the scale of the page that holds its row (the other
                         * INT8 form the talk leaves open); decoded by mla_decode_int8_paged  */
+  , MLA_KV_FP4 = 4 /* 336 bytes a latent row, all values in units of one kv_scale:
+                    *   0..255   columns 0..511, eight to a 32-bit little-endian word: column 8w + i has its
+                    *            e2m1 magnitude code (0, 1/2, 1, 3/2, 2, 3, 4, 6) in bits 4i..4i+2 and its
+                    *            sign in bit 8i + 7 (i < 4) or 8 (i - 4) + 3; the value is the magnitude times
+                    *            2^(e-5) with the exponent e of its 16 columns
+                    *   256..271 the exponents e, 0..11, of columns 16g..16g+15: a nibble each, low first
+                    *            (12..15 do not occur; they read as some finite value)
+                    *   272..335 the 64 rotated columns as e4m3 codes                               */
 } mla_kv_dtype_t;
 
 /* Decode plan: a plain value struct filled by mla_decode_plan(); callers treat the

@@ -105,7 +105,7 @@ std::unordered_map<std::string, mla_decode_plan_t> g_plan_cache;
 // int8 one and streams in about half the time, while the start-up (Q load and split, the
 // first tiles' latency) and the epilogue take about as long.
 constexpr long long kCombineTiles = 2;
-long long cta_fixed_tiles(int kv_dtype) { return kv_dtype == MLA_KV_E4M3 ? 10 : 3; }
+long long cta_fixed_tiles(int kv_dtype) { return kv_dtype == MLA_KV_E4M3 ? 10 : kv_dtype == MLA_KV_FP4 ? 6 : 3; }
 // (A pair takes about half as long for a tile as one CTA, and its start as long.  4 requests of 3K-12K
 // keys with 192 rows: 27.4 us planned with 5 to 16, 30.0 with 3; seven other sizes from 1000 keys to
 // 16 requests of 131K alike with 3 to 16.)
@@ -180,12 +180,12 @@ long long plan_cost(const std::vector<int>& tiles, int groups, int ct, int sms, 
 // with an e4m3 pool's larger fixed cost, 109 and remainders of 43.)  The candidate with the
 // lowest plan_cost wins, the one with fewer splits on a tie, so a split is only taken when
 // the model says it shortens the call.
-int choose_chunk_tiles(const std::vector<int>& lens, int groups, int sms, long long fixed) {
+int choose_chunk_tiles(const std::vector<int>& lens, int tile_keys, int groups, int sms, long long fixed) {
   std::vector<int> tiles;
   tiles.reserve(lens.size());
   int max_tiles = 1;
   for (int L : lens) {
-    tiles.push_back((L + kTileKeys - 1) / kTileKeys);
+    tiles.push_back((L + tile_keys - 1) / tile_keys);
     max_tiles = std::max(max_tiles, tiles.back());
   }
   auto ctas = [&](int ct) {
@@ -294,8 +294,7 @@ int make_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads,
   if (!seq_lens_host || !plan_out || batch < 1 || q_len < 1 || num_heads < 1 || max_pages_per_seq < 1 ||
       num_pages < 1)
     return MLA_ERR_INVALID_ARG;
-  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_E4M3 && kv_dtype != MLA_KV_INT8 && kv_dtype != MLA_KV_INT8_PAGE)
-    return MLA_ERR_INVALID_ARG;
+  if (!kv_dtype_ok(kv_dtype)) return MLA_ERR_INVALID_ARG;
   // q_len beyond a few drafts is the prefill of q_len new tokens over a paged prefix in
   // absorbed form (the same computation: new token t sees keys 0 .. L - q_len + t)
   if (q_len > 8192 || !page_size_ok(page_size) || static_cast<int64_t>(q_len) * num_heads > 131072)
@@ -339,13 +338,15 @@ int make_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads,
   pl.num_pages = num_pages;
   pl.num_sms = num_sms;
   pl.rows = q_len * num_heads;
-  pl.head_groups = (pl.rows + kGroupRows - 1) / kGroupRows;
+  const int group_rows = kv_dtype == MLA_KV_FP4 ? fp4_group_rows(pl.rows) : kGroupRows;
+  pl.head_groups = (pl.rows + group_rows - 1) / group_rows;
   // a tree over a bf16 pool with more than 48 rows runs on pairs of CTAs (and SMs)
   const bool pairs = tree && kv_dtype == MLA_KV_BF16 && pl.rows > kTreeNarrowRows;
   const int groups = pairs ? tree_pair_groups(pl.rows) : pl.head_groups;
   const int units = pairs ? std::max(1, num_sms / 2) : num_sms;
-  const int ct = choose_chunk_tiles(lens, groups, units, pairs ? kPairFixedTiles : cta_fixed_tiles(kv_dtype));
-  pl.chunk_tokens = ct * kTileKeys;
+  const int tile_keys = kv_dtype == MLA_KV_FP4 ? kFp4TileKeys : kTileKeys;
+  const int ct = choose_chunk_tiles(lens, tile_keys, groups, units, pairs ? kPairFixedTiles : cta_fixed_tiles(kv_dtype));
+  pl.chunk_tokens = ct * tile_keys;
   pl.max_seq_len = max_len;
   pl.max_splits = (max_len + pl.chunk_tokens - 1) / pl.chunk_tokens;
   if (pl.max_splits > 65535) return MLA_ERR_UNSUPPORTED;
@@ -436,7 +437,7 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
   // swizzled column blocks the MMAs read, in a single TMA instruction.
   CUtensorMap tm_q, tm_kv;
   memset(&tm_q, 0, sizeof tm_q);
-  if (partial) {
+  if (partial && plan->kv_dtype != MLA_KV_FP4) {  // (the 4-bit kernel reads q and pages by address)
     const uint64_t dims[3] = {64, static_cast<uint64_t>(plan->batch) * plan->rows, kLatentDim / 64};
     const uint64_t strides[2] = {row_bytes, 128};
     const uint32_t box[3] = {64, static_cast<uint32_t>(kGroupRows), kLatentDim / 64};
@@ -507,6 +508,7 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
   p.v_scale = kv8 ? kv_scale : 1.f;
   p.page_table = page_table;
   p.seq_lens = seq_lens;
+  p.q = static_cast<const __nv_bfloat16*>(q);
   p.kv_pool = static_cast<const uint8_t*>(kv_pages);
   p.page_scales = page_scales;
   p.inv_ref_scale = 1.f / kv_scale;
@@ -520,6 +522,7 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
     } else {
       p.ws_o = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + 256);
       p.ws_lse = reinterpret_cast<float*>(p.ws_o + parts * kValueDim);
+      if (plan->kv_dtype == MLA_KV_FP4) p.part_scale = static_cast<float*>(workspace);
     }
   }
   p.tree_mask = tree_mask;

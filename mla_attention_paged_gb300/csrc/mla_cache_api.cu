@@ -52,8 +52,7 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
                   void* stream) {
   const bool has_q = q_in != nullptr, has_kv = kv_in != nullptr;
   if (num_tokens < 0 || max_positions < 1 || !(eps >= 0.f)) return MLA_ERR_INVALID_ARG;
-  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_E4M3 && kv_dtype != MLA_KV_INT8 && kv_dtype != MLA_KV_INT8_PAGE)
-    return MLA_ERR_INVALID_ARG;
+  if (!kv_dtype_ok(kv_dtype)) return MLA_ERR_INVALID_ARG;
   if (has_q) {
     if (num_heads < 1 || q_in_token_stride < 0 || q_in_head_stride < 0) return MLA_ERR_INVALID_ARG;
     if (num_heads > 1024 || q_dim < 64 || q_dim > 576 || q_dim % 8 != 0) return MLA_ERR_UNSUPPORTED;
@@ -64,7 +63,7 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
   if (num_tokens == 0) return MLA_OK;
   if (!has_q && !has_kv) return MLA_ERR_INVALID_ARG;
   if (!cos_sin || !positions || !aligned(cos_sin, 16) || !aligned(positions, 4)) return MLA_ERR_INVALID_ARG;
-  const size_t pool_bytes = num_slots < 1 ? 0 : static_cast<size_t>(num_slots) * kLatentDim * (kv_dtype == MLA_KV_BF16 ? 2 : 1);
+  const size_t pool_bytes = num_slots < 1 ? 0 : static_cast<size_t>(num_slots) * kv_row_bytes(kv_dtype);
   if (has_q) {
     if (!q_out || !aligned(q_in, 16) || !aligned(q_out, 16) || (q_weight && !aligned(q_weight, 16)))
       return MLA_ERR_INVALID_ARG;
@@ -144,6 +143,7 @@ int mla_key_mass(const mla_decode_plan_t* plan, const void* q, const void* kv_pa
     return MLA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !(kv_scale > 0.f) || !(decay >= 0.f) || mass_stride < plan->max_seq_len) return MLA_ERR_INVALID_ARG;
   if (tree_mask && q_len > kMaxTreeDrafts) return MLA_ERR_UNSUPPORTED;
+  if (plan->kv_dtype == MLA_KV_FP4) return MLA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(plan->batch) * (plan->max_seq_len / 128 + 1) >= (int64_t(1) << 31)) return MLA_ERR_UNSUPPORTED;
   size_t need = 0;
   mla_key_mass_workspace(plan, &need);
@@ -212,8 +212,7 @@ int mla_kv_evict(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype,
   if (batch < 1 || num_pages < 1 || max_pages_per_seq < 1 || max_dst_pages < 1 || sink < 0 || recent < 0 ||
       max_seq_len < 0 || max_keep < 0)
     return MLA_ERR_INVALID_ARG;
-  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_E4M3 && kv_dtype != MLA_KV_INT8 && kv_dtype != MLA_KV_INT8_PAGE)
-    return MLA_ERR_INVALID_ARG;
+  if (!kv_dtype_ok(kv_dtype)) return MLA_ERR_INVALID_ARG;
   // a row's codes mean something else under another page's scale
   if (kv_dtype == MLA_KV_INT8_PAGE) return MLA_ERR_UNSUPPORTED;
   if (!page_size_ok(page_size) || batch > 65535 || max_seq_len > (1 << 24)) return MLA_ERR_UNSUPPORTED;
@@ -237,7 +236,7 @@ int mla_kv_evict(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype,
   p.kv_pages = static_cast<uint8_t*>(kv_pages);
   p.num_pages = num_pages;
   p.page_size = page_size;
-  p.row_bytes = kLatentDim * (kv_dtype == MLA_KV_BF16 ? 2 : 1);
+  p.row_bytes = kv_row_bytes(kv_dtype);
   p.page_table = page_table;
   p.max_pages = max_pages_per_seq;
   p.seq_lens = seq_lens;

@@ -1,0 +1,748 @@
+// mla_decode_fp4_sm103a.cu -- absorbed MLA decode over a 4-bit paged latent KV cache, sm_103a.
+//
+// What it computes: out[b,t,h] = sum_j softmax_j(scale q.k_j) k_j[:512] over the keys that draft t sees
+// (0 .. L - T + t, or a tree's mask), with the latent rows stored as e2m1 codes under a power of two per
+// 16 columns and the rotated columns as e4m3 codes (include/mla.h, MLA_KV_FP4), all times kv_scale.
+//
+// Every value of a row in units of kv_scale is an e4m3 number exactly: magnitude (2 bits of significand)
+// times 2^(e-5), e = 0..11, lies in 2^-6 .. 384.  So a tile is decoded to e4m3 codes, once, and both
+// products run on 8-bit tensor-core operands:
+//  * BMM1: S^T[key, row] = K Q^T, M = 128 keys, A = K from tensor memory (a key is a lane), B = the query
+//    rows, each bf16 row scaled by a power of two and split into q_hi = e4m3(q) and q_lo = e4m3(q - q_hi)
+//    (8 bits of significand: exact down to 2^-9 of the row's largest |q|), one product after the other
+//    into the same accumulator.  A from tensor memory keeps 72 KB a tile of operand reads off shared
+//    memory.
+//  * BMM2: O^T[value column, row] += V^T P^T, A = V^T, MN-major out of shared memory, B = the weights,
+//    P 2^6 split into p_hi = e4m3(P) and p_lo = e4m3(32 (P - p_hi)), stacked as 2 x NR columns so that V
+//    is read once; the epilogue adds O_hi + O_lo / 32.  (P 2^6 <= 2^8, kept to 2^-8 relative.)
+//  * A key is one thread's in the softmax, so a row's sum is kept per thread and its running maximum
+//    moves only when some score exceeds it by more than 2 (log2): ordinary tiles reduce nothing across
+//    threads but one vote.
+// One CTA per (group of NR rows, split, request), 128 keys a tile, 608 threads: softmax warps 0-7 (32 keys
+// and half of the rows each), decoding warps 8-15 (32 keys and half of the columns each; a row's codes go
+// to registers at once and free their stage), producer 16 (untiled bulk copies of 32 rows), BMM1 17, BMM2 18.
+// Every wait is bounded; on expiry the CTA records a timeout, drains its copies and MMAs, frees tensor
+// memory and returns.
+#include <cuda_fp16.h>
+
+#include "mla_internal.h"
+#include "sm103a_ptx.cuh"
+#include "tree_mask.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kTile = kFp4TileKeys;               // keys per tile
+constexpr int kSub = 32;                          // keys per raw stage (a quarter of a tile)
+constexpr int kRawStage = kSub * kFp4RowBytes;    // 10752
+constexpr int kVBlock = kTile * 64;               // 128 keys x 64 codes (64-byte swizzle)
+constexpr int kVTile = (kValueDim / 64) * kVBlock;
+constexpr int kKCols = kLatentDim / 4;            // tensor-memory columns of a decoded tile
+constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kDecodeWarps = 8;
+constexpr int kDecodeThreads = 32 * kDecodeWarps;
+constexpr int kWorkers = kSoftmaxThreads + kDecodeThreads;
+constexpr int kProducerWarp = 16, kBmm1Warp = 17, kBmm2Warp = 18;
+constexpr int kThreads = 608;
+constexpr int kMaxRaw = 6;
+constexpr int kMaxRows = 32;
+constexpr int kCtrlBytes = 3072;
+constexpr int kAbortTimeout = 1;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kPShift = 6.0f;    // P is formed times 2^6 ...
+constexpr float kThreshold = 2.0f; // ... and at most 2^8: the reference moves by more than this
+constexpr float kLoScale = 32.0f;  // p_lo carries 32 times the residual (at most 2^3)
+
+template <int NR>
+struct Map {
+  static constexpr int kRaw = NR == 16 ? 6 : 4;        // raw stages
+  static constexpr int kKBufs = NR == 16 ? 2 : 1;      // decoded K tiles in tensor memory
+  static constexpr int kQBlock = NR * 64;
+  static constexpr int kQPart = 9 * kQBlock;           // q_hi or q_lo
+  static constexpr int kPBuf = 2 * NR * kTile;
+  static constexpr int kOffV = 0;
+  static constexpr int kOffQ = kOffV + 2 * kVTile;
+  static constexpr int kOffP = kOffQ + 2 * kQPart;
+  static constexpr int kOffRaw = kOffP + 2 * kPBuf;
+  static constexpr int kOffCtrl = kOffRaw + kRaw * kRawStage;
+  static constexpr int kSmem = kOffCtrl + kCtrlBytes + 1024;
+  // tensor memory: O^T (4 chunks of hi | lo columns), S^T (2 buffers), K
+  static constexpr uint32_t kO = 0;
+  static constexpr uint32_t kS = 8 * NR;
+  static constexpr uint32_t kK = kS + 2 * NR;
+  static_assert(kK + kKBufs * kKCols <= kTmemCols, "tensor memory");
+  static_assert(kSmem <= 232448, "shared memory per block");
+  static_assert(kOffP % 1024 == 0 && kOffQ % 512 == 0 && kOffRaw % 16 == 0 && kOffCtrl % 16 == 0, "alignment");
+};
+
+struct Ctrl {
+  uint64_t raw_full[kMaxRaw];   // copies landed
+  uint64_t raw_empty[kMaxRaw];  // both warps of the stage's keys have it in registers
+  uint64_t q_ready;             // split queries written
+  uint64_t tile_full[2];        // tile decoded (V buffer parity)
+  uint64_t k_free[2];           // BMM1 of the tile done
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_full[2];
+  uint64_t o_done[2];           // BMM2 of the tile done
+  uint64_t drain1, drain2;
+  uint32_t tmem_base;
+  int abort_flag;
+  uint32_t bad[kMaxRaw];        // rows of the stage whose page lies outside the pool
+  alignas(16) float mult[kMaxRows];   // scale_log2 2^-s of the row's split; 0: no such row
+  alignas(16) float m[kMaxRows];      // reference maximum (log2 of the scaled score)
+  alignas(16) float off[kMaxRows];    // kPShift - m; -infinity: no such row
+  alignas(16) float alpha[kMaxRows];
+  alignas(16) float row_scale[kMaxRows];
+  alignas(16) float lse[kMaxRows];
+  alignas(16) int lim[kMaxRows];      // last key that the row sees; -1: none
+  alignas(16) uint64_t drafts[kMaxRows];
+  alignas(16) int wmax[4][kMaxRows];
+  alignas(16) float sums[2][4][kMaxRows];
+};
+static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
+
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  uint32_t h2;
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h2) : "r"(codes));
+  return h2;
+}
+
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
+
+__device__ __forceinline__ void st_shared_u8(uint32_t saddr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+// Eight 4-bit columns (a word of include/mla.h's row) as e4m3 codes: the magnitude's code is looked up by
+// a byte permute among the eight of its group's power of two (lo: magnitudes 0-3, hi: 4-7); the signs lie
+// where one mask (columns 0-3) or a shift by four (4-7) brings them to each byte's top bit.
+__device__ __forceinline__ void fp4_to_e4m3(uint32_t w, uint32_t lo, uint32_t hi, uint32_t& a, uint32_t& b) {
+  const uint32_t m = w & 0x77777777u;
+  a = __byte_perm(lo, hi, m) | (w & 0x80808080u);
+  b = __byte_perm(lo, hi, m >> 16) | ((w << 4) & 0x80808080u);
+}
+
+// Sum of v[r] over the warp's lanes, value r left in the lanes with lane / (32 / NR) == r.
+template <int NR>
+__device__ __forceinline__ float lanes_sum(float (&v)[NR], int lane) {
+#pragma unroll
+  for (int n = NR / 2, o = 16; o > 0; n >>= 1, o >>= 1) {
+    if (n >= 1) {
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const bool up = (lane & o) != 0;
+        const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+  return v[0];
+}
+
+template <int NR>
+__device__ __forceinline__ void load_s(uint32_t addr, uint32_t (&s)[NR]) {
+  if constexpr (NR == 8) tmem_ld8(addr, s);
+  if constexpr (NR == 16) tmem_ld16(addr, s);
+  if constexpr (NR == 32) tmem_ld32(addr, s);
+  tmem_ld_wait();
+}
+
+// kTree: drafts see each other by p.tree_mask instead of in order.
+template <int NR, bool kTree>
+__global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const DecodeParams p) {
+  using M = Map<NR>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + M::kOffCtrl);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int group = blockIdx.x;
+  // (launch order as the other decode kernels': split by split in a plan of several waves)
+  const int b = p.split_major ? blockIdx.y : blockIdx.z;
+  const int split = p.split_major ? blockIdx.z : blockIdx.y;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < M::kRaw; ++s) {
+      mbar_init(&ctrl->raw_full[s], 1);
+      mbar_init(&ctrl->raw_empty[s], 2);
+    }
+    mbar_init(&ctrl->q_ready, kDecodeWarps);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctrl->tile_full[s], kDecodeWarps);
+      mbar_init(&ctrl->k_free[s], 1);
+      mbar_init(&ctrl->s_full[s], 1);
+      mbar_init(&ctrl->s_free[s], kSoftmaxWarps);
+      mbar_init(&ctrl->p_full[s], kSoftmaxWarps);
+      mbar_init(&ctrl->o_done[s], 1);
+    }
+    mbar_init(&ctrl->drain1, 1);
+    mbar_init(&ctrl->drain2, 1);
+    ctrl->abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kBmm1Warp) {
+    tmem_alloc(&ctrl->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem_base;
+  // programmatic dependent launch: no input is read before the previous kernel has completed
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  if (p.part_scale && threadIdx.x == 0 && group == 0 && b == 0 && split == 0) *p.part_scale = p.v_scale;
+  const int L = p.seq_lens[b];
+  const bool bad_len = L < p.T || L > p.max_seq || static_cast<int64_t>(L) > static_cast<int64_t>(p.max_pages) * p.page_size;
+  if (bad_len && threadIdx.x == 0 && split == 0 && group == 0) atomicOr(p.status, kStatusDeviceArg);
+  const int kv_start = split * p.chunk;
+  if (bad_len || kv_start >= L) {  // (CTA-uniform) a bad length, or this request needs fewer splits
+    if (warp == kBmm1Warp) tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
+  const int kv_end = min(L, kv_start + p.chunk);
+  const int ntiles = (kv_end - kv_start + kTile - 1) / kTile;
+  const int nsplit_b = (L + p.chunk - 1) / p.chunk;
+  const int row0 = group * NR;
+  const int nrows = min(NR, p.R - row0);
+  volatile int* abort_flag = &ctrl->abort_flag;
+  const bool final_out = nsplit_b == 1;
+  bool worker_failed = false;
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------------ producer: raw rows, 32 keys a stage
+    const int P = p.page_size;
+    const int per = P < kSub ? kSub / P : 1;  // pages per stage
+    const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+    const int first_page = kv_start / P, last_page = (kv_end - 1) / P;
+    int base = first_page;
+    int cur = first_page + lane <= last_page ? __ldg(pt + first_page + lane) : 0;
+    int nxt = first_page + 32 + lane <= last_page ? __ldg(pt + first_page + 32 + lane) : 0;
+    const uint64_t policy = policy_evict_first();
+    bool bad_pid = false, ok = true;
+    int issued = 0;
+    const int nsub = (kv_end - kv_start + kSub - 1) / kSub;
+    for (int i = 0; i < 4 * ntiles; ++i) {
+      const int s = i % M::kRaw;
+      const int k0 = kv_start + i * kSub;
+      if (i < nsub) {
+        const int pg0 = k0 / P;
+        while (pg0 - base >= 32) {  // advance the window of page ids (warp-uniform; a stage's last pages may lie in its
+          base += 32;               // second half)
+          cur = nxt;
+          const int nb = base + 32 + lane;
+          nxt = nb <= last_page ? __ldg(pt + nb) : 0;
+        }
+        const int at = pg0 - base + (lane < per ? lane : 0);
+        const int lo = __shfl_sync(0xffffffffu, cur, at & 31), hi = __shfl_sync(0xffffffffu, nxt, at & 31);
+        const int pid = at < 32 ? lo : hi;
+        const int key = k0 + lane * P;  // this lane's first key
+        const int rows = lane < per ? max(0, min(min(P, kSub), kv_end - key)) : 0;
+        const bool outside = rows > 0 && (pid < 0 || pid >= p.num_pages);
+        bad_pid |= outside;
+        uint32_t bad = 0;
+        if (outside) bad = (rows >= 32 ? 0xffffffffu : ((1u << rows) - 1)) << (lane * P & 31);
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        const uint32_t bytes = outside ? 0u : static_cast<uint32_t>(rows * kFp4RowBytes);
+        const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+        if (i >= M::kRaw) {
+          bool w = true;
+          if (lane == 0) w = mbar_wait(&ctrl->raw_empty[s], ((i / M::kRaw) - 1) & 1, abort_flag);
+          ok = __shfl_sync(0xffffffffu, w, 0);
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          ctrl->bad[s] = bad;
+          mbar_arrive_expect_tx(&ctrl->raw_full[s], total);
+        }
+        __syncwarp();
+        if (bytes > 0)
+          bulk_load(smem + M::kOffRaw + s * kRawStage + lane * P * kFp4RowBytes,
+                    p.kv_pool + (static_cast<int64_t>(pid) * P + (P > kSub ? k0 % P : 0)) * kFp4RowBytes, bytes,
+                    &ctrl->raw_full[s], policy);
+      } else {  // the last tile's stages past its end: nothing to copy (their keys have weight 0)
+        if (i >= M::kRaw) {
+          bool w = true;
+          if (lane == 0) w = mbar_wait(&ctrl->raw_empty[s], ((i / M::kRaw) - 1) & 1, abort_flag);
+          ok = __shfl_sync(0xffffffffu, w, 0);
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          ctrl->bad[s] = 0xffffffffu;
+          mbar_arrive(&ctrl->raw_full[s]);
+        }
+      }
+      issued = i + 1;
+      __syncwarp();
+    }
+    if (__any_sync(0xffffffffu, bad_pid) && lane == 0) atomicOr(p.status, kStatusDeviceArg);
+    // copies still in flight (their readers may have given up) land before the CTA exits
+    for (int k = max(0, issued - M::kRaw); k < issued; ++k) drain_wait(&ctrl->raw_full[k % M::kRaw], (k / M::kRaw) & 1);
+  } else if (warp == kBmm1Warp) {
+    // ------------------------------------------------------------------ BMM1 issuer
+    const uint32_t idesc = make_idesc_e4m3(128, NR);
+    const uint64_t hi_desc = make_smem_desc_sw64(smem_u32(smem + M::kOffQ));
+    const uint64_t lo_desc = make_smem_desc_sw64(smem_u32(smem + M::kOffQ + M::kQPart));
+    bool ok = mbar_wait(&ctrl->q_ready, 0, abort_flag);
+    for (int j = 0; j < ntiles; ++j) {
+      const int sb = j & 1, kb = j % M::kKBufs;
+      if (ok) ok = mbar_wait(&ctrl->tile_full[sb], (j >> 1) & 1, abort_flag);
+      if (ok && j >= 2) ok = mbar_wait(&ctrl->s_free[sb], ((j - 2) >> 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + M::kS + sb * NR;
+      const uint32_t a = tmem + M::kK + kb * kKCols;
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < 9; ++c) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint64_t off = static_cast<uint64_t>((c * M::kQBlock + k * 32) >> 4);
+            umma_f8_ts(d, a + c * 16 + k * 8, hi_desc + off, idesc, (c | k) != 0 ? 1u : 0u);
+            umma_f8_ts(d, a + c * 16 + k * 8, lo_desc + off, idesc, 1u);
+          }
+        }
+        umma_commit(&ctrl->s_full[sb]);
+        umma_commit(&ctrl->k_free[kb]);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) {  // every MMA this warp issued completes before tensor memory is released
+      umma_commit(&ctrl->drain1);
+      drain_wait(&ctrl->drain1, 0);
+    }
+    __syncwarp();
+  } else if (warp == kBmm2Warp) {
+    // ------------------------------------------------------------------ BMM2 issuer
+    const uint32_t idesc = make_idesc_e4m3(128, 2 * NR, true, false);
+    bool ok = true;
+    for (int j = 0; j < ntiles; ++j) {
+      const int pb = j & 1;
+      if (ok) ok = mbar_wait(&ctrl->tile_full[pb], (j >> 1) & 1, abort_flag);
+      if (ok) ok = mbar_wait(&ctrl->p_full[pb], (j >> 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint64_t v_desc = make_smem_desc_sw64(smem_u32(smem + M::kOffV + pb * kVTile), kVBlock, 512);
+      const uint64_t p_desc = make_smem_desc(smem_u32(smem + M::kOffP + pb * M::kPBuf), 16, 1024);
+      if (elect_one()) {
+#pragma unroll
+        for (int qc = 0; qc < 4; ++qc) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f8(tmem + M::kO + qc * 2 * NR, v_desc + static_cast<uint64_t>((2 * qc * kVBlock + kk * 2048) >> 4),
+                    p_desc + static_cast<uint64_t>((kk * 32) >> 4), idesc, (j > 0 || kk > 0) ? 1u : 0u);
+        }
+        umma_commit(&ctrl->o_done[pb]);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) {
+      umma_commit(&ctrl->drain2);
+      drain_wait(&ctrl->drain2, 0);
+    }
+    __syncwarp();
+  } else if (warp >= kSoftmaxWarps) {
+    // ------------------------------------------------------------------ decoding warps
+    const int dw = warp - kSoftmaxWarps, quad = dw & 3, half = dw >> 2;
+    bool failed = false;
+    {
+      // Split of the queries: kPer adjacent threads a row, 16-byte chunks t, t + kPer, ...
+      constexpr int kPer = kDecodeThreads / NR, kChunks = (72 + kPer - 1) / kPer;
+      const int t = (threadIdx.x - kSoftmaxThreads) % kPer, r = (threadIdx.x - kSoftmaxThreads) / kPer;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(b) * p.R + row0 + r) * kLatentDim);
+      uint4 w[kChunks];
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = t + kPer * i;
+        w[i] = r < nrows && c < 72 ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
+      }
+#pragma unroll
+      for (int o = kPer / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      int sh = 0;  // the row's power of two: its largest |q| lands in [128, 256)
+      if (mx > 0.f) sh = min(126, max(-120, 7 - (static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu) - 127)));
+      const float mul = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = t + kPer * i;
+        if (c >= 72) continue;
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t h[2], l[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x0 = __uint_as_float(u[2 * k + e] << 16) * mul, x1 = __uint_as_float(u[2 * k + e] & 0xFFFF0000u) * mul;
+            h[e] = f32x2_to_e4m3x2(x0, x1);
+            const float2 v = f16x2_to_f32x2(e4m3x2_to_f16x2(h[e]));
+            l[e] = f32x2_to_e4m3x2(x0 - v.x, x1 - v.y);
+          }
+          hi[k] = h[0] | (h[1] << 16);
+          lo[k] = l[0] | (l[1] << 16);
+        }
+        const uint32_t at = smem_u32(smem + M::kOffQ) + (c >> 3) * M::kQBlock + r * 64 + ((((c >> 1) & 3) ^ ((r >> 1) & 3)) << 4) + (c & 1) * 8;
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + M::kQPart), "r"(lo[0]), "r"(lo[1]) : "memory");
+      }
+      if (t == 0) {
+        const bool real = r < nrows;
+        // (an infinite query has no finite score: its row becomes NaN)
+        ctrl->mult[r] = !real ? 0.f : mx == INFINITY ? NAN : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+        ctrl->m[r] = -INFINITY;
+        ctrl->off[r] = real ? INFINITY : -INFINITY;
+        const int draft = (row0 + r) / p.H;
+        ctrl->lim[r] = real ? L - p.T + draft : -1;
+        if (kTree) ctrl->drafts[r] = real ? p.tree_mask[static_cast<int64_t>(b) * p.T + draft] & draft_bits(p.T) : 0ull;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->q_ready);
+    }
+    const int row = quad * 32 + lane;  // this thread's key of a tile
+    const uint32_t v_row = smem_u32(smem + M::kOffV) + row * 64 + half * 4 * kVBlock;
+    const uint32_t sw = ((row >> 1) & 3) << 4;
+    const uint32_t k_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + M::kK;
+    for (int j = 0; j < ntiles; ++j) {
+      const int i = 4 * j + quad, s = i % M::kRaw, vb = j & 1, kb = j % M::kKBufs;
+      bool ok = mbar_wait(&ctrl->raw_full[s], (i / M::kRaw) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        failed = true;
+        break;
+      }
+      const uint32_t raw = smem_u32(smem + M::kOffRaw + s * kRawStage) + lane * kFp4RowBytes;
+      uint4 w[8], rope[2];
+      uint32_t ex[2];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = ld_shared_v4(raw + half * 128 + k * 16);
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(ex[0]), "=r"(ex[1]) : "r"(raw + 256 + half * 8));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) rope[k] = ld_shared_v4(raw + 272 + half * 32 + k * 16);
+      const uint32_t bad = ctrl->bad[s];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->raw_empty[s]);
+      if ((bad >> lane) & 1) {  // a row without a page, or past the end: zeros
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = make_uint4(0u, 0u, 0u, 0u);
+        rope[0] = rope[1] = make_uint4(0u, 0u, 0u, 0u);
+        ex[0] = ex[1] = 0u;
+      }
+      // the K columns and the V buffer are free once BMM1 and BMM2 of their last tile have completed
+      if (j >= M::kKBufs) ok = mbar_wait(&ctrl->k_free[kb], ((j / M::kKBufs) - 1) & 1, abort_flag);
+      if (ok && j >= 2) ok = mbar_wait(&ctrl->o_done[vb], ((j >> 1) - 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        failed = true;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t kcol = k_lane + kb * kKCols;
+      const uint32_t vrow = v_row + vb * kVTile;
+#pragma unroll
+      for (int k2 = 0; k2 < 4; ++k2) {  // 64 columns: a block of V, 16 columns of tensor memory
+        uint32_t o[16];
+#pragma unroll
+        for (int k1 = 0; k1 < 2; ++k1) {
+          const int k = 2 * k2 + k1;
+          const uint32_t word[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {  // 16 columns under one power of two
+            const uint32_t e = (ex[k >> 2] >> (8 * (k & 3) + 4 * g)) & 15u;
+            const uint32_t lo = e * 0x08080800u + 0x14100800u, hi = e * 0x08080808u + 0x24201C18u;
+            fp4_to_e4m3(word[2 * g], lo, hi, o[8 * k1 + 4 * g], o[8 * k1 + 4 * g + 1]);
+            fp4_to_e4m3(word[2 * g + 1], lo, hi, o[8 * k1 + 4 * g + 2], o[8 * k1 + 4 * g + 3]);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) st_shared_v4(vrow + k2 * kVBlock + ((q << 4) ^ sw), o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        tmem_st16(kcol + half * 64 + k2 * 16, o);
+      }
+      const uint32_t ro[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w, rope[1].x, rope[1].y, rope[1].z, rope[1].w};
+      tmem_st8(kcol + 128 + half * 8, ro);
+      tmem_st_wait();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->tile_full[vb]);
+    }
+    worker_failed = failed;
+  } else {
+    // ------------------------------------------------------------------ softmax: a key and RW rows per thread
+    constexpr int RW = NR / 2;
+    const int quad = warp & 3, r0 = (warp >> 2) * RW;  // rows r0 .. r0 + RW - 1 of the group
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    const int key_in = quad * 32 + lane;
+    const int p0 = L - p.T;  // first draft
+    float l_sum[RW], l_use[RW];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) l_sum[r] = l_use[r] = 0.f;
+    // byte key_in of P row r: 128-byte rows, 16-byte chunks under the row's swizzle (r0 is a multiple of 8)
+    const uint32_t p_key = smem_u32(smem + M::kOffP) + r0 * kTile + (key_in & 15);
+    const uint32_t p_chunk = (key_in >> 4) << 4;
+    bool failed = !mbar_wait(&ctrl->q_ready, 0, abort_flag);  // (the rows' factors and limits)
+    for (int j = 0; j < ntiles; ++j) {
+      const int sb = j & 1;
+      const int k0 = kv_start + j * kTile, key = k0 + key_in;
+      const bool edge = k0 + kTile > min(kv_end, kTree ? p0 : p0 + 1);  // some key here is not every row's
+      const uint32_t s_addr = tmem + lane_base + M::kS + sb * NR + r0;
+      bool fail = failed || !mbar_wait(&ctrl->s_full[sb], (j >> 1) & 1, abort_flag);
+      fail = __any_sync(0xffffffffu, fail);
+      float x[RW];
+      bool over = false;
+      auto sees = [&](int r) -> bool {  // (r within the group)
+        if (key >= kv_end) return false;
+        if (!kTree) return key <= ctrl->lim[r];
+        const int u = key - p0;
+        return ctrl->lim[r] >= 0 && (u < 0 || ((ctrl->drafts[r] >> u) & 1));
+      };
+      auto scores = [&]() {
+        uint32_t s[RW];
+        load_s<RW>(s_addr, s);
+        float top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < RW; r += 4) {
+          const float4 mu = *reinterpret_cast<const float4*>(&ctrl->mult[r0 + r]), of = *reinterpret_cast<const float4*>(&ctrl->off[r0 + r]);
+          x[r] = fmaf(__uint_as_float(s[r]), mu.x, of.x);
+          x[r + 1] = fmaf(__uint_as_float(s[r + 1]), mu.y, of.y);
+          x[r + 2] = fmaf(__uint_as_float(s[r + 2]), mu.z, of.z);
+          x[r + 3] = fmaf(__uint_as_float(s[r + 3]), mu.w, of.w);
+        }
+        if (edge) {
+#pragma unroll
+          for (int r = 0; r < RW; ++r)
+            if (!sees(r0 + r)) x[r] = -INFINITY;
+        }
+#pragma unroll
+        for (int r = 0; r < RW; ++r) top = fmaxf(top, x[r]);
+        over = top > kPShift + kThreshold;
+      };
+      if (!fail) {
+        tc_fence_after();
+        scores();
+      }
+      if (bar_or(1, kSoftmaxThreads, fail || over || *abort_flag != 0)) {
+        if (bar_or(1, kSoftmaxThreads, fail || *abort_flag != 0)) {
+          failed = true;
+          break;
+        }
+        // ---------------------------------------------------------------- some row's reference moves
+        {
+          uint32_t s[RW];
+          load_s<RW>(s_addr, s);
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            float v = __uint_as_float(s[r]) * ctrl->mult[r0 + r];
+            if (edge ? !sees(r0 + r) : ctrl->lim[r0 + r] < 0) v = -INFINITY;
+            const int i = __float_as_int(v);
+            const int top = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
+            if (lane == r) ctrl->wmax[quad][r0 + r] = top;
+          }
+        }
+        named_bar_sync(1, kSoftmaxThreads);
+        float m_new = -INFINITY, alpha = 1.f;  // of row `lane`, the same in every warp
+        if (lane < NR) {
+          int i = max(max(ctrl->wmax[0][lane], ctrl->wmax[1][lane]), max(ctrl->wmax[2][lane], ctrl->wmax[3][lane]));
+          i ^= (i >> 31) & 0x7fffffff;
+          const float top = __int_as_float(i), old = ctrl->m[lane];
+          m_new = old;
+          if (old == -INFINITY || top > old + kThreshold) {
+            alpha = old == -INFINITY ? 0.f : ex2_approx(old - top);
+            m_new = top;
+          }
+        }
+        const bool any = __any_sync(0xffffffffu, alpha != 1.f);
+        named_bar_sync(1, kSoftmaxThreads);
+        if (warp == 0 && lane < NR) {
+          ctrl->m[lane] = m_new;
+          // (no such row: -infinity; a row that has seen nothing: +infinity, so that its first key shows)
+          ctrl->off[lane] = ctrl->lim[lane] < 0 ? -INFINITY : m_new == -INFINITY ? INFINITY : kPShift - m_new;
+          ctrl->alpha[lane] = alpha;
+        }
+        named_bar_sync(1, kSoftmaxThreads);
+        scores();
+        if (any && j > 0) {
+          bool ok = mbar_wait(&ctrl->o_done[sb ^ 1], ((j - 1) >> 1) & 1, abort_flag);  // (a failure shows at the next barrier)
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            const float f = ctrl->alpha[r0 + r];
+            l_sum[r] *= f;
+            l_use[r] *= f;
+          }
+#pragma unroll 1
+          for (int c = warp >> 2; ok && c < 8 * NR / 16; c += 2) {  // 16 columns of this quadrant's lanes
+            uint32_t v[16];
+            const uint32_t at = tmem + lane_base + M::kO + c * 16;
+            const float* al = ctrl->alpha + (c * 16) % NR;
+            load_s<16>(at, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * al[i]);
+            tmem_st16(at, v);
+          }
+          tmem_st_wait();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->s_free[sb]);
+      if (j >= 2) {  // this P buffer's last reader
+        const bool ok = mbar_wait(&ctrl->o_done[sb], ((j >> 1) - 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) failed = true;  // (the others learn of it at the next barrier)
+      }
+      const uint32_t pb = p_key + sb * M::kPBuf;
+#pragma unroll
+      for (int r = 0; r < RW; r += 2) {
+        const float a = ex2_approx(x[r]), c = ex2_approx(x[r + 1]);
+        l_sum[r] += a;
+        l_sum[r + 1] += c;
+        const uint32_t ph = pack_f16x2(a, c);
+        const uint32_t hi = f16x2_to_e4m3x2(ph);
+        const uint32_t hb = e4m3x2_to_f16x2(hi);
+        uint32_t d, u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(ph), "r"(hb));  // (exact)
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(d), "r"(0x50005000u));  // times 32
+        const uint32_t lo = f16x2_to_e4m3x2(d);
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(u) : "r"(e4m3x2_to_f16x2(lo)), "r"(0x28002800u), "r"(hb));  // hi + lo / 32
+        const float2 uf = f16x2_to_f32x2(u);
+        l_use[r] += uf.x;
+        l_use[r + 1] += uf.y;
+        const uint32_t a0 = pb + r * kTile + (p_chunk ^ ((r & 7) << 4)), a1 = pb + (r + 1) * kTile + (p_chunk ^ (((r + 1) & 7) << 4));
+        st_shared_u8(a0, hi);
+        st_shared_u8(a1, hi >> 8);
+        st_shared_u8(a0 + NR * kTile, lo);
+        st_shared_u8(a1 + NR * kTile, lo >> 8);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->p_full[sb]);
+    }
+    if (!failed) failed = !mbar_wait(&ctrl->o_done[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1, abort_flag);
+    const float ls = lanes_sum<RW>(l_sum, lane), lu = lanes_sum<RW>(l_use, lane);
+    if (lane % (32 / RW) == 0) {
+      ctrl->sums[0][quad][r0 + lane / (32 / RW)] = ls;
+      ctrl->sums[1][quad][r0 + lane / (32 / RW)] = lu;
+    }
+    named_bar_sync(1, kSoftmaxThreads);
+    if (warp == 0 && lane < NR) {
+      const float s = (ctrl->sums[0][0][lane] + ctrl->sums[0][1][lane]) + (ctrl->sums[0][2][lane] + ctrl->sums[0][3][lane]);
+      const float u = (ctrl->sums[1][0][lane] + ctrl->sums[1][1][lane]) + (ctrl->sums[1][2][lane] + ctrl->sums[1][3][lane]);
+      // (a row that sees nothing has sums of 0; a NaN goes on)
+      ctrl->row_scale[lane] = u != 0.f ? (final_out ? p.v_scale : 1.f) / u : 0.f;
+      ctrl->lse[lane] = s != 0.f ? (ctrl->m[lane] + __log2f(s) - kPShift) * 0.69314718055994530942f : -INFINITY;
+    }
+    worker_failed = failed;
+  }
+  if (warp < kSoftmaxWarps + kDecodeWarps) {
+    // ------------------------------------------------------------------ output: a chunk of 128 value columns a warp
+    if (!bar_or(2, kWorkers, worker_failed || *abort_flag != 0)) {
+      tc_fence_after();
+      const int quad = warp & 3, qc = warp >> 2, col = qc * 128 + quad * 32 + lane;
+      const uint32_t stage = smem_u32(smem + M::kOffV);  // [NR][512] 16-bit (every BMM2 has completed)
+      const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + M::kO + qc * 2 * NR;
+#pragma unroll
+      for (int h = 0; h < NR; h += 16) {
+        uint32_t hi[16], lo[16];
+        tmem_ld16(at + h, hi);
+        load_s<16>(at + NR + h, lo);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float v = (__uint_as_float(hi[r]) + __uint_as_float(lo[r]) * (1.f / kLoScale)) * ctrl->row_scale[h + r];
+          // (a split's partial is f16 in units of the codes, at most 384; the combine scales it)
+          st_shared_u16(stage + ((h + r) * kValueDim + col) * 2, out_bits<true>(v, final_out));
+        }
+      }
+      if (warp == 0 && lane < nrows) {
+        if (final_out)
+          p.lse[static_cast<int64_t>(b) * p.R + row0 + lane] = ctrl->lse[lane];
+        else
+          p.ws_lse[(static_cast<int64_t>(b) * p.max_splits + split) * p.R + row0 + lane] = ctrl->lse[lane];
+      }
+      named_bar_sync(2, kWorkers);
+      uint8_t* dst = reinterpret_cast<uint8_t*>(
+          final_out ? p.out + (static_cast<int64_t>(b) * p.R + row0) * kValueDim
+                    : p.ws_o + ((static_cast<int64_t>(b) * p.max_splits + split) * p.R + row0) * kValueDim);
+      for (int i = threadIdx.x; i < nrows * 64; i += kWorkers)
+        *reinterpret_cast<uint4*>(dst + i * 16) = ld_shared_v4(stage + i * 16);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && ctrl->abort_flag == kAbortTimeout) atomicOr(p.status, kStatusTimeout);
+  // every store of this CTA is issued: the combine grid may be scheduled now
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == kBmm1Warp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+int fp4_group_rows(int R) { return R <= 16 ? 16 : 32; }
+
+cudaError_t launch_decode_partial_fp4(const DecodeParams& p, cudaStream_t stream) {
+  // [32 rows][tree]
+  static constexpr decltype(&decode_partial_fp4_kernel<16, false>) kernels[4] = {
+      decode_partial_fp4_kernel<16, false>, decode_partial_fp4_kernel<16, true>, decode_partial_fp4_kernel<32, false>,
+      decode_partial_fp4_kernel<32, true>};
+  static constexpr int smem[2] = {Map<16>::kSmem, Map<32>::kSmem};
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_device != dev) {
+    for (int i = 0; i < 4; ++i) {
+      e = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, smem[i / 2]);
+      if (e != cudaSuccess) return e;
+    }
+    configured_device = dev;
+  }
+  const int rows = fp4_group_rows(p.R), wide = rows == 32 ? 1 : 0;
+  const int groups = (p.R + rows - 1) / rows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = p.split_major ? dim3(groups, p.B, p.max_splits) : dim3(groups, p.max_splits, p.B);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem[wide];
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernels[2 * wide + (p.tree_mask ? 1 : 0)], p);
+}
+
+}  // namespace mla

@@ -974,7 +974,7 @@ __global__ void __launch_bounds__(kCombineThreads) decode_combine_kernel(const D
   }
   if (active) {
     const bool some = kTree ? w_run != 0.f : w_run > 0.f;  // (kTree passes a NaN on)
-    const float inv = some ? (kPart == kPartF16 ? p.v_scale : 1.f) / w_run : 0.f;
+    const float inv = some ? (kPart == kPartF16 ? (p.part_scale ? *p.part_scale : p.v_scale) : 1.f) / w_run : 0.f;
     uint4 pk;
     pk.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
     pk.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
@@ -1040,6 +1040,7 @@ cudaError_t launch_decode_partial(const DecodeParams& p, const CUtensorMap& tm_q
                                   int head_groups, cudaStream_t stream) {
   switch (p.kv_dtype) {
     case kKvE4m3: return launch_decode_partial_e4m3(p, tm_q, tm_kv, head_groups, stream);
+    case kKvFp4: return launch_decode_partial_fp4(p, stream);
     case kKvInt8:
       return p.tree_mask ? launch_partial_impl<kKvInt8, true>(p, tm_q, tm_kv, head_groups, stream)
                          : launch_partial_impl<kKvInt8, false>(p, tm_q, tm_kv, head_groups, stream);
@@ -1089,7 +1090,8 @@ cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernels[wide ? kPartF32 : p.tree_mask ? kPartF16 : kPartBf16], p);
+  const bool f16 = p.tree_mask || p.kv_dtype == kKvFp4;
+  return cudaLaunchKernelEx(&cfg, kernels[wide ? kPartF32 : f16 ? kPartF16 : kPartBf16], p);
 }
 
 }  // namespace mla

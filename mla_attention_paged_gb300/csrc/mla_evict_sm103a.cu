@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const EvictPa
   if (kCtas > 1) cluster.sync();  // no CTA leaves while another may read its counts
 }
 
-// kChunks: 16-byte pieces of a row (72 of bf16, 36 of 8-bit codes).
+// kChunks: 16-byte pieces of a row (72 of bf16, 36 of 8-bit codes, 21 of a 4-bit row: 13 rows a warp).
 template <int kChunks>
 __global__ void __launch_bounds__(32 * kCopyWarps) kv_copy_kernel(const EvictParams p) {
   constexpr int kRows = 32 * kLanePieces / kChunks;  // rows a warp copies
@@ -333,8 +333,8 @@ cudaError_t launch_kv_evict(const EvictParams& params, cudaStream_t stream) {
   if (e != cudaSuccess || p.max_keep == 0) return e;
   const int rows = 32 * kLanePieces / (p.row_bytes / 16) * kCopyWarps;
   const dim3 grid((p.max_keep + rows - 1) / rows, p.B);
-  return p.row_bytes == 2 * kLatentDim ? launch_dependent(kv_copy_kernel<72>, grid, 32 * kCopyWarps, 0, 1, p, stream)
-                                       : launch_dependent(kv_copy_kernel<36>, grid, 32 * kCopyWarps, 0, 1, p, stream);
+  auto copy = p.row_bytes == 2 * kLatentDim ? kv_copy_kernel<72> : p.row_bytes == kLatentDim ? kv_copy_kernel<36> : kv_copy_kernel<21>;
+  return launch_dependent(copy, grid, 32 * kCopyWarps, 0, 1, p, stream);
 }
 
 }  // namespace mla

@@ -27,6 +27,10 @@ constexpr int kKvBf16 = 0;
 constexpr int kKvE4m3 = 1;
 constexpr int kKvInt8 = 2;
 constexpr int kKvInt8Page = 3;  // int8 codes times a scale per page
+constexpr int kKvFp4 = 4;       // e2m1 codes times a power of two per 16 columns, e4m3 rotated columns
+
+constexpr int kFp4RowBytes = 336;  // a latent row: 256 bytes of codes, 16 of exponents, 64 rotated
+constexpr int kFp4TileKeys = 128;  // keys per decode tile
 
 // Device status word bits (OR-ed by kernels, read and cleared by mla_get_status).
 constexpr unsigned kStatusTimeout = 1u;
@@ -37,19 +41,22 @@ struct DecodeParams {
   int page_size, max_pages;     // page geometry and page_table row stride
   int chunk, max_splits, max_seq;
   int split_major;              // grid (groups, B, splits) when set, else (groups, splits, B)
-  int kv_dtype;                 // kKvBf16, kKvE4m3, kKvInt8 or kKvInt8Page
+  int kv_dtype;                 // kKvBf16, kKvE4m3, kKvInt8, kKvInt8Page or kKvFp4
   int64_t num_pages;            // pages in the pool: a page id outside [0, num_pages) is reported
   float scale_log2;             // softmax scale * log2(e) (* kv_scale for an 8-bit pool)
   float v_scale;                // 1, or kv_scale for an 8-bit pool (applied in the epilogue)
   const int32_t* page_table;
   const int32_t* seq_lens;
-  const uint8_t* kv_pool;       // pool base (the 8-bit path reads raw rows from here)
+  const __nv_bfloat16* q;       // [B, T, H, 576] (kKvFp4; the others read it through a tensor map)
+  const uint8_t* kv_pool;       // pool base (the int8 and 4-bit paths read raw rows from here)
   const float* page_scales;     // kKvInt8Page: [num_pages] scale of each page's codes
   float inv_ref_scale;          // kKvInt8Page: 1 / kv_scale (page scales are applied relative to it)
   __nv_bfloat16* out;           // [B, T, H, 512]
   float* lse;                   // [B, T, H]
   __nv_bfloat16* ws_o;          // [B, max_splits, R, 512] partial outputs (normalised, bf16)
   float* ws_lse;                // [B, max_splits, R] partial log-sum-exp (natural log)
+  float* part_scale;            // kKvFp4: v_scale for the combine, left by the partial kernel in the workspace's
+                                // first bytes (a combine on its own is not given kv_scale); else null
   unsigned* status;             // device status word
   // tree decode (tree_mask non-null): [B, T] bit u of word (b, t) = draft t sees draft u; the
   // split partials are f16 in units of the codes in ws_o (8-bit pools), or fp32 in ws_of
@@ -153,6 +160,8 @@ unsigned* status_ptr();  // device address of the current device's status word
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const uint64_t* dims,
               const uint64_t* strides, const uint32_t* box,
               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+inline bool kv_dtype_ok(int t) { return t >= kKvBf16 && t <= kKvFp4; }
+inline int kv_row_bytes(int t) { return t == kKvBf16 ? 2 * kLatentDim : t == kKvFp4 ? kFp4RowBytes : kLatentDim; }
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool page_size_ok(int P) { return P == 8 || P == 16 || P == 32 || P == 64 || P == 128 || P == 256; }
 
@@ -174,6 +183,9 @@ cudaError_t launch_decode_partial_e4m3(const DecodeParams& p, const CUtensorMap&
 // tensor memory, a three-tile ring (mla_decode_narrow_sm103a.cu).
 cudaError_t launch_decode_partial_narrow(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv,
                                          cudaStream_t stream);
+// Decode over a 4-bit pool (trees too).
+cudaError_t launch_decode_partial_fp4(const DecodeParams& p, cudaStream_t stream);
+int fp4_group_rows(int R);  // folded rows per CTA
 // Tree decode over a bf16 pool for requests of more than kTreeNarrowRows folded rows (pairs of CTAs).
 cudaError_t launch_decode_tree_pair(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                     const CUtensorMap& tm_v, cudaStream_t stream);

@@ -26,6 +26,7 @@ MLA_KV_BF16 = 0
 MLA_KV_E4M3 = 1
 MLA_KV_INT8 = 2
 MLA_KV_INT8_PAGE = 3
+MLA_KV_FP4 = 4
 
 # Every function include/mla.h declares; each is given its C signature in _load().
 EXPORTED = ["mla_decode_plan", "mla_decode", "mla_decode_partial", "mla_decode_combine", "mla_decode_noalloc",
@@ -126,7 +127,8 @@ def _stream_handle(stream):
 
 
 _POOL_DTYPE = {MLA_KV_BF16: (torch.bfloat16,), MLA_KV_E4M3: (torch.uint8, torch.float8_e4m3fn),
-               MLA_KV_INT8: (torch.int8,), MLA_KV_INT8_PAGE: (torch.int8,)}
+               MLA_KV_INT8: (torch.int8,), MLA_KV_INT8_PAGE: (torch.int8,), MLA_KV_FP4: (torch.uint8,)}
+FP4_ROW_BYTES = 336  # a latent row of a 4-bit pool (include/mla.h)
 
 
 def _refuse(what: str, why: str):
@@ -157,7 +159,7 @@ def _want_rows(what, dev, name, t, dtype, rows):
 def _want_pool(what, kv_pages, kv_dtype):
     """The latent pool: its device number, address, pages and page size."""
     dev, shape, dtype = kv_pages.get_device(), kv_pages.shape, kv_pages.dtype
-    if len(shape) != 3 or shape[2] != 576:
+    if len(shape) != 3 or shape[2] != (FP4_ROW_BYTES if kv_dtype == MLA_KV_FP4 else 576):
         _refuse(what, f"kv_pages has shape {tuple(shape)}")
     if dtype not in _POOL_DTYPE.get(kv_dtype, ()):
         _refuse(what, f"kv_pages is {dtype} for kv_dtype {kv_dtype}")

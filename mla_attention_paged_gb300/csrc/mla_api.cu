@@ -437,7 +437,7 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
   // swizzled column blocks the MMAs read, in a single TMA instruction.
   CUtensorMap tm_q, tm_kv;
   memset(&tm_q, 0, sizeof tm_q);
-  if (partial && plan->kv_dtype != MLA_KV_FP4) {  // (the 4-bit kernel reads q and pages by address)
+  if (partial && plan->kv_dtype != MLA_KV_FP4) {  // (the 4-bit kernel reads q by address)
     const uint64_t dims[3] = {64, static_cast<uint64_t>(plan->batch) * plan->rows, kLatentDim / 64};
     const uint64_t strides[2] = {row_bytes, 128};
     const uint32_t box[3] = {64, static_cast<uint32_t>(kGroupRows), kLatentDim / 64};
@@ -461,6 +461,14 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
       if (!make_map(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, kv_pages, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B))
         return MLA_ERR_CUDA;
     }
+  }
+  if (partial && plan->kv_dtype == MLA_KV_FP4) {
+    // rows of 336 bytes as 84 32-bit elements, a stage's share of a page at a time
+    const uint64_t dims[2] = {kFp4RowBytes / 4, static_cast<uint64_t>(plan->num_pages) * plan->page_size};
+    const uint64_t strides[1] = {kFp4RowBytes};
+    const uint32_t box[2] = {kFp4RowBytes / 4, static_cast<uint32_t>(std::min(plan->page_size, 64))};
+    if (!make_map(&tm_kv, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, kv_pages, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return MLA_ERR_CUDA;
   }
   CUtensorMap tm_v;
   memset(&tm_v, 0, sizeof tm_v);

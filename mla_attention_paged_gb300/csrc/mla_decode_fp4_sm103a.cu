@@ -20,7 +20,7 @@
 //    threads but one vote.
 // One CTA per (group of NR rows, split, request), 128 keys a tile, 608 threads: softmax warps 0-7 (32 keys
 // and half of the rows each), decoding warps 8-15 (32 keys and half of the columns each; a row's codes go
-// to registers at once and free their stage), producer 16 (untiled bulk copies of 32 rows), BMM1 17, BMM2 18.
+// to registers at once and free their stage), producer 16 (boxes of up to 64 rows), BMM1 17, BMM2 18.
 // Every wait is bounded; on expiry the CTA records a timeout, drains its copies and MMAs, frees tensor
 // memory and returns.
 #include <cuda_fp16.h>
@@ -33,8 +33,8 @@ namespace mla {
 namespace {
 
 constexpr int kTile = kFp4TileKeys;               // keys per tile
-constexpr int kSub = 32;                          // keys per raw stage (a quarter of a tile)
-constexpr int kRawStage = kSub * kFp4RowBytes;    // 10752
+constexpr int kSub = 64;                          // keys per raw stage (half a tile)
+constexpr int kRawStage = kSub * kFp4RowBytes;    // 21504
 constexpr int kVBlock = kTile * 64;               // 128 keys x 64 codes (64-byte swizzle)
 constexpr int kVTile = (kValueDim / 64) * kVBlock;
 constexpr int kKCols = kLatentDim / 4;            // tensor-memory columns of a decoded tile
@@ -45,7 +45,7 @@ constexpr int kDecodeThreads = 32 * kDecodeWarps;
 constexpr int kWorkers = kSoftmaxThreads + kDecodeThreads;
 constexpr int kProducerWarp = 16, kBmm1Warp = 17, kBmm2Warp = 18;
 constexpr int kThreads = 608;
-constexpr int kMaxRaw = 6;
+constexpr int kMaxRaw = 3;
 constexpr int kMaxRows = 32;
 constexpr int kCtrlBytes = 3072;
 constexpr int kAbortTimeout = 1;
@@ -56,7 +56,7 @@ constexpr float kLoScale = 32.0f;  // p_lo carries 32 times the residual (at mos
 
 template <int NR>
 struct Map {
-  static constexpr int kRaw = NR == 16 ? 6 : 4;        // raw stages
+  static constexpr int kRaw = NR == 16 ? 3 : 2;        // raw stages
   static constexpr int kKBufs = NR == 16 ? 2 : 1;      // decoded K tiles in tensor memory
   static constexpr int kQBlock = NR * 64;
   static constexpr int kQPart = 9 * kQBlock;           // q_hi or q_lo
@@ -78,9 +78,10 @@ struct Map {
 
 struct Ctrl {
   uint64_t raw_full[kMaxRaw];   // copies landed
-  uint64_t raw_empty[kMaxRaw];  // both warps of the stage's keys have it in registers
+  uint64_t raw_empty[kMaxRaw];  // the four warps of the stage's keys have it in registers
   uint64_t q_ready;             // split queries written
-  uint64_t tile_full[2];        // tile decoded (V buffer parity)
+  uint64_t k_full[2];           // tile decoded into tensor memory (tile parity)
+  uint64_t v_full[2];           // and copied into its V buffer
   uint64_t k_free[2];           // BMM1 of the tile done
   uint64_t s_full[2], s_free[2];
   uint64_t p_full[2];
@@ -88,7 +89,6 @@ struct Ctrl {
   uint64_t drain1, drain2;
   uint32_t tmem_base;
   int abort_flag;
-  uint32_t bad[kMaxRaw];        // rows of the stage whose page lies outside the pool
   alignas(16) float mult[kMaxRows];   // scale_log2 2^-s of the row's split; 0: no such row
   alignas(16) float m[kMaxRows];      // reference maximum (log2 of the scaled score)
   alignas(16) float off[kMaxRows];    // kPShift - m; -infinity: no such row
@@ -176,7 +176,8 @@ __device__ __forceinline__ void load_s(uint32_t addr, uint32_t (&s)[NR]) {
 
 // kTree: drafts see each other by p.tree_mask instead of in order.
 template <int NR, bool kTree>
-__global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const __grid_constant__ CUtensorMap tm_kv,
+                                                                         const DecodeParams p) {
   using M = Map<NR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -191,11 +192,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const D
   if (threadIdx.x == 0) {
     for (int s = 0; s < M::kRaw; ++s) {
       mbar_init(&ctrl->raw_full[s], 1);
-      mbar_init(&ctrl->raw_empty[s], 2);
+      mbar_init(&ctrl->raw_empty[s], 4);
     }
     mbar_init(&ctrl->q_ready, kDecodeWarps);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&ctrl->tile_full[s], kDecodeWarps);
+      mbar_init(&ctrl->k_full[s], kDecodeWarps);
+      mbar_init(&ctrl->v_full[s], kDecodeWarps);
       mbar_init(&ctrl->k_free[s], 1);
       mbar_init(&ctrl->s_full[s], 1);
       mbar_init(&ctrl->s_free[s], kSoftmaxWarps);
@@ -207,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const D
     ctrl->abort_flag = 0;
     fence_mbarrier_init();
   }
+  if (warp == kProducerWarp && lane == 0) tma_prefetch_desc(&tm_kv);
   if (warp == kBmm1Warp) {
     tmem_alloc(&ctrl->tmem_base, kTmemCols);
     tmem_relinquish();
@@ -238,71 +241,48 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const D
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ producer: raw rows, 32 keys a stage
-    const int P = p.page_size;
-    const int per = P < kSub ? kSub / P : 1;  // pages per stage
+    const int lg = __ffs(p.page_size) - 1;          // (a power of two)
+    const int per = max(1, kSub >> lg);             // pages per stage
+    const int box_bytes = min(p.page_size, kSub) * kFp4RowBytes;
     const int32_t* pt = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-    const int first_page = kv_start / P, last_page = (kv_end - 1) / P;
-    int base = first_page;
-    int cur = first_page + lane <= last_page ? __ldg(pt + first_page + lane) : 0;
-    int nxt = first_page + 32 + lane <= last_page ? __ldg(pt + first_page + 32 + lane) : 0;
+    const int last_page = (kv_end - 1) >> lg;
+    int base = kv_start >> lg;
+    int cur = base + lane <= last_page ? __ldg(pt + base + lane) : 0;
+    int nxt = base + 32 + lane <= last_page ? __ldg(pt + base + 32 + lane) : 0;
     const uint64_t policy = policy_evict_first();
+    const unsigned n_pages = static_cast<unsigned>(min(p.num_pages, static_cast<int64_t>(0x7fffffff)));
     bool bad_pid = false, ok = true;
     int issued = 0;
-    const int nsub = (kv_end - kv_start + kSub - 1) / kSub;
-    for (int i = 0; i < 4 * ntiles; ++i) {
-      const int s = i % M::kRaw;
-      const int k0 = kv_start + i * kSub;
-      if (i < nsub) {
-        const int pg0 = k0 / P;
-        while (pg0 - base >= 32) {  // advance the window of page ids (warp-uniform; a stage's last pages may lie in its
-          base += 32;               // second half)
-          cur = nxt;
-          const int nb = base + 32 + lane;
-          nxt = nb <= last_page ? __ldg(pt + nb) : 0;
-        }
-        const int at = pg0 - base + (lane < per ? lane : 0);
-        const int lo = __shfl_sync(0xffffffffu, cur, at & 31), hi = __shfl_sync(0xffffffffu, nxt, at & 31);
-        const int pid = at < 32 ? lo : hi;
-        const int key = k0 + lane * P;  // this lane's first key
-        const int rows = lane < per ? max(0, min(min(P, kSub), kv_end - key)) : 0;
-        const bool outside = rows > 0 && (pid < 0 || pid >= p.num_pages);
-        bad_pid |= outside;
-        uint32_t bad = 0;
-        if (outside) bad = (rows >= 32 ? 0xffffffffu : ((1u << rows) - 1)) << (lane * P & 31);
-        bad = __reduce_or_sync(0xffffffffu, bad);
-        const uint32_t bytes = outside ? 0u : static_cast<uint32_t>(rows * kFp4RowBytes);
-        const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
-        if (i >= M::kRaw) {
-          bool w = true;
-          if (lane == 0) w = mbar_wait(&ctrl->raw_empty[s], ((i / M::kRaw) - 1) & 1, abort_flag);
-          ok = __shfl_sync(0xffffffffu, w, 0);
-          if (!ok) break;
-        }
-        if (lane == 0) {
-          ctrl->bad[s] = bad;
-          mbar_arrive_expect_tx(&ctrl->raw_full[s], total);
-        }
-        __syncwarp();
-        if (bytes > 0)
-          bulk_load(smem + M::kOffRaw + s * kRawStage + lane * P * kFp4RowBytes,
-                    p.kv_pool + (static_cast<int64_t>(pid) * P + (P > kSub ? k0 % P : 0)) * kFp4RowBytes, bytes,
-                    &ctrl->raw_full[s], policy);
-      } else {  // the last tile's stages past its end: nothing to copy (their keys have weight 0)
-        if (i >= M::kRaw) {
-          bool w = true;
-          if (lane == 0) w = mbar_wait(&ctrl->raw_empty[s], ((i / M::kRaw) - 1) & 1, abort_flag);
-          ok = __shfl_sync(0xffffffffu, w, 0);
-          if (!ok) break;
-        }
-        if (lane == 0) {
-          ctrl->bad[s] = 0xffffffffu;
-          mbar_arrive(&ctrl->raw_full[s]);
-        }
+    int s = 0;
+    uint32_t parity = 1;  // of the stage's previous release (none to wait for in the first round)
+    for (int i = 0; i < 2 * ntiles; ++i) {
+      const int k0 = kv_start + i * kSub, pg0 = k0 >> lg;
+      const int npg = k0 < kv_end ? min(per, last_page - pg0 + 1) : 0;  // (none: past the end of the last tile)
+      if (pg0 - base >= 32) {  // advance the window of page ids (warp-uniform; a stage's pages lie in one half: both
+        base += 32;            // start at a multiple of `per` pages)
+        cur = nxt;
+        const int nb = base + 32 + lane;
+        nxt = nb <= last_page ? __ldg(pt + nb) : 0;
       }
-      issued = i + 1;
+      // (everything but the copies is done before the wait)
+      const int pid = __shfl_sync(0xffffffffu, cur, (pg0 + lane - base) & 31);  // lane k: the stage's k-th page
+      // a page id outside the pool: a box wholly before the first row, which arrives as zeros
+      const bool outside = static_cast<unsigned>(pid) >= n_pages;
+      bad_pid |= outside && lane < npg;
+      const int y = outside ? -kSub : (pid << lg) + (k0 & (p.page_size - 1));
+      uint8_t* dst = smem + M::kOffRaw + s * kRawStage;
+      ok = mbar_wait(&ctrl->raw_empty[s], parity, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&ctrl->raw_full[s], static_cast<uint32_t>(npg * box_bytes));
       __syncwarp();
+      if (lane < npg) tma_load_2d(dst + lane * box_bytes, &tm_kv, &ctrl->raw_full[s], 0, y, policy);
+      issued = i + 1;
+      if (++s == M::kRaw) {
+        s = 0;
+        parity ^= 1u;
+      }
     }
-    if (__any_sync(0xffffffffu, bad_pid) && lane == 0) atomicOr(p.status, kStatusDeviceArg);
+    if (bad_pid) atomicOr(p.status, kStatusDeviceArg);
     // copies still in flight (their readers may have given up) land before the CTA exits
     for (int k = max(0, issued - M::kRaw); k < issued; ++k) drain_wait(&ctrl->raw_full[k % M::kRaw], (k / M::kRaw) & 1);
   } else if (warp == kBmm1Warp) {
@@ -313,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const D
     bool ok = mbar_wait(&ctrl->q_ready, 0, abort_flag);
     for (int j = 0; j < ntiles; ++j) {
       const int sb = j & 1, kb = j % M::kKBufs;
-      if (ok) ok = mbar_wait(&ctrl->tile_full[sb], (j >> 1) & 1, abort_flag);
+      if (ok) ok = mbar_wait(&ctrl->k_full[sb], (j >> 1) & 1, abort_flag);
       if (ok && j >= 2) ok = mbar_wait(&ctrl->s_free[sb], ((j - 2) >> 1) & 1, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
@@ -345,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const D
     bool ok = true;
     for (int j = 0; j < ntiles; ++j) {
       const int pb = j & 1;
-      if (ok) ok = mbar_wait(&ctrl->tile_full[pb], (j >> 1) & 1, abort_flag);
+      if (ok) ok = mbar_wait(&ctrl->v_full[pb], (j >> 1) & 1, abort_flag);
       if (ok) ok = mbar_wait(&ctrl->p_full[pb], (j >> 1) & 1, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
@@ -430,70 +410,86 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const D
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->q_ready);
     }
+    // A tile's codes go to tensor memory first (K) and from there to shared memory (V), one tile later where
+    // two K tiles fit: BMM1 and the softmax then need not wait for a V buffer, nor the next tile's decoding.
     const int row = quad * 32 + lane;  // this thread's key of a tile
     const uint32_t v_row = smem_u32(smem + M::kOffV) + row * 64 + half * 4 * kVBlock;
     const uint32_t sw = ((row >> 1) & 3) << 4;
     const uint32_t k_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + M::kK;
-    for (int j = 0; j < ntiles; ++j) {
-      const int i = 4 * j + quad, s = i % M::kRaw, vb = j & 1, kb = j % M::kKBufs;
-      bool ok = mbar_wait(&ctrl->raw_full[s], (i / M::kRaw) & 1, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) {
-        failed = true;
-        break;
-      }
-      const uint32_t raw = smem_u32(smem + M::kOffRaw + s * kRawStage) + lane * kFp4RowBytes;
-      uint4 w[8], rope[2];
-      uint32_t ex[2];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = ld_shared_v4(raw + half * 128 + k * 16);
-      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(ex[0]), "=r"(ex[1]) : "r"(raw + 256 + half * 8));
-#pragma unroll
-      for (int k = 0; k < 2; ++k) rope[k] = ld_shared_v4(raw + 272 + half * 32 + k * 16);
-      const uint32_t bad = ctrl->bad[s];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctrl->raw_empty[s]);
-      if ((bad >> lane) & 1) {  // a row without a page, or past the end: zeros
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = make_uint4(0u, 0u, 0u, 0u);
-        rope[0] = rope[1] = make_uint4(0u, 0u, 0u, 0u);
-        ex[0] = ex[1] = 0u;
-      }
-      // the K columns and the V buffer are free once BMM1 and BMM2 of their last tile have completed
-      if (j >= M::kKBufs) ok = mbar_wait(&ctrl->k_free[kb], ((j / M::kKBufs) - 1) & 1, abort_flag);
-      if (ok && j >= 2) ok = mbar_wait(&ctrl->o_done[vb], ((j >> 1) - 1) & 1, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) {
-        failed = true;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t kcol = k_lane + kb * kKCols;
-      const uint32_t vrow = v_row + vb * kVTile;
-#pragma unroll
-      for (int k2 = 0; k2 < 4; ++k2) {  // 64 columns: a block of V, 16 columns of tensor memory
-        uint32_t o[16];
-#pragma unroll
-        for (int k1 = 0; k1 < 2; ++k1) {
-          const int k = 2 * k2 + k1;
-          const uint32_t word[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {  // 16 columns under one power of two
-            const uint32_t e = (ex[k >> 2] >> (8 * (k & 3) + 4 * g)) & 15u;
-            const uint32_t lo = e * 0x08080800u + 0x14100800u, hi = e * 0x08080808u + 0x24201C18u;
-            fp4_to_e4m3(word[2 * g], lo, hi, o[8 * k1 + 4 * g], o[8 * k1 + 4 * g + 1]);
-            fp4_to_e4m3(word[2 * g + 1], lo, hi, o[8 * k1 + 4 * g + 2], o[8 * k1 + 4 * g + 3]);
-          }
+    constexpr int kLag = M::kKBufs - 1;
+    for (int j = 0; j < ntiles + kLag; ++j) {
+      bool ok = true;
+      if (j < ntiles) {
+        const int i = 2 * j + (quad >> 1), s = i % M::kRaw, kb = j % M::kKBufs;
+        ok = mbar_wait(&ctrl->raw_full[s], (i / M::kRaw) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) {
+          failed = true;
+          break;
         }
+        const uint32_t raw = smem_u32(smem + M::kOffRaw + s * kRawStage) + ((quad & 1) * 32 + lane) * kFp4RowBytes;
+        uint4 w[8], rope[2];
+        uint32_t ex[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) st_shared_v4(vrow + k2 * kVBlock + ((q << 4) ^ sw), o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-        tmem_st16(kcol + half * 64 + k2 * 16, o);
+        for (int k = 0; k < 8; ++k) w[k] = ld_shared_v4(raw + half * 128 + k * 16);
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(ex[0]), "=r"(ex[1]) : "r"(raw + 256 + half * 8));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) rope[k] = ld_shared_v4(raw + 272 + half * 32 + k * 16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->raw_empty[s]);
+        // the K columns are free once BMM1 of their last tile has completed (this warp's own reads have)
+        if (j >= M::kKBufs) ok = mbar_wait(&ctrl->k_free[kb], ((j / M::kKBufs) - 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t kcol = k_lane + kb * kKCols;
+#pragma unroll
+        for (int k2 = 0; k2 < 4; ++k2) {  // 64 columns: 16 columns of tensor memory
+          uint32_t o[16];
+#pragma unroll
+          for (int k1 = 0; k1 < 2; ++k1) {
+            const int k = 2 * k2 + k1;
+            const uint32_t word[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {  // 16 columns under one power of two
+              const uint32_t e = (ex[k >> 2] >> (8 * (k & 3) + 4 * g)) & 15u;
+              const uint32_t lo = e * 0x08080800u + 0x14100800u, hi = e * 0x08080808u + 0x24201C18u;
+              fp4_to_e4m3(word[2 * g], lo, hi, o[8 * k1 + 4 * g], o[8 * k1 + 4 * g + 1]);
+              fp4_to_e4m3(word[2 * g + 1], lo, hi, o[8 * k1 + 4 * g + 2], o[8 * k1 + 4 * g + 3]);
+            }
+          }
+          tmem_st16(kcol + half * 64 + k2 * 16, o);
+        }
+        const uint32_t ro[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w, rope[1].x, rope[1].y, rope[1].z, rope[1].w};
+        tmem_st8(kcol + 128 + half * 8, ro);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->k_full[j & 1]);
       }
-      const uint32_t ro[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w, rope[1].x, rope[1].y, rope[1].z, rope[1].w};
-      tmem_st8(kcol + 128 + half * 8, ro);
-      tmem_st_wait();
+      const int jv = j - kLag;
+      if (jv < 0) continue;
+      // the V buffer is free once BMM2 of its last tile has completed
+      if (jv >= 2) ok = mbar_wait(&ctrl->o_done[jv & 1], ((jv >> 1) - 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        failed = true;
+        break;
+      }
+      const uint32_t vrow = v_row + (jv & 1) * kVTile;
+      const uint32_t from = k_lane + (jv % M::kKBufs) * kKCols + half * 64;
+#pragma unroll
+      for (int k2 = 0; k2 < 4; k2 += 2) {
+        uint32_t o[32];
+        tmem_ld32(from + k2 * 16, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          st_shared_v4(vrow + (k2 + (q >> 2)) * kVBlock + (((q & 3) << 4) ^ sw), o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+      }
       fence_proxy_async_smem();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctrl->tile_full[vb]);
+      if (lane == 0) mbar_arrive(&ctrl->v_full[jv & 1]);
     }
     worker_failed = failed;
   } else {
@@ -713,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const D
 
 int fp4_group_rows(int R) { return R <= 16 ? 16 : 32; }
 
-cudaError_t launch_decode_partial_fp4(const DecodeParams& p, cudaStream_t stream) {
+cudaError_t launch_decode_partial_fp4(const DecodeParams& p, const CUtensorMap& tm_kv, cudaStream_t stream) {
   // [32 rows][tree]
   static constexpr decltype(&decode_partial_fp4_kernel<16, false>) kernels[4] = {
       decode_partial_fp4_kernel<16, false>, decode_partial_fp4_kernel<16, true>, decode_partial_fp4_kernel<32, false>,
@@ -742,7 +738,7 @@ cudaError_t launch_decode_partial_fp4(const DecodeParams& p, cudaStream_t stream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernels[2 * wide + (p.tree_mask ? 1 : 0)], p);
+  return cudaLaunchKernelEx(&cfg, kernels[2 * wide + (p.tree_mask ? 1 : 0)], tm_kv, p);
 }
 
 }  // namespace mla

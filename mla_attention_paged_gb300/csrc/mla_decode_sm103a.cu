@@ -1040,7 +1040,7 @@ cudaError_t launch_decode_partial(const DecodeParams& p, const CUtensorMap& tm_q
                                   int head_groups, cudaStream_t stream) {
   switch (p.kv_dtype) {
     case kKvE4m3: return launch_decode_partial_e4m3(p, tm_q, tm_kv, head_groups, stream);
-    case kKvFp4: return launch_decode_partial_fp4(p, stream);
+    case kKvFp4: return launch_decode_partial_fp4(p, tm_kv, stream);
     case kKvInt8:
       return p.tree_mask ? launch_partial_impl<kKvInt8, true>(p, tm_q, tm_kv, head_groups, stream)
                          : launch_partial_impl<kKvInt8, false>(p, tm_q, tm_kv, head_groups, stream);

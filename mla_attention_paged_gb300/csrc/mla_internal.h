@@ -184,7 +184,7 @@ cudaError_t launch_decode_partial_e4m3(const DecodeParams& p, const CUtensorMap&
 cudaError_t launch_decode_partial_narrow(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv,
                                          cudaStream_t stream);
 // Decode over a 4-bit pool (trees too).
-cudaError_t launch_decode_partial_fp4(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_decode_partial_fp4(const DecodeParams& p, const CUtensorMap& tm_kv, cudaStream_t stream);
 int fp4_group_rows(int R);  // folded rows per CTA
 // Tree decode over a bf16 pool for requests of more than kTreeNarrowRows folded rows (pairs of CTAs).
 cudaError_t launch_decode_tree_pair(const DecodeParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,

@@ -97,7 +97,8 @@ typedef struct mla_decode_plan_t {
   int32_t max_splits;        /* splits of the longest request                            */
   int32_t max_seq_len;       /* longest planned request; device seq_lens must not exceed */
   int32_t split_major;       /* launch order of the partial kernel's CTAs: 1 = split by
-                                split (plans of more than one wave), 0 = request by request */
+                                split (plans of more than one wave), 0 = request by request,
+                                2 = whole splits, then remainders (4-bit pools)          */
   size_t workspace_bytes;    /* bytes mla_decode needs in `workspace` (0 = none)         */
 } mla_decode_plan_t;
 

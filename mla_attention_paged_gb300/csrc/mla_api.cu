@@ -115,15 +115,22 @@ constexpr long long kPairFixedTiles = 8;
 // split s + 1, so that short remainders go last) for one row group; request by request
 // for several, whose row groups share each tile through L2 and so run best side by side
 // on one request's keys.
-bool split_major_order(int groups) { return groups == 1; }
+// A 4-bit pool's kernel finds its splits itself (kWholeFirst: all whole splits, then the remainders), up to
+// kFp4ListBatch requests, whose lengths each CTA then looks through.
+constexpr int kByRequest = 0, kBySplit = 1, kWholeFirst = 2;
+constexpr int kFp4ListBatch = 128;
+int launch_order(int groups, int kv_dtype, int batch) {
+  if (kv_dtype == MLA_KV_FP4 && batch <= kFp4ListBatch) return kWholeFirst;
+  return groups == 1 ? kBySplit : kByRequest;
+}
 
 // Estimated duration of a decode call whose splits are ct tiles long: the partial kernel's
-// CTAs, in the grid's launch order (group fastest, then split_major_order's), are
+// CTAs, in the grid's launch order (group fastest, then launch_order's), are
 // dispatched each onto the SM that frees first; CTAs of splits a request does not have
 // exit at once and cost nothing.  Plus the combine, when some request is split.
 // `bound`: the caller only needs costs up to it; once the estimate is known to exceed it,
 // some value above it is returned without finishing the schedule.
-long long plan_cost(const std::vector<int>& tiles, int groups, int ct, int sms, long long fixed,
+long long plan_cost(const std::vector<int>& tiles, int order, int groups, int ct, int sms, long long fixed,
                     long long bound = std::numeric_limits<long long>::max()) {
   int max_splits = 1;
   long long n_ctas = 0, longest = 0, work = 0;
@@ -156,7 +163,12 @@ long long plan_cost(const std::vector<int>& tiles, int groups, int ct, int sms, 
       return span + combine <= bound;  // (the span only grows)
     };
     bool go = true;
-    if (split_major_order(groups)) {
+    if (order == kWholeFirst) {
+      for (size_t i = 0; go && i < tiles.size(); ++i)
+        for (int s = 0; go && (s + 1) * static_cast<long long>(ct) <= tiles[i]; ++s) go = dispatch(tiles[i], s);
+      for (size_t i = 0; go && i < tiles.size(); ++i)
+        if (tiles[i] % ct != 0) go = dispatch(tiles[i], tiles[i] / ct);
+    } else if (order == kBySplit) {
       for (int s = 0; go && s < max_splits; ++s)
         for (size_t i = 0; go && i < tiles.size(); ++i)
           if (s * static_cast<long long>(ct) < tiles[i]) go = dispatch(tiles[i], s);
@@ -180,7 +192,7 @@ long long plan_cost(const std::vector<int>& tiles, int groups, int ct, int sms, 
 // with an e4m3 pool's larger fixed cost, 109 and remainders of 43.)  The candidate with the
 // lowest plan_cost wins, the one with fewer splits on a tie, so a split is only taken when
 // the model says it shortens the call.
-int choose_chunk_tiles(const std::vector<int>& lens, int tile_keys, int groups, int sms, long long fixed) {
+int choose_chunk_tiles(const std::vector<int>& lens, int tile_keys, int order, int groups, int sms, long long fixed) {
   std::vector<int> tiles;
   tiles.reserve(lens.size());
   int max_tiles = 1;
@@ -228,9 +240,9 @@ int choose_chunk_tiles(const std::vector<int>& lens, int tile_keys, int groups, 
   // A candidate wins with a lower cost, or an equal one and fewer splits (a longer chunk),
   // so costs above the best so far need not be finished.
   int best = max_tiles;
-  long long best_cost = plan_cost(tiles, groups, max_tiles, sms, fixed);
+  long long best_cost = plan_cost(tiles, order, groups, max_tiles, sms, fixed);
   auto consider = [&](int ct) {
-    const long long c = plan_cost(tiles, groups, ct, sms, fixed, best_cost);
+    const long long c = plan_cost(tiles, order, groups, ct, sms, fixed, best_cost);
     if (c < best_cost || (c == best_cost && ct > best)) {
       best = ct;
       best_cost = c;
@@ -345,7 +357,8 @@ int make_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads,
   const int groups = pairs ? tree_pair_groups(pl.rows) : pl.head_groups;
   const int units = pairs ? std::max(1, num_sms / 2) : num_sms;
   const int tile_keys = kv_dtype == MLA_KV_FP4 ? kFp4TileKeys : kTileKeys;
-  const int ct = choose_chunk_tiles(lens, tile_keys, groups, units, pairs ? kPairFixedTiles : cta_fixed_tiles(kv_dtype));
+  const int order = launch_order(groups, kv_dtype, batch);
+  const int ct = choose_chunk_tiles(lens, tile_keys, order, groups, units, pairs ? kPairFixedTiles : cta_fixed_tiles(kv_dtype));
   pl.chunk_tokens = ct * tile_keys;
   pl.max_seq_len = max_len;
   pl.max_splits = (max_len + pl.chunk_tokens - 1) / pl.chunk_tokens;
@@ -354,7 +367,7 @@ int make_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads,
     // more CTAs with work than SMs, one row group: launch split by split, as the cost model assumed
     long long n_ctas = 0;
     for (int L : lens) n_ctas += (L + pl.chunk_tokens - 1) / pl.chunk_tokens;
-    pl.split_major = (n_ctas * groups > units && split_major_order(groups)) ? 1 : 0;
+    pl.split_major = order == kWholeFirst ? kWholeFirst : (n_ctas * groups > units && order == kBySplit) ? 1 : 0;
   }
   pl.workspace_bytes = partial_bytes(pl, tree);
   {

@@ -18,9 +18,9 @@
 //  * A key is one thread's in the softmax, so a row's sum is kept per thread and its running maximum
 //    moves only when some score exceeds it by more than 2 (log2): ordinary tiles reduce nothing across
 //    threads but one vote.
-// One CTA per (group of NR rows, split, request), 128 keys a tile, 608 threads: softmax warps 0-7 (32 keys
+// One CTA per (group of NR rows, split, request), 128 keys a tile, 576 threads: softmax warps 0-7 (32 keys
 // and half of the rows each), decoding warps 8-15 (32 keys and half of the columns each; a row's codes go
-// to registers at once and free their stage), producer 16 (boxes of up to 64 rows), BMM1 17, BMM2 18.
+// to registers at once and free their stage), producer 16 (boxes of up to 64 rows), MMA 17.
 // Every wait is bounded; on expiry the CTA records a timeout, drains its copies and MMAs, frees tensor
 // memory and returns.
 #include <cuda_fp16.h>
@@ -43,8 +43,8 @@ constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kDecodeWarps = 8;
 constexpr int kDecodeThreads = 32 * kDecodeWarps;
 constexpr int kWorkers = kSoftmaxThreads + kDecodeThreads;
-constexpr int kProducerWarp = 16, kBmm1Warp = 17, kBmm2Warp = 18;
-constexpr int kThreads = 608;
+constexpr int kProducerWarp = 16, kMmaWarp = 17;
+constexpr int kThreads = 576;
 constexpr int kMaxRaw = 3;
 constexpr int kMaxRows = 32;
 constexpr int kCtrlBytes = 3072;
@@ -86,9 +86,10 @@ struct Ctrl {
   uint64_t s_full[2], s_free[2];
   uint64_t p_full[2];
   uint64_t o_done[2];           // BMM2 of the tile done
-  uint64_t drain1, drain2;
+  uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
+  int item[2];                  // request and split (request -1: none)
   alignas(16) float mult[kMaxRows];   // scale_log2 2^-s of the row's split; 0: no such row
   alignas(16) float m[kMaxRows];      // reference maximum (log2 of the scaled score)
   alignas(16) float off[kMaxRows];    // kPShift - m; -infinity: no such row
@@ -166,6 +167,37 @@ __device__ __forceinline__ float lanes_sum(float (&v)[NR], int lane) {
   return v[0];
 }
 
+// The item-th split of the batch in the order "whole splits, then remainders", by a whole warp: request and
+// split to out[0], out[1]; request -1 past the last.  A bad length counts as none (item 0 reports it).
+__device__ __forceinline__ void find_split(const DecodeParams& p, int item, int lane, int* out) {
+  int b = -1, split = 0;
+  const bool first = item == 0;
+  for (int pass = 0; pass < 2 && b < 0; ++pass) {
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      int L = b0 + lane < p.B ? __ldg(p.seq_lens + b0 + lane) : p.T;
+      const bool bad = L < p.T || L > p.max_seq || static_cast<int64_t>(L) > static_cast<int64_t>(p.max_pages) * p.page_size;
+      if (bad && first && pass == 0) atomicOr(p.status, kStatusDeviceArg);
+      if (bad || b0 + lane >= p.B) L = 0;
+      const int whole = L / p.chunk, count = pass == 0 ? whole : (L > whole * p.chunk ? 1 : 0);
+      int sum = count;  // inclusive, over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      const int total = __shfl_sync(0xffffffffu, sum, 31);
+      if (item < total) {
+        const int at = __ffs(__ballot_sync(0xffffffffu, sum > item)) - 1;
+        b = b0 + at;
+        split = __shfl_sync(0xffffffffu, pass == 0 ? item - (sum - count) : whole, at);
+        break;
+      }
+      item -= total;
+    }
+  }
+  if (lane == 0) out[0] = b, out[1] = split;
+}
+
 template <int NR>
 __device__ __forceinline__ void load_s(uint32_t addr, uint32_t (&s)[NR]) {
   if constexpr (NR == 8) tmem_ld8(addr, s);
@@ -184,10 +216,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + M::kOffCtrl);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int group = blockIdx.x;
-  // (launch order as the other decode kernels': split by split in a plan of several waves)
-  const int b = p.split_major ? blockIdx.y : blockIdx.z;
-  const int split = p.split_major ? blockIdx.z : blockIdx.y;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < M::kRaw; ++s) {
@@ -204,13 +232,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
       mbar_init(&ctrl->p_full[s], kSoftmaxWarps);
       mbar_init(&ctrl->o_done[s], 1);
     }
-    mbar_init(&ctrl->drain1, 1);
-    mbar_init(&ctrl->drain2, 1);
+    mbar_init(&ctrl->drain, 1);
     ctrl->abort_flag = 0;
     fence_mbarrier_init();
   }
   if (warp == kProducerWarp && lane == 0) tma_prefetch_desc(&tm_kv);
-  if (warp == kBmm1Warp) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&ctrl->tmem_base, kTmemCols);
     tmem_relinquish();
   }
@@ -221,13 +248,28 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
   // programmatic dependent launch: no input is read before the previous kernel has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if (p.part_scale && threadIdx.x == 0 && group == 0 && b == 0 && split == 0) *p.part_scale = p.v_scale;
+  if (p.part_scale && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) *p.part_scale = p.v_scale;
+  // Which split this CTA takes: whole splits first, then the remainders (split_major 2), split by split (1) or
+  // request by request (0).  Splits that a request does not have come last in the first order and end at once: in
+  // the others they hold up the CTAs behind them, which measured 24 us on 16 requests of 8K-131K keys.
+  int group = blockIdx.x, b = p.split_major ? blockIdx.y : blockIdx.z, split = p.split_major ? blockIdx.z : blockIdx.y;
+  if (p.split_major == 2) {
+    const int groups = (p.R + NR - 1) / NR;
+    group = blockIdx.x % groups;
+    if (warp == 0) find_split(p, blockIdx.x / groups, lane, ctrl->item);
+    __syncthreads();
+    b = ctrl->item[0], split = ctrl->item[1];
+    if (b < 0) {  // (CTA-uniform) no such split
+      if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+      return;
+    }
+  }
   const int L = p.seq_lens[b];
   const bool bad_len = L < p.T || L > p.max_seq || static_cast<int64_t>(L) > static_cast<int64_t>(p.max_pages) * p.page_size;
   if (bad_len && threadIdx.x == 0 && split == 0 && group == 0) atomicOr(p.status, kStatusDeviceArg);
   const int kv_start = split * p.chunk;
   if (bad_len || kv_start >= L) {  // (CTA-uniform) a bad length, or this request needs fewer splits
-    if (warp == kBmm1Warp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
     return;
   }
   const int kv_end = min(L, kv_start + p.chunk);
@@ -285,67 +327,62 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
     if (bad_pid) atomicOr(p.status, kStatusDeviceArg);
     // copies still in flight (their readers may have given up) land before the CTA exits
     for (int k = max(0, issued - M::kRaw); k < issued; ++k) drain_wait(&ctrl->raw_full[k % M::kRaw], (k / M::kRaw) & 1);
-  } else if (warp == kBmm1Warp) {
-    // ------------------------------------------------------------------ BMM1 issuer
-    const uint32_t idesc = make_idesc_e4m3(128, NR);
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------ MMA issuer: BMM1 of a tile goes before BMM2 of
+    // the last one, so that its K columns and the next softmax wait for one product, not two
+    const uint32_t idesc1 = make_idesc_e4m3(128, NR);
+    const uint32_t idesc2 = make_idesc_e4m3(128, 2 * NR, true, false);
     const uint64_t hi_desc = make_smem_desc_sw64(smem_u32(smem + M::kOffQ));
     const uint64_t lo_desc = make_smem_desc_sw64(smem_u32(smem + M::kOffQ + M::kQPart));
     bool ok = mbar_wait(&ctrl->q_ready, 0, abort_flag);
-    for (int j = 0; j < ntiles; ++j) {
-      const int sb = j & 1, kb = j % M::kKBufs;
-      if (ok) ok = mbar_wait(&ctrl->k_full[sb], (j >> 1) & 1, abort_flag);
-      if (ok && j >= 2) ok = mbar_wait(&ctrl->s_free[sb], ((j - 2) >> 1) & 1, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      const uint32_t d = tmem + M::kS + sb * NR;
-      const uint32_t a = tmem + M::kK + kb * kKCols;
-      if (elect_one()) {
+    for (int j = 0; j <= ntiles; ++j) {
+      if (j < ntiles) {
+        const int sb = j & 1, kb = j % M::kKBufs;
+        if (ok) ok = mbar_wait(&ctrl->k_full[sb], (j >> 1) & 1, abort_flag);
+        if (ok && j >= 2) ok = mbar_wait(&ctrl->s_free[sb], ((j - 2) >> 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + M::kS + sb * NR;
+        const uint32_t a = tmem + M::kK + kb * kKCols;
+        if (elect_one()) {
 #pragma unroll
-        for (int c = 0; c < 9; ++c) {
+          for (int c = 0; c < 9; ++c) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint64_t off = static_cast<uint64_t>((c * M::kQBlock + k * 32) >> 4);
-            umma_f8_ts(d, a + c * 16 + k * 8, hi_desc + off, idesc, (c | k) != 0 ? 1u : 0u);
-            umma_f8_ts(d, a + c * 16 + k * 8, lo_desc + off, idesc, 1u);
+            for (int k = 0; k < 2; ++k) {
+              const uint64_t off = static_cast<uint64_t>((c * M::kQBlock + k * 32) >> 4);
+              umma_f8_ts(d, a + c * 16 + k * 8, hi_desc + off, idesc1, (c | k) != 0 ? 1u : 0u);
+              umma_f8_ts(d, a + c * 16 + k * 8, lo_desc + off, idesc1, 1u);
+            }
           }
+          umma_commit(&ctrl->s_full[sb]);
+          umma_commit(&ctrl->k_free[kb]);
         }
-        umma_commit(&ctrl->s_full[sb]);
-        umma_commit(&ctrl->k_free[kb]);
+        __syncwarp();
       }
-      __syncwarp();
-    }
-    if (elect_one()) {  // every MMA this warp issued completes before tensor memory is released
-      umma_commit(&ctrl->drain1);
-      drain_wait(&ctrl->drain1, 0);
-    }
-    __syncwarp();
-  } else if (warp == kBmm2Warp) {
-    // ------------------------------------------------------------------ BMM2 issuer
-    const uint32_t idesc = make_idesc_e4m3(128, 2 * NR, true, false);
-    bool ok = true;
-    for (int j = 0; j < ntiles; ++j) {
-      const int pb = j & 1;
-      if (ok) ok = mbar_wait(&ctrl->v_full[pb], (j >> 1) & 1, abort_flag);
-      if (ok) ok = mbar_wait(&ctrl->p_full[pb], (j >> 1) & 1, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      const uint64_t v_desc = make_smem_desc_sw64(smem_u32(smem + M::kOffV + pb * kVTile), kVBlock, 512);
-      const uint64_t p_desc = make_smem_desc(smem_u32(smem + M::kOffP + pb * M::kPBuf), 16, 1024);
-      if (elect_one()) {
+      if (j > 0) {
+        const int jv = j - 1, pb = jv & 1;
+        if (ok) ok = mbar_wait(&ctrl->v_full[pb], (jv >> 1) & 1, abort_flag);
+        if (ok) ok = mbar_wait(&ctrl->p_full[pb], (jv >> 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const uint64_t v_desc = make_smem_desc_sw64(smem_u32(smem + M::kOffV + pb * kVTile), kVBlock, 512);
+        const uint64_t p_desc = make_smem_desc(smem_u32(smem + M::kOffP + pb * M::kPBuf), 16, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int qc = 0; qc < 4; ++qc) {
+          for (int qc = 0; qc < 4; ++qc) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_f8(tmem + M::kO + qc * 2 * NR, v_desc + static_cast<uint64_t>((2 * qc * kVBlock + kk * 2048) >> 4),
-                    p_desc + static_cast<uint64_t>((kk * 32) >> 4), idesc, (j > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f8(tmem + M::kO + qc * 2 * NR, v_desc + static_cast<uint64_t>((2 * qc * kVBlock + kk * 2048) >> 4),
+                      p_desc + static_cast<uint64_t>((kk * 32) >> 4), idesc2, (jv > 0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(&ctrl->o_done[pb]);
         }
-        umma_commit(&ctrl->o_done[pb]);
+        __syncwarp();
       }
-      __syncwarp();
     }
-    if (elect_one()) {
-      umma_commit(&ctrl->drain2);
-      drain_wait(&ctrl->drain2, 0);
+    if (elect_one()) {  // every MMA completes before tensor memory is released
+      umma_commit(&ctrl->drain);
+      drain_wait(&ctrl->drain, 0);
     }
     __syncwarp();
   } else if (warp >= kSoftmaxWarps) {
@@ -410,34 +447,38 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->q_ready);
     }
-    // A tile's codes go to tensor memory first (K) and from there to shared memory (V), one tile later where
-    // two K tiles fit: BMM1 and the softmax then need not wait for a V buffer, nor the next tile's decoding.
+    // A tile's codes go to tensor memory first (K) and from there to shared memory (V), one tile later where two K
+    // tiles fit: BMM1 and the softmax then need not wait for a V buffer, nor the next tile's decoding.
     const int row = quad * 32 + lane;  // this thread's key of a tile
     const uint32_t v_row = smem_u32(smem + M::kOffV) + row * 64 + half * 4 * kVBlock;
     const uint32_t sw = ((row >> 1) & 3) << 4;
-    const uint32_t k_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + M::kK;
-    constexpr int kLag = M::kKBufs - 1;
+    const uint32_t k_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + M::kK + half * 64;
+    const uint32_t raw_at = ((quad & 1) * 32 + lane) * kFp4RowBytes;
+    int s = (quad >> 1) % M::kRaw;
+    uint32_t raw_parity = 0;
+    constexpr int kLag = M::kKBufs - 1;  // with two K tiles, the V copy runs a tile behind
     for (int j = 0; j < ntiles + kLag; ++j) {
       bool ok = true;
       if (j < ntiles) {
-        const int i = 2 * j + (quad >> 1), s = i % M::kRaw, kb = j % M::kKBufs;
-        ok = mbar_wait(&ctrl->raw_full[s], (i / M::kRaw) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) {
-          failed = true;
-          break;
-        }
-        const uint32_t raw = smem_u32(smem + M::kOffRaw + s * kRawStage) + ((quad & 1) * 32 + lane) * kFp4RowBytes;
         uint4 w[8], rope[2];
         uint32_t ex[2];
+        ok = mbar_wait(&ctrl->raw_full[s], raw_parity, abort_flag);
+        const uint32_t raw = smem_u32(smem + M::kOffRaw + s * kRawStage) + raw_at;
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k] = ld_shared_v4(raw + half * 128 + k * 16);
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(ex[0]), "=r"(ex[1]) : "r"(raw + 256 + half * 8));
 #pragma unroll
         for (int k = 0; k < 2; ++k) rope[k] = ld_shared_v4(raw + 272 + half * 32 + k * 16);
+        const int kb = j % M::kKBufs;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctrl->raw_empty[s]);
+        s += 2;
+        if (s >= M::kRaw) {
+          s -= M::kRaw;
+          raw_parity ^= 1u;
+        }
         // the K columns are free once BMM1 of their last tile has completed (this warp's own reads have)
-        if (j >= M::kKBufs) ok = mbar_wait(&ctrl->k_free[kb], ((j / M::kKBufs) - 1) & 1, abort_flag);
+        if (ok && j >= M::kKBufs) ok = mbar_wait(&ctrl->k_free[kb], ((j / M::kKBufs) - 1) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
           break;
@@ -459,10 +500,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
               fp4_to_e4m3(word[2 * g + 1], lo, hi, o[8 * k1 + 4 * g + 2], o[8 * k1 + 4 * g + 3]);
             }
           }
-          tmem_st16(kcol + half * 64 + k2 * 16, o);
+          tmem_st16(kcol + k2 * 16, o);
         }
         const uint32_t ro[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w, rope[1].x, rope[1].y, rope[1].z, rope[1].w};
-        tmem_st8(kcol + 128 + half * 8, ro);
+        tmem_st8(kcol + 128 - half * 56, ro);  // (columns 128 + 8 half of the tile)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -477,15 +518,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
         break;
       }
       const uint32_t vrow = v_row + (jv & 1) * kVTile;
-      const uint32_t from = k_lane + (jv % M::kKBufs) * kKCols + half * 64;
+      const uint32_t from = k_lane + (jv % M::kKBufs) * kKCols;
+      uint32_t o[2][32];
+      tmem_ld32(from, o[0]);
+      tmem_ld32(from + 32, o[1]);
+      tmem_ld_wait();
 #pragma unroll
-      for (int k2 = 0; k2 < 4; k2 += 2) {
-        uint32_t o[32];
-        tmem_ld32(from + k2 * 16, o);
-        tmem_ld_wait();
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          st_shared_v4(vrow + (k2 + (q >> 2)) * kVBlock + (((q & 3) << 4) ^ sw), o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+      for (int q = 0; q < 16; ++q) {
+        const uint32_t* c = &o[q >> 3][4 * (q & 7)];
+        st_shared_v4(vrow + (q >> 2) * kVBlock + (((q & 3) << 4) ^ sw), c[0], c[1], c[2], c[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -699,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
   if (threadIdx.x == 0 && ctrl->abort_flag == kAbortTimeout) atomicOr(p.status, kStatusTimeout);
   // every store of this CTA is issued: the combine grid may be scheduled now
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == kBmm1Warp) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -729,7 +770,9 @@ cudaError_t launch_decode_partial_fp4(const DecodeParams& p, const CUtensorMap& 
   const int rows = fp4_group_rows(p.R), wide = rows == 32 ? 1 : 0;
   const int groups = (p.R + rows - 1) / rows;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = p.split_major ? dim3(groups, p.B, p.max_splits) : dim3(groups, p.max_splits, p.B);
+  cfg.gridDim = p.split_major == 2   ? dim3(static_cast<unsigned>(groups) * p.B * p.max_splits)
+                : p.split_major == 1 ? dim3(groups, p.B, p.max_splits)
+                                     : dim3(groups, p.max_splits, p.B);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem[wide];
   cfg.stream = stream;

@@ -46,6 +46,7 @@ constexpr int kWorkers = kSoftmaxThreads + kDecodeThreads;
 constexpr int kProducerWarp = 16, kMmaWarp = 17;
 constexpr int kThreads = 576;
 constexpr int kMaxRaw = 3;
+constexpr int kMaxFull = 6;
 constexpr int kMaxRows = 32;
 constexpr int kCtrlBytes = 3072;
 constexpr int kAbortTimeout = 1;
@@ -57,6 +58,7 @@ constexpr float kLoScale = 32.0f;  // p_lo carries 32 times the residual (at mos
 template <int NR>
 struct Map {
   static constexpr int kRaw = NR == 16 ? 3 : 2;        // raw stages
+  static constexpr int kFull = NR == 16 ? 6 : 2;       // least common multiple of the stages and a tile's two
   static constexpr int kKBufs = NR == 16 ? 2 : 1;      // decoded K tiles in tensor memory
   static constexpr int kQBlock = NR * 64;
   static constexpr int kQPart = 9 * kQBlock;           // q_hi or q_lo
@@ -77,7 +79,9 @@ struct Map {
 };
 
 struct Ctrl {
-  uint64_t raw_full[kMaxRaw];   // copies landed
+  // Copies landed.  A wait by parity has to see every phase of its barrier, and a decoding warp reads every other
+  // stage only: so a barrier of its own for each stage and half of a tile.
+  uint64_t raw_full[kMaxFull];
   uint64_t raw_empty[kMaxRaw];  // the four warps of the stage's keys have it in registers
   uint64_t q_ready;             // split queries written
   uint64_t k_full[2];           // tile decoded into tensor memory (tile parity)
@@ -123,8 +127,8 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 
 __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
 
-__device__ __forceinline__ void st_shared_u8(uint32_t saddr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+__device__ __forceinline__ void st_shared_v2(uint32_t saddr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(saddr), "r"(a), "r"(b) : "memory");
 }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -146,6 +150,16 @@ __device__ __forceinline__ void fp4_to_e4m3(uint32_t w, uint32_t lo, uint32_t hi
   const uint32_t m = w & 0x77777777u;
   a = __byte_perm(lo, hi, m) | (w & 0x80808080u);
   b = __byte_perm(lo, hi, m >> 16) | ((w << 4) & 0x80808080u);
+}
+
+// P as BMM2's B operand, MN-major: 2 NR bytes a key (hi of the NR rows, then lo), so that a thread stores its
+// key's rows whole.  32-byte rows are swizzled by 32 bytes (code 6: the 16-byte chunk's bit XORed with bit 2 of
+// the key), 64-byte rows by 64 (code 4: two bits with bits 1-2); groups of eight keys follow one another.
+template <int NR>
+__device__ __forceinline__ uint64_t p_smem_desc(uint32_t saddr) {
+  constexpr uint64_t kSwizzle = NR == 16 ? 6 : kSwizzle64B;
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16 * NR >> 4) << 16) |
+         (static_cast<uint64_t>(16 * NR >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (kSwizzle << 61);
 }
 
 // Sum of v[r] over the warp's lanes, value r left in the lanes with lane / (32 / NR) == r.
@@ -218,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    for (int s = 0; s < M::kFull; ++s) mbar_init(&ctrl->raw_full[s], 1);
     for (int s = 0; s < M::kRaw; ++s) {
-      mbar_init(&ctrl->raw_full[s], 1);
       mbar_init(&ctrl->raw_empty[s], 4);
     }
     mbar_init(&ctrl->q_ready, kDecodeWarps);
@@ -315,9 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
       uint8_t* dst = smem + M::kOffRaw + s * kRawStage;
       ok = mbar_wait(&ctrl->raw_empty[s], parity, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;
-      if (lane == 0) mbar_arrive_expect_tx(&ctrl->raw_full[s], static_cast<uint32_t>(npg * box_bytes));
+      uint64_t* full = &ctrl->raw_full[i % M::kFull];
+      if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(npg * box_bytes));
       __syncwarp();
-      if (lane < npg) tma_load_2d(dst + lane * box_bytes, &tm_kv, &ctrl->raw_full[s], 0, y, policy);
+      if (lane < npg) tma_load_2d(dst + lane * box_bytes, &tm_kv, full, 0, y, policy);
       issued = i + 1;
       if (++s == M::kRaw) {
         s = 0;
@@ -326,12 +341,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
     }
     if (bad_pid) atomicOr(p.status, kStatusDeviceArg);
     // copies still in flight (their readers may have given up) land before the CTA exits
-    for (int k = max(0, issued - M::kRaw); k < issued; ++k) drain_wait(&ctrl->raw_full[k % M::kRaw], (k / M::kRaw) & 1);
+    for (int k = max(0, issued - M::kRaw); k < issued; ++k) drain_wait(&ctrl->raw_full[k % M::kFull], (k / M::kFull) & 1);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issuer: BMM1 of a tile goes before BMM2 of
     // the last one, so that its K columns and the next softmax wait for one product, not two
     const uint32_t idesc1 = make_idesc_e4m3(128, NR);
-    const uint32_t idesc2 = make_idesc_e4m3(128, 2 * NR, true, false);
+    const uint32_t idesc2 = make_idesc_e4m3(128, 2 * NR, true, true);
     const uint64_t hi_desc = make_smem_desc_sw64(smem_u32(smem + M::kOffQ));
     const uint64_t lo_desc = make_smem_desc_sw64(smem_u32(smem + M::kOffQ + M::kQPart));
     bool ok = mbar_wait(&ctrl->q_ready, 0, abort_flag);
@@ -345,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
         const uint32_t d = tmem + M::kS + sb * NR;
         const uint32_t a = tmem + M::kK + kb * kKCols;
         if (elect_one()) {
-#pragma unroll
+#pragma unroll 1  // (unrolled, the descriptors of all 36 products would be kept in registers, or spilled)
           for (int c = 0; c < 9; ++c) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -366,14 +381,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const uint64_t v_desc = make_smem_desc_sw64(smem_u32(smem + M::kOffV + pb * kVTile), kVBlock, 512);
-        const uint64_t p_desc = make_smem_desc(smem_u32(smem + M::kOffP + pb * M::kPBuf), 16, 1024);
+        const uint64_t p_desc = p_smem_desc<NR>(smem_u32(smem + M::kOffP + pb * M::kPBuf));
         if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
           for (int qc = 0; qc < 4; ++qc) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               umma_f8(tmem + M::kO + qc * 2 * NR, v_desc + static_cast<uint64_t>((2 * qc * kVBlock + kk * 2048) >> 4),
-                      p_desc + static_cast<uint64_t>((kk * 32) >> 4), idesc2, (jv > 0 || kk > 0) ? 1u : 0u);
+                      p_desc + static_cast<uint64_t>((kk * 32 * 2 * NR) >> 4), idesc2, (jv > 0 || kk > 0) ? 1u : 0u);
           }
           umma_commit(&ctrl->o_done[pb]);
         }
@@ -430,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
           lo[k] = l[0] | (l[1] << 16);
         }
         const uint32_t at = smem_u32(smem + M::kOffQ) + (c >> 3) * M::kQBlock + r * 64 + ((((c >> 1) & 3) ^ ((r >> 1) & 3)) << 4) + (c & 1) * 8;
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + M::kQPart), "r"(lo[0]), "r"(lo[1]) : "memory");
+        st_shared_v2(at, hi[0], hi[1]);
+        st_shared_v2(at + M::kQPart, lo[0], lo[1]);
       }
       if (t == 0) {
         const bool real = r < nrows;
@@ -454,15 +469,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
     const uint32_t sw = ((row >> 1) & 3) << 4;
     const uint32_t k_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + M::kK + half * 64;
     const uint32_t raw_at = ((quad & 1) * 32 + lane) * kFp4RowBytes;
-    int s = (quad >> 1) % M::kRaw;
-    uint32_t raw_parity = 0;
     constexpr int kLag = M::kKBufs - 1;  // with two K tiles, the V copy runs a tile behind
     for (int j = 0; j < ntiles + kLag; ++j) {
       bool ok = true;
       if (j < ntiles) {
         uint4 w[8], rope[2];
         uint32_t ex[2];
-        ok = mbar_wait(&ctrl->raw_full[s], raw_parity, abort_flag);
+        const int i = 2 * j + (quad >> 1), s = i % M::kRaw;
+        ok = mbar_wait(&ctrl->raw_full[i % M::kFull], (i / M::kFull) & 1, abort_flag);
         const uint32_t raw = smem_u32(smem + M::kOffRaw + s * kRawStage) + raw_at;
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k] = ld_shared_v4(raw + half * 128 + k * 16);
@@ -472,11 +486,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
         const int kb = j % M::kKBufs;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctrl->raw_empty[s]);
-        s += 2;
-        if (s >= M::kRaw) {
-          s -= M::kRaw;
-          raw_parity ^= 1u;
-        }
         // the K columns are free once BMM1 of their last tile has completed (this warp's own reads have)
         if (ok && j >= M::kKBufs) ok = mbar_wait(&ctrl->k_free[kb], ((j / M::kKBufs) - 1) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -543,9 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
     float l_sum[RW], l_use[RW];
 #pragma unroll
     for (int r = 0; r < RW; ++r) l_sum[r] = l_use[r] = 0.f;
-    // byte key_in of P row r: 128-byte rows, 16-byte chunks under the row's swizzle (r0 is a multiple of 8)
-    const uint32_t p_key = smem_u32(smem + M::kOffP) + r0 * kTile + (key_in & 15);
-    const uint32_t p_chunk = (key_in >> 4) << 4;
+    // this thread's bytes of P: hi of its RW rows, lo of them NR bytes further (under the key's swizzle)
+    const uint32_t p_sw = NR == 16 ? ((key_in >> 2) & 1) << 4 : ((key_in >> 1) & 3) << 4;
+    const uint32_t p_hi = smem_u32(smem + M::kOffP) + key_in * 2 * NR + (static_cast<uint32_t>(r0) ^ p_sw);
+    const uint32_t p_lo = smem_u32(smem + M::kOffP) + key_in * 2 * NR + (static_cast<uint32_t>(NR + r0) ^ p_sw);
     bool failed = !mbar_wait(&ctrl->q_ready, 0, abort_flag);  // (the rows' factors and limits)
     for (int j = 0; j < ntiles; ++j) {
       const int sb = j & 1;
@@ -657,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
         const bool ok = mbar_wait(&ctrl->o_done[sb], ((j >> 1) - 1) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) failed = true;  // (the others learn of it at the next barrier)
       }
-      const uint32_t pb = p_key + sb * M::kPBuf;
+      uint32_t hi4[RW / 4], lo4[RW / 4];
 #pragma unroll
       for (int r = 0; r < RW; r += 2) {
         const float a = ex2_approx(x[r]), c = ex2_approx(x[r + 1]);
@@ -674,11 +684,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
         const float2 uf = f16x2_to_f32x2(u);
         l_use[r] += uf.x;
         l_use[r + 1] += uf.y;
-        const uint32_t a0 = pb + r * kTile + (p_chunk ^ ((r & 7) << 4)), a1 = pb + (r + 1) * kTile + (p_chunk ^ (((r + 1) & 7) << 4));
-        st_shared_u8(a0, hi);
-        st_shared_u8(a1, hi >> 8);
-        st_shared_u8(a0 + NR * kTile, lo);
-        st_shared_u8(a1 + NR * kTile, lo >> 8);
+        hi4[r >> 2] = (r & 2) ? __byte_perm(hi4[r >> 2], hi, 0x5410) : hi;
+        lo4[r >> 2] = (r & 2) ? __byte_perm(lo4[r >> 2], lo, 0x5410) : lo;
+      }
+      const uint32_t pb = sb * M::kPBuf;
+      if constexpr (RW == 8) {
+        st_shared_v2(p_hi + pb, hi4[0], hi4[1]);
+        st_shared_v2(p_lo + pb, lo4[0], lo4[1]);
+      } else {
+        st_shared_v4(p_hi + pb, hi4[0], hi4[1], hi4[2], hi4[3]);
+        st_shared_v4(p_lo + pb, lo4[0], lo4[1], lo4[2], lo4[3]);
       }
       fence_proxy_async_smem();
       tc_fence_before();

@@ -277,6 +277,25 @@ def test_rising_scores(mla):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H,page", [(1, 16, 64), (2, 16, 8), (6, 40, 32)])
+def test_repeated_calls_agree_to_the_bit(mla, T, H, page):
+    """Many row groups over the same pages (whose copies come back early from L2), 300 times."""
+    lens = [128 * 9 + T - 1, 2049, 640]
+    q, pool, table = make(lens, T, H, page, 3, True)
+    d = "cuda"
+    a = (q.to(d), pool.to(d), table.to(d), torch.tensor(lens, dtype=torch.int32, device=d))
+    for sms in (1, 20, 152):
+        plan = mla.decode_plan(lens, T, H, page, table.shape[1], pool.shape[0], mla.MLA_KV_FP4, sms)
+        first = mla.decode(plan, *a, SCALE, KV_SCALE)
+        differ = torch.zeros((), dtype=torch.int64, device=d)
+        for _ in range(100):
+            out, lse = mla.decode(plan, *a, SCALE, KV_SCALE)
+            differ += (out != first[0]).sum() + (lse != first[1]).sum()
+        assert int(differ) == 0
+        check(*first, reference(q, pool, table, lens, chain(3, T)))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,H", [(3, 4), (3, 16), (6, 16)])
 def test_not_finite_keys_reach_only_those_that_see_them(mla, T, H):
     """A draft whose rotated columns are NaN codes: NaN for the rows that see it, nothing for the others."""

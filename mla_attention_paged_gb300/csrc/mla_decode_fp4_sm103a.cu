@@ -48,11 +48,12 @@ constexpr int kThreads = 576;
 constexpr int kMaxRaw = 3;
 constexpr int kMaxFull = 6;
 constexpr int kMaxRows = 32;
-constexpr int kCtrlBytes = 3072;
+constexpr int kCtrlBytes = 4096;
 constexpr int kAbortTimeout = 1;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kPShift = 6.0f;    // P is formed times 2^6 ...
 constexpr float kThreshold = 2.0f; // ... and at most 2^8: the reference moves by more than this
+constexpr int kNoScore = static_cast<int>(0x807fffffu);  // -infinity as an ordered integer
 constexpr float kLoScale = 32.0f;  // p_lo carries 32 times the residual (at most 2^3)
 
 template <int NR>
@@ -95,14 +96,13 @@ struct Ctrl {
   int abort_flag;
   int item[2];                  // request and split (request -1: none)
   alignas(16) float mult[kMaxRows];   // scale_log2 2^-s of the row's split; 0: no such row
-  alignas(16) float m[kMaxRows];      // reference maximum (log2 of the scaled score)
-  alignas(16) float off[kMaxRows];    // kPShift - m; -infinity: no such row
-  alignas(16) float alpha[kMaxRows];
+  alignas(16) float off[kSoftmaxWarps][kMaxRows];  // kPShift - reference maximum, a copy for each warp
+  alignas(16) int top[3][kMaxRows];   // largest score (ordered as an integer) of the rows that outgrew their reference, by
+                                      // tile: written before a tile's vote, read after it, cleared after the next one
   alignas(16) float row_scale[kMaxRows];
   alignas(16) float lse[kMaxRows];
   alignas(16) int lim[kMaxRows];      // last key that the row sees; -1: none
   alignas(16) uint64_t drafts[kMaxRows];
-  alignas(16) int wmax[4][kMaxRows];
   alignas(16) float sums[2][4][kMaxRows];
 };
 static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
@@ -135,6 +135,14 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -459,8 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
         const bool real = r < nrows;
         // (an infinite query has no finite score: its row becomes NaN)
         ctrl->mult[r] = !real ? 0.f : mx == INFINITY ? NAN : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-        ctrl->m[r] = -INFINITY;
-        ctrl->off[r] = real ? INFINITY : -INFINITY;
+        // (no such row: -infinity; a row that has seen nothing: +infinity, so that its first key shows)
+        for (int w = 0; w < kSoftmaxWarps; ++w) ctrl->off[w][r] = real ? INFINITY : -INFINITY;
+        for (int k = 0; k < 3; ++k) ctrl->top[k][r] = kNoScore;
         const int draft = (row0 + r) / p.H;
         ctrl->lim[r] = real ? L - p.T + draft : -1;
         if (kTree) ctrl->drafts[r] = real ? p.tree_mask[static_cast<int64_t>(b) * p.T + draft] & draft_bits(p.T) : 0ull;
@@ -569,6 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
     const uint32_t p_hi = smem_u32(smem + M::kOffP) + key_in * 2 * NR + (static_cast<uint32_t>(r0) ^ p_sw);
     const uint32_t p_lo = smem_u32(smem + M::kOffP) + key_in * 2 * NR + (static_cast<uint32_t>(NR + r0) ^ p_sw);
     bool failed = !mbar_wait(&ctrl->q_ready, 0, abort_flag);  // (the rows' factors and limits)
+    float m = -INFINITY;  // reference maximum (log2 of the scaled score) of row `lane`, the same in every warp
+    int third = 0;        // j % 3
     for (int j = 0; j < ntiles; ++j) {
       const int sb = j & 1;
       const int k0 = kv_start + j * kTile, key = k0 + key_in;
@@ -577,20 +588,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
       bool fail = failed || !mbar_wait(&ctrl->s_full[sb], (j >> 1) & 1, abort_flag);
       fail = __any_sync(0xffffffffu, fail);
       float x[RW];
-      bool over = false;
       auto sees = [&](int r) -> bool {  // (r within the group)
         if (key >= kv_end) return false;
         if (!kTree) return key <= ctrl->lim[r];
         const int u = key - p0;
         return ctrl->lim[r] >= 0 && (u < 0 || ((ctrl->drafts[r] >> u) & 1));
       };
+      // x = score - reference + kPShift (log2); -infinity where a row does not see the key
       auto scores = [&]() {
         uint32_t s[RW];
         load_s<RW>(s_addr, s);
-        float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < RW; r += 4) {
-          const float4 mu = *reinterpret_cast<const float4*>(&ctrl->mult[r0 + r]), of = *reinterpret_cast<const float4*>(&ctrl->off[r0 + r]);
+          const float4 mu = *reinterpret_cast<const float4*>(&ctrl->mult[r0 + r]), of = *reinterpret_cast<const float4*>(&ctrl->off[warp][r0 + r]);
           x[r] = fmaf(__uint_as_float(s[r]), mu.x, of.x);
           x[r + 1] = fmaf(__uint_as_float(s[r + 1]), mu.y, of.y);
           x[r + 2] = fmaf(__uint_as_float(s[r + 2]), mu.z, of.z);
@@ -601,83 +611,88 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
           for (int r = 0; r < RW; ++r)
             if (!sees(r0 + r)) x[r] = -INFINITY;
         }
-#pragma unroll
-        for (int r = 0; r < RW; ++r) top = fmaxf(top, x[r]);
-        over = top > kPShift + kThreshold;
       };
+      bool over = false;  // (warp-uniform) some row outgrew its reference here
       if (!fail) {
         tc_fence_after();
         scores();
+        float top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < RW; ++r) top = fmaxf(top, x[r]);
+        over = __any_sync(0xffffffffu, top > kPShift + kThreshold);
+        if (over) {
+          uint32_t s[RW];
+          load_s<RW>(s_addr, s);
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            const bool here = x[r] > kPShift + kThreshold;
+            if (__any_sync(0xffffffffu, here)) {
+              const int i = __float_as_int(here ? __uint_as_float(s[r]) * ctrl->mult[r0 + r] : -INFINITY);
+              const int best = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
+              if (lane == 0) atomicMax(&ctrl->top[third][r0 + r], best);
+            }
+          }
+        }
       }
+      // one vote a tile; ordinary tiles reduce nothing else across threads
       if (bar_or(1, kSoftmaxThreads, fail || over || *abort_flag != 0)) {
         if (bar_or(1, kSoftmaxThreads, fail || *abort_flag != 0)) {
           failed = true;
           break;
         }
-        // ---------------------------------------------------------------- some row's reference moves
-        {
-          uint32_t s[RW];
-          load_s<RW>(s_addr, s);
-#pragma unroll
-          for (int r = 0; r < RW; ++r) {
-            float v = __uint_as_float(s[r]) * ctrl->mult[r0 + r];
-            if (edge ? !sees(r0 + r) : ctrl->lim[r0 + r] < 0) v = -INFINITY;
-            const int i = __float_as_int(v);
-            const int top = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
-            if (lane == r) ctrl->wmax[quad][r0 + r] = top;
-          }
-        }
-        named_bar_sync(1, kSoftmaxThreads);
-        float m_new = -INFINITY, alpha = 1.f;  // of row `lane`, the same in every warp
+        // ---------------------------------------------------------------- some rows' references move
+        float alpha = 1.f;
         if (lane < NR) {
-          int i = max(max(ctrl->wmax[0][lane], ctrl->wmax[1][lane]), max(ctrl->wmax[2][lane], ctrl->wmax[3][lane]));
+          int i = ctrl->top[third][lane];
           i ^= (i >> 31) & 0x7fffffff;
-          const float top = __int_as_float(i), old = ctrl->m[lane];
-          m_new = old;
-          if (old == -INFINITY || top > old + kThreshold) {
-            alpha = old == -INFINITY ? 0.f : ex2_approx(old - top);
-            m_new = top;
+          const float best = __int_as_float(i);
+          if (m == -INFINITY) {
+            m = best;
+          } else if (best > m + kThreshold) {
+            alpha = ex2_approx(m - best);
+            m = best;
           }
+          if (i != __float_as_int(-INFINITY)) ctrl->off[warp][lane] = kPShift - m;
         }
-        const bool any = __any_sync(0xffffffffu, alpha != 1.f);
-        named_bar_sync(1, kSoftmaxThreads);
-        if (warp == 0 && lane < NR) {
-          ctrl->m[lane] = m_new;
-          // (no such row: -infinity; a row that has seen nothing: +infinity, so that its first key shows)
-          ctrl->off[lane] = ctrl->lim[lane] < 0 ? -INFINITY : m_new == -INFINITY ? INFINITY : kPShift - m_new;
-          ctrl->alpha[lane] = alpha;
-        }
-        named_bar_sync(1, kSoftmaxThreads);
+        const uint32_t moved = __ballot_sync(0xffffffffu, alpha != 1.f);
+        __syncwarp();
         scores();
-        if (any && j > 0) {
-          bool ok = mbar_wait(&ctrl->o_done[sb ^ 1], ((j - 1) >> 1) & 1, abort_flag);  // (a failure shows at the next barrier)
-          ok = __all_sync(0xffffffffu, ok);
-          tc_fence_after();
+        if (moved != 0) {
+          // what the moved rows have accumulated, once BMM2 of the last tile has completed: their sums, and their columns
+          // of O, hi and lo of two chunks a warp
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
-            const float f = ctrl->alpha[r0 + r];
-            l_sum[r] *= f;
-            l_use[r] *= f;
+            if ((moved >> (r0 + r)) & 1) {
+              const float f = __shfl_sync(0xffffffffu, alpha, r0 + r);
+              l_sum[r] *= f;
+              l_use[r] *= f;
+            }
           }
-#pragma unroll 1
-          for (int c = warp >> 2; ok && c < 8 * NR / 16; c += 2) {  // 16 columns of this quadrant's lanes
-            uint32_t v[16];
-            const uint32_t at = tmem + lane_base + M::kO + c * 16;
-            const float* al = ctrl->alpha + (c * 16) % NR;
-            load_s<16>(at, v);
+          const bool ok = mbar_wait(&ctrl->o_done[sb ^ 1], ((j - 1) >> 1) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) failed = true;  // (the others learn of it at the next vote)
+          tc_fence_after();
+          for (uint32_t left = failed ? 0u : moved; left != 0; left &= left - 1) {
+            const int r = __ffs(left) - 1;
+            const float f = __shfl_sync(0xffffffffu, alpha, r);
+            const uint32_t at = tmem + lane_base + M::kO + (warp >> 2) * 4 * NR + r;
+            uint32_t v[4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * al[i]);
-            tmem_st16(at, v);
+            for (int k = 0; k < 4; ++k) tmem_ld1(at + k * NR, v[k]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_st1(at + k * NR, __float_as_uint(__uint_as_float(v[k]) * f));
           }
           tmem_st_wait();
         }
       }
+      if (warp == 0 && lane < NR) ctrl->top[third == 0 ? 2 : third - 1][lane] = kNoScore;  // (the last tile's: all have read it)
+      third = third == 2 ? 0 : third + 1;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->s_free[sb]);
       if (j >= 2) {  // this P buffer's last reader
         const bool ok = mbar_wait(&ctrl->o_done[sb], ((j >> 1) - 1) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) failed = true;  // (the others learn of it at the next barrier)
+        if (!__all_sync(0xffffffffu, ok)) failed = true;  // (the others learn of it at the next vote)
       }
       uint32_t hi4[RW / 4], lo4[RW / 4];
 #pragma unroll
@@ -724,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
       const float u = (ctrl->sums[1][0][lane] + ctrl->sums[1][1][lane]) + (ctrl->sums[1][2][lane] + ctrl->sums[1][3][lane]);
       // (a row that sees nothing has sums of 0; a NaN goes on)
       ctrl->row_scale[lane] = u != 0.f ? (final_out ? p.v_scale : 1.f) / u : 0.f;
-      ctrl->lse[lane] = s != 0.f ? (ctrl->m[lane] + __log2f(s) - kPShift) * 0.69314718055994530942f : -INFINITY;
+      ctrl->lse[lane] = s != 0.f ? (m + __log2f(s) - kPShift) * 0.69314718055994530942f : -INFINITY;
     }
     worker_failed = failed;
   }

@@ -52,7 +52,8 @@ constexpr int kCtrlBytes = 4096;
 constexpr int kAbortTimeout = 1;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kPShift = 6.0f;    // P is formed times 2^6 ...
-constexpr float kThreshold = 2.0f; // ... and at most 2^8: the reference moves by more than this
+constexpr float kThreshold = 2.0f; // ... and at most 2^8: the reference moves when a score exceeds it by more than this,
+constexpr float kMargin = 1.0f;    // to so much above the score (a step of p_lo is then 2^-19 of the largest weight)
 constexpr int kNoScore = static_cast<int>(0x807fffffu);  // -infinity as an ordered integer
 constexpr float kLoScale = 32.0f;  // p_lo carries 32 times the residual (at most 2^3)
 
@@ -359,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
     for (int k = max(0, issued - M::kRaw); k < issued; ++k) drain_wait(&ctrl->raw_full[k % M::kFull], (k / M::kFull) & 1);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issuer: BMM1 of a tile goes before BMM2 of
-    // the last one, so that its K columns and the next softmax wait for one product, not two
+    // the last one, so that its K columns and the next softmax wait for one product, not two.  (Issuing whichever was
+    // ready first, by polling: 135 us where this takes 107.)
     const uint32_t idesc1 = make_idesc_e4m3(128, NR);
     const uint32_t idesc2 = make_idesc_e4m3(128, 2 * NR, true, true);
     const uint64_t hi_desc = make_smem_desc_sw64(smem_u32(smem + M::kOffQ));
@@ -621,13 +623,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
         for (int r = 0; r < RW; ++r) top = fmaxf(top, x[r]);
         over = __any_sync(0xffffffffu, top > kPShift + kThreshold);
         if (over) {
-          uint32_t s[RW];
+          uint32_t s[RW], rows = 0;
           load_s<RW>(s_addr, s);
 #pragma unroll
+          for (int r = 0; r < RW; ++r) rows |= x[r] > kPShift + kThreshold ? 1u << r : 0u;
+          const uint32_t any = __reduce_or_sync(0xffffffffu, rows);
+#pragma unroll
           for (int r = 0; r < RW; ++r) {
-            const bool here = x[r] > kPShift + kThreshold;
-            if (__any_sync(0xffffffffu, here)) {
-              const int i = __float_as_int(here ? __uint_as_float(s[r]) * ctrl->mult[r0 + r] : -INFINITY);
+            if ((any >> r) & 1) {
+              const int i = __float_as_int((rows >> r) & 1 ? __uint_as_float(s[r]) * ctrl->mult[r0 + r] : -INFINITY);
               const int best = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
               if (lane == 0) atomicMax(&ctrl->top[third][r0 + r], best);
             }
@@ -647,10 +651,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
           i ^= (i >> 31) & 0x7fffffff;
           const float best = __int_as_float(i);
           if (m == -INFINITY) {
-            m = best;
+            m = best + kMargin;
           } else if (best > m + kThreshold) {
-            alpha = ex2_approx(m - best);
-            m = best;
+            alpha = ex2_approx(m - best - kMargin);
+            m = best + kMargin;
           }
           if (i != __float_as_int(-INFINITY)) ctrl->off[warp][lane] = kPShift - m;
         }

@@ -69,8 +69,8 @@ typedef enum mla_kv_dtype_t {
                     * per-tensor scale is the plainest form it leaves open.)               */
   MLA_KV_INT8_PAGE = 3 /* int8 codes, each page with its own scale: a latent element is its
                         * code times the scale of the page that holds its row (the other
-                        * INT8 form the talk leaves open); decoded by mla_decode_int8_paged  */
-  , MLA_KV_FP4 = 4 /* 336 bytes a latent row, all values in units of one kv_scale:
+                        * INT8 form the talk leaves open); decoded by mla_decode_int8_paged  */,
+  MLA_KV_FP4 = 4 /* 336 bytes a latent row, all values in units of one kv_scale:
                     *   0..255   columns 0..511, eight to a 32-bit little-endian word: column 8w + i has its
                     *            e2m1 magnitude code (0, 1/2, 1, 3/2, 2, 3, 4, 6) in bits 4i..4i+2 and its
                     *            sign in bit 8i + 7 (i < 4) or 8 (i - 4) + 3; the value is the magnitude times
@@ -92,7 +92,8 @@ typedef struct mla_decode_plan_t {
   int64_t num_pages;         /* pages in the pool (first dimension of kv_pages)          */
   int32_t num_sms;           /* SMs the split count was sized for                        */
   int32_t rows;              /* T*H folded query rows per request                        */
-  int32_t head_groups;       /* CTAs along the folded row axis (64 rows each)            */
+  int32_t head_groups;       /* CTAs along the folded row axis (64 rows each; over a 4-bit
+                                pool 32, or 16 for at most 16 rows)                      */
   int32_t chunk_tokens;      /* keys per split (multiple of 64)                          */
   int32_t max_splits;        /* splits of the longest request                            */
   int32_t max_seq_len;       /* longest planned request; device seq_lens must not exceed */
@@ -133,14 +134,14 @@ int mla_decode_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_
 
 /* Absorbed MLA decode with speculative draft tokens over the paged latent cache.
  *   q          : [B, T, H, 576] bf16.  Folded row m = t*H + h of request b.
- *   kv_pages   : [num_pages, page_size, 576] bf16, e4m3 or int8 bytes (plan->kv_dtype);
- *                the allocation must hold all num_pages pages in the plan's format (the
+ *   kv_pages   : [num_pages, page_size, 576] bf16, e4m3 or int8 bytes, or [.., 336] bytes of
+ *                MLA_KV_FP4 (plan->kv_dtype); the allocation must hold all num_pages pages in the plan's format (the
  *                library cannot check it: a pool of another format is read out of bounds).
  *   page_table : [B, max_pages_per_seq] int32; latent row j of request b is
  *                kv_pages[page_table[b, j / page_size], j % page_size, :].
  *   seq_lens   : [B] int32 device copy of the planned lengths (each <= max_seq_len).
  *   scale      : softmax scale applied to q . k.
- *   kv_scale   : per-tensor dequantisation scale of an 8-bit pool (ignored for bf16).
+ *   kv_scale   : per-tensor dequantisation scale of an 8-bit or 4-bit pool (ignored for bf16).
  *   out        : [B, T, H, 512] bf16, out[b,t,h] = sum_j softmax_j(scale q.k_j) v_j with
  *                draft t seeing keys 0 .. L_b - T + t and v_j = k_j[:512].
  *   lse        : [B, T, H] fp32, natural-log log-sum-exp of the scaled scores.
@@ -322,7 +323,11 @@ int mla_prefill_paged(const void* q, const void* k_pages, const void* v_pages, c
  *   key  : c = kv_in[n, :512]; c' = c / sqrt(mean(c^2) + eps) * kv_weight (kv_weight NULL: c' = c);
  *          the latent row [c', rot(kv_in[n, 512:576], x)] goes to pool row slots[n], as bf16, or as
  *          the codes of the values over kv_scale (nearest, ties to even; saturated to +-448 or
- *          +-127; a NaN encodes as the e4m3 NaN, as int8 0).
+ *          +-127; a NaN encodes as the e4m3 NaN, as int8 0).  A 4-bit row: y = value times 1/kv_scale (rounded
+ *          to fp32); 16 columns whose largest |y| is t take the smallest exponent e of 0..11 with t <= 7 2^(e-5), and
+ *          the nearest code of y 2^(5-e) (ties to the even code; saturated to +-6; a NaN encodes as 0); the rotated columns
+ *          are e4m3 codes.  Here the mean is that of the exact squares, rounded once to fp32, and no product is fused
+ *          with a sum, so that the codes are those of the formula to the bit.
  *   query: v = q_in[n, h, :q_dim]; v' = v / sqrt(mean(v^2) + eps) * q_weight over the whole width
  *          (q_weight NULL: v' = v); q_out[n, h] = [v'[:q_dim-64], rot(v'[q_dim-64:], x)].
  *   rot  : pair i of 32 is columns (2i, 2i+1) (interleaved != 0) or (i, i+32); (a, b) becomes
@@ -341,8 +346,8 @@ int mla_prefill_paged(const void* q, const void* k_pages, const void* v_pages, c
  *   slots       : [num_tokens] int64: page id * page_size + offset of the key's pool row; negative =
  *                 a padded token whose key is not stored (its queries still are).  Slots that are
  *                 not negative must differ: a row that two tokens name holds bytes of either.
- *   kv_pages    : the pool, num_slots = num_pages * page_size rows of 576 elements of kv_dtype.
- *   kv_scale    : scale of an e4m3 or int8 pool (ignored for bf16).
+ *   kv_pages    : the pool, num_slots = num_pages * page_size rows of kv_dtype.
+ *   kv_scale    : scale of an e4m3, int8 or 4-bit pool (ignored for bf16).
  * Pointers are 16-byte aligned (positions 4, slots 8).  kv_in, q_in and q_out lie outside the pool, and
  * q_out holds no element of kv_in, the weights, cos_sin, positions or slots.
  * Rows that no token names are left as they were.  num_tokens 0 does nothing.  Launched as a programmatic dependent like mla_decode.
@@ -357,6 +362,26 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
                   float eps, const float* cos_sin, int max_positions, const int32_t* positions,
                   const int64_t* slots, int num_tokens, int interleaved, void* kv_pages, int64_t num_slots,
                   int kv_dtype, float kv_scale, void* stream);
+
+/* Latent rows of requests, read out of the pages of any pool format into contiguous bf16 rows (a prefill that
+ * projects a cached prefix up again needs them so): for r = cu_rows[b] .. cu_rows[b+1] - 1,
+ *   out[r, :] = bf16(value of row r - cu_rows[b] of request b),
+ * a value being its code times kv_scale (MLA_KV_INT8_PAGE: its page's scale) in fp32, rounded once; bf16 rows are
+ * copied.
+ *   kv_pages, page_table : as mla_decode, [batch, max_pages_per_seq].
+ *   page_scales : [num_pages] for an MLA_KV_INT8_PAGE pool, else NULL.
+ *   kv_scale    : > 0 (ignored for bf16 and for a scale per page).
+ *   cu_rows     : [batch + 1] int32 prefix sums on the device.
+ *   total_rows  : host bound on cu_rows[batch], the rows of out.  0 does nothing.
+ *   out         : bf16, rows out_row_stride elements apart (at least 576, a multiple of 8), 16-byte aligned; it lies
+ *                 outside the pool, the table, cu_rows and the scales.  Rows of no request are left as they were.
+ * Launched as a programmatic dependent like mla_decode.  Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (page_size),
+ * MLA_ERR_CUDA.  Device-side, recorded as MLA_ERR_DEVICE_ARG: cu_rows below 0 or beyond total_rows (those rows are not
+ * written), a request longer than its page-table row (the rows beyond are not written), a page id outside
+ * [0, num_pages) (its rows are zeros). */
+int mla_kv_gather(const void* kv_pages, int64_t num_pages, int page_size, int kv_dtype, float kv_scale, const float* page_scales,
+                  const int32_t* page_table, int max_pages_per_seq, const int32_t* cu_rows, int batch, int total_rows,
+                  void* out, int64_t out_row_stride, void* stream);
 
 /* The attention weight that each cached key received in a decode step, accumulated over steps:
  *   mass[b, j] = decay * mass[b, j] + sum over rows (t, h) that see key j of
@@ -375,7 +400,7 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
  *                 aligned (NULL when that is 0, as it is for at most 128 rows q_len * num_heads);
  *                 overwritten; calls that share one are stream-ordered.
  * Launched as a programmatic dependent like mla_decode.  Errors: MLA_ERR_INVALID_ARG,
- * MLA_ERR_UNSUPPORTED (tree_mask with more than 64 drafts; batch times the longest request beyond
+ * MLA_ERR_UNSUPPORTED (tree_mask with more than 64 drafts; a 4-bit pool; batch times the longest request beyond
  * 2^38 keys), MLA_ERR_WORKSPACE_TOO_SMALL, MLA_ERR_CUDA.  Device-side, recorded as
  * MLA_ERR_DEVICE_ARG: a length below q_len or beyond the plan (that request's row is left as it
  * was), a page id outside [0, num_pages) (its rows count as zeros) and, on a page that a request
@@ -397,7 +422,7 @@ int mla_key_mass(const mla_decode_plan_t* plan, const void* q, const void* kv_pa
  * Entries of kept and mass_out from K on, and pool rows that are no destination, are left as they
  * were.  Rows are copied because a source page may be a prefix that other requests share; the
  * caller releases the old pages.  Keys keep the rotation of their old positions.
- *   kv_pages       : [num_pages, page_size, 576] of kv_dtype (bf16, e4m3 or int8).
+ *   kv_pages       : [num_pages, page_size] rows of kv_dtype (bf16, e4m3, int8 or 4-bit).
  *   page_table     : [batch, max_pages_per_seq] int32 source pages.
  *   seq_lens, keep_lens : [batch] int32 (device).
  *   mass           : fp32, row b at mass + b * mass_stride (elements; >= max_seq_len).

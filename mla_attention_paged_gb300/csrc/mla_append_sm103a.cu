@@ -21,6 +21,7 @@
 // takes 22.8 for 8191 tokens of 16 normed 192-wide heads and their keys: 5.3 TB/s.)
 #include <cuda_fp8.h>
 
+#include "fp4_rows.cuh"
 #include "mla_internal.h"
 #include "sm103a_ptx.cuh"
 
@@ -95,6 +96,37 @@ __device__ __forceinline__ void rotate(float (&f)[8], const Turn& t, int l, bool
   }
 }
 
+// rotate, each product and sum rounded by itself.
+__device__ __forceinline__ void rotate_exact(float (&f)[8], const Turn& t, int l, bool interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = f[2 * i], b = f[2 * i + 1];
+      f[2 * i] = __fsub_rn(__fmul_rn(a, t.c[i]), __fmul_rn(b, t.s[i]));
+      f[2 * i + 1] = __fadd_rn(__fmul_rn(b, t.c[i]), __fmul_rn(a, t.s[i]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, f[i], 4);
+      const float x = __fmul_rn(f[i], t.c[i]), y = __fmul_rn(other, t.s[i]);
+      f[i] = l < 4 ? __fsub_rn(x, y) : __fadd_rn(x, y);
+    }
+  }
+}
+
+// A sum and the error of its rounding (exact after each addition: the two-sum of Knuth, The Art of Computer
+// Programming, volume 2, 4.2.2; errors themselves are summed plainly).
+struct Sum {
+  float hi, lo;
+};
+
+__device__ __forceinline__ Sum add(const Sum& s, float x) {
+  const float t = __fadd_rn(s.hi, x), u = __fsub_rn(t, s.hi);
+  const float err = __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, u)), __fsub_rn(x, u));
+  return {t, __fadd_rn(s.lo, err)};
+}
+
 __device__ __forceinline__ void scale8(float (&f)[8], float inv, const uint4& w) {
   float g[8];
   unpack8(w, g);
@@ -133,7 +165,9 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale, bool i
 // registers) measured 22.8 us on 8191 tokens of 16 normed 192-wide heads against 25.0 at four and
 // 29 spilling at six; streaming loads and stores (nothing is read again) 24.6 against 26.8.
 // The first k_warps warps of the grid take keys, the others queries.
-template <int kChunks, int kSteps, int kKeyLanes>
+// A 4-bit row (kFp4) is written to the bit of the plain formula, since a code of four bits may hang on the last bit of
+// the norm: the squares (exact) are summed with their rounding errors, and the rotation uses no fused multiply-adds.
+template <int kChunks, int kSteps, int kKeyLanes, bool kFp4>
 __global__ void __launch_bounds__(32 * kWarps, kChunks <= 2 ? 5 : 1) kv_append_kernel(const AppendParams p, int64_t k_warps, int warps_per_token) {
   // programmatic dependent launch: no input is read before the previous kernel has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -225,7 +259,24 @@ __global__ void __launch_bounds__(32 * kWarps, kChunks <= 2 ? 5 : 1) kv_append_k
   Turn turn;
   load_turn(turn, p.cos_sin + (live ? static_cast<int64_t>(pos) * kRope : 0), l, inter);
   float inv = 1.f;
-  if (p.kv_weight) {
+  if (kFp4 && p.kv_weight) {
+    Sum ss = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kLatentChunks; ++i) {
+      float f[8];
+      unpack8(w[i], f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ss = add(ss, f[k] * f[k]);
+    }
+#pragma unroll
+    for (int o = kKeyLanes / 2; o > 0; o >>= 1) {
+      const Sum other = {__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)};
+      ss = add(ss, other.hi);
+      ss.lo += other.lo;
+    }
+    inv = 1.f / sqrtf((ss.hi + ss.lo) / static_cast<float>(kValueDim) + p.eps);
+    inv = __shfl_sync(0xffffffffu, inv, 0, kKeyLanes);  // (one lane's, whatever the order of the errors' sum)
+  } else if (p.kv_weight) {
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < kLatentChunks; ++i) {
@@ -240,10 +291,35 @@ __global__ void __launch_bounds__(32 * kWarps, kChunks <= 2 ? 5 : 1) kv_append_k
     const int c = i < kLatentChunks ? kl + kKeyLanes * i : kValueDim / 8 + kl;
     float f[8];
     unpack8(w[i], f);
-    if (i == kLatentChunks)
-      rotate(f, turn, l, inter);
-    else if (p.kv_weight)
+    if (i == kLatentChunks) {
+      if (kFp4)
+        rotate_exact(f, turn, l, inter);
+      else
+        rotate(f, turn, l, inter);
+    } else if (p.kv_weight) {
       scale8(f, inv, __ldg(reinterpret_cast<const uint4*>(p.kv_weight) + c));
+    }
+    if constexpr (kFp4) {
+      // values over kv_scale; 16 columns, two lanes', share an exponent, and four lanes' two exponents a byte
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        f[k] *= p.kv_scale;  // (1 / kv_scale)
+        if (i < kLatentChunks && f[k] != f[k]) f[k] = 0.f;  // (no code for a NaN)
+        top = fmaxf(top, fabsf(f[k]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      const int e = fp4_exponent(top), next = __shfl_xor_sync(0xffffffffu, e, 2);
+      if (!live) continue;
+      uint8_t* at = p.kv_pages + slot * kFp4RowBytes;
+      if (i < kLatentChunks) {
+        reinterpret_cast<uint32_t*>(at)[c] = fp4_encode8(f, e);
+        if ((c & 3) == 0) at[kFp4ExpAt + c / 4] = static_cast<uint8_t>(e | (next << 4));
+      } else if (kl < 8) {
+        reinterpret_cast<uint2*>(at + kFp4RopeAt)[kl] = codes8(f, 1.f, false);
+      }
+      continue;
+    }
     if (!live || (i == kLatentChunks && kl >= 8)) continue;
     const int64_t at = slot * (kLatentDim / 8) + c;
     if (p.kv_dtype == kKvBf16)
@@ -274,8 +350,14 @@ cudaError_t launch_chunks(const AppendParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, 1, 32>, p, k_warps, per_token)
-             : cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, kManySteps, kManyKeyLanes>, p, k_warps, per_token);
+  if (p.kv_dtype == kKvFp4) {
+    AppendParams q = p;
+    q.kv_scale = 1.f / p.kv_scale;
+    return few ? cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, 1, 32, true>, q, k_warps, per_token)
+               : cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, kManySteps, kManyKeyLanes, true>, q, k_warps, per_token);
+  }
+  return few ? cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, 1, 32, false>, p, k_warps, per_token)
+             : cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, kManySteps, kManyKeyLanes, false>, p, k_warps, per_token);
 }
 
 }  // namespace

@@ -125,6 +125,44 @@ int mla_kv_append(const void* q_in, int64_t q_in_token_stride, int64_t q_in_head
   return launch_kv_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
+int mla_kv_gather(const void* kv_pages, int64_t num_pages, int page_size, int kv_dtype, float kv_scale, const float* page_scales,
+                  const int32_t* page_table, int max_pages_per_seq, const int32_t* cu_rows, int batch, int total_rows,
+                  void* out, int64_t out_row_stride, void* stream) {
+  if (batch < 1 || total_rows < 0 || num_pages < 1 || max_pages_per_seq < 1 || !kv_dtype_ok(kv_dtype)) return MLA_ERR_INVALID_ARG;
+  if ((kv_dtype == MLA_KV_INT8_PAGE) != (page_scales != nullptr)) return MLA_ERR_INVALID_ARG;
+  if (!page_size_ok(page_size)) return MLA_ERR_UNSUPPORTED;
+  if (total_rows == 0) return MLA_OK;
+  if (!kv_pages || !page_table || !cu_rows || !out) return MLA_ERR_INVALID_ARG;
+  if (!aligned(kv_pages, 16) || !aligned(page_scales, 4) || !aligned(page_table, 4) || !aligned(cu_rows, 4) || !aligned(out, 16))
+    return MLA_ERR_INVALID_ARG;
+  if (out_row_stride < kLatentDim || out_row_stride % 8 != 0 || !(kv_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  // rows are written while others of the pool, and lengths, are still to be read
+  const size_t span = (static_cast<size_t>(total_rows - 1) * out_row_stride + kLatentDim) * 2;
+  if (overlap(kv_pages, static_cast<size_t>(num_pages) * page_size * kv_row_bytes(kv_dtype), out, span) ||
+      overlap(page_table, static_cast<size_t>(batch) * max_pages_per_seq * 4, out, span) ||
+      overlap(cu_rows, (static_cast<size_t>(batch) + 1) * 4, out, span) ||
+      (page_scales && overlap(page_scales, static_cast<size_t>(num_pages) * 4, out, span)))
+    return MLA_ERR_INVALID_ARG;
+  GatherParams p;
+  memset(&p, 0, sizeof p);
+  p.status = status_ptr();
+  if (!p.status) return MLA_ERR_CUDA;
+  p.kv_pages = static_cast<const uint8_t*>(kv_pages);
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.kv_dtype = kv_dtype;
+  p.kv_scale = kv_scale;
+  p.page_scales = page_scales;
+  p.page_table = page_table;
+  p.max_pages = max_pages_per_seq;
+  p.B = batch;
+  p.total = total_rows;
+  p.cu_rows = cu_rows;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.out_stride = out_row_stride;
+  return launch_kv_gather(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
 int mla_key_mass_workspace(const mla_decode_plan_t* plan, size_t* bytes_out) {
   if (!plan || !bytes_out) return MLA_ERR_INVALID_ARG;
   *bytes_out = key_mass_part_bytes(plan->batch, plan->rows, plan->max_seq_len);

@@ -25,6 +25,7 @@
 // memory and returns.
 #include <cuda_fp16.h>
 
+#include "fp4_rows.cuh"
 #include "mla_internal.h"
 #include "sm103a_ptx.cuh"
 #include "tree_mask.cuh"
@@ -150,15 +151,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
-}
-
-// Eight 4-bit columns (a word of include/mla.h's row) as e4m3 codes: the magnitude's code is looked up by
-// a byte permute among the eight of its group's power of two (lo: magnitudes 0-3, hi: 4-7); the signs lie
-// where one mask (columns 0-3) or a shift by four (4-7) brings them to each byte's top bit.
-__device__ __forceinline__ void fp4_to_e4m3(uint32_t w, uint32_t lo, uint32_t hi, uint32_t& a, uint32_t& b) {
-  const uint32_t m = w & 0x77777777u;
-  a = __byte_perm(lo, hi, m) | (w & 0x80808080u);
-  b = __byte_perm(lo, hi, m >> 16) | ((w << 4) & 0x80808080u);
 }
 
 // P as BMM2's B operand, MN-major: 2 NR bytes a key (hi of the NR rows, then lo), so that a thread stores its
@@ -526,7 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
 #pragma unroll
             for (int g = 0; g < 2; ++g) {  // 16 columns under one power of two
               const uint32_t e = (ex[k >> 2] >> (8 * (k & 3) + 4 * g)) & 15u;
-              const uint32_t lo = e * 0x08080800u + 0x14100800u, hi = e * 0x08080808u + 0x24201C18u;
+              uint32_t lo, hi;
+              fp4_table(e, lo, hi);
               fp4_to_e4m3(word[2 * g], lo, hi, o[8 * k1 + 4 * g], o[8 * k1 + 4 * g + 1]);
               fp4_to_e4m3(word[2 * g + 1], lo, hi, o[8 * k1 + 4 * g + 2], o[8 * k1 + 4 * g + 3]);
             }

@@ -107,6 +107,21 @@ struct AppendParams {
   unsigned* status;
 };
 
+// Rows of requests out of the pages, as contiguous bf16 rows.
+struct GatherParams {
+  const uint8_t* kv_pages;
+  int64_t num_pages;
+  int page_size, kv_dtype;
+  float kv_scale;
+  const float* page_scales;     // kKvInt8Page: [num_pages]
+  const int32_t* page_table;
+  int max_pages, B, total;
+  const int32_t* cu_rows;       // [B + 1]
+  __nv_bfloat16* out;
+  int64_t out_stride;           // elements
+  unsigned* status;
+};
+
 // Eviction: selection of the kept keys, then the copy of their rows into new pages.
 struct EvictParams {
   uint8_t* kv_pages;
@@ -165,6 +180,7 @@ inline int kv_row_bytes(int t) { return t == kKvBf16 ? 2 * kLatentDim : t == kKv
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool page_size_ok(int P) { return P == 8 || P == 16 || P == 32 || P == 64 || P == 128 || P == 256; }
 
+cudaError_t launch_kv_gather(const GatherParams& p, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 // tm_q: bf16 pools only.
 cudaError_t launch_key_mass(const KeyMassParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_kv, int num_sms,

@@ -33,7 +33,7 @@ EXPORTED = ["mla_decode_plan", "mla_decode", "mla_decode_partial", "mla_decode_c
             "mla_decode_int8_paged",
             "mla_prefill_varlen", "mla_prefill_paged", "mla_get_status", "mla_status_string", "mla_version", "mla_set_profile_events",
             "mla_profile_elapsed_ms", "mla_selftest_wait_timeout", "mla_kv_append", "mla_kv_evict",
-            "mla_decode_tree_plan", "mla_decode_tree", "mla_key_mass_workspace", "mla_key_mass"]
+            "mla_decode_tree_plan", "mla_decode_tree", "mla_key_mass_workspace", "mla_key_mass", "mla_kv_gather"]
 
 
 class MlaError(RuntimeError):
@@ -87,6 +87,8 @@ def _load() -> ctypes.CDLL:
     lib.mla_kv_append.restype = i32
     lib.mla_kv_append.argtypes = [P, i64, i64, P, i64, i64, i32, i32, P, P, i64, P, f32, P, i32, P, P, i32, i32, P, i64,
                                   i32, f32, P]
+    lib.mla_kv_gather.restype = i32
+    lib.mla_kv_gather.argtypes = [P, i64, i32, i32, f32, P, P, i32, P, i32, i32, P, i64, P]
     lib.mla_kv_evict.restype = i32
     lib.mla_kv_evict.argtypes = [P, i64, i32, i32, P, i32, P, P, P, i64, P, i32, i32, i32, i32, i32, i32, P, i64, P, P,
                                  i64, P]
@@ -423,6 +425,23 @@ def kv_append(q: torch.Tensor | None, kv: torch.Tensor | None, positions: torch.
     _call(what, dev, stream, lib.mla_kv_append, *qa, *ka, eps, table, cos_sin.shape[0], pos, slot, n, 1 if interleaved else 0,
           pool, rows, kv_dtype, kv_scale)
     return q_out
+
+
+def kv_gather(kv_pages: torch.Tensor, page_table: torch.Tensor, cu_rows: torch.Tensor, out: torch.Tensor,
+              kv_dtype: int = MLA_KV_BF16, kv_scale: float = 1.0, page_scales=None, *, stream=None) -> torch.Tensor:
+    """mla_kv_gather through the C ABI: the latent rows of each request, out of the pages, into rows
+    cu_rows[b] .. cu_rows[b+1]-1 of out [N,576] bf16 (its rows may be strided).  cu_rows [B+1] int32 on
+    the device.  Returns out."""
+    what = "mla_kv_gather"
+    dev, pool, pages, page_size = _want_pool(what, kv_pages, kv_dtype)
+    B = cu_rows.numel() - 1
+    if out.get_device() != dev or out.dtype is not torch.bfloat16 or out.dim() != 2 or out.shape[1] != 576 or out.stride(1) != 1:
+        _refuse(what, f"out is {out.dtype} {tuple(out.shape)} on {out.device}")
+    _call(what, dev, stream, lib.mla_kv_gather, pool, pages, page_size, kv_dtype, kv_scale,
+          None if page_scales is None else _want(what, dev, "page_scales", page_scales, torch.float32, (pages,)),
+          *_want_rows(what, dev, "page_table", page_table, torch.int32, B), _want(what, dev, "cu_rows", cu_rows, torch.int32, (B + 1,)),
+          B, out.shape[0], out.data_ptr(), out.stride(0) if out.shape[0] > 1 else 576)
+    return out
 
 
 def key_mass_workspace_for(plan: DecodePlan, device) -> torch.Tensor | None:

@@ -444,6 +444,54 @@ int mla_kv_evict(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype,
                  int recent, int max_seq_len, int max_keep, int32_t* kept, int64_t kept_stride,
                  int32_t* new_lens, float* mass_out, int64_t mass_out_stride, void* stream);
 
+/* The pages of a cache, kept on the device.  A cache has num_slots requests, slot s with the pages
+ * page_table[s, 0 .. ceil(seq_lens[s] / page_size) - 1] (entries from there on mean nothing), and a count refs[page]
+ * of the entries that refer to each page; 0 is a free page.  Pages may be shared: full ones only, since appended rows
+ * go into the last.  The caller takes new pages from the free ones (mla_page_free lists them) and sets their counts to 1.
+ *   kv_pages   : the pool, [num_pages, page_size] rows of kv_dtype (any).
+ *   page_scales: [num_pages] for an MLA_KV_INT8_PAGE pool (they go with the pages), else NULL.
+ *   page_table : [num_slots, max_pages_per_seq] int32.    seq_lens : [num_slots] int32.    refs : [num_pages] int32.
+ * All on the device; what a call writes shares no memory with anything else that it takes.  Kernels are programmatic
+ * dependents like mla_decode's.  Errors of all: MLA_ERR_INVALID_ARG (more than 2^30 pages too), MLA_ERR_UNSUPPORTED (page_size not 8..256, more
+ * than 65535 listed slots), MLA_ERR_CUDA.
+ *
+ * mla_page_fork: for each i < count, slot children[i] becomes a copy of slot parents[i]: it shares the full pages
+ * (their counts go up by 1); a partial last page is copied to page new_pages[i], whose count becomes 1 (not looked at
+ * where the parent's last page is full); the length is the parent's.  What the child held before is not given back.
+ * children differ from one another and from every parent of the call, new pages differ and are free.
+ * Device-side, recorded as MLA_ERR_DEVICE_ARG, that child left as it was: a slot outside the table, a child that a
+ * child before it or a parent names, a length below 0 or beyond the row, and, where one is needed, a new page outside the
+ * pool, not free, or named before in new_pages, or a last page outside the pool.  A full page outside the pool is
+ * copied as it is, and recorded.
+ *
+ * mla_page_free: for each i < count, slot slots[i] shrinks to keep_lens[i] <= its length (0: it ends): the counts
+ * of the pages behind go down by 1, and seq_lens[slots[i]] = keep_lens[i].  The pages whose count came to 0 by this call
+ * stand in freed[0 .. *num_freed - 1] in ascending order; entries behind are left as they were.  page_table is
+ * not changed.
+ *   freed : [num_pages] int32.    num_freed : int32.
+ * Device-side, recorded as MLA_ERR_DEVICE_ARG: a slot outside the table or listed before, a length beyond the row or
+ * below keep_lens[i], keep_lens[i] < 0 (that slot is left as it was); an entry outside the pool, or one more for a page
+ * than its count (the entry is passed over).
+ *
+ * mla_page_compact: pages with a count move so that they are 0 .. *num_live - 1: the k-th free page below *num_live
+ * takes the k-th counted page from *num_live on.  Rows, counts, page scales and the tables of all slots follow; free pages
+ * keep their rows.
+ *   num_live  : int32.
+ *   workspace : of the size mla_page_compact_workspace gives, 256-byte aligned; overwritten; calls that share one are
+ *               stream-ordered.  MLA_ERR_WORKSPACE_TOO_SMALL.
+ * Device-side, recorded as MLA_ERR_DEVICE_ARG: a table entry outside the pool, or from *num_live on whose page
+ * has no count (left as it was), a length beyond the row (its whole row is rewritten). */
+int mla_page_fork(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype, float* page_scales, int32_t* page_table,
+                  int max_pages_per_seq, int32_t* seq_lens, int num_slots, int32_t* refs, const int32_t* parents,
+                  const int32_t* children, const int32_t* new_pages, int count, void* stream);
+int mla_page_free(const int32_t* page_table, int max_pages_per_seq, int32_t* seq_lens, int num_slots, int page_size, int32_t* refs,
+                  int64_t num_pages, const int32_t* slots, const int32_t* keep_lens, int count, int32_t* freed, int32_t* num_freed,
+                  void* stream);
+int mla_page_compact_workspace(int64_t num_pages, size_t* bytes_out);
+int mla_page_compact(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype, float* page_scales, int32_t* page_table,
+                     int max_pages_per_seq, const int32_t* seq_lens, int num_slots, int32_t* refs, int32_t* num_live,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
 /* Read and clear the current device's status word after synchronising `stream`.
  * Returns MLA_OK, MLA_ERR_TIMEOUT or MLA_ERR_DEVICE_ARG (first recorded), or
  * MLA_ERR_CUDA if the read itself fails.  This call synchronises: keep it off the hot

@@ -18,7 +18,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmla.so")
 SOURCES = ["mla_api.cu", "mla_decode_sm103a.cu", "mla_decode_e4m3_sm103a.cu", "mla_decode_narrow_sm103a.cu", "mla_decode_tree_sm103a.cu",
            "mla_prefill_sm103a.cu", "mla_noalloc.cu", "mla_cache_api.cu", "mla_append_sm103a.cu", "mla_evict_sm103a.cu",
-           "mla_key_mass_sm103a.cu", "mla_decode_fp4_sm103a.cu", "mla_gather_sm103a.cu"]
+           "mla_key_mass_sm103a.cu", "mla_decode_fp4_sm103a.cu", "mla_gather_sm103a.cu",
+           "mla_pages_api.cu", "mla_pages_sm103a.cu"]
 HEADERS = ["mla_internal.h", "sm103a_ptx.cuh", "kv8_decode.cuh", "tree_mask.cuh", "fp4_rows.cuh", os.path.join("..", "..", "include", "mla.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

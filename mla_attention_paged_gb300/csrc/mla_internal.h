@@ -107,6 +107,58 @@ struct AppendParams {
   unsigned* status;
 };
 
+// Pages of a cache: counts of the table entries that refer to each.
+struct ForkParams {
+  uint8_t* kv_pages;
+  int num_pages, page_size, row_bytes;
+  float* page_scales;           // kKvInt8Page: [num_pages]
+  int32_t* page_table;          // [slots][max_pages]
+  int max_pages;
+  int32_t* seq_lens;            // [slots]
+  int slots;
+  int32_t* refs;                // [num_pages]
+  const int32_t* parents;       // [n] slots
+  const int32_t* children;
+  const int32_t* new_pages;
+  int n;
+  unsigned* status;
+};
+
+struct FreeParams {
+  const int32_t* page_table;
+  int max_pages;
+  int32_t* seq_lens;
+  int slots, page_size;
+  int32_t* refs;
+  int num_pages;
+  const int32_t* list;          // [n] slots
+  const int32_t* keep_lens;
+  int n;
+  int32_t* freed;
+  int32_t* num_freed;
+  unsigned* status;
+};
+
+struct CompactParams {
+  uint8_t* kv_pages;
+  int num_pages, page_size, row_bytes;
+  float* page_scales;
+  int32_t* page_table;
+  int max_pages;
+  const int32_t* seq_lens;
+  int slots;
+  int32_t* refs;
+  int32_t* num_live;
+  // workspace: live pages and moves; where each page from the live ones on goes (-1: nowhere); holes ascending; pages that
+  // move, from the last and from the first
+  int32_t* head;
+  int32_t* remap;
+  int32_t* holes;
+  int32_t* movers;
+  int32_t* movers_up;
+  unsigned* status;
+};
+
 // Rows of requests out of the pages, as contiguous bf16 rows.
 struct GatherParams {
   const uint8_t* kv_pages;
@@ -180,6 +232,9 @@ inline int kv_row_bytes(int t) { return t == kKvBf16 ? 2 * kLatentDim : t == kKv
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool page_size_ok(int P) { return P == 8 || P == 16 || P == 32 || P == 64 || P == 128 || P == 256; }
 
+cudaError_t launch_page_fork(const ForkParams& p, cudaStream_t stream);
+cudaError_t launch_page_free(const FreeParams& p, cudaStream_t stream);
+cudaError_t launch_page_compact(const CompactParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv_gather(const GatherParams& p, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 // tm_q: bf16 pools only.

@@ -33,7 +33,8 @@ EXPORTED = ["mla_decode_plan", "mla_decode", "mla_decode_partial", "mla_decode_c
             "mla_decode_int8_paged",
             "mla_prefill_varlen", "mla_prefill_paged", "mla_get_status", "mla_status_string", "mla_version", "mla_set_profile_events",
             "mla_profile_elapsed_ms", "mla_selftest_wait_timeout", "mla_kv_append", "mla_kv_evict",
-            "mla_decode_tree_plan", "mla_decode_tree", "mla_key_mass_workspace", "mla_key_mass", "mla_kv_gather"]
+            "mla_decode_tree_plan", "mla_decode_tree", "mla_key_mass_workspace", "mla_key_mass", "mla_kv_gather",
+            "mla_page_fork", "mla_page_free", "mla_page_compact_workspace", "mla_page_compact"]
 
 
 class MlaError(RuntimeError):
@@ -87,6 +88,14 @@ def _load() -> ctypes.CDLL:
     lib.mla_kv_append.restype = i32
     lib.mla_kv_append.argtypes = [P, i64, i64, P, i64, i64, i32, i32, P, P, i64, P, f32, P, i32, P, P, i32, i32, P, i64,
                                   i32, f32, P]
+    lib.mla_page_fork.restype = i32
+    lib.mla_page_fork.argtypes = [P, i64, i32, i32, P, P, i32, P, i32, P, P, P, P, i32, P]
+    lib.mla_page_free.restype = i32
+    lib.mla_page_free.argtypes = [P, i32, P, i32, i32, P, i64, P, P, i32, P, P, P]
+    lib.mla_page_compact_workspace.restype = i32
+    lib.mla_page_compact_workspace.argtypes = [i64, ctypes.POINTER(sz)]
+    lib.mla_page_compact.restype = i32
+    lib.mla_page_compact.argtypes = [P, i64, i32, i32, P, P, i32, P, i32, P, P, P, sz, P]
     lib.mla_kv_gather.restype = i32
     lib.mla_kv_gather.argtypes = [P, i64, i32, i32, f32, P, P, i32, P, i32, i32, P, i64, P]
     lib.mla_kv_evict.restype = i32
@@ -501,6 +510,67 @@ def kv_evict(kv_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.T
           *_want_rows(what, dev, "kept", kept, i32, B), _want(what, dev, "new_lens", new_lens, i32, (B,)),
           *_want_rows(what, dev, "mass_out", mass_out, f32, B))
     return kept, new_lens, mass_out
+
+
+def page_fork(kv_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor, parents: torch.Tensor,
+              children: torch.Tensor, new_pages: torch.Tensor, kv_dtype: int = MLA_KV_BF16, page_scales=None, *, stream=None) -> None:
+    """mla_page_fork through the C ABI: slots ``children`` [n] become copies of slots ``parents`` [n]: full
+    pages shared, a partial last one copied to ``new_pages`` [n].  page_table [slots, any], seq_lens
+    [slots] and refs [num_pages], all int32, are changed in place."""
+    what = "mla_page_fork"
+    dev, pool, pages, page_size = _want_pool(what, kv_pages, kv_dtype)
+    i32, n, slots = torch.int32, parents.numel(), seq_lens.numel()
+    _call(what, dev, stream, lib.mla_page_fork, pool, pages, page_size, kv_dtype,
+          None if page_scales is None else _want(what, dev, "page_scales", page_scales, torch.float32, (pages,)),
+          *_want_rows(what, dev, "page_table", page_table, i32, slots), _want(what, dev, "seq_lens", seq_lens, i32, (slots,)), slots,
+          _want(what, dev, "refs", refs, i32, (pages,)), _want(what, dev, "parents", parents, i32, (n,)),
+          _want(what, dev, "children", children, i32, (n,)), _want(what, dev, "new_pages", new_pages, i32, (n,)), n)
+
+
+def page_free(page_table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor, slots: torch.Tensor, keep_lens: torch.Tensor,
+              page_size: int, freed=None, num_freed=None, *, stream=None):
+    """mla_page_free through the C ABI: slots ``slots`` [n] shrink to ``keep_lens`` [n] (0: they end).  seq_lens and
+    refs [num_pages] are changed in place.  Returns (freed [num_pages] int32: the pages that came free,
+    ascending, and zeros behind them where it is allocated here; num_freed [1] int32)."""
+    what = "mla_page_free"
+    dev, i32, n = refs.get_device(), torch.int32, slots.numel()
+    pages = refs.numel()
+    if dev >= 0 and (freed is None or num_freed is None):
+        with _on(stream):
+            freed = torch.zeros(pages, dtype=i32, device=refs.device) if freed is None else freed
+            num_freed = torch.zeros(1, dtype=i32, device=refs.device) if num_freed is None else num_freed
+    r = _want(what, dev, "refs", refs, i32, (pages,))
+    _call(what, dev, stream, lib.mla_page_free, *_want_rows(what, dev, "page_table", page_table, i32, seq_lens.numel()),
+          _want(what, dev, "seq_lens", seq_lens, i32, (seq_lens.numel(),)), seq_lens.numel(), page_size, r, pages,
+          _want(what, dev, "slots", slots, i32, (n,)), _want(what, dev, "keep_lens", keep_lens, i32, (n,)), n,
+          _want(what, dev, "freed", freed, i32, (pages,)), _want(what, dev, "num_freed", num_freed, i32, (1,)))
+    return freed, num_freed
+
+
+def page_compact_workspace_for(num_pages: int, device) -> torch.Tensor:
+    """Allocate (with torch) a workspace of the size page_compact needs for a pool of num_pages pages."""
+    need = ctypes.c_size_t()
+    _check(lib.mla_page_compact_workspace(int(num_pages), ctypes.byref(need)), "mla_page_compact_workspace")
+    return torch.empty(need.value, dtype=torch.uint8, device=device)
+
+
+def page_compact(kv_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor,
+                 kv_dtype: int = MLA_KV_BF16, num_live=None, workspace=None, page_scales=None, *, stream=None) -> torch.Tensor:
+    """mla_page_compact through the C ABI: the pages that anything refers to move to 0 .. num_live - 1;
+    page_table, refs and page_scales follow in place.  Returns num_live [1] int32."""
+    what = "mla_page_compact"
+    dev, pool, pages, page_size = _want_pool(what, kv_pages, kv_dtype)
+    if dev >= 0 and (num_live is None or workspace is None):
+        with _on(stream):
+            num_live = torch.zeros(1, dtype=torch.int32, device=kv_pages.device) if num_live is None else num_live
+            workspace = page_compact_workspace_for(pages, kv_pages.device) if workspace is None else workspace
+    ws, ws_bytes = _want_workspace(what, dev, workspace)
+    i32, slots = torch.int32, seq_lens.numel()
+    _call(what, dev, stream, lib.mla_page_compact, pool, pages, page_size, kv_dtype,
+          None if page_scales is None else _want(what, dev, "page_scales", page_scales, torch.float32, (pages,)),
+          *_want_rows(what, dev, "page_table", page_table, i32, slots), _want(what, dev, "seq_lens", seq_lens, i32, (slots,)), slots,
+          _want(what, dev, "refs", refs, i32, (pages,)), _want(what, dev, "num_live", num_live, i32, (1,)), ws, ws_bytes)
+    return num_live
 
 
 def set_profile_events(start=None, stop=None) -> None:

@@ -2,16 +2,22 @@
 // or end give them back, and a pool with holes is compacted.  A count per page says how many table entries
 // refer to it (0: free).
 //
-// All of it is integer bookkeeping of some microseconds around copies at memory speed:
+// All of it is integer bookkeeping of some microseconds, bound by its chain of dependent loads and launches, around
+// copies at memory speed:
 //  * fork: a cluster of four CTAs per child copies the table row, counts up the shared pages and copies the
 //    parent's partial last page.  The checks are made by each CTA for itself; what they read and the call writes
-//    (the count of the new page) is written after a cluster barrier.
+//    (the count of the new page) is written after a cluster barrier.  (4 children of 2000 tokens 2.7 us, 64 of up to
+//    32768 3.4 us.)
 //  * free: counts go down in one grid, a cluster of four CTAs per slot (a page that nothing refers to any more is
-//    marked in its count), and one cluster of eight CTAs then lists the marked pages in ascending order: each warp counts
-//    in a range of its own, a scan over warps and CTAs places the ranges, and the warp writes what it counted.  No
-//    atomics order anything.
+//    marked in its count), and one cluster of eight CTAs then lists the marked pages in ascending order: each warp marks
+//    in a range of its own, a scan over warps and CTAs places the ranges, and the warp writes what it marked.  No
+//    atomics order anything.  (The 16384 last tokens of 16 requests, 88 thousand pages: 7.6 us; 256 of 512 requests, 345
+//    thousand pages: 16.0, the list 9.8 of them.  A cluster of 16, opt-in, listed these in 8.2, but took 0.6 to 3 us more
+//    on small pools; one of four 15.1.)
 //  * compact: the same scan over the counts pairs the k-th hole below the number of live pages with the k-th
-//    live page above it; one grid then copies the pages and rewrites the tables.
+//    live page above it; then a CTA an SM moves the pages by bulk copies through a ring in shared memory, while its other
+//    warps rewrite the tables.  (412 MB read and written: 132 us with the scan, 6.2 TB/s; through registers 141; stages
+//    of 16 KB 136, of 4 KB 214, half of the ring 142.)
 #include "mla_internal.h"
 #include "sm103a_ptx.cuh"
 
@@ -26,7 +32,10 @@ constexpr int kScanThreads = 1024;
 constexpr int kScanWarps = kScanThreads / 32;
 constexpr int kScanCluster = 8;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBytes = 4 * 16 * kMoveThreads;  // of a page, a CTA at a time
+constexpr int kMoveBytes = 8192;  // of a page, a copy
+constexpr int kMoveStages = 24;
+constexpr int kMoveLag = 8;  // copies to global memory that may still read their stages
+constexpr int kMoveSmem = kMoveStages * kMoveBytes;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -124,7 +133,7 @@ __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(const ForkParam
 constexpr int kFreed = 1 << 30;
 
 __global__ void __launch_bounds__(kDropThreads) page_drop_kernel(const FreeParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
   const int i = blockIdx.y, t = threadIdx.x;
   const uint32_t rank = cluster_rank();
   const int slot = __ldg(p.list + i), keep = __ldg(p.keep_lens + i);
@@ -198,67 +207,116 @@ __device__ __forceinline__ void scan_range(int num_pages, int& from, int& to) {
   to = static_cast<int>(min(static_cast<int64_t>(num_pages), static_cast<int64_t>(w + 1) * per));
 }
 
-// How many counts in [from, to) answer `is`.  (Eight loads of a lane in flight.)
-template <typename F>
-__device__ __forceinline__ int warp_count(const int32_t* refs, int from, int to, F is) {
+// Which of a warp's pages a predicate marks, 32 to a word.  The first kept words of a warp stay in shared memory; of
+// larger pools the rest is read again.  (Reading everything again, 32 counts at a time, took 10 of 22 us for a third of a
+// million pages.)
+constexpr int kKept = 256;  // words: pools of 2 million pages
+constexpr int kInFlight = 16;
+
+struct Marks {
+  uint32_t word[kScanWarps][kKept];
+};
+
+// Words of the pages [from, to) for which is(page, count) holds; f(index, word) of each.
+template <typename Is, typename F>
+__device__ __forceinline__ void each_word(const int32_t* refs, int from, int to, Is is, F f) {
   const int lane = threadIdx.x & 31;
-  int n = 0;
-  for (int x = from; x < to; x += 32 * 8) {
-    int v[8];
+  int x = from;
+  for (; x + 32 * kInFlight <= to; x += 32 * kInFlight) {
+    const int32_t* at = refs + x + lane;
+    int v[kInFlight];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = x + 32 * k + lane < to ? refs[x + 32 * k + lane] : 0;
+    for (int k = 0; k < kInFlight; ++k) v[k] = at[32 * k];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) n += __popc(__ballot_sync(0xffffffffu, x + 32 * k + lane < to && is(v[k])));
+    for (int k = 0; k < kInFlight; ++k) f((x - from) / 32 + k, __ballot_sync(0xffffffffu, is(x + 32 * k + lane, v[k])));
   }
+  for (; x < to; x += 32 * 4) {
+    int v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = x + 32 * k + lane < to ? refs[x + 32 * k + lane] : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (x + 32 * k < to) f((x - from) / 32 + k, __ballot_sync(0xffffffffu, is(x + 32 * k + lane, v[k])));
+  }
+}
+
+// How many there are; the words that fit are kept.
+template <typename Is>
+__device__ __forceinline__ int mark(Marks& marks, const int32_t* refs, int from, int to, Is is) {
+  const int lane = threadIdx.x & 31;
+  uint32_t* words = marks.word[threadIdx.x >> 5];
+  int n = 0;
+  const int kept = min(to, from + 32 * kKept);
+  each_word(refs, from, kept, is, [&](int i, uint32_t m) {
+    if (lane == 0) words[i] = m;
+  });
+  __syncwarp();
+  for (int i = lane; from + 32 * i < kept; i += 32) n += __popc(words[i]);
+  n = __reduce_add_sync(0xffffffffu, n);
+  each_word(refs, kept, to, is, [&](int, uint32_t m) { n += __popc(m); });
   return n;
 }
 
-__global__ void __cluster_dims__(kScanCluster, 1, 1) __launch_bounds__(kScanThreads) page_list_kernel(const FreeParams p) {
+template <typename Is, typename F>
+__device__ __forceinline__ void each_marked(const Marks& marks, const int32_t* refs, int from, int to, Is is, F f) {
+  for (int i = 0; i < kKept && from + 32 * i < to; ++i) f(from + 32 * i, marks.word[threadIdx.x >> 5][i]);
+  const int rest = from + 32 * kKept;
+  if (rest < to) each_word(refs, rest, to, is, [&](int i, uint32_t m) { f(rest + 32 * i, m); });
+}
+
+__global__ void __launch_bounds__(kScanThreads) page_list_kernel(const FreeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ Scan scan;
+  __shared__ Marks marks;
   const int lane = threadIdx.x & 31;
   int from, to, total;
   scan_range(p.num_pages, from, to);
-  int at = cluster_prefix(scan, warp_count(p.refs, from, to, [](int v) { return v <= -kFreed; }), total);
-  for (int x = from; x < to; x += 32) {
-    const int v = x + lane < to ? p.refs[x + lane] : 0;
-    const unsigned m = __ballot_sync(0xffffffffu, v <= -kFreed);
-    if (v <= -kFreed) p.freed[at + __popc(m & ((1u << lane) - 1))] = x + lane;
-    if (v < 0) p.refs[x + lane] = 0;
+  // a count below 0 becomes 0 once it is not read again
+  const auto freed = [&](int page, int v) {
+    if (v < 0 && page - from < 32 * kKept) p.refs[page] = 0;
+    return v <= -kFreed;
+  };
+  const auto freed_rest = [&](int page, int v) {
+    if (v < 0) p.refs[page] = 0;
+    return v <= -kFreed;
+  };
+  const int mine = mark(marks, p.refs, from, to, freed);
+  int at = cluster_prefix(scan, mine, total);
+  each_marked(marks, p.refs, from, to, freed_rest, [&](int x, uint32_t m) {
+    if (m >> lane & 1) p.freed[at + __popc(m & ((1u << lane) - 1))] = x + lane;
     at += __popc(m);
-  }
+  });
   if (cluster_rank() == 0 && threadIdx.x == 0) *p.num_freed = total;
   cluster_sync();  // (no CTA ends while another reads its total)
 }
 
 // ----------------------------------------------------------------------------------------- compact
-__global__ void __cluster_dims__(kScanCluster, 1, 1) __launch_bounds__(kScanThreads) page_pair_kernel(const CompactParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(kScanThreads) page_pair_kernel(const CompactParams p) {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
   __shared__ Scan scan;
+  __shared__ Marks marks;
   __shared__ int holes_here;
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) holes_here = 0;
   int from, to, live;
   scan_range(p.num_pages, from, to);
   // live pages before each warp's range, and in all
-  int at = cluster_prefix(scan, warp_count(p.refs, from, to, [](int v) { return v > 0; }), live);
+  const auto used = [](int, int v) { return v > 0; };
+  int at = cluster_prefix(scan, mark(marks, p.refs, from, to, used), live);
   // hole h < live is number h - (live pages before h); live page x >= live is number live - 1 - (live pages before x)
   // from the end
   int holes = 0;
-  for (int x = from; x < to; x += 32) {
-    const int page = x + lane;
-    const bool in = page < to, used = in && p.refs[page] > 0;
-    const unsigned m = __ballot_sync(0xffffffffu, used);
-    const int before = at + __popc(m & ((1u << lane) - 1));
-    const bool hole = in && !used && page < live;
+  each_marked(marks, p.refs, from, to, used, [&](int x, uint32_t m) {
+    const int page = x + lane, before = at + __popc(m & ((1u << lane) - 1));
+    const bool in = page < to, here = m >> lane & 1, hole = in && !here && page < live;
     if (hole) p.holes[page - before] = page;
     if (in && page >= live) {
-      if (used) p.movers[live - 1 - before] = page;
+      if (here) p.movers[live - 1 - before] = page;
       p.remap[page] = -1;
     }
     holes += __popc(__ballot_sync(0xffffffffu, hole));
     at += __popc(m);
-  }
+  });
   if (lane == 0) atomicAdd(&holes_here, holes);
   cluster_sync();
   int moves = 0;
@@ -280,14 +338,81 @@ __global__ void __cluster_dims__(kScanCluster, 1, 1) __launch_bounds__(kScanThre
 }
 
 __global__ void __launch_bounds__(kMoveThreads) page_move_kernel(const CompactParams p) {
+  extern __shared__ __align__(128) uint8_t stages[];
+  __shared__ uint64_t full[kMoveStages];
+  __shared__ int abort_flag;
+  const int t = threadIdx.x, lane = t & 31;
+  if (t == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < kMoveStages; ++s) mbar_init(full + s, 1);
+    fence_mbarrier_init();
+  }
+  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int live = p.head[0], moves = p.head[1], t = threadIdx.x;
-  // tables: a warp a stretch of 32 x 8 entries
-  {
-    const int lane = t & 31;
+  const int live = p.head[0], moves = p.head[1];
+  if (t < 32) {
+    // pages: a ring of slices through shared memory.  The lanes work out 32 slices at a time, ahead of their use (one
+    // thread that did it slice by slice waited for their indexes: 196 us where plain copies took 142), and lane s knows
+    // where the slice of stage s goes.
+    const int64_t page_bytes = static_cast<int64_t>(p.page_size) * p.row_bytes;
+    const int slices = static_cast<int>((page_bytes + kMoveBytes - 1) / kMoveBytes);
+    const int64_t all = static_cast<int64_t>(moves) * slices;
+    const int64_t mine = all > blockIdx.x ? (all - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    struct Slice {
+      int64_t from, to;
+      uint32_t bytes;
+    };
+    const auto slice = [&](int64_t i) {
+      if (i >= mine) return Slice{0, 0, 0};
+      const int64_t u = blockIdx.x + i * gridDim.x;
+      const int k = static_cast<int>(u / slices), s = static_cast<int>(u % slices);
+      const int64_t at = static_cast<int64_t>(s) * kMoveBytes;
+      return Slice{p.movers_up[k] * page_bytes + at, p.holes[k] * page_bytes + at, static_cast<uint32_t>(min(static_cast<int64_t>(kMoveBytes), page_bytes - at))};
+    };
+    const uint64_t policy = policy_evict_first();
+    Slice now = slice(lane), later = slice(32 + lane), held = {0, 0, 0};
+    const auto load = [&](int64_t i) {  // (i one by one)
+      const int r = static_cast<int>(i & 31), s = static_cast<int>(i % kMoveStages);
+      if (r == 0 && i > 0) {
+        now = later;
+        later = slice(i + 32 + lane);
+      }
+      const Slice x = {__shfl_sync(0xffffffffu, now.from, r), __shfl_sync(0xffffffffu, now.to, r), __shfl_sync(0xffffffffu, now.bytes, r)};
+      if (lane == s) {
+        held = x;
+        mbar_arrive_expect_tx(full + s, x.bytes);
+        bulk_load(stages + s * kMoveBytes, p.kv_pages + x.from, x.bytes, full + s, policy);
+      }
+    };
+    for (int64_t i = 0; i < min(mine, static_cast<int64_t>(kMoveStages)); ++i) load(i);
+    for (int64_t i = 0; i < mine; ++i) {
+      const int s = static_cast<int>(i % kMoveStages);
+      const bool landed = mbar_wait(full + s, (i / kMoveStages) & 1, &abort_flag);
+      if (!__all_sync(0xffffffffu, landed)) {
+        if (lane == 0) atomicOr(p.status, kStatusTimeout);
+        for (int64_t j = i + 1; j < min(mine, max(i - kMoveLag, int64_t(0)) + kMoveStages); ++j) {  // what is in flight lands first
+          abort_flag = 0;
+          if (!mbar_wait(full + j % kMoveStages, (j / kMoveStages) & 1, &abort_flag)) break;
+        }
+        break;
+      }
+      const int64_t to = __shfl_sync(0xffffffffu, held.to, s);
+      const uint32_t bytes = __shfl_sync(0xffffffffu, held.bytes, s);
+      if (lane == 0) bulk_store(p.kv_pages + to, stages + s * kMoveBytes, bytes);
+      // the stage of the copy before the last kMoveLag takes a slice again
+      const int64_t next = i - kMoveLag + kMoveStages;
+      if (i >= kMoveLag && next < mine) {
+        if (lane == 0) bulk_wait_read<kMoveLag>();
+        __syncwarp();
+        load(next);
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  } else {
+    // tables: a warp a stretch of 32 x 8 entries
     const int64_t stretches = (p.max_pages + 255) / 256, units = stretches * p.slots;
     bool bad = false;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (t >> 5); u < units; u += static_cast<int64_t>(gridDim.x) * (kMoveThreads / 32)) {
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32 - 1) + (t >> 5) - 1; u < units; u += static_cast<int64_t>(gridDim.x) * (kMoveThreads / 32 - 1)) {
       const int slot = static_cast<int>(u / stretches), j0 = static_cast<int>(u % stretches) * 256;
       const int L = __ldg(p.seq_lens + slot);
       if (L <= 0) continue;
@@ -312,28 +437,12 @@ __global__ void __launch_bounds__(kMoveThreads) page_move_kernel(const CompactPa
     }
     if (bad) atomicOr(p.status, kStatusDeviceArg);
   }
-  // pages: a CTA a slice of one at a time, four loads of a thread in flight
-  const int64_t page_bytes = static_cast<int64_t>(p.page_size) * p.row_bytes;
-  const int slices = static_cast<int>((page_bytes + kMoveBytes - 1) / kMoveBytes);
-  for (int64_t u = blockIdx.x; u < static_cast<int64_t>(moves) * slices; u += gridDim.x) {
-    const int k = static_cast<int>(u / slices), s = static_cast<int>(u % slices);
-    const int64_t at = static_cast<int64_t>(s) * kMoveBytes;
-    const int pieces = static_cast<int>(min(static_cast<int64_t>(kMoveBytes), page_bytes - at) / 16);
-    const uint4* src = reinterpret_cast<const uint4*>(p.kv_pages + p.movers_up[k] * page_bytes + at);
-    uint4* dst = reinterpret_cast<uint4*>(p.kv_pages + p.holes[k] * page_bytes + at);
-    uint4 v[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (t + c * kMoveThreads < pieces) v[c] = __ldcs(src + t + c * kMoveThreads);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (t + c * kMoveThreads < pieces) __stcs(dst + t + c * kMoveThreads, v[c]);
-  }
 }
 
 template <typename K, typename P>
-cudaError_t launch_dependent(K kernel, dim3 grid, int threads, int cluster, const P& p, cudaStream_t stream) {
+cudaError_t launch_dependent(K kernel, dim3 grid, int threads, int cluster, int smem, const P& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
@@ -354,22 +463,41 @@ cudaError_t launch_dependent(K kernel, dim3 grid, int threads, int cluster, cons
 }  // namespace
 
 cudaError_t launch_page_fork(const ForkParams& p, cudaStream_t stream) {
-  return launch_dependent(page_fork_kernel, dim3(kForkCluster, p.n), kForkThreads, kForkCluster, p, stream);
+  return launch_dependent(page_fork_kernel, dim3(kForkCluster, p.n), kForkThreads, kForkCluster, 0, p, stream);
 }
 
 cudaError_t launch_page_free(const FreeParams& p, cudaStream_t stream) {
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_device != dev) {
+    e = cudaFuncSetAttribute(page_list_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
   if (p.n > 0) {
-    const cudaError_t e = launch_dependent(page_drop_kernel, dim3(kDropCluster, p.n), kDropThreads, kDropCluster, p, stream);
+    e = launch_dependent(page_drop_kernel, dim3(kDropCluster, p.n), kDropThreads, kDropCluster, 0, p, stream);
     if (e != cudaSuccess) return e;
   }
-  return launch_dependent(page_list_kernel, dim3(kScanCluster), kScanThreads, 1, p, stream);
+  return launch_dependent(page_list_kernel, dim3(kScanCluster), kScanThreads, kScanCluster, 0, p, stream);
 }
 
 cudaError_t launch_page_compact(const CompactParams& p, int num_sms, cudaStream_t stream) {
-  const cudaError_t e = launch_dependent(page_pair_kernel, dim3(kScanCluster), kScanThreads, 1, p, stream);
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // as many CTAs as the SMs hold: which slices there are is known on the device alone
-  return launch_dependent(page_move_kernel, dim3(8 * num_sms), kMoveThreads, 1, p, stream);
+  if (configured_device != dev) {
+    e = cudaFuncSetAttribute(page_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(page_pair_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
+  e = launch_dependent(page_pair_kernel, dim3(kScanCluster), kScanThreads, kScanCluster, 0, p, stream);
+  if (e != cudaSuccess) return e;
+  // a CTA an SM: which slices there are is known on the device alone
+  return launch_dependent(page_move_kernel, dim3(num_sms), kMoveThreads, 1, kMoveSmem, p, stream);
 }
 
 }  // namespace mla

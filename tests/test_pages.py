@@ -445,3 +445,34 @@ def test_pools_beyond_32_bits(mla):
     assert table.tolist() == [[0, 1], [0, 2]] and refs[:3].tolist() == [2, 1, 1] and not refs[3:].any()
     assert torch.equal(pool[0], rows[0]) and torch.equal(pool[1], rows[1]) and torch.equal(pool[2, :100], rows[1, :100])
     assert mla.get_status() == mla.MLA_OK
+
+
+@pytest.mark.gpu
+def test_millions_of_pages(mla):
+    """More pages than the scan keeps marks of: half of 2.3 million are given back, the others (5.9 GB with the holes) move."""
+    page, n = 8, 2_300_003
+    g = torch.Generator(device="cuda").manual_seed(6)
+    order = torch.randperm(n, generator=g, device="cuda").int()
+    kept = n // 2
+    table = order.view(1, n).clone()
+    lens, refs = dev([n * page]), torch.ones(n, dtype=torch.int32, device="cuda")
+    freed, count = mla.page_free(table, lens, refs, dev([0]), dev([kept * page - 3]), page)
+    gone = order[kept:].sort().values
+    assert int(count) == n - kept and torch.equal(freed[:n - kept], gone) and not freed[n - kept:].any()
+    assert int(lens) == kept * page - 3 and int(refs.sum()) == kept and not refs[gone.long()].any()
+    pool = torch.empty(n, page, 336, dtype=torch.uint8, device="cuda")
+    name = torch.arange(n, dtype=torch.int32, device="cuda")
+    for r in (0, page - 1):  # each page's first and last bytes say which it is
+        pool[:, r, (0 if r == 0 else 332):][:, :4] = name.view(torch.uint8).view(n, 4)
+    assert int(mla.page_compact(pool, table, lens, refs, 4)) == kept
+    now = table[0, :kept].long()
+    assert torch.equal(now.sort().values, torch.arange(kept, device="cuda"))
+    assert (refs[:kept] == 1).all() and not refs[kept:].any() and torch.equal(table[0, kept:], order[kept:])
+    for r in (0, page - 1):
+        there = pool[:, r, (0 if r == 0 else 332):][:, :4].contiguous().view(torch.int32).flatten()
+        assert torch.equal(there[now], order[:kept])
+    stay = order[:kept] < kept
+    assert torch.equal(now[stay], order[:kept][stay].long())  # what lies below stays
+    moved = now[~stay][order[:kept][~stay].argsort()]  # ascending pages take ascending holes
+    assert torch.equal(moved, moved.sort().values)
+    assert mla.get_status() == mla.MLA_OK

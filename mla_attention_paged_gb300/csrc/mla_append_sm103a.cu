@@ -21,6 +21,8 @@
 // takes 22.8 for 8191 tokens of 16 normed 192-wide heads and their keys: 5.3 TB/s.)
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "fp4_rows.cuh"
 #include "mla_internal.h"
 #include "sm103a_ptx.cuh"
@@ -31,6 +33,7 @@ namespace {
 constexpr int kRope = 64;
 constexpr int kWarps = 4;
 constexpr int kManySteps = 2;
+constexpr int kManySteps64 = 4;  // heads of the 64 rotated columns alone: 128 bytes a step
 constexpr int kManyKeyLanes = 16;
 constexpr int64_t kFewRows = 12288;
 
@@ -168,7 +171,7 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale, bool i
 // A 4-bit row (kFp4) is written to the bit of the plain formula, since a code of four bits may hang on the last bit of
 // the norm: the squares (exact) are summed with their rounding errors, and the rotation uses no fused multiply-adds.
 template <int kChunks, int kSteps, int kKeyLanes, bool kFp4>
-__global__ void __launch_bounds__(32 * kWarps, kChunks <= 2 ? 5 : 1) kv_append_kernel(const AppendParams p, int64_t k_warps, int warps_per_token) {
+__global__ void __launch_bounds__(32 * kWarps, kChunks == 0 && kSteps > 1 ? 6 : kChunks <= 2 ? 5 : 1) kv_append_kernel(const AppendParams p, int64_t k_warps, int warps_per_token) {
   // programmatic dependent launch: no input is read before the previous kernel has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, sub = lane >> 3, l = lane & 7;
@@ -260,13 +263,21 @@ __global__ void __launch_bounds__(32 * kWarps, kChunks <= 2 ? 5 : 1) kv_append_k
   load_turn(turn, p.cos_sin + (live ? static_cast<int64_t>(pos) * kRope : 0), l, inter);
   float inv = 1.f;
   if (kFp4 && p.kv_weight) {
-    Sum ss = {0.f, 0.f};
+    // (a chain of its own for every chunk: each addition waits for the one before it)
+    Sum part[kLatentChunks];
 #pragma unroll
     for (int i = 0; i < kLatentChunks; ++i) {
       float f[8];
       unpack8(w[i], f);
+      part[i] = {f[0] * f[0], 0.f};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss = add(ss, f[k] * f[k]);
+      for (int k = 1; k < 8; ++k) part[i] = add(part[i], f[k] * f[k]);
+    }
+    Sum ss = part[0];
+#pragma unroll
+    for (int i = 1; i < kLatentChunks; ++i) {
+      ss = add(ss, part[i].hi);
+      ss.lo += part[i].lo;
     }
 #pragma unroll
     for (int o = kKeyLanes / 2; o > 0; o >>= 1) {
@@ -337,7 +348,10 @@ cudaError_t launch_chunks(const AppendParams& p, cudaStream_t stream) {
   // 2.6 / 3.1, 6.1 / 5.3; 8 heads of 576 normed 7.9 / 6.9, 10.7 / 8.9, 13.0 / 11.2, 36.7 / 27.4.  (Wide
   // rows cross at about 9000, 64 columns at about 20000: one border between them for all.)
   const bool few = static_cast<int64_t>(p.tokens) * (p.heads > 0 ? p.heads : 16) <= kFewRows;
-  const int steps = few ? 1 : kManySteps, key_rows = few ? 1 : 32 / kManyKeyLanes;
+  // (rows of 64 columns alone: 8191 tokens of 16 heads with their keys 10.7 us at two steps, five CTAs; 9.3 at four steps,
+  // six CTAs; into 4-bit rows 13.7 and 11.5)
+  const bool four = kChunks == 0 && p.heads > 4 * kManySteps;
+  const int steps = few ? 1 : four ? kManySteps64 : kManySteps, key_rows = few ? 1 : 32 / kManyKeyLanes;
   const int per_token = (p.heads + 4 * steps - 1) / (4 * steps);
   const int64_t k_warps = p.kv_in ? (p.tokens + key_rows - 1) / key_rows : 0;
   const int64_t warps = k_warps + static_cast<int64_t>(p.tokens) * per_token;
@@ -350,14 +364,15 @@ cudaError_t launch_chunks(const AppendParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.kv_dtype == kKvFp4) {
-    AppendParams q = p;
-    q.kv_scale = 1.f / p.kv_scale;
-    return few ? cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, 1, 32, true>, q, k_warps, per_token)
-               : cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, kManySteps, kManyKeyLanes, true>, q, k_warps, per_token);
-  }
-  return few ? cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, 1, 32, false>, p, k_warps, per_token)
-             : cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, kManySteps, kManyKeyLanes, false>, p, k_warps, per_token);
+  AppendParams q = p;
+  if (p.kv_dtype == kKvFp4) q.kv_scale = 1.f / p.kv_scale;
+  const auto go = [&](auto fp4) {
+    if (few) return cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, 1, 32, fp4.value>, q, k_warps, per_token);
+    if constexpr (kChunks == 0)
+      if (four) return cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, kManySteps64, kManyKeyLanes, fp4.value>, q, k_warps, per_token);
+    return cudaLaunchKernelEx(&cfg, kv_append_kernel<kChunks, kManySteps, kManyKeyLanes, fp4.value>, q, k_warps, per_token);
+  };
+  return p.kv_dtype == kKvFp4 ? go(std::true_type{}) : go(std::false_type{});
 }
 
 }  // namespace

@@ -96,7 +96,7 @@ struct Ctrl {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  int item[2];                  // request and split (request -1: none)
+  int item[3];                  // request, split and length (request -1: none)
   alignas(16) float mult[kMaxRows];   // scale_log2 2^-s of the row's split; 0: no such row
   alignas(16) float off[kSoftmaxWarps][kMaxRows];  // kPShift - reference maximum, a copy for each warp
   alignas(16) int top[3][kMaxRows];   // largest score (ordered as an integer) of the rows that outgrew their reference, by
@@ -170,9 +170,10 @@ __device__ __forceinline__ void release_stage(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-// Sum of v[r] over the warp's lanes, value r left in the lanes with lane / (32 / NR) == r.
-template <int NR>
-__device__ __forceinline__ float lanes_sum(float (&v)[NR], int lane) {
+// Sum (or largest) of v[r] over the warp's lanes, value r left in the lanes with lane / (32 / NR) == r.
+template <int NR, bool kMax = false>
+__device__ __forceinline__ float lanes_reduce(float (&v)[NR], int lane) {
+  const auto both = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
 #pragma unroll
   for (int n = NR / 2, o = 16; o > 0; n >>= 1, o >>= 1) {
     if (n >= 1) {
@@ -180,26 +181,28 @@ __device__ __forceinline__ float lanes_sum(float (&v)[NR], int lane) {
       for (int i = 0; i < n; ++i) {
         const bool up = (lane & o) != 0;
         const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        v[i] = both(keep, __shfl_xor_sync(0xffffffffu, send, o));
       }
     } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+      v[0] = both(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
     }
   }
   return v[0];
 }
 
-// The item-th split of the batch in the order "whole splits, then remainders", by a whole warp: request and
-// split to out[0], out[1]; request -1 past the last.  A bad length counts as none (item 0 reports it).
+// The item-th split of the batch in the order "whole splits, then remainders", by a whole warp: request, split and the
+// request's length to out[0 .. 2]; request -1 past the last.  A bad length counts as none (item 0 reports it).
 __device__ __forceinline__ void find_split(const DecodeParams& p, int item, int lane, int* out) {
-  int b = -1, split = 0;
+  int b = -1, split = 0, len = 0, L = 0;
   const bool first = item == 0;
   for (int pass = 0; pass < 2 && b < 0; ++pass) {
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      int L = b0 + lane < p.B ? __ldg(p.seq_lens + b0 + lane) : p.T;
-      const bool bad = L < p.T || L > p.max_seq || static_cast<int64_t>(L) > static_cast<int64_t>(p.max_pages) * p.page_size;
-      if (bad && first && pass == 0) atomicOr(p.status, kStatusDeviceArg);
-      if (bad || b0 + lane >= p.B) L = 0;
+      if (pass == 0 || p.B > 32) {  // (32 requests are read once)
+        L = b0 + lane < p.B ? __ldg(p.seq_lens + b0 + lane) : p.T;
+        const bool bad = L < p.T || L > p.max_seq || static_cast<int64_t>(L) > static_cast<int64_t>(p.max_pages) * p.page_size;
+        if (bad && first && pass == 0) atomicOr(p.status, kStatusDeviceArg);
+        if (bad || b0 + lane >= p.B) L = 0;
+      }
       const int whole = L / p.chunk, count = pass == 0 ? whole : (L > whole * p.chunk ? 1 : 0);
       int sum = count;  // inclusive, over the lanes
 #pragma unroll
@@ -212,12 +215,13 @@ __device__ __forceinline__ void find_split(const DecodeParams& p, int item, int 
         const int at = __ffs(__ballot_sync(0xffffffffu, sum > item)) - 1;
         b = b0 + at;
         split = __shfl_sync(0xffffffffu, pass == 0 ? item - (sum - count) : whole, at);
+        len = __shfl_sync(0xffffffffu, L, at);
         break;
       }
       item -= total;
     }
   }
-  if (lane == 0) out[0] = b, out[1] = split;
+  if (lane == 0) out[0] = b, out[1] = split, out[2] = len;
 }
 
 template <int NR>
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
       return;
     }
   }
-  const int L = p.seq_lens[b];
+  const int L = p.split_major == 2 ? ctrl->item[2] : p.seq_lens[b];
   const bool bad_len = L < p.T || L > p.max_seq || static_cast<int64_t>(L) > static_cast<int64_t>(p.max_pages) * p.page_size;
   if (bad_len && threadIdx.x == 0 && split == 0 && group == 0) atomicOr(p.status, kStatusDeviceArg);
   const int kv_start = split * p.chunk;
@@ -616,19 +620,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
         for (int r = 0; r < RW; ++r) top = fmaxf(top, x[r]);
         over = __any_sync(0xffffffffu, top > kPShift + kThreshold);
         if (over) {
-          uint32_t s[RW], rows = 0;
+          // (all rows' largest scores at once, by halves: 0.2 us where a reduction for each row that needs it took 1.0 for
+          // the first tile's 16)
+          uint32_t s[RW];
           load_s<RW>(s_addr, s);
+          float top_of[RW];
 #pragma unroll
-          for (int r = 0; r < RW; ++r) rows |= x[r] > kPShift + kThreshold ? 1u << r : 0u;
-          const uint32_t any = __reduce_or_sync(0xffffffffu, rows);
-#pragma unroll
-          for (int r = 0; r < RW; ++r) {
-            if ((any >> r) & 1) {
-              const int i = __float_as_int((rows >> r) & 1 ? __uint_as_float(s[r]) * ctrl->mult[r0 + r] : -INFINITY);
-              const int best = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
-              if (lane == 0) atomicMax(&ctrl->top[third][r0 + r], best);
-            }
+          for (int r = 0; r < RW; r += 4) {
+            const float4 mu = *reinterpret_cast<const float4*>(&ctrl->mult[r0 + r]);
+            top_of[r] = x[r] == -INFINITY ? -INFINITY : __uint_as_float(s[r]) * mu.x;
+            top_of[r + 1] = x[r + 1] == -INFINITY ? -INFINITY : __uint_as_float(s[r + 1]) * mu.y;
+            top_of[r + 2] = x[r + 2] == -INFINITY ? -INFINITY : __uint_as_float(s[r + 2]) * mu.z;
+            top_of[r + 3] = x[r + 3] == -INFINITY ? -INFINITY : __uint_as_float(s[r + 3]) * mu.w;
           }
+          const int i = __float_as_int(lanes_reduce<RW, true>(top_of, lane));
+          if (lane % (32 / RW) == 0) atomicMax(&ctrl->top[third][r0 + lane / (32 / RW)], i ^ ((i >> 31) & 0x7fffffff));
         }
       }
       // one vote a tile; ordinary tiles reduce nothing else across threads
@@ -725,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
       if (lane == 0) mbar_arrive(&ctrl->p_full[sb]);
     }
     if (!failed) failed = !mbar_wait(&ctrl->o_done[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1, abort_flag);
-    const float ls = lanes_sum<RW>(l_sum, lane), lu = lanes_sum<RW>(l_use, lane);
+    const float ls = lanes_reduce<RW>(l_sum, lane), lu = lanes_reduce<RW>(l_use, lane);
     if (lane % (32 / RW) == 0) {
       ctrl->sums[0][quad][r0 + lane / (32 / RW)] = ls;
       ctrl->sums[1][quad][r0 + lane / (32 / RW)] = lu;

@@ -25,6 +25,8 @@
 // memory and returns.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "fp4_rows.cuh"
 #include "mla_internal.h"
 #include "sm103a_ptx.cuh"
@@ -756,25 +758,35 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
                     : p.ws_o + ((static_cast<int64_t>(b) * p.max_splits + split) * p.R + row0) * kValueDim);
       const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + M::kO + qc * 2 * NR;
       const bool odd = lane & 1;
+      const auto store = [&](auto final_rows) {
+        uint32_t hi[NR], lo[NR];
+        if constexpr (NR == 16) {
+          tmem_ld16(at, hi);
+          tmem_ld16(at + NR, lo);
+        } else {
+          tmem_ld32(at, hi);
+          tmem_ld32(at + NR, lo);
+        }
+        tmem_ld_wait();
 #pragma unroll
-      for (int h = 0; h < NR; h += 16) {
-        uint32_t hi[16], lo[16];
-        tmem_ld16(at + h, hi);
-        load_s<16>(at + NR + h, lo);
-#pragma unroll
-        for (int r = 0; r < 16; r += 2) {
+        for (int r = 0; r < NR; r += 2) {
           // two rows: even lanes store two columns of the first, odd lanes of the second (through shared memory in rows,
           // this took 0.9 us more at 32 rows)
           // (a split's partial is f16 in units of the codes, at most 384; the combine scales it)
-          const float2 scale = *reinterpret_cast<const float2*>(&ctrl->row_scale[h + r]);
-          const uint32_t v0 = out_bits<true>((__uint_as_float(hi[r]) + __uint_as_float(lo[r]) * (1.f / kLoScale)) * scale.x, final_out);
-          const uint32_t v1 = out_bits<true>((__uint_as_float(hi[r + 1]) + __uint_as_float(lo[r + 1]) * (1.f / kLoScale)) * scale.y, final_out);
-          const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-          const int row = h + r + (odd ? 1 : 0);
+          const float2 scale = *reinterpret_cast<const float2*>(&ctrl->row_scale[r]);
+          const float v0 = (__uint_as_float(hi[r]) + __uint_as_float(lo[r]) * (1.f / kLoScale)) * scale.x;
+          const float v1 = (__uint_as_float(hi[r + 1]) + __uint_as_float(lo[r + 1]) * (1.f / kLoScale)) * scale.y;
+          const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+          const float left = odd ? other : v0, right = odd ? v1 : other;
+          const int row = r + (odd ? 1 : 0);
           if (row < nrows)
-            *reinterpret_cast<uint32_t*>(dst + row * kValueDim + (col & ~1)) = odd ? __byte_perm(other, v1, 0x5410) : __byte_perm(v0, other, 0x5410);
+            *reinterpret_cast<uint32_t*>(dst + row * kValueDim + (col & ~1)) = final_rows.value ? pack_bf16x2(left, right) : pack_f16x2(left, right);
         }
-      }
+      };
+      if (final_out)
+        store(std::true_type{});
+      else
+        store(std::false_type{});
       if (warp == 0 && lane < nrows) {
         if (final_out)
           p.lse[static_cast<int64_t>(b) * p.R + row0 + lane] = ctrl->lse[lane];

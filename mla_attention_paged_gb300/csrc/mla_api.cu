@@ -184,9 +184,9 @@ long long plan_cost(const std::vector<int>& tiles, int order, int groups, int ct
 // longest request when it is shorter).  Candidates: the smallest chunk for which the
 // partial kernel needs no more CTAs than the GPU has SMs (one wave; when the unsplit call
 // already fits), the longest request cut into 1-4 splits (1-32 with several row groups
-// that the others leave badly balanced, below), and, for calls of one row group,
+// that the others leave badly balanced, below), and, for calls of one row group and all of a 4-bit pool's,
 // the chunks that share all tiles evenly over one or two waves of SMs (the one-wave one and
-// up to 8 tiles more).  (A batch of equal requests that one wave leaves a few SMs short of,
+// up to 8 tiles more; 4-bit, 16 requests of 64K keys, 64 rows: 219 us without them, 206 with).  (A batch of equal requests that one wave leaves a few SMs short of,
 // e.g. 16 x 1024 tiles on 152 SMs as 144 CTAs of 114, then runs as 144 CTAs of 108 plus 16
 // remainders of 52, the remainders launched last and paired up on the SMs that free first;
 // with an e4m3 pool's larger fixed cost, 109 and remainders of 43.)  The candidate with the
@@ -224,14 +224,14 @@ int choose_chunk_tiles(const std::vector<int>& lens, int tile_keys, int order, i
     }
     cands.push_back(a);
   }
-  if (groups == 1) {
+  if (groups == 1 || order == kWholeFirst) {
     long long total = 0;
-    for (int t : tiles) total += t;
+    for (int t : tiles) total += static_cast<long long>(t) * groups;
     for (int waves = 1; waves <= 2; ++waves) {
       const long long base = (total + static_cast<long long>(waves) * sms - 1) / (static_cast<long long>(waves) * sms);
       // one wave: also up to 8 tiles longer, which shortens the remainders that run two to
-      // an SM (a larger fixed cost per CTA wants shorter remainders)
-      for (int d = 0; d <= (waves == 1 ? 8 : 0); ++d) {
+      // an SM (a larger fixed cost per CTA wants shorter remainders); two waves too where remainders go last
+      for (int d = 0; d <= (waves == 1 || order == kWholeFirst ? 8 : 0); ++d) {
         const long long ct = base + d;
         if (ct >= lo && ct < max_tiles) cands.push_back(static_cast<int>(ct));
       }

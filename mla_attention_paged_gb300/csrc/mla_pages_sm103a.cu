@@ -56,6 +56,22 @@ __device__ __forceinline__ int read_cluster(const int* p, uint32_t rank) {
   return v;
 }
 
+// Untiled bulk copy shared -> global (addresses 16-byte aligned, size a multiple of 16), a group of its own; its stage may
+// be written again once all but the kPending newest groups have read theirs.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(
+                   reinterpret_cast<uint64_t>(dst)),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+
+template <int kPending>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+}
+
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // ----------------------------------------------------------------------------------------- fork
 __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(const ForkParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");

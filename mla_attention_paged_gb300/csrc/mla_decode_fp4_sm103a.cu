@@ -107,7 +107,7 @@ struct Ctrl {
   alignas(16) float lse[kMaxRows];
   alignas(16) int lim[kMaxRows];      // last key that the row sees; -1: none
   alignas(16) uint64_t drafts[kMaxRows];
-  alignas(16) float sums[2][4][kMaxRows];
+  alignas(16) float sums[4][kMaxRows];
 };
 static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
 
@@ -571,9 +571,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const int key_in = quad * 32 + lane;
     const int p0 = L - p.T;  // first draft
-    float l_sum[RW], l_use[RW];
+    float l_sum[RW];
 #pragma unroll
-    for (int r = 0; r < RW; ++r) l_sum[r] = l_use[r] = 0.f;
+    for (int r = 0; r < RW; ++r) l_sum[r] = 0.f;
     // this thread's bytes of P: hi of its RW rows, lo of them NR bytes further (under the key's swizzle)
     const uint32_t p_sw = NR == 16 ? ((key_in >> 2) & 1) << 4 : ((key_in >> 1) & 3) << 4;
     const uint32_t p_hi = smem_u32(smem + M::kOffP) + key_in * 2 * NR + (static_cast<uint32_t>(r0) ^ p_sw);
@@ -668,9 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
             if ((moved >> (r0 + r)) & 1) {
-              const float f = __shfl_sync(0xffffffffu, alpha, r0 + r);
-              l_sum[r] *= f;
-              l_use[r] *= f;
+              l_sum[r] *= __shfl_sync(0xffffffffu, alpha, r0 + r);
             }
           }
           const bool ok = mbar_wait(&ctrl->o_done[sb ^ 1], ((j - 1) >> 1) & 1, abort_flag);
@@ -708,14 +706,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
         const uint32_t ph = pack_f16x2(a, c);
         const uint32_t hi = f16x2_to_e4m3x2(ph);
         const uint32_t hb = e4m3x2_to_f16x2(hi);
-        uint32_t d, u;
+        uint32_t d;
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(ph), "r"(hb));  // (exact)
         asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(d), "r"(0x50005000u));  // times 32
         const uint32_t lo = f16x2_to_e4m3x2(d);
-        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(u) : "r"(e4m3x2_to_f16x2(lo)), "r"(0x28002800u), "r"(hb));  // hi + lo / 32
-        const float2 uf = f16x2_to_f32x2(u);
-        l_use[r] += uf.x;
-        l_use[r + 1] += uf.y;
         hi4[r >> 2] = (r & 2) ? __byte_perm(hi4[r >> 2], hi, 0x5410) : hi;
         lo4[r >> 2] = (r & 2) ? __byte_perm(lo4[r >> 2], lo, 0x5410) : lo;
       }
@@ -732,17 +726,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->p_full[sb]);
     }
-    const float ls = lanes_reduce<RW>(l_sum, lane), lu = lanes_reduce<RW>(l_use, lane);
-    if (lane % (32 / RW) == 0) {
-      ctrl->sums[0][quad][r0 + lane / (32 / RW)] = ls;
-      ctrl->sums[1][quad][r0 + lane / (32 / RW)] = lu;
-    }
+    const float ls = lanes_reduce<RW>(l_sum, lane);
+    if (lane % (32 / RW) == 0) ctrl->sums[quad][r0 + lane / (32 / RW)] = ls;
     named_bar_sync(1, kSoftmaxThreads);
     if (warp == 0 && lane < NR) {
-      const float s = (ctrl->sums[0][0][lane] + ctrl->sums[0][1][lane]) + (ctrl->sums[0][2][lane] + ctrl->sums[0][3][lane]);
-      const float u = (ctrl->sums[1][0][lane] + ctrl->sums[1][1][lane]) + (ctrl->sums[1][2][lane] + ctrl->sums[1][3][lane]);
-      // (a row that sees nothing has sums of 0; a NaN goes on)
-      ctrl->row_scale[lane] = u != 0.f ? (final_out ? p.v_scale : 1.f) / u : 0.f;
+      const float s = (ctrl->sums[0][lane] + ctrl->sums[1][lane]) + (ctrl->sums[2][lane] + ctrl->sums[3][lane]);
+      // (a row that sees nothing has a sum of 0; a NaN goes on)
+      ctrl->row_scale[lane] = s != 0.f ? (final_out ? p.v_scale : 1.f) / s : 0.f;
       ctrl->lse[lane] = s != 0.f ? (m + __log2f(s) - kPShift) * 0.69314718055994530942f : -INFINITY;
     }
     if (!failed) failed = !mbar_wait(&ctrl->o_done[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1, abort_flag);

@@ -65,6 +65,7 @@ struct Map {
   static constexpr int kRaw = NR == 16 ? 3 : 2;        // raw stages
   static constexpr int kFull = NR == 16 ? 6 : 2;       // least common multiple of the stages and a tile's two
   static constexpr int kKBufs = NR == 16 ? 2 : 1;      // decoded K tiles in tensor memory
+  static constexpr bool kHalves = NR == 32;            // one tile: handed over and freed in two halves
   static constexpr int kQBlock = NR * 64;
   static constexpr int kQPart = 9 * kQBlock;           // q_hi or q_lo
   static constexpr int kPBuf = 2 * NR * kTile;
@@ -368,22 +369,40 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
     for (int j = 0; j <= ntiles; ++j) {
       if (j < ntiles) {
         const int sb = j & 1, kb = j % M::kKBufs;
-        if (ok) ok = mbar_wait(&ctrl->k_full[sb], (j >> 1) & 1, abort_flag);
-        if (ok && j >= 2) ok = mbar_wait(&ctrl->s_free[sb], ((j - 2) >> 1) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_fence_after();
         const uint32_t d = tmem + M::kS + sb * NR;
         const uint32_t a = tmem + M::kK + kb * kKCols;
-        if (elect_one()) {
-#pragma unroll 1  // (unrolled, the descriptors of all 36 products would be kept in registers, or spilled)
-          for (int c = 0; c < 9; ++c) {
+        if (ok && j >= 2) ok = mbar_wait(&ctrl->s_free[sb], ((j - 2) >> 1) & 1, abort_flag);
+        if (ok) ok = M::kHalves ? mbar_wait(&ctrl->k_full[0], j & 1, abort_flag) : mbar_wait(&ctrl->k_full[sb], (j >> 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const auto block = [&](int c, bool more) {  // 64 columns
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint64_t off = static_cast<uint64_t>((c * M::kQBlock + k * 32) >> 4);
-              umma_f8_ts(d, a + c * 16 + k * 8, hi_desc + off, idesc1, (c | k) != 0 ? 1u : 0u);
-              umma_f8_ts(d, a + c * 16 + k * 8, lo_desc + off, idesc1, 1u);
-            }
+          for (int k = 0; k < 2; ++k) {
+            const uint64_t off = static_cast<uint64_t>((c * M::kQBlock + k * 32) >> 4);
+            umma_f8_ts(d, a + c * 16 + k * 8, hi_desc + off, idesc1, more || k != 0 ? 1u : 0u);
+            umma_f8_ts(d, a + c * 16 + k * 8, lo_desc + off, idesc1, 1u);
           }
+        };
+        // (unrolled, the descriptors of all 36 products would be kept in registers, or spilled)
+        if constexpr (M::kHalves) {
+          if (elect_one()) {
+#pragma unroll 1
+            for (int c = 0; c < 6; c += c == 1 ? 3 : 1) block(c, c != 0);  // columns 0-127, 256-383
+            umma_commit(&ctrl->k_free[0]);
+          }
+          __syncwarp();
+          ok = mbar_wait(&ctrl->k_full[1], j & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll 1
+            for (int c = 2; c < 9; c += c == 3 ? 3 : 1) block(c, true);
+            umma_commit(&ctrl->s_full[sb]);
+            umma_commit(&ctrl->k_free[1]);
+          }
+        } else if (elect_one()) {
+#pragma unroll 1
+          for (int c = 0; c < 9; ++c) block(c, c != 0);
           umma_commit(&ctrl->s_full[sb]);
           umma_commit(&ctrl->k_free[kb]);
         }
@@ -507,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
         constexpr int kRelease = M::kKBufs == 2 ? 0 : -1;
         if (kRelease < 0) release_stage(&ctrl->raw_empty[s], lane);
         // the K columns are free once BMM1 of their last tile has completed (this warp's own reads have)
-        if (ok && j >= M::kKBufs) ok = mbar_wait(&ctrl->k_free[kb], ((j / M::kKBufs) - 1) & 1, abort_flag);
+        if (ok && j >= M::kKBufs) ok = mbar_wait(&ctrl->k_free[M::kHalves ? 0 : kb], ((j / M::kKBufs) - 1) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
           break;
@@ -532,13 +551,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
           }
           tmem_st16(kcol + k2 * 16, o);
           if (k2 == kRelease) release_stage(&ctrl->raw_empty[s], lane);
+          if (M::kHalves && k2 == 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctrl->k_full[0]);
+            if (j >= 1) ok = mbar_wait(&ctrl->k_free[1], (j - 1) & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+          }
+        }
+        if (!ok) {
+          failed = true;
+          break;
         }
         const uint32_t ro[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w, rope[1].x, rope[1].y, rope[1].z, rope[1].w};
         tmem_st8(kcol + 128 - half * 56, ro);  // (columns 128 + 8 half of the tile)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctrl->k_full[j & 1]);
+        if (lane == 0) mbar_arrive(&ctrl->k_full[M::kHalves ? 1 : j & 1]);
       }
       const int jv = j - kLag;
       if (jv < 0) continue;

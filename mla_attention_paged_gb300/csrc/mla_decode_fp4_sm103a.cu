@@ -672,59 +672,57 @@ __global__ void __launch_bounds__(kThreads, 1) decode_partial_fp4_kernel(const _
         }
       }
       // one vote a tile; ordinary tiles reduce nothing else across threads
+      float alpha = 1.f;
+      uint32_t moved = 0;
       if (bar_or(1, kSoftmaxThreads, fail || over || *abort_flag != 0)) {
         if (bar_or(1, kSoftmaxThreads, fail || *abort_flag != 0)) {
           failed = true;
           break;
         }
         // ---------------------------------------------------------------- some rows' references move
-        float alpha = 1.f;
         if (lane < NR) {
           int i = ctrl->top[third][lane];
           i ^= (i >> 31) & 0x7fffffff;
           const float best = __int_as_float(i);
           if (m == -INFINITY) {
             m = best + kMargin;
-          } else if (best > m + kThreshold) {
+          } else if (best > m) {  // (where one row has to move, those that need not yet go along: 114.0 -> 112.4 us)
             alpha = ex2_approx(m - best - kMargin);
             m = best + kMargin;
           }
           if (i != __float_as_int(-INFINITY)) ctrl->off[warp][lane] = kPShift - m;
         }
-        const uint32_t moved = __ballot_sync(0xffffffffu, alpha != 1.f);
+        moved = __ballot_sync(0xffffffffu, alpha != 1.f);
         __syncwarp();
         scores();
-        if (moved != 0) {
-          // what the moved rows have accumulated, once BMM2 of the last tile has completed: their sums, and their columns
-          // of O, hi and lo of two chunks a warp
-#pragma unroll
-          for (int r = 0; r < RW; ++r) {
-            if ((moved >> (r0 + r)) & 1) {
-              l_sum[r] *= __shfl_sync(0xffffffffu, alpha, r0 + r);
-            }
-          }
-          const bool ok = mbar_wait(&ctrl->o_done[sb ^ 1], ((j - 1) >> 1) & 1, abort_flag);
-          if (!__all_sync(0xffffffffu, ok)) failed = true;  // (the others learn of it at the next vote)
-          tc_fence_after();
-          for (uint32_t left = failed ? 0u : moved; left != 0; left &= left - 1) {
-            const int r = __ffs(left) - 1;
-            const float f = __shfl_sync(0xffffffffu, alpha, r);
-            const uint32_t at = tmem + lane_base + M::kO + (warp >> 2) * 4 * NR + r;
-            uint32_t v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tmem_ld1(at + k * NR, v[k]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tmem_st1(at + k * NR, __float_as_uint(__uint_as_float(v[k]) * f));
-          }
-          tmem_st_wait();
-        }
       }
       if (warp == 0 && lane < NR) ctrl->top[third == 0 ? 2 : third - 1][lane] = kNoScore;  // (the last tile's: all have read it)
       third = third == 2 ? 0 : third + 1;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->s_free[sb]);
+      if (moved != 0) {
+        // what the moved rows have accumulated, once BMM2 of the last tile has completed: their sums, and their columns of
+        // O, hi and lo of two chunks a warp
+#pragma unroll
+        for (int r = 0; r < RW; ++r)
+          if ((moved >> (r0 + r)) & 1) l_sum[r] *= __shfl_sync(0xffffffffu, alpha, r0 + r);
+        const bool ok = mbar_wait(&ctrl->o_done[sb ^ 1], ((j - 1) >> 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) failed = true;  // (the others learn of it at the next vote)
+        tc_fence_after();
+        for (uint32_t left = failed ? 0u : moved; left != 0; left &= left - 1) {
+          const int r = __ffs(left) - 1;
+          const float f = __shfl_sync(0xffffffffu, alpha, r);
+          const uint32_t at = tmem + lane_base + M::kO + (warp >> 2) * 4 * NR + r;
+          uint32_t v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld1(at + k * NR, v[k]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_st1(at + k * NR, __float_as_uint(__uint_as_float(v[k]) * f));
+        }
+        tmem_st_wait();
+      }
       if (j >= 2) {  // this P buffer's last reader
         const bool ok = mbar_wait(&ctrl->o_done[sb], ((j >> 1) - 1) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) failed = true;  // (the others learn of it at the next vote)

@@ -5,9 +5,9 @@
 // the scale, in fp32, rounded once.
 //
 // Bound by memory: each row is read once and 1152 bytes are written.  A row is 72 chunks of eight columns, a
-// lane takes three; a warp has the loads of four rows in flight (336-byte rows are three loads of 4, 4 and 8 bytes a
-// lane and the exponents).  64192 rows of 4-bit pages: 17.3 us, 5.5 TB/s; warps that took more rows in steps, the
-// next ones' places read ahead, 16.0 to 19.2 by rows and steps and pool, none better in all.
+// lane takes three; a warp has the loads of two rows in flight (336-byte rows are three loads of 4, 4 and 8 bytes a
+// lane and the exponents).  64192 rows of 4-bit pages: 15.0 us, 6.3 TB/s; one row a warp 17.5, four 16.0 (65536 bf16
+// rows 21.4, 22.3, 22.3); with codes decoded to e4m3, converted and multiplied 17.3 at four, the issue slots 72 % busy.
 #include <cuda_fp8.h>
 
 #include "fp4_rows.cuh"
@@ -18,7 +18,7 @@ namespace mla {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kRows = 4;  // rows a warp takes
+constexpr int kRows = 2;  // rows a warp takes
 constexpr int kChunks = kLatentDim / 8;
 
 __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t codes) {
@@ -40,8 +40,28 @@ __device__ __forceinline__ uint2 scaled4(uint32_t w, float scale, bool int8) {
   return make_uint2(pack_bf16x2(x.x * scale, x.y * scale), pack_bf16x2(y.x * scale, y.y * scale));
 }
 
+// Eight 4-bit columns as bf16: low and high bytes of each value are looked up in their group's table (a value is
+// one of eight magnitudes, whose products with the scale are the table, and a sign).
+__device__ __forceinline__ uint4 fp4_to_bf16(uint32_t w, const uint4& table) {
+  const uint32_t m = w & 0x77777777u;
+  const uint32_t la = __byte_perm(table.x, table.y, m), ha = __byte_perm(table.z, table.w, m) | (w & 0x80808080u);
+  const uint32_t lb = __byte_perm(table.x, table.y, m >> 16), hb = __byte_perm(table.z, table.w, m >> 16) | ((w << 4) & 0x80808080u);
+  return make_uint4(__byte_perm(la, ha, 0x5140), __byte_perm(la, ha, 0x7362), __byte_perm(lb, hb, 0x5140), __byte_perm(lb, hb, 0x7362));
+}
+
 template <int kKv>
 __global__ void __launch_bounds__(32 * kWarps) kv_gather_kernel(const GatherParams p) {
+  __shared__ uint4 tables[16];  // kKvFp4: by exponent, low bytes of the eight magnitudes, then high bytes
+  if constexpr (kKv == kKvFp4) {
+    static_assert(32 * kWarps == 16 * 8, "a thread for each entry");
+    const int e = threadIdx.x >> 3, i = threadIdx.x & 7;
+    const float magnitude = i < 2 ? 0.5f * i : __uint_as_float(static_cast<uint32_t>(127 + (i >> 1) - 1) << 23 | (i & 1) << 22);
+    const uint32_t v = pack_bf16x2(magnitude * __uint_as_float(static_cast<uint32_t>(127 + e - kFp4ExpBias) << 23) * p.kv_scale, 0.f);
+    uint8_t* bytes = reinterpret_cast<uint8_t*>(tables + e);
+    bytes[i] = static_cast<uint8_t>(v);
+    bytes[8 + i] = static_cast<uint8_t>(v >> 8);
+    __syncthreads();
+  }
   // programmatic dependent launch: no input is read before the previous kernel has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -121,15 +141,13 @@ __global__ void __launch_bounds__(32 * kWarps) kv_gather_kernel(const GatherPara
       if (c >= kChunks) continue;
       uint4 x = v[k][i];
       if constexpr (kKv != kKvBf16) {
-        uint32_t a = x.x, d = x.y;
         if (kKv == kKvFp4 && i < 2) {
-          uint32_t tl, th;
-          fp4_table(x.y, tl, th);
-          fp4_to_e4m3(x.x, tl, th, a, d);
+          x = fp4_to_bf16(x.x, tables[x.y]);
+        } else {
+          constexpr bool kInt8 = kKv == kKvInt8 || kKv == kKvInt8Page;
+          const uint2 l = scaled4(x.x, scale[k], kInt8), h = scaled4(x.y, scale[k], kInt8);
+          x = make_uint4(l.x, l.y, h.x, h.y);
         }
-        constexpr bool kInt8 = kKv == kKvInt8 || kKv == kKvInt8Page;
-        const uint2 l = scaled4(a, scale[k], kInt8), h = scaled4(d, scale[k], kInt8);
-        x = make_uint4(l.x, l.y, h.x, h.y);
       }
       out[c] = x;
     }

@@ -41,14 +41,13 @@ __device__ __forceinline__ int fp4_exponent(float top) {
 // Eight columns (in units of kv_scale, no NaN) as a word of codes under exponent e: nearest, ties to even, saturated.
 __device__ __forceinline__ uint32_t fp4_encode8(const float (&f)[8], int e) {
   const float scale = __uint_as_float(static_cast<uint32_t>(127 + kFp4ExpBias - e) << 23);
-  uint32_t w = 0;
+  uint32_t n = 0;  // eight nibbles, sign above magnitude
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t two = __nv_cvt_float2_to_fp4x2(make_float2(f[2 * i] * scale, f[2 * i + 1] * scale), __NV_E2M1, cudaRoundNearest);
-    w |= (two & 0x77u) << (8 * i);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w |= (__float_as_uint(f[i]) >> 31) << (i < 4 ? 8 * i + 7 : 8 * (i - 4) + 3);
+  for (int i = 0; i < 4; ++i)
+    n |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(f[2 * i] * scale, f[2 * i + 1] * scale), __NV_E2M1, cudaRoundNearest)) << (8 * i);
+  // signs: columns 0-3 to the bytes' top bits, 4-7 to their bits 3
+  const uint32_t s = n & 0x88888888u, x = __byte_perm(s, 0, 0x1100), y = __byte_perm(s, 0, 0x3322);
+  const uint32_t w = (n & 0x77777777u) | ((x << 4) & 0x00800080u) | (x & 0x80008000u) | (y & 0x00080008u) | ((y >> 4) & 0x08000800u);
   return w;
 }
 

@@ -100,6 +100,8 @@ typedef struct mla_decode_plan_t {
   int32_t split_major;       /* launch order of the partial kernel's CTAs: 1 = split by
                                 split (plans of more than one wave), 0 = request by request,
                                 2 = whole splits, then remainders (4-bit pools)          */
+  int32_t num_splits;        /* split_major 2: splits of the planned requests in all;
+                                else 0                                                  */
   size_t workspace_bytes;    /* bytes mla_decode needs in `workspace` (0 = none)         */
 } mla_decode_plan_t;
 
@@ -447,13 +449,15 @@ int mla_kv_evict(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype,
 /* The pages of a cache, kept on the device.  A cache has num_slots requests, slot s with the pages
  * page_table[s, 0 .. ceil(seq_lens[s] / page_size) - 1] (entries from there on mean nothing), and a count refs[page]
  * of the entries that refer to each page; 0 is a free page.  Pages may be shared: full ones only, since appended rows
- * go into the last.  The caller takes new pages from the free ones (mla_page_free lists them) and sets their counts to 1.
+ * go into the last.  (A slot that mla_page_free shrinks into a page that others share is forked before rows are appended to
+ * it: the fork's partial last page is its own.)  The caller takes new pages from the free ones (mla_page_free lists
+ * them) and sets their counts to 1.
  *   kv_pages   : the pool, [num_pages, page_size] rows of kv_dtype (any).
  *   page_scales: [num_pages] for an MLA_KV_INT8_PAGE pool (they go with the pages), else NULL.
  *   page_table : [num_slots, max_pages_per_seq] int32.    seq_lens : [num_slots] int32.    refs : [num_pages] int32.
  * All on the device; what a call writes shares no memory with anything else that it takes.  Kernels are programmatic
- * dependents like mla_decode's.  Errors of all: MLA_ERR_INVALID_ARG (more than 2^30 pages too), MLA_ERR_UNSUPPORTED (page_size not 8..256, more
- * than 65535 listed slots), MLA_ERR_CUDA.
+ * dependents like mla_decode's.  Counts are not negative.  Errors of all: MLA_ERR_INVALID_ARG (more than 2^30 pages
+ * too), MLA_ERR_UNSUPPORTED (page_size not 8..256, more than 65535 listed slots), MLA_ERR_CUDA.
  *
  * mla_page_fork: for each i < count, slot children[i] becomes a copy of slot parents[i]: it shares the full pages
  * (their counts go up by 1); a partial last page is copied to page new_pages[i], whose count becomes 1 (not looked at

@@ -118,7 +118,7 @@ constexpr long long kPairFixedTiles = 8;
 // A 4-bit pool's kernel finds its splits itself (kWholeFirst: all whole splits, then the remainders), up to
 // kFp4ListBatch requests, whose lengths each CTA then looks through.
 constexpr int kByRequest = 0, kBySplit = 1, kWholeFirst = 2;
-constexpr int kFp4ListBatch = 128;
+constexpr int kFp4ListBatch = 512;  // (a thread a request)
 int launch_order(int groups, int kv_dtype, int batch) {
   if (kv_dtype == MLA_KV_FP4 && batch <= kFp4ListBatch) return kWholeFirst;
   return groups == 1 ? kBySplit : kByRequest;
@@ -367,6 +367,7 @@ int make_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_heads,
     // more CTAs with work than SMs, one row group: launch split by split, as the cost model assumed
     long long n_ctas = 0;
     for (int L : lens) n_ctas += (L + pl.chunk_tokens - 1) / pl.chunk_tokens;
+    if (order == kWholeFirst) pl.num_splits = static_cast<int32_t>(n_ctas);
     pl.split_major = order == kWholeFirst ? kWholeFirst : (n_ctas * groups > units && order == kBySplit) ? 1 : 0;
   }
   pl.workspace_bytes = partial_bytes(pl, tree);
@@ -522,6 +523,7 @@ int decode_stages(const mla_decode_plan_t* plan, const void* q, const void* kv_p
   p.max_splits = plan->max_splits;
   p.max_seq = plan->max_seq_len;
   p.split_major = plan->split_major;
+  p.num_splits = plan->num_splits;
   p.kv_dtype = plan->kv_dtype;
   p.num_pages = plan->num_pages;
   const bool kv8 = plan->kv_dtype != MLA_KV_BF16;

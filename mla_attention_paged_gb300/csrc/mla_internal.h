@@ -40,6 +40,7 @@ struct DecodeParams {
   int B, T, H, R;               // R = T*H folded rows per request
   int page_size, max_pages;     // page geometry and page_table row stride
   int chunk, max_splits, max_seq;
+  int num_splits;               // split_major 2: of the planned lengths, all requests (0: not known)
   int split_major;              // grid (groups, B, splits) when set, else (groups, splits, B)
   int kv_dtype;                 // kKvBf16, kKvE4m3, kKvInt8, kKvInt8Page or kKvFp4
   int64_t num_pages;            // pages in the pool: a page id outside [0, num_pages) is reported

@@ -226,6 +226,38 @@ def test_drafts_in_order(mla, lens, T, H, page, sms):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B", [31, 33, 70, 512, 513])
+@pytest.mark.parametrize("T,H", [(1, 16), (2, 20)])
+def test_batches(mla, B, T, H):
+    """Many requests, two of them long: whole splits first up to 512 requests, beyond that in the orders of other pools."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(T, 140, (B,), generator=g).tolist()
+    lens[B // 3], lens[B - 1] = 6000, 3333
+    out, lse, ref, plan = run(mla, lens, T, H, 16, None, seed=B)
+    assert plan.max_splits > 1 and (plan.split_major == 2) == (B <= 512)
+    assert plan.num_splits == (sum(-(-n // plan.chunk_tokens) for n in lens) if B <= 512 else 0)
+    check(out, lse, ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H", [(1, 16), (2, 16), (3, 16)])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("B,L", [(7, 2000), (40, 4500)])
+def test_more_and_fewer_splits_than_planned(mla, T, H, tree, B, L):
+    """Planned for one long request among short ones, run with all of them long: of 40 requests the grid has a CTA for each planned
+    split, and CTAs take several.  And run with fewer splits than planned."""
+    q, pool, table = make([L] * B, T, H, 16, 77)
+    make_plan = mla.decode_tree_plan if tree else mla.decode_plan
+    plan = make_plan([L] + [100] * (B - 1), T, H, 16, table.shape[1], pool.shape[0], mla.MLA_KV_FP4)
+    assert plan.max_splits > 1 and plan.num_splits == plan.max_splits + B - 1
+    words = chain(B, T) if tree else None
+    for lens in ([L] * B, [L - 97 * i for i in range(B)], [50] * (B - 1) + [129]):
+        out, lse = call(mla, plan, q, pool, table, lens, words)
+        assert mla.get_status() == mla.MLA_OK
+        check(out, lse, reference(q, pool, table, lens, chain(B, T)))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("lens,T,H,page,sms", [c for c in CASES if c[1] <= 64])
 def test_random_trees(mla, lens, T, H, page, sms):
     lens = [max(n, T) for n in lens]

@@ -104,6 +104,8 @@ std::unordered_map<std::string, mla_decode_plan_t> g_plan_cache;
 // in tile units depends on the pool format: an e4m3 tile holds half the bytes of a bf16 or
 // int8 one and streams in about half the time, while the start-up (Q load and split, the
 // first tiles' latency) and the epilogue take about as long.
+// (A 4-bit pool's tile has 128 keys; 16 rows start in about 3.5 of them, 32 in 3; planned with 6, the 13 sizes tried from
+// 1000 keys to 16 requests of 131K took as long as with 2 to 4 or up to 6 % less.)
 constexpr long long kCombineTiles = 2;
 long long cta_fixed_tiles(int kv_dtype) { return kv_dtype == MLA_KV_E4M3 ? 10 : kv_dtype == MLA_KV_FP4 ? 6 : 3; }
 // (A pair takes about half as long for a tile as one CTA, and its start as long.  4 requests of 3K-12K

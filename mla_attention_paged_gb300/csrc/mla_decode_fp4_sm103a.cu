@@ -510,6 +510,7 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
         }
         tc_fence_after();
         const uint32_t kcol = k_lane + kb * kKCols;
+        const uint32_t nibble[2][2] = {{ex[0] & 0x0F0F0F0Fu, ex[1] & 0x0F0F0F0Fu}, {(ex[0] >> 4) & 0x0F0F0F0Fu, (ex[1] >> 4) & 0x0F0F0F0Fu}};
 #pragma unroll
         for (int k2 = 0; k2 < 4; ++k2) {  // 64 columns: 16 columns of tensor memory
           uint32_t o[16];
@@ -519,7 +520,7 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
             const uint32_t word[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
             for (int g = 0; g < 2; ++g) {  // 16 columns under one power of two
-              const uint32_t e = (ex[k >> 2] >> (8 * (k & 3) + 4 * g)) & 15u;
+              const uint32_t e = __byte_perm(nibble[g][k >> 2], 0u, 0x4440u | (k & 3));
               uint32_t lo, hi;
               fp4_table(e, lo, hi);
               fp4_to_e4m3(word[2 * g], lo, hi, o[8 * k1 + 4 * g], o[8 * k1 + 4 * g + 1]);

@@ -13,11 +13,11 @@
 //    into the same accumulator.  A from tensor memory keeps 72 KB a tile of operand reads off shared
 //    memory.
 //  * BMM2: O^T[value column, row] += V^T P^T, A = V^T, MN-major out of shared memory, B = the weights,
-//    P 2^6 split into p_hi = e4m3(P) and p_lo = e4m3(32 (P - p_hi)), stacked as 2 x NR columns so that V
-//    is read once; the epilogue adds O_hi + O_lo / 32.  (P 2^6 <= 2^8, kept to 2^-9 relative down to 2^-11 of
-//    the largest weight and to 2^-20 of it below.)
+//    P 2^6 split into p_hi = e4m3(P) and p_lo = e4m3(28 (P - p_hi)), stacked as 2 x NR columns so that V
+//    is read once; the epilogue adds O_hi + O_lo / 28.  (P 2^6 <= 2^8.8 < 448, its residual at most 16: kept to 2^-9
+//    relative down to 2^-11 of the largest weight and to 2^-20 of it below.)
 //  * A key is one thread's in the softmax, so a row's sum is kept per thread and its running maximum
-//    moves only when some score exceeds it by more than 2 (log2): ordinary tiles reduce nothing across
+//    moves only when some score exceeds it by more than 2.8 (log2): ordinary tiles reduce nothing across
 //    threads but one vote.
 // One CTA per (group of NR rows, split, request), 128 keys a tile, 576 threads: softmax warps 0-7 (32 keys
 // and half of the rows each), decoding warps 8-15 (32 keys and half of the columns each; a row's codes go
@@ -25,8 +25,8 @@
 // What bounds it: a tile's chain of decoding, BMM1, softmax and BMM2 (2.5k cycles at 16 rows, 2.9k at 32, where its 43 KB
 // take 1.85k at the copy rate): small products, 52 of them, that one thread issues beside four busy warps (2.1k of the 2.9k;
 // 1.4k alone on an SM), decoding at half the integer pipe, and one or two tiles in tensor memory to overlap them.
-// 16 requests of 8K-131K keys (375 MB, 55 us of bytes): 88 us at 16 rows; at 32 rows 112.5, of which 13 are rescalings (99.7
-// with scores that move no maximum).
+// 16 requests of 8K-131K keys (375 MB, 55 us of bytes): 87 us at 16 rows; at 32 rows 108.0, of which 9 are references that
+// move (99.3 with scores that move none): the next tile then waits for BMM2 of the last.
 // Every wait is bounded; on expiry the CTA records a timeout, drains its copies and MMAs, frees tensor
 // memory and returns.
 #include <cuda_fp16.h>
@@ -63,10 +63,10 @@ constexpr int kAbortTimeout = 1;
 constexpr int64_t kMostEmpty = 304;  // CTAs without a split that a grid may have: two for each SM
 constexpr uint32_t kTmemCols = 512;
 constexpr float kPShift = 6.0f;    // P is formed times 2^6 ...
-constexpr float kThreshold = 2.0f; // ... and at most 2^8: the reference moves when a score exceeds it by more than this,
-constexpr float kMargin = 1.0f;    // to so much above the score (a step of p_lo is then 2^-19 of the largest weight)
-constexpr int kNoScore = static_cast<int>(0x807fffffu);  // -infinity as an ordered integer
-constexpr float kLoScale = 32.0f;  // p_lo carries 32 times the residual (at most 2^3)
+constexpr float kThreshold = 2.8f; // ... and at most 2^8.8: the reference moves when a score exceeds it by more than this,
+constexpr float kMargin = 0.8f;    // to so much above the score (half a step of p_lo is then 2^-20 of the largest weight)
+constexpr float kLoScale = 28.0f;  // p_lo carries 28 times the residual (at most 16).  With 32, 2 and 1 in these places, the same
+                                   // error below, references moved more often: 112.4 against 108.0 us on 32 rows
 
 template <int NR>
 struct Map {
@@ -716,7 +716,7 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
         const uint32_t hb = e4m3x2_to_f16x2(hi);
         uint32_t d;
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(ph), "r"(hb));  // (exact)
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(d), "r"(0x50005000u));  // times 32
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(d), "r"(0x4F004F00u));  // times 28
         const uint32_t lo = f16x2_to_e4m3x2(d);
         hi4[r >> 2] = (r & 2) ? __byte_perm(hi4[r >> 2], hi, 0x5410) : hi;
         lo4[r >> 2] = (r & 2) ? __byte_perm(lo4[r >> 2], lo, 0x5410) : lo;

@@ -3,7 +3,7 @@
 The refusals run on the CPU.  The GPU cases compare every output with the definition in 64 bits on the
 values that the pool's codes stand for.  Tolerances, with w_j the exact weights and W = sum_j w_j |v_j|:
   * the output's own rounding, 2^-8 |out|, and 2^-11 W for a split's f16 partial;
-  * a weight is carried as hi + lo / 32, both e4m3: hi is off by at most 2^-4, lo by at most 2^-5 of that
+  * a weight is carried as hi + lo / 28, both e4m3: hi is off by at most 2^-4, lo by at most 2^-5 of that
     residual's binade top, together 2^-9 of the weight, and by 2^-11 from the f16 value that is split; with as
     much for what the normalisation adds, 2^-8 + 2^-10 of W; below e4m3's normal
     range the error is at most 2^-20 of the largest weight for each of the n keys, n 2^-20 max|v| w_max;

@@ -65,6 +65,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kPShift = 6.0f;    // P is formed times 2^6 ...
 constexpr float kThreshold = 2.8f; // ... and at most 2^8.8: the reference moves when a score exceeds it by more than this,
 constexpr float kMargin = 0.8f;    // to so much above the score (half a step of p_lo is then 2^-20 of the largest weight)
+constexpr int kNoScore = static_cast<int>(0x807fffffu);  // -infinity as an ordered integer
 constexpr float kLoScale = 28.0f;  // p_lo carries 28 times the residual (at most 16).  With 32, 2 and 1 in these places, the same
                                    // error below, references moved more often: 112.4 against 108.0 us on 32 rows
 

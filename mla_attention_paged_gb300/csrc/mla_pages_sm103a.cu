@@ -11,9 +11,9 @@
 //  * free: counts go down in one grid, a cluster of four CTAs per slot (a page that nothing refers to any more is
 //    marked in its count), and one cluster of eight CTAs then lists the marked pages in ascending order: each warp marks
 //    in a range of its own, a scan over warps and CTAs places the ranges, and the warp writes what it marked.  No
-//    atomics order anything.  (The 16384 last tokens of 16 requests, 88 thousand pages: 7.6 us; 256 of 512 requests, 345
-//    thousand pages: 16.0, the list 9.8 of them.  A cluster of 16, opt-in, listed these in 8.2, but took 0.6 to 3 us more
-//    on small pools; one of four 15.1.)
+//    atomics order anything.  (64 tokens of each of 16 requests, 88 thousand pages: 7.5 us; 256 of 512 requests, 345 thousand
+//    pages: 16.0, the list 9.8 of them.  A cluster of 16, opt-in, listed these in 8.2, but took 0.6 to 3 us more on small
+//    pools; one of four 15.1.  Both steps in one cluster saved a launch and took 8.9 and 38.8 us: eight SMs' atomics.)
 //  * compact: the same scan over the counts pairs the k-th hole below the number of live pages with the k-th
 //    live page above it; then a CTA an SM moves the pages by bulk copies through a ring in shared memory, while its other
 //    warps rewrite the tables.  (412 MB read and written: 132 us with the scan, 6.2 TB/s; through registers 141; stages
@@ -483,17 +483,8 @@ cudaError_t launch_page_fork(const ForkParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_page_free(const FreeParams& p, cudaStream_t stream) {
-  static thread_local int configured_device = -1;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (configured_device != dev) {
-    e = cudaFuncSetAttribute(page_list_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    configured_device = dev;
-  }
   if (p.n > 0) {
-    e = launch_dependent(page_drop_kernel, dim3(kDropCluster, p.n), kDropThreads, kDropCluster, 0, p, stream);
+    const cudaError_t e = launch_dependent(page_drop_kernel, dim3(kDropCluster, p.n), kDropThreads, kDropCluster, 0, p, stream);
     if (e != cudaSuccess) return e;
   }
   return launch_dependent(page_list_kernel, dim3(kScanCluster), kScanThreads, kScanCluster, 0, p, stream);
@@ -506,7 +497,6 @@ cudaError_t launch_page_compact(const CompactParams& p, int num_sms, cudaStream_
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
     e = cudaFuncSetAttribute(page_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(page_pair_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }

@@ -25,7 +25,7 @@
 // What bounds it: a tile's chain of decoding, BMM1, softmax and BMM2 (2.5k cycles at 16 rows, 2.9k at 32, where its 43 KB
 // take 1.85k at the copy rate): small products, 52 of them, that one thread issues beside four busy warps (2.1k of the 2.9k;
 // 1.4k alone on an SM), decoding at half the integer pipe, and one or two tiles in tensor memory to overlap them.
-// 16 requests of 8K-131K keys (375 MB, 55 us of bytes): 87 us at 16 rows; at 32 rows 108.0, of which 9 are references that
+// 16 requests of 8K-131K keys (375 MB, 55 us of bytes): 87 us at 16 rows; at 32 rows 108.7, of which 9 are references that
 // move (99.3 with scores that move none): the next tile then waits for BMM2 of the last.
 // Every wait is bounded; on expiry the CTA records a timeout, drains its copies and MMAs, frees tensor
 // memory and returns.
@@ -64,10 +64,11 @@ constexpr int64_t kMostEmpty = 304;  // CTAs without a split that a grid may hav
 constexpr uint32_t kTmemCols = 512;
 constexpr float kPShift = 6.0f;    // P is formed times 2^6 ...
 constexpr float kThreshold = 2.8f; // ... and at most 2^8.8: the reference moves when a score exceeds it by more than this,
-constexpr float kMargin = 0.8f;    // to so much above the score (half a step of p_lo is then 2^-20 of the largest weight)
+constexpr float kMargin = 0.6780719f;  // to so much above the score, whose weight is then 40, an e4m3 number: a weight that
+                                   // dominates its row has no error (half a step of p_lo is 2^-20.1 of the largest weight)
 constexpr int kNoScore = static_cast<int>(0x807fffffu);  // -infinity as an ordered integer
 constexpr float kLoScale = 28.0f;  // p_lo carries 28 times the residual (at most 16).  With 32, 2 and 1 in these places, the same
-                                   // error below, references moved more often: 112.4 against 108.0 us on 32 rows
+                                   // error below, references moved more often: 112.4 us on 32 rows
 
 template <int NR>
 struct Map {

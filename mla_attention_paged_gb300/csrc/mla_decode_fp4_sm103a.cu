@@ -905,7 +905,7 @@ cudaError_t launch_decode_partial_fp4(const DecodeParams& p, const CUtensorMap& 
   const int64_t most = static_cast<int64_t>(p.B) * p.max_splits;
   const bool more = p.split_major == 2 && p.num_splits > 0 && groups * (most - p.num_splits) > kMostEmpty;
   const int64_t listed = more ? std::min<int64_t>(p.num_splits, 0x7fffffff / groups) : most;
-  if (p.split_major == 2 && groups * listed > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (p.split_major == 2 && (groups * listed > 0x7fffffff || p.B > kThreads)) return cudaErrorInvalidConfiguration;
   cfg.gridDim = p.split_major == 2   ? dim3(static_cast<unsigned>(groups * listed))
                 : p.split_major == 1 ? dim3(groups, p.B, p.max_splits)
                                      : dim3(groups, p.max_splits, p.B);

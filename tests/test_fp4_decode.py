@@ -309,6 +309,34 @@ def test_rising_scores(mla):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H", [16, 32])
+@pytest.mark.parametrize("share", [0.5, 0.99, 0.0])
+@pytest.mark.parametrize("first", [0, 19999])
+def test_a_heavy_key_and_an_even_tail(mla, H, share, first):
+    """20000 keys of one score each and one key that takes `share` of the weight, first or last: the tail's weights are far
+    below the largest, where few of their bits are carried."""
+    n = 20001
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(n, 576, generator=g) / KV_SCALE
+    x[:, :16] = 0
+    x[:, 512:] = 0
+    if share:
+        x[first, :16] = 256.0
+    pages = -(-n // 64)
+    pool = fp4_rows.encode(torch.cat([x, torch.zeros(pages * 64 - n, 576)])).view(pages, 64, 336)
+    q = torch.zeros(1, 1, H, 576)
+    q[..., :16] = math.log(20000.0 * share / (1 - share)) / (SCALE * KV_SCALE * 256.0 * 16) if share else 0.0
+    q = q.bfloat16()
+    table = torch.arange(pages, dtype=torch.int32)[None]
+    plan = mla.decode_plan([n], 1, H, 64, pages, pages, mla.MLA_KV_FP4)
+    out, lse = call(mla, plan, q, pool, table, [n], None)
+    ref = reference(q, pool, table, [n], chain(1, 1))
+    check(out, lse, ref)
+    # random signs of the values: far inside the bound, which adds every key's error up
+    assert ((out.double().cpu() - ref[0]).abs() <= 2.0 ** -8 * ref[0].abs() + 2.0 ** -7 * ref[2]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,H,page", [(1, 16, 64), (2, 16, 8), (6, 40, 32)])
 def test_repeated_calls_agree_to_the_bit(mla, T, H, page):
     """Many row groups over the same pages (whose copies come back early from L2), 300 times."""

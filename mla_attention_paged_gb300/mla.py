@@ -128,18 +128,21 @@ def _check(code: int, what: str):
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def _stream_handle(stream):
     if stream is None:
+        if torch.cuda.is_initialized():
+            return _raw_stream(_current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 _POOL_DTYPE = {MLA_KV_BF16: (torch.bfloat16,), MLA_KV_E4M3: (torch.uint8, torch.float8_e4m3fn),
                MLA_KV_INT8: (torch.int8,), MLA_KV_INT8_PAGE: (torch.int8,), MLA_KV_FP4: (torch.uint8,)}
 FP4_ROW_BYTES = 336  # a latent row of a 4-bit pool (include/mla.h)
+_ROW_BYTES = {MLA_KV_BF16: 1152, MLA_KV_E4M3: 576, MLA_KV_INT8: 576, MLA_KV_INT8_PAGE: 576, MLA_KV_FP4: FP4_ROW_BYTES}
 
 
 def _refuse(what: str, why: str):
@@ -175,6 +178,13 @@ def _want_pool(what, kv_pages, kv_dtype):
     if dtype not in _POOL_DTYPE.get(kv_dtype, ()):
         _refuse(what, f"kv_pages is {dtype} for kv_dtype {kv_dtype}")
     return dev, _want(what, dev, "kv_pages", kv_pages, dtype), shape[0], shape[1]
+
+
+def _hold_pool(what, plan, kv_pages):
+    """A pool of another format would be read past its end, or as other rows."""
+    kind, bytes_ = plan.kv_dtype, kv_pages.numel() * kv_pages.element_size()
+    if bytes_ < plan.num_pages * plan.page_size * _ROW_BYTES.get(kind, 0) or (kv_pages.shape[-1] == FP4_ROW_BYTES) != (kind == MLA_KV_FP4):
+        _refuse(what, f"kv_pages is {kv_pages.dtype} {tuple(kv_pages.shape)}, not the plan's {plan.num_pages} pages of kv_dtype {kind}")
 
 
 def _want_workspace(what, dev, workspace):
@@ -243,6 +253,7 @@ def decode(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, page_table
            seq_lens: torch.Tensor, scale: float, kv_scale: float = 1.0, out=None, lse=None, workspace=None,
            stream=None):
     """mla_decode through the C ABI.  Returns (out [B,T,H,512] bf16, lse [B,T,H] fp32)."""
+    _hold_pool("mla_decode", plan, kv_pages)
     B, T, H, D = q.shape
     if out is None:
         out = torch.empty(B, T, H, 512, dtype=torch.bfloat16, device=q.device)
@@ -263,6 +274,7 @@ def decode_int8_paged(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor,
                       lse=None, workspace=None, stream=None):
     """mla_decode_int8_paged through the C ABI: an int8 pool with one fp32 scale per page
     (page_scales [num_pages] on the device).  Returns (out [B,T,H,512] bf16, lse [B,T,H] fp32)."""
+    _hold_pool("mla_decode_int8_paged", plan, kv_pages)
     B, T, H, D = q.shape
     if out is None:
         out = torch.empty(B, T, H, 512, dtype=torch.bfloat16, device=q.device)
@@ -283,6 +295,7 @@ def decode_partial(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, pa
                    workspace=None, stream=None):
     """mla_decode_partial through the C ABI (stage 1 of decode): returns (out, lse, workspace);
     multi-split requests are finished by decode_combine with the same out/lse/workspace."""
+    _hold_pool("mla_decode_partial", plan, kv_pages)
     B, T, H, D = q.shape
     if out is None:
         out = torch.empty(B, T, H, 512, dtype=torch.bfloat16, device=q.device)
@@ -314,6 +327,7 @@ def decode_noalloc(plan: DecodePlan, q: torch.Tensor, kv_pages: torch.Tensor, pa
                    seq_lens: torch.Tensor, scale: float, kv_scale: float = 1.0, out=None, lse=None, stream=None):
     """mla_decode_noalloc through the C ABI: decode with the split-KV scratch in the
     library's fixed 32 MiB device buffer instead of a workspace.  Returns (out, lse)."""
+    _hold_pool("mla_decode_noalloc", plan, kv_pages)
     B, T, H, D = q.shape
     if out is None:
         out = torch.empty(B, T, H, 512, dtype=torch.bfloat16, device=q.device)

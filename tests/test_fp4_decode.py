@@ -95,6 +95,20 @@ def test_binding_refuses_other_pools(mla, shape, dtype):
     assert e.value.code == mla.MLA_ERR_INVALID_ARG
 
 
+def test_binding_refuses_pools_of_another_size(mla):
+    """A pool of 8-bit rows under a 4-bit plan, one of 4-bit rows under another, and one of too few pages."""
+    i = torch.zeros(2, dtype=torch.int32)
+    q = torch.zeros(2, 4, 16, 576).bfloat16()
+    fp4, e4m3 = (torch.zeros(400, 64, n, dtype=torch.uint8) for n in (336, 576))
+    plan = _plan(mla)
+    other = mla.decode_plan([9000, 300], 4, 16, 64, 200, 400, mla.MLA_KV_E4M3, 152)
+    for call in (mla.decode, mla.decode_partial, mla.decode_noalloc):
+        for p, pool in ((plan, e4m3), (plan, fp4[:399]), (other, fp4), (other, e4m3[:399])):
+            with pytest.raises(mla.MlaError) as e:
+                call(p, q, pool, i, i, SCALE)
+            assert e.value.code == mla.MLA_ERR_INVALID_ARG
+
+
 # ------------------------------------------------------------------------------ reference
 def chain(B, T):
     """Drafts in order, as a tree's words."""

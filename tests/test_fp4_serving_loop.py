@@ -213,3 +213,47 @@ def test_a_step_in_one_graph(mla):
         assert all(torch.equal(a, b) for a, b in zip(*results))
         assert int(count) == 2 and int(live) == L // page + 2 and torch.isfinite(lse).all()
     assert mla.get_status() == mla.MLA_OK
+
+
+def test_calls_on_two_streams_at_once(mla):
+    """Attention over one pool on two streams, each with its workspace, while a third forks, frees and compacts another cache:
+    the same bytes as one after the other."""
+    from test_fp4_decode import make
+    from test_pages import Cache
+    calls = []
+    for seed, (lens, T_, H_) in enumerate((([5000, 777, 64], 1, 16), ([3000, 2500], 3, 16))):
+        q, pool, table = make(lens, T_, H_, 16, seed)
+        plan = mla.decode_plan(lens, T_, H_, 16, table.shape[1], pool.shape[0], mla.MLA_KV_FP4)
+        args = (plan, q.to(D), pool.to(D), table.to(D), ints(lens), SCALE, KV_SCALE)
+        calls.append((args, mla.workspace_for(plan, D), mla.decode(*args)))
+    c = Cache(7, [100, 333, 64, 7], 16, spare=12, slots=8)
+    start = [t.cuda() for t in (c.pool, c.table, c.lens, c.refs)]
+    now = [t.clone() for t in start]
+    new, freed, n = ints(c.unused[:2]), torch.zeros_like(now[3]), ints([0])
+    pages_ws, live = mla.page_compact_workspace_for(len(c.refs), D), ints([0])
+    p, ch, sl, keep = ints([1, 3]), ints([4, 5]), ints([1, 5]), ints([160, 2])
+    want = None
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for i in range(30):
+        got = []
+        for s, (args, ws, _) in zip(streams, calls):
+            with torch.cuda.stream(s):
+                got.append(mla.decode(*args, workspace=ws))
+        with torch.cuda.stream(streams[2]):
+            for t, v in zip(now, start):
+                t.copy_(v)
+            mla.page_fork(now[0], now[1], now[2], now[3], p, ch, new, mla.MLA_KV_FP4)
+            mla.page_free(now[1], now[2], now[3], sl, keep, 16, freed, n)
+            mla.page_compact(now[0], now[1], now[2], now[3], mla.MLA_KV_FP4, live, pages_ws)
+        torch.cuda.synchronize()
+        for (out, lse), (_, _, ref) in zip(got, calls):
+            assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+        if want is None:
+            assert not c.fork([1, 3], [4, 5], c.unused[:2])
+            want, bad = c.free([1, 5], [160, 2])
+            assert not bad and c.compact() == (int(live), False)
+        assert freed[:int(n)].tolist() == want
+        for t, v in zip(now, (c.pool, c.table, c.lens, c.refs)):
+            assert torch.equal(t.cpu(), v)
+    assert mla.get_status() == mla.MLA_OK

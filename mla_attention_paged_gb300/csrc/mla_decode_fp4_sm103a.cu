@@ -539,7 +539,8 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctrl->k_full[0]);
             if (j >= 1) ok = mbar_wait(&ctrl->k_free[1], (j - 1) & 1, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            ok = __all_sync(0xffffffffu, ok);  // (what follows the loop asks it again)
+            if (!ok) break;
             tc_fence_after();
           }
         }

@@ -135,7 +135,8 @@ int mla_kv_gather(const void* kv_pages, int64_t num_pages, int page_size, int kv
   if (!kv_pages || !page_table || !cu_rows || !out) return MLA_ERR_INVALID_ARG;
   if (!aligned(kv_pages, 16) || !aligned(page_scales, 4) || !aligned(page_table, 4) || !aligned(cu_rows, 4) || !aligned(out, 16))
     return MLA_ERR_INVALID_ARG;
-  if (out_row_stride < kLatentDim || out_row_stride % 8 != 0 || !(kv_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  if (out_row_stride < kLatentDim || out_row_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_INT8_PAGE && !(kv_scale > 0.f)) return MLA_ERR_INVALID_ARG;
   // rows are written while others of the pool, and lengths, are still to be read
   const size_t span = (static_cast<size_t>(total_rows - 1) * out_row_stride + kLatentDim) * 2;
   if (overlap(kv_pages, static_cast<size_t>(num_pages) * page_size * kv_row_bytes(kv_dtype), out, span) ||

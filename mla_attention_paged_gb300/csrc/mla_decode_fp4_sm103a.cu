@@ -14,11 +14,20 @@
 //    memory.
 //  * BMM2: O^T[value column, row] += V^T P^T, A = V^T, MN-major out of shared memory, B = the weights,
 //    P 2^6 split into p_hi = e4m3(P) and p_lo = e4m3(28 (P - p_hi)), stacked as 2 x NR columns so that V
-//    is read once; the epilogue adds O_hi + O_lo / 28.  (P 2^6 <= 2^8.8 < 448, its residual at most 16: kept to 2^-9
-//    relative down to 2^-11 of the largest weight and to 2^-20 of it below.)
-//  * A key is one thread's in the softmax, so a row's sum is kept per thread and its running maximum
-//    moves only when some score exceeds it by more than 2.8 (log2): ordinary tiles reduce nothing across
-//    threads but one vote.
+//    is read once; the epilogue adds O_hi + O_lo / 28.  (P 2^6 <= 448, its residual at most 16: kept to 2^-9
+//    relative where P 2^6 >= 2^-6, to 2^-14.8 absolute below.)
+//  * A key is one thread's in the softmax, so a row's sum is kept per thread and its reference, which takes the
+//    place of a running maximum, moves only when some score exceeds it by more than 2.8 (log2): ordinary tiles
+//    reduce nothing across threads but one vote and a word of marks.
+//  * A reference also goes down.  Behind a key that dominates its row (an attention sink) every other weight would
+//    fall below what hi + lo hold: of 20000 even keys behind one of 99 % nothing or twice their weight was left, by
+//    chance.  O and the sums are fp32 and have room above: where no weight of a whole tile reaches 2^-2, the row's
+//    reference is lowered by 2^8 and what it has accumulated multiplied by as much.  Warps mark such rows after their
+//    weights are written, read all marks after the next vote and move at the tile after it, so no wait is added: two tiles
+//    go by.  A first key that stands alone in its tile, or one 2^8 above the reference, gets 448 and the keys beside
+//    it the whole range below.  (16 requests of 8K-131K keys: 99.2 -> 100.8 us at 32 rows of flat scores, 86.0 -> 89.5
+//    at 16.  Deciding in the same tile took 104.7 and 91.5; a vote on each warp's own marks 132 at 32 rows of normal scores,
+//    111 here.)
 // One CTA per (group of NR rows, split, request), 128 keys a tile, 576 threads: softmax warps 0-7 (32 keys
 // and half of the rows each), decoding warps 8-15 (32 keys and half of the columns each; a row's codes go
 // to registers at once and free their stage), producer 16 (boxes of up to 64 rows), MMA 17.
@@ -27,8 +36,8 @@
 // each, V in 0.5k, V and P as BMM2's operands 0.6-0.8k, queries 0.15-0.3k, P.  One thread issues 52 small products beside
 // four busy warps for 2.1k of the 2.9k (1.4k alone on an SM), decoding takes half the integer pipe, and one or two tiles fit
 // in tensor memory to overlap them.
-// 16 requests of 8K-131K keys (375 MB, 55 us of bytes): 87 us at 16 rows; at 32 rows 108.7, of which 9 are references that
-// move (99.3 with scores that move none): the next tile then waits for BMM2 of the last.
+// 16 requests of 8K-131K keys (375 MB, 55 us of bytes): 90 us at 16 rows; at 32 rows 111, of which 10 are references that
+// move (101 with scores that move none): the next tile then waits for BMM2 of the last.
 // Every wait is bounded; on expiry the CTA records a timeout, drains its copies and MMAs, frees tensor
 // memory and returns.
 #include <cuda_fp16.h>
@@ -67,7 +76,12 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kPShift = 6.0f;    // P is formed times 2^6 ...
 constexpr float kThreshold = 2.8f; // ... and at most 2^8.8: the reference moves when a score exceeds it by more than this,
 constexpr float kMargin = 0.6780719f;  // to so much above the score, whose weight is then 40, an e4m3 number: a weight that
-                                   // dominates its row has no error (half a step of p_lo is 2^-20.1 of the largest weight)
+                                   // dominates its row has no error
+constexpr float kFar = 8.f;        // A first key, or one so far above the reference, whose weight may be all that counts of its
+constexpr float kFarMargin = -2.8073549f;  // tile, gets 448, the largest weight: the keys beside it keep the most bits
+constexpr float kDrop = 8.f;       // A reference goes down so far where a tile's largest weight is at most 2^-2 ...
+constexpr float kDropFactor = 256.f;
+constexpr float kDepth = 40.f;     // ... until it is this far below the highest that it has been
 constexpr int kNoScore = static_cast<int>(0x807fffffu);  // -infinity as an ordered integer
 constexpr float kLoScale = 28.0f;  // p_lo carries 28 times the residual (at most 16).  With 32, 2 and 1 in these places, the same
                                    // error below, references moved more often: 112.4 us on 32 rows
@@ -117,6 +131,8 @@ struct Ctrl {
   alignas(16) float off[kSoftmaxWarps][kMaxRows];  // kPShift - reference maximum, a copy for each warp
   alignas(16) int top[3][kMaxRows];   // largest score (ordered as an integer) of the rows that outgrew their reference, by
                                       // tile: written before a tile's vote, read after it, cleared after the next one
+  alignas(16) uint32_t low[2][kSoftmaxWarps];  // rows (row_mark) of which a warp's keys all weigh less than 2^-2, by tile parity
+  alignas(16) uint32_t alone[kSoftmaxWarps];   // and where first keys are
   alignas(16) float row_scale[kMaxRows];
   alignas(16) float lse[kMaxRows];
   alignas(16) int lim[kMaxRows];      // last key that the row sees; -1: none
@@ -238,6 +254,18 @@ __device__ __forceinline__ void find_split(const DecodeParams& p, int item, bool
   if ((rest >> lane & 1) && item - wholes == rest_at) ctrl->item[0] = t, ctrl->item[1] = whole, ctrl->item[2] = L;
   if (t == 0) ctrl->item[3] = wholes + rests;
   __syncthreads();
+}
+
+// Where a warp's marks hold its row r.
+__device__ __forceinline__ uint32_t row_mark(int r) { return 0x80u << 8 * (r & 3) >> (r >> 2); }
+
+// The rows of which no lane has a weight of 2^-2 or more: hi4 holds their e4m3 codes, four rows a word.
+template <int N>
+__device__ __forceinline__ uint32_t low_rows(const uint32_t (&hi4)[N]) {
+  uint32_t some = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) some |= ((hi4[k] + 0x58585858u) & 0x80808080u) >> k;  // (0x28 is the code of 2^-2, 0x7F the largest)
+  return ~__reduce_or_sync(0xffffffffu, some);
 }
 
 template <int NR>
@@ -595,6 +623,13 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
     const uint32_t p_lo = smem_u32(smem + M::kOffP) + key_in * 2 * NR + (static_cast<uint32_t>(NR + r0) ^ p_sw);
     bool failed = !mbar_wait(&ctrl->q_ready, 0, abort_flag);  // (the rows' factors and limits)
     float m = -INFINITY;  // reference maximum (log2 of the scaled score) of row `lane`, the same in every warp
+    float peak = -INFINITY;  // the largest it has been
+    uint32_t may_sink = 0;   // marks of this warp's rows whose reference may go down
+    const int half = lane < RW ? 0 : 1;  // of the rows
+    const uint32_t mark = lane < NR ? row_mark(lane % RW) : 0u;
+    const auto marks = [&](bool of_row) { return __reduce_or_sync(0xffffffffu, half == r0 / RW && of_row ? mark : 0u); };
+    if (lane == 0) ctrl->low[1][warp] = 0;
+    uint32_t sunk = 0;       // rows whose reference goes down at the next tile
     int third = 0;        // j % 3
     for (int j = 0; j < ntiles; ++j) {
       const int sb = j & 1;
@@ -604,6 +639,16 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
       bool fail = failed || !mbar_wait(&ctrl->s_full[sb], (j >> 1) & 1, abort_flag);
       fail = __any_sync(0xffffffffu, fail);
       float x[RW];
+      float alpha = 1.f;
+      if (sunk != 0) {
+        if ((sunk >> lane) & 1) {
+          m -= kDrop;
+          alpha = kDropFactor;
+          ctrl->off[warp][lane] = kPShift - m;
+        }
+        may_sink = marks(m > peak - kDepth);
+        __syncwarp();
+      }
       auto sees = [&](int r) -> bool {  // (r within the group)
         if (key >= kv_end) return false;
         if (!kTree) return key <= ctrl->lim[r];
@@ -628,6 +673,23 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
             if (!sees(r0 + r)) x[r] = -INFINITY;
         }
       };
+      // every row's largest score here into top[third]: all rows at once, by halves (0.2 us where a reduction for each row that
+      // needs it took 1.0 for the first tile's 16)
+      auto tops = [&]() {
+        uint32_t s[RW];
+        load_s<RW>(s_addr, s);
+        float top_of[RW];
+#pragma unroll
+        for (int r = 0; r < RW; r += 4) {
+          const float4 mu = *reinterpret_cast<const float4*>(&ctrl->mult[r0 + r]);
+          top_of[r] = x[r] == -INFINITY ? -INFINITY : __uint_as_float(s[r]) * mu.x;
+          top_of[r + 1] = x[r + 1] == -INFINITY ? -INFINITY : __uint_as_float(s[r + 1]) * mu.y;
+          top_of[r + 2] = x[r + 2] == -INFINITY ? -INFINITY : __uint_as_float(s[r + 2]) * mu.z;
+          top_of[r + 3] = x[r + 3] == -INFINITY ? -INFINITY : __uint_as_float(s[r + 3]) * mu.w;
+        }
+        const int i = __float_as_int(lanes_reduce<RW, true>(top_of, lane));
+        if (lane % (32 / RW) == 0) atomicMax(&ctrl->top[third][r0 + lane / (32 / RW)], i ^ ((i >> 31) & 0x7fffffff));
+      };
       bool over = false;  // (warp-uniform) some row outgrew its reference here
       if (!fail) {
         tc_fence_after();
@@ -637,48 +699,65 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
         for (int r = 0; r < RW; ++r) top = fmaxf(top, x[r]);
         over = __any_sync(0xffffffffu, top > kPShift + kThreshold);
         if (over) {
-          // (all rows' largest scores at once, by halves: 0.2 us where a reduction for each row that needs it took 1.0 for
-          // the first tile's 16)
-          uint32_t s[RW];
-          load_s<RW>(s_addr, s);
-          float top_of[RW];
-#pragma unroll
-          for (int r = 0; r < RW; r += 4) {
-            const float4 mu = *reinterpret_cast<const float4*>(&ctrl->mult[r0 + r]);
-            top_of[r] = x[r] == -INFINITY ? -INFINITY : __uint_as_float(s[r]) * mu.x;
-            top_of[r + 1] = x[r + 1] == -INFINITY ? -INFINITY : __uint_as_float(s[r + 1]) * mu.y;
-            top_of[r + 2] = x[r + 2] == -INFINITY ? -INFINITY : __uint_as_float(s[r + 2]) * mu.z;
-            top_of[r + 3] = x[r + 3] == -INFINITY ? -INFINITY : __uint_as_float(s[r + 3]) * mu.w;
-          }
-          const int i = __float_as_int(lanes_reduce<RW, true>(top_of, lane));
-          if (lane % (32 / RW) == 0) atomicMax(&ctrl->top[third][r0 + lane / (32 / RW)], i ^ ((i >> 31) & 0x7fffffff));
+          tops();
         }
       }
       // one vote a tile; ordinary tiles reduce nothing else across threads
-      float alpha = 1.f;
-      uint32_t moved = 0;
+      uint32_t moved = sunk;
       if (bar_or(1, kSoftmaxThreads, fail || over || *abort_flag != 0)) {
         if (bar_or(1, kSoftmaxThreads, fail || *abort_flag != 0)) {
           failed = true;
           break;
         }
         // ---------------------------------------------------------------- some rows' references move
+        bool first = false;  // the row's first keys
         if (lane < NR) {
           int i = ctrl->top[third][lane];
           i ^= (i >> 31) & 0x7fffffff;
           const float best = __int_as_float(i);
-          if (m == -INFINITY) {
-            m = best + kMargin;
-          } else if (best > m) {  // (where one row has to move, those that need not yet go along: 114.0 -> 112.4 us)
-            alpha = ex2_approx(m - best - kMargin);
-            m = best + kMargin;
-          }
+          float to = m;
+          first = m == -INFINITY && best != -INFINITY;
+          if (m == -INFINITY)
+            to = best + kMargin;
+          else if (best > m)  // (where one row has to move, those that need not yet go along: 114.0 -> 112.4 us)
+            to = best + (best > m + kFar ? kFarMargin : kMargin);
+          if (m != -INFINITY && to != m) alpha *= ex2_approx(m - to);
+          m = to;
+          peak = fmaxf(peak, m);
           if (i != __float_as_int(-INFINITY)) ctrl->off[warp][lane] = kPShift - m;
         }
         moved = __ballot_sync(0xffffffffu, alpha != 1.f);
         __syncwarp();
         scores();
+        // First keys of which one stands alone: so far above 32 others, one warp's, that its weight may go up to the largest
+        const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+        if (firsts != 0) {  // (the same in all warps)
+          uint32_t far = 0, seen = 0;
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            far |= x[r] >= -2.f ? row_mark(r) : 0u;
+            seen |= x[r] != -INFINITY ? row_mark(r) : 0u;  // (keys that a row does not see leave none alone)
+          }
+          far = __reduce_or_sync(0xffffffffu, far), seen = __reduce_or_sync(0xffffffffu, seen);
+          if (lane == 0) ctrl->alone[warp] = seen & ~far;
+          named_bar_sync(1, kSoftmaxThreads);
+          const uint4 by = *reinterpret_cast<const uint4*>(&ctrl->alone[4 * half]);
+          const bool alone = first && ((by.x | by.y | by.z | by.w) & mark) != 0;
+          if (__any_sync(0xffffffffu, alone)) {  // (the same in all warps)
+            if (alone) {
+              m += kFarMargin - kMargin;
+              peak = m;
+              ctrl->off[warp][lane] = kPShift - m;
+            }
+            __syncwarp();
+            scores();
+          }
+        }
+        may_sink = marks(m > peak - kDepth);
       }
+      // Rows that lay far below their reference throughout the last tile (all warps' marks are there since the vote, and all warps
+      // find the same): it goes down, for the next tile.
+      const uint4 low_by = *reinterpret_cast<const uint4*>(&ctrl->low[sb ^ 1][4 * half]);
       if (warp == 0 && lane < NR) ctrl->top[third == 0 ? 2 : third - 1][lane] = kNoScore;  // (the last tile's: all have read it)
       third = third == 2 ? 0 : third + 1;
       tc_fence_before();
@@ -738,6 +817,10 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->p_full[sb]);
+      uint32_t low = low_rows(hi4) & may_sink;
+      if (edge && !kTree) low &= marks(ctrl->lim[lane % NR] >= k0);  // (rows that see none of these keys stay)
+      if (lane == 0) ctrl->low[sb][warp] = low;
+      sunk = __ballot_sync(0xffffffffu, (low_by.x & low_by.y & low_by.z & low_by.w & mark) != 0) & ~moved;
     }
     const float ls = lanes_reduce<RW>(l_sum, lane);
     if (lane % (32 / RW) == 0) ctrl->sums[quad][r0 + lane / (32 / RW)] = ls;

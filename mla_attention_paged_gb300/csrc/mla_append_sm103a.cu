@@ -36,6 +36,7 @@ constexpr int kManySteps = 2;
 constexpr int kManySteps64 = 4;  // heads of the 64 rotated columns alone: 128 bytes a step
 constexpr int kManyKeyLanes = 16;
 constexpr int64_t kFewRows = 12288;
+constexpr int64_t kOneWave = 152 * 28;  // warps of two steps: seven CTAs an SM
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -348,12 +349,18 @@ cudaError_t launch_chunks(const AppendParams& p, cudaStream_t stream) {
   // 2.6 / 3.1, 6.1 / 5.3; 8 heads of 576 normed 7.9 / 6.9, 10.7 / 8.9, 13.0 / 11.2, 36.7 / 27.4.  (Wide
   // rows cross at about 9000, 64 columns at about 20000: one border between them for all.)
   const bool few = static_cast<int64_t>(p.tokens) * (p.heads > 0 ? p.heads : 16) <= kFewRows;
-  // (rows of 64 columns alone: 8191 tokens of 16 heads with their keys 10.7 us at two steps, five CTAs; 9.3 at four steps,
-  // six CTAs; into 4-bit rows 13.7 and 11.5)
-  const bool four = kChunks == 0 && p.heads > 4 * kManySteps;
-  const int steps = few ? 1 : four ? kManySteps64 : kManySteps, key_rows = few ? 1 : 32 / kManyKeyLanes;
-  const int per_token = (p.heads + 4 * steps - 1) / (4 * steps);
+  const int key_rows = few ? 1 : 32 / kManyKeyLanes;
   const int64_t k_warps = p.kv_in ? (p.tokens + key_rows - 1) / key_rows : 0;
+  // Rows of 64 columns alone take four steps where two would be more than one wave of warps, and where four leave no more
+  // places of a token's last warp idle.  GPU us at two steps / four: 16 heads 1.96 / 2.07 at 1125 tokens, 2.33 / 2.32 at 1875,
+  // 2.34 / 2.38 at 2125, 2.82 / 2.38 at 2375, 6.0 / 5.1 at 8192; 9 heads 2.07 / 2.08 at 2000, 2.68 / 2.17 at 2444; 20 heads
+  // (24 places or 32) 2.33 / 2.46 at 1300, 3.89 / 3.82 at 3000; 16 heads with their keys 2.98 / 2.98 at 1625 tokens, 3.13 /
+  // 3.06 at 1875, 8.6 / 7.7 at 8192.
+  const int warps2 = (p.heads + 4 * kManySteps - 1) / (4 * kManySteps), warps4 = (p.heads + 4 * kManySteps64 - 1) / (4 * kManySteps64);
+  const bool four = kChunks == 0 && p.heads > 4 * kManySteps && warps4 * kManySteps64 == warps2 * kManySteps &&
+                    k_warps + static_cast<int64_t>(p.tokens) * warps2 > kOneWave;
+  const int steps = few ? 1 : four ? kManySteps64 : kManySteps;
+  const int per_token = (p.heads + 4 * steps - 1) / (4 * steps);
   const int64_t warps = k_warps + static_cast<int64_t>(p.tokens) * per_token;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps));

@@ -333,7 +333,8 @@ int mla_prefill_paged(const void* q, const void* k_pages, const void* v_pages, c
  *          to fp32); 16 columns whose largest |y| is t take the smallest exponent e of 0..11 with t <= 7 2^(e-5), and
  *          the nearest code of y 2^(5-e) (ties to the even code; saturated to +-6; a NaN encodes as 0); the rotated columns
  *          are e4m3 codes.  Here the mean is that of the exact squares, rounded once to fp32, and no product is fused
- *          with a sum, so that the codes are those of the formula to the bit.
+ *          with a sum, so that the codes are those of the formula to the bit.  (With kv_weight one NaN or infinity among the 512
+ *          columns leaves nothing of the others: 512 zeros in a 4-bit or int8 row, which nothing reports.)
  *   query: v = q_in[n, h, :q_dim]; v' = v / sqrt(mean(v^2) + eps) * q_weight over the whole width
  *          (q_weight NULL: v' = v); q_out[n, h] = [v'[:q_dim-64], rot(v'[q_dim-64:], x)].
  *   rot  : pair i of 32 is columns (2i, 2i+1) (interleaved != 0) or (i, i+32); (a, b) becomes
@@ -427,7 +428,8 @@ int mla_key_mass(const mla_decode_plan_t* plan, const void* q, const void* kv_pa
  *   kept[b, i] = kept[i], mass_out[b, i] = mass[b, kept[i]], new_lens[b] = K
  * Entries of kept and mass_out from K on, and pool rows that are no destination, are left as they
  * were.  Rows are copied because a source page may be a prefix that other requests share; the
- * caller releases the old pages.  Keys keep the rotation of their old positions.
+ * caller releases the old pages.  Keys keep the rotation of their old positions.  (mla_key_mass does not take a 4-bit
+ * pool: masses of its keys are the caller's own.)
  *   kv_pages       : [num_pages, page_size] rows of kv_dtype (bf16, e4m3, int8 or 4-bit).
  *   page_table     : [batch, max_pages_per_seq] int32 source pages.
  *   seq_lens, keep_lens : [batch] int32 (device).
@@ -483,7 +485,8 @@ int mla_kv_evict(void* kv_pages, int64_t num_pages, int page_size, int kv_dtype,
  *
  * mla_page_compact: pages with a count move so that they are 0 .. *num_live - 1: the k-th free page below *num_live
  * takes the k-th counted page from *num_live on.  Rows, counts, page scales and the tables of all slots follow; free pages
- * keep their rows.
+ * keep their rows.  Entries from a slot's length on are not rewritten, although a page there that has a count may move: pages are
+ * taken ahead of the length after this call, not before.
  *   num_live  : int32.
  *   workspace : of the size mla_page_compact_workspace gives, 256-byte aligned; overwritten; calls that share one are
  *               stream-ordered.  MLA_ERR_WORKSPACE_TOO_SMALL.

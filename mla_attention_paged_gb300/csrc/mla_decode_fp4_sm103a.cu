@@ -71,7 +71,8 @@ constexpr int kMaxFull = 6;
 constexpr int kMaxRows = 32;
 constexpr int kCtrlBytes = 4096;
 constexpr int kAbortTimeout = 1;
-constexpr int64_t kMostEmpty = 304;  // CTAs without a split that a grid may have: two for each SM
+constexpr int64_t kMostEmpty = 304;  // CTAs without a split that a grid may have: two for each of the GPU's 152 SMs, however
+                                     // many of them the plan was made for
 constexpr uint32_t kTmemCols = 512;
 constexpr float kPShift = 6.0f;    // P is formed times 2^6 ...
 constexpr float kThreshold = 2.8f; // ... and at most 2^8.8: the reference moves when a score exceeds it by more than this,
@@ -272,7 +273,6 @@ template <int NR>
 __device__ __forceinline__ void load_s(uint32_t addr, uint32_t (&s)[NR]) {
   if constexpr (NR == 8) tmem_ld8(addr, s);
   if constexpr (NR == 16) tmem_ld16(addr, s);
-  if constexpr (NR == 32) tmem_ld32(addr, s);
   tmem_ld_wait();
 }
 
@@ -314,7 +314,7 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
   bool worker_failed = false;
 
   if (warp == kProducerWarp) {
-    // ------------------------------------------------------------------ producer: raw rows, 32 keys a stage
+    // ------------------------------------------------------------------ producer: raw rows, 64 keys a stage
     const int lg = __ffs(p.page_size) - 1;          // (a power of two)
     const int per = max(1, kSub >> lg);             // pages per stage
     const int box_bytes = min(p.page_size, kSub) * kFp4RowBytes;

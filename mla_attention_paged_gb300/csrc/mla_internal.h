@@ -41,7 +41,7 @@ struct DecodeParams {
   int page_size, max_pages;     // page geometry and page_table row stride
   int chunk, max_splits, max_seq;
   int num_splits;               // split_major 2: of the planned lengths, all requests (0: not known)
-  int split_major;              // grid (groups, B, splits) when set, else (groups, splits, B)
+  int split_major;              // grid: 1 (groups, B, splits), 0 (groups, splits, B), 2 a list of (split, group), kKvFp4 only
   int kv_dtype;                 // kKvBf16, kKvE4m3, kKvInt8, kKvInt8Page or kKvFp4
   int64_t num_pages;            // pages in the pool: a page id outside [0, num_pages) is reported
   float scale_log2;             // softmax scale * log2(e) (* kv_scale for an 8-bit pool)
@@ -49,12 +49,12 @@ struct DecodeParams {
   const int32_t* page_table;
   const int32_t* seq_lens;
   const __nv_bfloat16* q;       // [B, T, H, 576] (kKvFp4; the others read it through a tensor map)
-  const uint8_t* kv_pool;       // pool base (the int8 and 4-bit paths read raw rows from here)
+  const uint8_t* kv_pool;       // pool base (the int8 path reads raw rows from here)
   const float* page_scales;     // kKvInt8Page: [num_pages] scale of each page's codes
   float inv_ref_scale;          // kKvInt8Page: 1 / kv_scale (page scales are applied relative to it)
   __nv_bfloat16* out;           // [B, T, H, 512]
   float* lse;                   // [B, T, H]
-  __nv_bfloat16* ws_o;          // [B, max_splits, R, 512] partial outputs (normalised, bf16)
+  __nv_bfloat16* ws_o;          // [B, max_splits, R, 512] partial outputs (normalised, bf16; kKvFp4: f16 in units of the codes)
   float* ws_lse;                // [B, max_splits, R] partial log-sum-exp (natural log)
   float* part_scale;            // kKvFp4: v_scale for the combine, left by the partial kernel in the workspace's
                                 // first bytes (a combine on its own is not given kv_scale); else null

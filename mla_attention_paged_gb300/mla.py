@@ -181,7 +181,8 @@ def _want_pool(what, kv_pages, kv_dtype):
 
 
 def _hold_pool(what, plan, kv_pages):
-    """A pool of another format would be read past its end, or as other rows."""
+    """The tensor holds all of the plan's num_pages pages in its format, as the header asks: of another format it would be
+    read as other rows, and with fewer bytes past its end."""
     kind, bytes_ = plan.kv_dtype, kv_pages.numel() * kv_pages.element_size()
     if bytes_ < plan.num_pages * plan.page_size * _ROW_BYTES.get(kind, 0) or (kv_pages.shape[-1] == FP4_ROW_BYTES) != (kind == MLA_KV_FP4):
         _refuse(what, f"kv_pages is {kv_pages.dtype} {tuple(kv_pages.shape)}, not the plan's {plan.num_pages} pages of kv_dtype {kind}")

@@ -31,10 +31,10 @@
 // One CTA per (group of NR rows, split, request), 128 keys a tile, 576 threads: softmax warps 0-7 (32 keys
 // and half of the rows each), decoding warps 8-15 (32 keys and half of the columns each; a row's codes go
 // to registers at once and free their stage), producer 16 (boxes of up to 64 rows), MMA 17.
-// What bounds it: shared memory, and a tile's chain of decoding, BMM1, softmax and BMM2.  A tile takes 2.5k cycles at 16 rows
-// and 2.9k at 32 (its 43 KB 1.85k at the copy rate), of which shared memory is busy 2.0k and 2.4k: rows in and out 0.34k
+// What bounds it: shared memory, and a tile's chain of decoding, BMM1, softmax and BMM2.  A tile takes 2.6k cycles at 16 rows
+// and 2.95k at 32 (its 43 KB 1.85k at the copy rate), of which shared memory is busy 2.0k and 2.4k: rows in and out 0.34k
 // each, V in 0.5k, V and P as BMM2's operands 0.6-0.8k, queries 0.15-0.3k, P.  One thread issues 52 small products beside
-// four busy warps for 2.1k of the 2.9k (1.4k alone on an SM), decoding takes half the integer pipe, and one or two tiles fit
+// four busy warps for 2.1k of the 2.95k (1.4k alone on an SM), decoding takes half the integer pipe, and one or two tiles fit
 // in tensor memory to overlap them.
 // 16 requests of 8K-131K keys (375 MB, 55 us of bytes): 90 us at 16 rows; at 32 rows 111, of which 10 are references that
 // move (101 with scores that move none): the next tile then waits for BMM2 of the last.

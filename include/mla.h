@@ -145,9 +145,10 @@ int mla_decode_plan(int batch, const int32_t* seq_lens_host, int q_len, int num_
  *   scale      : softmax scale applied to q . k.
  *   kv_scale   : per-tensor dequantisation scale of an 8-bit or 4-bit pool (ignored for bf16).
  *                (Over a 4-bit pool a query element is exact down to 2^-9 of its row's largest and taken to 2^-17 of that
- *                below.  A key's weight is carried to 2^-9 of itself, or to 2^-12 of its row's largest among the 128 keys
- *                of its tile where that is more (tiles begin at multiples of 128).  Beside a key that stands far above all
- *                others of its tile, and in the two tiles behind it, weights are carried to 2^-20 of that key's.)
+ *                below.  A key's weight is carried to 2^-9 of itself or, where that is more, to the lesser of 2^-20 of its
+ *                row's largest and 2^-9 of its row's largest among the 128 keys of its tile (tiles begin at multiples of
+ *                128); beside a key far above all others of its tile and in the three tiles behind it, up to nine where such
+ *                keys come again and again, to 2^-20 of that key's.)
  *   out        : [B, T, H, 512] bf16, out[b,t,h] = sum_j softmax_j(scale q.k_j) v_j with
  *                draft t seeing keys 0 .. L_b - T + t and v_j = k_j[:512].
  *   lse        : [B, T, H] fp32, natural-log log-sum-exp of the scaled scores.

@@ -21,13 +21,17 @@
 //    reduce nothing across threads but one vote and a word of marks.
 //  * A reference also goes down.  Behind a key that dominates its row (an attention sink) every other weight would
 //    fall below what hi + lo hold: of 20000 even keys behind one of 99 % nothing or twice their weight was left, by
-//    chance.  O and the sums are fp32 and have room above: where no weight of a whole tile reaches 2^-2, the row's
+//    chance.  O and the sums are fp32 and have room above: where no weight reaches 2^-5 in two tiles on end, the row's
 //    reference is lowered by 2^8 and what it has accumulated multiplied by as much.  Warps mark such rows after their
-//    weights are written, read all marks after the next vote and move at the tile after it, so no wait is added: two tiles
-//    go by.  A first key that stands alone in its tile, or one 2^8 above the reference, gets 448 and the keys beside
-//    it the whole range below.  (16 requests of 8K-131K keys: 99.2 -> 100.8 us at 32 rows of flat scores, 86.0 -> 89.5
+//    weights are written, read all marks after the next vote and move at the tile after it, so no wait is added: three
+//    tiles go by.  A first key that stands alone in its tile, or one 2^8 above the reference, gets 448 and the keys beside
+//    it the whole range below.  (16 requests of 8K-131K keys: 99.2 -> 101.0 us at 32 rows of flat scores, 86.0 -> 89.9
 //    at 16.  Deciding in the same tile took 104.7 and 91.5; a vote on each warp's own marks 132 at 32 rows of normal scores,
 //    111 here.)
+//    Very uneven scores lower references that soon rise again, two waits for BMM2 where there was one: with deviations
+//    of 2.6, 3.5 and 5.2 (nats) 32 rows take 119.6, 125.3 and 144.9 us, without 115.5, 118.3 and 122.6.  So a row that
+//    has risen again waits for twice as many low tiles, up to eight.  (2^-5 is the least that leaves hi normal; lowered
+//    from 2^-2, after one tile, 128, 143 and 158.)
 // One CTA per (group of NR rows, split, request), 128 keys a tile, 576 threads: softmax warps 0-7 (32 keys
 // and half of the rows each), decoding warps 8-15 (32 keys and half of the columns each; a row's codes go
 // to registers at once and free their stage), producer 16 (boxes of up to 64 rows), MMA 17.
@@ -80,8 +84,10 @@ constexpr float kMargin = 0.6780719f;  // to so much above the score, whose weig
                                    // dominates its row has no error
 constexpr float kFar = 8.f;        // A first key, or one so far above the reference, whose weight may be all that counts of its
 constexpr float kFarMargin = -2.8073549f;  // tile, gets 448, the largest weight: the keys beside it keep the most bits
-constexpr float kDrop = 8.f;       // A reference goes down so far where a tile's largest weight is at most 2^-2 ...
+constexpr uint32_t kLowCodes = 0x70707070u;  // brings the e4m3 code of 2^-5, 0x10, to a byte's top bit, and of 448 not past it
+constexpr float kDrop = 8.f;       // a reference goes down so far where a row's tiles weigh less than 2^-5 ...
 constexpr float kDropFactor = 256.f;
+constexpr int kLowTiles = 2, kMostLowTiles = 8;  // ... so many on end, at first and after it came up again ...
 constexpr float kDepth = 40.f;     // ... until it is this far below the highest that it has been
 constexpr int kNoScore = static_cast<int>(0x807fffffu);  // -infinity as an ordered integer
 constexpr float kLoScale = 28.0f;  // p_lo carries 28 times the residual (at most 16).  With 32, 2 and 1 in these places, the same
@@ -132,8 +138,8 @@ struct Ctrl {
   alignas(16) float off[kSoftmaxWarps][kMaxRows];  // kPShift - reference maximum, a copy for each warp
   alignas(16) int top[3][kMaxRows];   // largest score (ordered as an integer) of the rows that outgrew their reference, by
                                       // tile: written before a tile's vote, read after it, cleared after the next one
-  alignas(16) uint32_t low[2][kSoftmaxWarps];  // rows (row_mark) of which a warp's keys all weigh less than 2^-2, by tile parity
-  alignas(16) uint32_t alone[kSoftmaxWarps];   // and where first keys are
+  alignas(16) uint32_t low[2][kSoftmaxWarps];  // rows (row_mark) of which a warp's keys all weigh less than 2^-5, by tile parity
+  alignas(16) uint32_t alone[kSoftmaxWarps];   // and less than 2^-2, where first keys are
   alignas(16) float row_scale[kMaxRows];
   alignas(16) float lse[kMaxRows];
   alignas(16) int lim[kMaxRows];      // last key that the row sees; -1: none
@@ -260,12 +266,12 @@ __device__ __forceinline__ void find_split(const DecodeParams& p, int item, bool
 // Where a warp's marks hold its row r.
 __device__ __forceinline__ uint32_t row_mark(int r) { return 0x80u << 8 * (r & 3) >> (r >> 2); }
 
-// The rows of which no lane has a weight of 2^-2 or more: hi4 holds their e4m3 codes, four rows a word.
+// The rows of which no lane has a weight of 2^-5 or more: hi4 holds their e4m3 codes, four rows a word.
 template <int N>
 __device__ __forceinline__ uint32_t low_rows(const uint32_t (&hi4)[N]) {
   uint32_t some = 0;
 #pragma unroll
-  for (int k = 0; k < N; ++k) some |= ((hi4[k] + 0x58585858u) & 0x80808080u) >> k;  // (0x28 is the code of 2^-2, 0x7F the largest)
+  for (int k = 0; k < N; ++k) some |= ((hi4[k] + kLowCodes) & 0x80808080u) >> k;
   return ~__reduce_or_sync(0xffffffffu, some);
 }
 
@@ -624,7 +630,7 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
     bool failed = !mbar_wait(&ctrl->q_ready, 0, abort_flag);  // (the rows' factors and limits)
     float m = -INFINITY;  // reference maximum (log2 of the scaled score) of row `lane`, the same in every warp
     float peak = -INFINITY;  // the largest it has been
-    uint32_t may_sink = 0;   // marks of this warp's rows whose reference may go down
+    int low_for = 0, low_needed = kLowTiles;  // tiles on end that row `lane` has been low for; as many as lower its reference
     const int half = lane < RW ? 0 : 1;  // of the rows
     const uint32_t mark = lane < NR ? row_mark(lane % RW) : 0u;
     const auto marks = [&](bool of_row) { return __reduce_or_sync(0xffffffffu, half == r0 / RW && of_row ? mark : 0u); };
@@ -646,7 +652,6 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
           alpha = kDropFactor;
           ctrl->off[warp][lane] = kPShift - m;
         }
-        may_sink = marks(m > peak - kDepth);
         __syncwarp();
       }
       auto sees = [&](int r) -> bool {  // (r within the group)
@@ -721,6 +726,7 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
             to = best + kMargin;
           else if (best > m)  // (where one row has to move, those that need not yet go along: 114.0 -> 112.4 us)
             to = best + (best > m + kFar ? kFarMargin : kMargin);
+          if (to > m && m < peak) low_needed = min(2 * low_needed, kMostLowTiles);
           if (m != -INFINITY && to != m) alpha *= ex2_approx(m - to);
           m = to;
           peak = fmaxf(peak, m);
@@ -753,10 +759,9 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
             scores();
           }
         }
-        may_sink = marks(m > peak - kDepth);
       }
-      // Rows that lay far below their reference throughout the last tile (all warps' marks are there since the vote, and all warps
-      // find the same): it goes down, for the next tile.
+      // the rows that lay far below their reference throughout the last tile: all warps' marks are there since the vote, and all
+      // warps find the same
       const uint4 low_by = *reinterpret_cast<const uint4*>(&ctrl->low[sb ^ 1][4 * half]);
       if (warp == 0 && lane < NR) ctrl->top[third == 0 ? 2 : third - 1][lane] = kNoScore;  // (the last tile's: all have read it)
       third = third == 2 ? 0 : third + 1;
@@ -817,10 +822,11 @@ __device__ __forceinline__ void take_split(const CUtensorMap& tm_kv, const Decod
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctrl->p_full[sb]);
-      uint32_t low = low_rows(hi4) & may_sink;
+      uint32_t low = low_rows(hi4);
       if (edge && !kTree) low &= marks(ctrl->lim[lane % NR] >= k0);  // (rows that see none of these keys stay)
       if (lane == 0) ctrl->low[sb][warp] = low;
-      sunk = __ballot_sync(0xffffffffu, (low_by.x & low_by.y & low_by.z & low_by.w & mark) != 0) & ~moved;
+      low_for = (low_by.x & low_by.y & low_by.z & low_by.w & mark) != 0 && !((moved >> lane) & 1) ? low_for + 1 : 0;
+      sunk = __ballot_sync(0xffffffffu, low_for >= low_needed && m > peak - kDepth);
     }
     const float ls = lanes_reduce<RW>(l_sum, lane);
     if (lane % (32 / RW) == 0) ctrl->sums[quad][r0 + lane / (32 / RW)] = ls;

@@ -7,9 +7,10 @@ that the codes stand for.  Tolerances, of non-negative terms w_j v_j:
     residual's binade top, together 2^-9 of the weight; 2^-11 for the f16; as much as these once more for what a sum of
     them may differ from the rounded terms' (the sum that divides them is of the unrounded weights);
   * below lo's normal range it is off by at most half of lo's last step, 2^-10 / 28 < 2^-14.8, in units in which a tile's
-    largest weight is more than 2^-2, so 2^-12.8 of that, once the reference has followed it down: by 2^8 two tiles after a tile
-    that lay at most at 2^-2.  Beside a heavy key, which is 448 in these units, and in the two tiles behind it, that is 2^-23.6
-    of its weight (at least 40 where several stand at one height: 2^-20.1), 2^-8 of that in the next two, and so on.
+    largest weight is at least 2^-5, so 2^-9.8 of that, once the reference has followed it down: by 2^8 after two tiles below
+    2^-5 and one that goes by.  Beside a heavy key, which is 448 in these units, and in the three tiles behind it, that is
+    2^-23.6 of its weight, 2^-8 of that in the next three, and so on.  Of several at one height the least weight is 40, and
+    references that have come up again wait for more tiles: 2^-20.1 up to the next heavy key.
     And it is never off by more than itself: what is carried is between 0 and twice the weight;
   * the output's rounding 2^-8, a split's f16 partial 2^-11 and 2^-25 of the codes' unit;
   * scores: A = scale sum_i |q_i k_i|, the largest of any key: 36 accumulation steps 2^-17 A, the query's split at most
@@ -70,16 +71,16 @@ def floors(w, v, heavy):
     tiles = -(-n // 128)
     per = torch.zeros(H, tiles * 128, dtype=torch.float64, device=w.device)
     per[:, :n] = w
-    floor = per.view(H, tiles, 128).amax(-1) * 2.0 ** -12.8
+    floor = per.view(H, tiles, 128).amax(-1) * 2.0 ** -9.8
     for j in heavy:
-        for t in range(j // 128, min(tiles, j // 128 + 13)):
-            down = max(0, t - j // 128 - 1) // 2 * 8
-            floor[:, t] = torch.maximum(floor[:, t], per[:, j] * 2.0 ** ((-23.6 if len(heavy) == 1 else -20.1) - down))
+        for t in range(j // 128, min(tiles, j // 128 + 19)):
+            down = max(0, t - j // 128 - 1) // 3 * 8
+            floor[:, t] = torch.maximum(floor[:, t], per[:, j] * 2.0 ** (-23.6 - down if len(heavy) == 1 else -20.1))
     for j in heavy:
         others = (w[:, j // 128 * 128:(j // 128 + 1) * 128] * 1.0)
         others[:, j % 128] = 0
         top = per[:, j] * 2.0 ** (-23.6 if len(heavy) == 1 else -20.1)
-        floor[:, j // 128] = torch.maximum(top, others.amax(-1) * 2.0 ** -12.8)
+        floor[:, j // 128] = torch.maximum(top, others.amax(-1) * 2.0 ** -9.8)
     floor = floor.repeat_interleave(128, 1)[:, :n]
     return torch.minimum(floor, w) @ v
 
